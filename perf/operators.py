@@ -269,10 +269,10 @@ def run(st):
         return dict(logp=gbce.linear_selective_logsoftmax(st["hidden"], st["weight"], st["index"], T,
                                                           st["mask"]))
     if op == "logp_step":
-        logp, lse = gbce.linear_selective_logsoftmax(st["hidden"], st["weight"], st["index"], T,
-                                                     st["mask"], want_lse=True)
+        logp, state = gbce.linear_selective_logsoftmax(st["hidden"], st["weight"], st["index"], T,
+                                                       st["mask"], with_state=True)
         dh, dw = gbce.linear_selective_logsoftmax_bwd(st["hidden"], st["weight"], st["index"],
-                                                      st["grad_logp"], logp, lse, T, st["mask"])
+                                                      st["grad_logp"], logp, state, T, st["mask"])
         return dict(logp=logp, dhidden=dh, dweight=dw)
     if op == "lookup":
         return dict(rows=gbce.embedding_lookup(st["weight"], st["tokens"], st["scale"]))
