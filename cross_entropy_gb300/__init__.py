@@ -26,6 +26,11 @@ Functions (same names as the C ABI):
   head ("Fix softmax collapse ...", "Summary", first bullet), with
   :func:`gather_slice_partials` moving the per-slice statistics between
   ranks through torch.distributed.
+* :func:`linear_selective_logsoftmax` (and ``_bwd``), :func:`linear_ce_fwd`,
+  :func:`linear_ce_bwd`, :func:`linear_ce_fwd_bwd_fused` -- the same two from
+  hidden states and the head's weight, without keeping the logits; and
+  :func:`embedding_lookup` (and ``_bwd``), the same table's lookup (module
+  ``linear``).
 
 Caller-supplied output, scratch and status tensors are checked for device,
 dtype and size before any GPU work: the kernels write through their data
@@ -75,6 +80,24 @@ _SIGNATURES = {
                                    _vp, _vp, _vp]),
     "vocab_slice_grad": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp,
                                 _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "gbce_linear_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i32, _i32]),
+    "linear_selective_logsoftmax": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp,
+                                           _i64, _f32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "linear_selective_logsoftmax_bwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp,
+                                               _i64, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                                               _i64, _i32, _vp, _sz, _vp, _vp]),
+    "linear_ce_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _i32,
+                             _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "linear_ce_bwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _i32,
+                             _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _sz, _vp, _vp]),
+    "linear_ce_fwd_bwd_fused": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64,
+                                       _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
+                                       _i32, _vp, _sz, _vp, _vp]),
+    "gbce_embedding_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "embedding_lookup": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i64,
+                                _vp, _vp]),
+    "embedding_lookup_bwd": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i64,
+                                    _i32, _vp, _sz, _vp, _vp]),
 }
 MAX_SLICES = 64
 
@@ -599,3 +622,10 @@ def vocab_slice_grad(logits_slice: torch.Tensor, index, vocab_offset: int, vocab
     _check(st, "vocab_slice_grad")
     return dlogits
 
+
+# ------------------------------------------- from hidden states; table lookup
+
+from .linear import (LinearCeForward, LinearCeFused, embedding_lookup,  # noqa: E402,F401
+                     embedding_lookup_bwd, linear_ce_bwd, linear_ce_fwd,
+                     linear_ce_fwd_bwd_fused, linear_selective_logsoftmax,
+                     linear_selective_logsoftmax_bwd, linear_workspace_size)

@@ -1,0 +1,89 @@
+// Internal interface of the calls that start from hidden states: the logits
+// are tiles of hidden . weight^T that never reach memory as a whole.
+//
+//   z[i, v]  = sum_d hidden[i, d] weight[v, d]
+//   stats    = per (row, vocabulary tile): max and sum of exp over the columns
+//              that the row does not gather, and its gathered columns' logits
+//   dz[i, v] = coef_i 2^{(z - M_i) c} / S_i, gathered columns in the expm1 form
+//   dhidden  = alpha dz . weight          dweight = alpha dz^T . hidden
+//
+// Rows that take no part (masked, ignored, or with a label out of range) are
+// left out first: the kernels work on the live rows, packed one after another.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gbce {
+
+// Rows of the packed buffers are padded to this many; one vocabulary tile of
+// the statistics is this wide.
+constexpr int kLinRowPad = 256;
+constexpr int kLinTileV = 256;
+// Vocabulary columns in one piece of the backward: a multiple of this.
+constexpr int64_t kLinPieceUnit = 76 * 256;
+
+// First words of the workspace, written by the plan kernel (n_live, n_items)
+// and the prepare kernel (alpha).
+struct LinHeader {
+    int64_t n_items;  // rows that count towards the mean
+    int32_t n_live;   // rows packed
+    float alpha;      // factor of both gradients that is the same for every row
+};
+
+// row_map values of rows that are not packed.
+constexpr int32_t kLinRowSkipped = -1;  // masked or ignored: zeros
+constexpr int32_t kLinRowBad = -2;      // a target out of range: NaN
+
+struct LinParams {
+    const void *hidden, *weight;
+    int64_t hidden_stride, weight_stride;  // elements
+    int64_t rows, vocab, dim;
+    bool bf16;
+    const int64_t *targets;  // [rows, k]
+    int64_t k;
+    bool token_ce;        // k = 1 targets are labels, ignore_index rows are skipped
+    bool whole_rows;      // a row with any target out of range is left out whole
+    int64_t ignore_index;
+    const uint8_t *row_mask;
+    float T, c;           // temperature, log2(e) / T
+
+    // forward outputs, by original row (each nullable)
+    float *logp_out;      // [rows, k]
+    float *state_out;     // [rows, 2] max and sum over the row's columns
+    float *loss_rows;     // [rows]
+    int64_t *n_items_out; // [1]
+
+    // backward
+    const float *grad_out;    // CE: [rows] or [1]; selective: [rows, k]
+    int reduction;            // CE: 0 none, 1 sum, 2 mean
+    const int64_t *n_items;   // CE mean; null: the header's
+    const float *saved_logp, *saved_state;
+    void *dhidden, *dweight;  // either may be null
+    int64_t dhidden_stride, dweight_stride;
+    bool accumulate;          // dweight += instead of =
+
+    // workspace
+    LinHeader *head;
+    int32_t *row_list, *row_map;  // packed -> original, original -> packed
+    int32_t *tgt;                 // [rows_pad, k] packed targets (-1: out of range)
+    float *xt;                    // [rows_pad, k] their logits
+    float2 *partials;             // [rows_pad, tiles]
+    float2 *grow;                 // [rows_pad] (M, coef / S)
+    float *dzt;                   // [rows_pad, k] dz of the gathered columns
+    void *hpack;                  // packed live rows
+    void *dz;                     // [rows_pad, piece]
+    float *dh;                    // [splits, rows_pad, dim]
+    int64_t rows_pad, tiles, piece;
+
+    int32_t *dev_status;
+};
+
+cudaError_t lin_plan(const LinParams &p, cudaStream_t s);
+cudaError_t lin_pack(const LinParams &p, cudaStream_t s);
+cudaError_t lin_stats(const LinParams &p, cudaStream_t s);
+cudaError_t lin_combine(const LinParams &p, cudaStream_t s);
+cudaError_t lin_prepare(const LinParams &p, cudaStream_t s);
+cudaError_t lin_grads(const LinParams &p, cudaStream_t s);
+
+}  // namespace gbce

@@ -1,0 +1,451 @@
+// C-ABI entry points of the calls that start from hidden states (declared in
+// include/gbce.h): host-side argument checks, workspace layout, dispatch.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/gbce.h"
+#include "gbce_internal.h"
+#include "gbce_linear.h"
+
+using gbce::LinParams;
+
+namespace {
+
+constexpr int64_t kMaxVocab = INT32_MAX - 64;
+constexpr int64_t kMaxRows = int64_t{1} << 24;
+constexpr int64_t kMaxDim = int64_t{1} << 20;
+// Bytes of dz that one piece of the vocabulary may take beyond its smallest
+// width (kLinPieceUnit columns).
+constexpr int64_t kPieceBytes = int64_t{512} << 20;
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+size_t elem_size(gbce_dtype dt) { return dt == GBCE_BF16 ? 2 : 4; }
+
+struct Layout {
+    size_t head, row_list, row_map, tgt, xt, partials, loss, logp, state, grow, dzt, hpack, dz, dh;
+    size_t total;
+    int64_t rows_pad, tiles, piece;
+};
+
+// Where everything lies in the workspace.  With `backward`, the buffers of
+// the gradient (and of the statistics, which a fused call needs too).
+Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt, bool backward)
+{
+    Layout w{};
+    size_t off = 0;
+    const auto take = [&off](int64_t n, size_t bytes) {
+        const size_t at = off;
+        off += align_up(static_cast<size_t>(n) * bytes, 256);
+        return at;
+    };
+    const size_t es = elem_size(dt);
+    w.rows_pad = round_up(rows, gbce::kLinRowPad);
+    w.tiles = (vocab + gbce::kLinTileV - 1) / gbce::kLinTileV;
+    w.head = take(1, sizeof(gbce::LinHeader));
+    w.row_list = take(rows, 4);
+    w.row_map = take(rows, 4);
+    w.tgt = take(w.rows_pad * k, 4);
+    w.xt = take(w.rows_pad * k, 4);
+    w.loss = take(rows, 4);
+    w.hpack = take(w.rows_pad * dim, es);
+    w.partials = take(w.rows_pad * w.tiles, 8);
+    if (backward) {
+        w.logp = take(rows * k, 4);
+        w.state = take(rows * 2, 4);
+        w.grow = take(w.rows_pad, 8);
+        w.dzt = take(w.rows_pad * k, 4);
+        const int64_t full = round_up(vocab, gbce::kLinTileV);
+        int64_t units = kPieceBytes / (w.rows_pad * gbce::kLinPieceUnit * static_cast<int64_t>(es));
+        units = units < 1 ? 1 : units;
+        w.piece = units * gbce::kLinPieceUnit < full ? units * gbce::kLinPieceUnit : full;
+        w.dz = take(w.rows_pad * w.piece, es);
+        w.dh = take(w.rows_pad * dim, 4);
+    }
+    w.total = off;
+    return w;
+}
+
+bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
+size_t span(int64_t rows, int64_t stride, int64_t dim, gbce_dtype dt)
+{
+    return static_cast<size_t>((rows - 1) * stride + dim) * elem_size(dt);
+}
+
+// A [n, dim] matrix of rows `stride` apart: addressable and of its type's alignment.
+gbce_status check_matrix(const void *p, int64_t n, int64_t stride, int64_t dim, gbce_dtype dt)
+{
+    if (p == nullptr || stride < dim || stride > (INT64_MAX / 16) / (n > 0 ? n : 1))
+        return GBCE_EINVAL;
+    return reinterpret_cast<uintptr_t>(p) % elem_size(dt) == 0 ? GBCE_OK : GBCE_EDTYPE;
+}
+
+struct Shape {
+    const void *hidden;
+    int64_t hidden_stride;
+    const void *weight;
+    int64_t weight_stride;
+    gbce_dtype dtype;
+    int64_t rows, vocab, dim, k;
+    float temperature;
+};
+
+gbce_status check_shape(const Shape &a)
+{
+    if (a.dtype != GBCE_F32 && a.dtype != GBCE_BF16)
+        return GBCE_EDTYPE;
+    if (a.rows < 0 || a.rows > kMaxRows || a.vocab < 1 || a.vocab > kMaxVocab || a.dim < 1 ||
+        a.dim > kMaxDim || a.k < 1 || a.k > GBCE_MAX_K)
+        return GBCE_EINVAL;
+    if (!(std::isfinite(a.temperature) && a.temperature > 0.0f))
+        return GBCE_EINVAL;
+    if (a.rows == 0)
+        return GBCE_OK;
+    const gbce_status st = check_matrix(a.hidden, a.rows, a.hidden_stride, a.dim, a.dtype);
+    return st != GBCE_OK ? st : check_matrix(a.weight, a.vocab, a.weight_stride, a.dim, a.dtype);
+}
+
+struct Grads {
+    void *dhidden;
+    int64_t dhidden_stride;
+    void *dweight;
+    int64_t dweight_stride;
+    bool accumulate;
+};
+
+gbce_status check_grads(const Shape &a, const Grads &g)
+{
+    if (g.dhidden == nullptr && g.dweight == nullptr)
+        return GBCE_EINVAL;
+    const size_t hb = span(a.rows, a.hidden_stride, a.dim, a.dtype);
+    const size_t wb = span(a.vocab, a.weight_stride, a.dim, a.dtype);
+    size_t db = 0;
+    if (g.dhidden != nullptr) {
+        const gbce_status st = check_matrix(g.dhidden, a.rows, g.dhidden_stride, a.dim, a.dtype);
+        if (st != GBCE_OK)
+            return st;
+        db = span(a.rows, g.dhidden_stride, a.dim, a.dtype);
+        if (overlap(g.dhidden, db, a.hidden, hb) || overlap(g.dhidden, db, a.weight, wb))
+            return GBCE_EINVAL;
+    }
+    if (g.dweight != nullptr) {
+        const gbce_status st = check_matrix(g.dweight, a.vocab, g.dweight_stride, a.dim, a.dtype);
+        if (st != GBCE_OK)
+            return st;
+        const size_t n = span(a.vocab, g.dweight_stride, a.dim, a.dtype);
+        if (overlap(g.dweight, n, a.hidden, hb) || overlap(g.dweight, n, a.weight, wb) ||
+            (g.dhidden != nullptr && overlap(g.dweight, n, g.dhidden, db)))
+            return GBCE_EINVAL;
+    }
+    return GBCE_OK;
+}
+
+gbce_status check_workspace(const void *ws, size_t bytes, const Layout &w)
+{
+    if (ws == nullptr || bytes < w.total || reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+        return GBCE_EWORKSPACE;
+    return GBCE_OK;
+}
+
+template <typename P>
+P *at(void *ws, size_t off)
+{
+    return reinterpret_cast<P *>(static_cast<char *>(ws) + off);
+}
+
+LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32_t *dev_status)
+{
+    LinParams p{};
+    p.hidden = a.hidden;
+    p.weight = a.weight;
+    p.hidden_stride = a.hidden_stride;
+    p.weight_stride = a.weight_stride;
+    p.rows = a.rows;
+    p.vocab = a.vocab;
+    p.dim = a.dim;
+    p.bf16 = a.dtype == GBCE_BF16;
+    p.k = a.k;
+    p.T = a.temperature;
+    p.c = static_cast<float>(1.4426950408889634 / static_cast<double>(a.temperature));
+    p.head = at<gbce::LinHeader>(ws, w.head);
+    p.row_list = at<int32_t>(ws, w.row_list);
+    p.row_map = at<int32_t>(ws, w.row_map);
+    p.tgt = at<int32_t>(ws, w.tgt);
+    p.xt = at<float>(ws, w.xt);
+    p.partials = at<float2>(ws, w.partials);
+    p.hpack = at<void>(ws, w.hpack);
+    if (backward) {
+        p.grow = at<float2>(ws, w.grow);
+        p.dzt = at<float>(ws, w.dzt);
+        p.dz = at<void>(ws, w.dz);
+        p.dh = at<float>(ws, w.dh);
+    }
+    p.rows_pad = w.rows_pad;
+    p.tiles = w.tiles;
+    p.piece = w.piece;
+    p.dev_status = dev_status;
+    return p;
+}
+
+void set_grads(LinParams &p, const Grads &g)
+{
+    p.dhidden = g.dhidden;
+    p.dweight = g.dweight;
+    p.dhidden_stride = g.dhidden_stride;
+    p.dweight_stride = g.dweight_stride;
+    p.accumulate = g.accumulate;
+}
+
+cudaError_t select_rows(const LinParams &p, cudaStream_t s)
+{
+    const cudaError_t e = gbce::lin_plan(p, s);
+    return e != cudaSuccess ? e : gbce::lin_pack(p, s);
+}
+
+cudaError_t forward(const LinParams &p, cudaStream_t s)
+{
+    const cudaError_t e = gbce::lin_stats(p, s);
+    return e != cudaSuccess ? e : gbce::lin_combine(p, s);
+}
+
+cudaError_t backward(const LinParams &p, cudaStream_t s)
+{
+    const cudaError_t e = gbce::lin_prepare(p, s);
+    return e != cudaSuccess ? e : gbce::lin_grads(p, s);
+}
+
+bool valid_reduction(gbce_reduction r) { return r == GBCE_NONE || r == GBCE_SUM || r == GBCE_MEAN; }
+
+gbce_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GBCE_OK : GBCE_ECUDA; }
+
+// dweight of a call without rows: zeros, unless it accumulates.
+cudaError_t zero_dweight(const Shape &a, const Grads &g, cudaStream_t s)
+{
+    if (g.dweight == nullptr || g.accumulate)
+        return cudaSuccess;
+    const size_t es = elem_size(a.dtype);
+    return cudaMemset2DAsync(g.dweight, static_cast<size_t>(g.dweight_stride) * es, 0,
+                             static_cast<size_t>(a.dim) * es, static_cast<size_t>(a.vocab), s);
+}
+
+// The loss, and with `g` both gradients after it.
+gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
+                    gbce_reduction reduction, const float *grad_out, float *loss_out,
+                    float *logp_out, float *row_state_out, int64_t *n_items_out, const Grads *g,
+                    void *workspace, size_t workspace_bytes, int32_t *dev_status, cudaStream_t s)
+{
+    gbce_status st = check_shape(a);
+    if (st != GBCE_OK)
+        return st;
+    if (!valid_reduction(reduction))
+        return GBCE_EINVAL;
+    if (a.rows == 0) {
+        if (reduction != GBCE_NONE && loss_out == nullptr)
+            return GBCE_EINVAL;
+        cudaError_t e = g != nullptr ? zero_dweight(a, *g, s) : cudaSuccess;
+        if (e == cudaSuccess && reduction != GBCE_NONE)
+            e = cudaMemsetAsync(loss_out, 0, sizeof(float), s);
+        if (e == cudaSuccess && n_items_out != nullptr)
+            e = cudaMemsetAsync(n_items_out, 0, sizeof(int64_t), s);
+        return cuda_status(e);
+    }
+    if (labels == nullptr || loss_out == nullptr)
+        return GBCE_EINVAL;
+    if (g != nullptr && (st = check_grads(a, *g)) != GBCE_OK)
+        return st;
+    const Layout w = layout(a.rows, a.vocab, a.dim, 1, a.dtype, g != nullptr);
+    if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
+        return st;
+    LinParams p = params(a, w, workspace, g != nullptr, dev_status);
+    p.targets = labels;
+    p.token_ce = true;
+    p.ignore_index = ignore_index;
+    p.reduction = static_cast<int>(reduction);
+    p.n_items_out = n_items_out;
+    p.loss_rows = reduction == GBCE_NONE ? loss_out : at<float>(workspace, w.loss);
+    // the gradient takes the log-probs and the row states, wanted or not
+    p.logp_out = logp_out != nullptr || g == nullptr ? logp_out : at<float>(workspace, w.logp);
+    p.state_out = row_state_out != nullptr || g == nullptr ? row_state_out
+                                                           : at<float>(workspace, w.state);
+    cudaError_t e = select_rows(p, s);
+    if (e == cudaSuccess)
+        e = forward(p, s);
+    if (e == cudaSuccess && reduction != GBCE_NONE)
+        e = gbce::launch_reduce_loss(p.loss_rows, labels, a.rows, ignore_index,
+                                     static_cast<int>(reduction), &p.head->n_items, nullptr,
+                                     loss_out, s);
+    if (e != cudaSuccess || g == nullptr)
+        return cuda_status(e);
+    p.grad_out = grad_out;
+    p.saved_logp = p.logp_out;
+    p.saved_state = p.state_out;
+    set_grads(p, *g);
+    return cuda_status(backward(p, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gbce_linear_workspace_size(int64_t rows, int64_t vocab, int64_t dim, int64_t k,
+                                  gbce_dtype dtype, int backward)
+{
+    if ((dtype != GBCE_F32 && dtype != GBCE_BF16) || rows <= 0 || rows > kMaxRows || vocab < 1 ||
+        vocab > kMaxVocab || dim < 1 || dim > kMaxDim || k < 1 || k > GBCE_MAX_K)
+        return 0;
+    return layout(rows, vocab, dim, k, dtype, backward != 0).total;
+}
+
+gbce_status linear_selective_logsoftmax(const void *hidden, int64_t hidden_row_stride,
+                                        const void *weight, int64_t weight_row_stride,
+                                        gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim,
+                                        const int64_t *index, int64_t k, float temperature,
+                                        const uint8_t *row_mask, float *logp_out,
+                                        float *row_state_out, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    const Shape a{hidden, hidden_row_stride, weight, weight_row_stride, dtype,
+                  rows,   vocab,             dim,    k,                 temperature};
+    gbce_status st = check_shape(a);
+    if (st != GBCE_OK || rows == 0)
+        return st;
+    if (index == nullptr || logp_out == nullptr)
+        return GBCE_EINVAL;
+    const Layout w = layout(rows, vocab, dim, k, dtype, false);
+    if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
+        return st;
+    LinParams p = params(a, w, workspace, false, dev_status);
+    p.targets = index;
+    p.row_mask = row_mask;
+    p.logp_out = logp_out;
+    p.state_out = row_state_out;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = select_rows(p, s);
+    if (e == cudaSuccess)
+        e = forward(p, s);
+    return cuda_status(e);
+}
+
+gbce_status linear_selective_logsoftmax_bwd(
+    const void *hidden, int64_t hidden_row_stride, const void *weight, int64_t weight_row_stride,
+    gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim, const int64_t *index, int64_t k,
+    float temperature, const uint8_t *row_mask, const float *grad_logp, const float *saved_logp,
+    const float *row_state, void *dhidden, int64_t dhidden_row_stride, void *dweight,
+    int64_t dweight_row_stride, int accumulate, void *workspace, size_t workspace_bytes,
+    int32_t *dev_status, void *stream)
+{
+    const Shape a{hidden, hidden_row_stride, weight, weight_row_stride, dtype,
+                  rows,   vocab,             dim,    k,                 temperature};
+    const Grads g{dhidden, dhidden_row_stride, dweight, dweight_row_stride, accumulate != 0};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    gbce_status st = check_shape(a);
+    if (st != GBCE_OK)
+        return st;
+    if (rows == 0)
+        return cuda_status(zero_dweight(a, g, s));
+    if (index == nullptr || grad_logp == nullptr || saved_logp == nullptr || row_state == nullptr)
+        return GBCE_EINVAL;
+    if ((st = check_grads(a, g)) != GBCE_OK)
+        return st;
+    const Layout w = layout(rows, vocab, dim, k, dtype, true);
+    if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
+        return st;
+    LinParams p = params(a, w, workspace, true, dev_status);
+    p.targets = index;
+    p.whole_rows = true;
+    p.row_mask = row_mask;
+    p.grad_out = grad_logp;
+    p.saved_logp = saved_logp;
+    p.saved_state = row_state;
+    set_grads(p, g);
+    cudaError_t e = select_rows(p, s);
+    if (e == cudaSuccess)
+        e = backward(p, s);
+    return cuda_status(e);
+}
+
+gbce_status linear_ce_fwd(const void *hidden, int64_t hidden_row_stride, const void *weight,
+                          int64_t weight_row_stride, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t dim, const int64_t *labels, int64_t ignore_index,
+                          float temperature, gbce_reduction reduction, float *loss_out,
+                          float *logp_out, float *row_state_out, int64_t *n_items_out,
+                          void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                          void *stream)
+{
+    const Shape a{hidden, hidden_row_stride, weight, weight_row_stride, dtype,
+                  rows,   vocab,             dim,    1,                 temperature};
+    return ce_call(a, labels, ignore_index, reduction, nullptr, loss_out, logp_out, row_state_out,
+                   n_items_out, nullptr, workspace, workspace_bytes, dev_status,
+                   static_cast<cudaStream_t>(stream));
+}
+
+gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const void *weight,
+                          int64_t weight_row_stride, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t dim, const int64_t *labels, int64_t ignore_index,
+                          float temperature, gbce_reduction reduction, const float *grad_out,
+                          const float *saved_logp, const float *row_state, const int64_t *n_items,
+                          void *dhidden, int64_t dhidden_row_stride, void *dweight,
+                          int64_t dweight_row_stride, int accumulate, void *workspace,
+                          size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    const Shape a{hidden, hidden_row_stride, weight, weight_row_stride, dtype,
+                  rows,   vocab,             dim,    1,                 temperature};
+    const Grads g{dhidden, dhidden_row_stride, dweight, dweight_row_stride, accumulate != 0};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    gbce_status st = check_shape(a);
+    if (st != GBCE_OK)
+        return st;
+    if (!valid_reduction(reduction))
+        return GBCE_EINVAL;
+    if (rows == 0)
+        return cuda_status(zero_dweight(a, g, s));
+    if (labels == nullptr || grad_out == nullptr || saved_logp == nullptr || row_state == nullptr ||
+        (reduction == GBCE_MEAN && n_items == nullptr))
+        return GBCE_EINVAL;
+    if ((st = check_grads(a, g)) != GBCE_OK)
+        return st;
+    const Layout w = layout(rows, vocab, dim, 1, dtype, true);
+    if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
+        return st;
+    LinParams p = params(a, w, workspace, true, dev_status);
+    p.targets = labels;
+    p.token_ce = true;
+    p.ignore_index = ignore_index;
+    p.grad_out = grad_out;
+    p.reduction = static_cast<int>(reduction);
+    p.n_items = n_items;
+    p.saved_logp = saved_logp;
+    p.saved_state = row_state;
+    set_grads(p, g);
+    cudaError_t e = select_rows(p, s);
+    if (e == cudaSuccess)
+        e = backward(p, s);
+    return cuda_status(e);
+}
+
+gbce_status linear_ce_fwd_bwd_fused(
+    const void *hidden, int64_t hidden_row_stride, const void *weight, int64_t weight_row_stride,
+    gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim, const int64_t *labels,
+    int64_t ignore_index, float temperature, gbce_reduction reduction, const float *grad_out,
+    float *loss_out, float *logp_out, float *row_state_out, int64_t *n_items_out, void *dhidden,
+    int64_t dhidden_row_stride, void *dweight, int64_t dweight_row_stride, int accumulate,
+    void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    const Shape a{hidden, hidden_row_stride, weight, weight_row_stride, dtype,
+                  rows,   vocab,             dim,    1,                 temperature};
+    const Grads g{dhidden, dhidden_row_stride, dweight, dweight_row_stride, accumulate != 0};
+    if (rows > 0 && grad_out == nullptr)
+        return GBCE_EINVAL;
+    return ce_call(a, labels, ignore_index, reduction, grad_out, loss_out, logp_out, row_state_out,
+                   n_items_out, &g, workspace, workspace_bytes, dev_status,
+                   static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -398,6 +398,140 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
                              int32_t *dev_status, void *stream);
 
 /*
+ * The calls that start from hidden states: the logits are
+ *   logits[r, v] = sum_d hidden[r, d] weight[v, d]
+ * (the language-model head), and no more of them than a tile is ever kept.
+ * Log-probs, losses and gradients are those of the calls above on these
+ * logits, the gradients with respect to hidden and weight:
+ *   dhidden = dlogits . weight          dweight = dlogits^T . hidden.
+ *
+ * Source: the operators "softmax cross-entropy / selective log-softmax
+ * behind a linear head" that the unsloth-zoo #2080 commit quoted on "Fix
+ * softmax collapse ..." describes ("Fix": the running sum excludes the
+ * target, log p_t = -softplus(log s_others + m - z_t), the target's gradient
+ * by -expm1(log p_t)), row selection before any vocabulary work from
+ * ms-swift PR #10353, "PR information".
+ *
+ *  - Types.  hidden, weight and their gradients have one type, fp32 or bf16.
+ *    Products are summed in fp32; log-probs, losses and row states are fp32.
+ *    In a bf16 call the gradient of the logits is rounded once to bf16
+ *    before the products that give dhidden and dweight, which are summed in
+ *    fp32 and rounded once.
+ *  - Layout.  hidden: [rows, dim], weight: [vocab, dim], rows hidden_row_stride
+ *    and weight_row_stride elements apart (>= dim), any alignment of the
+ *    element type; likewise dhidden and dweight.  Rows of 16-byte multiples
+ *    are read in place, others are laid out anew in the workspace.
+ *  - Rows left out (row_mask[r] == 0, or label == ignore_index) are neither
+ *    read nor multiplied, whatever they hold: log p 0, loss 0, row state
+ *    (-inf, 0), dhidden 0, no part in dweight.
+ *  - A label outside [0, vocab), or in the backward an index outside it,
+ *    sets its dev_status bit, makes the row's log p, loss and dhidden NaN
+ *    and leaves the row out of dweight.  In the selective forward an index
+ *    outside [0, vocab) makes its own log p NaN only.
+ *  - Row state.  row_state[r] = (M, S): the max of the row's logits and
+ *    sum_v exp((z_v - M) / T), as vocab_slice_combine gives it.  A backward
+ *    call takes it with the forward's log p; it forms the logits again, by
+ *    the same steps.
+ *  - dweight with accumulate != 0: dweight += the gradient (read, added in
+ *    fp32, rounded once), else dweight = the gradient, rows of the table
+ *    that get none being zeros.  dhidden or dweight may be NULL: it is not
+ *    computed.
+ *  - workspace: gbce_linear_workspace_size bytes, 16-byte aligned, of one
+ *    call at a time (a captured graph keeps its own).
+ *  - Sums are in a fixed order: the same call gives the same bits.
+ * Errors: GBCE_EINVAL for rows outside [0, 2^24], dim outside [1, 2^20],
+ * vocab < 1, strides below dim, k, temperature and NULL pointers as above,
+ * outputs that overlap an input or each other, no gradient wanted at all;
+ * GBCE_EDTYPE; GBCE_EWORKSPACE.  Label smoothing, DFT, soft-capping and the
+ * entropy are not available on this path.
+ */
+
+/* Bytes of workspace of a call; backward: 0 for the two forward calls.
+ * A pure function of its arguments; 0 for arguments that no call takes. */
+size_t gbce_linear_workspace_size(int64_t rows, int64_t vocab, int64_t dim, int64_t k,
+                                  gbce_dtype dtype, int backward);
+
+/* selective_logsoftmax of hidden . weight^T.  row_state_out: [rows, 2] or NULL. */
+gbce_status linear_selective_logsoftmax(const void *hidden, int64_t hidden_row_stride,
+                                        const void *weight, int64_t weight_row_stride,
+                                        gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim,
+                                        const int64_t *index, int64_t k, float temperature,
+                                        const uint8_t *row_mask, float *logp_out,
+                                        float *row_state_out, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Gradient of sum_k grad_logp[r, k] * logp[r, k] with respect to hidden and
+ * weight.  grad_logp, saved_logp: [rows, k]; row_state: [rows, 2]. */
+gbce_status linear_selective_logsoftmax_bwd(
+    const void *hidden, int64_t hidden_row_stride, const void *weight, int64_t weight_row_stride,
+    gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim, const int64_t *index, int64_t k,
+    float temperature, const uint8_t *row_mask, const float *grad_logp, const float *saved_logp,
+    const float *row_state, void *dhidden, int64_t dhidden_row_stride, void *dweight,
+    int64_t dweight_row_stride, int accumulate, void *workspace, size_t workspace_bytes,
+    int32_t *dev_status, void *stream);
+
+/* ce_fwd of hidden . weight^T; logp_out, row_state_out and n_items_out may be NULL. */
+gbce_status linear_ce_fwd(const void *hidden, int64_t hidden_row_stride, const void *weight,
+                          int64_t weight_row_stride, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t dim, const int64_t *labels, int64_t ignore_index,
+                          float temperature, gbce_reduction reduction, float *loss_out,
+                          float *logp_out, float *row_state_out, int64_t *n_items_out,
+                          void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                          void *stream);
+
+/* Both gradients from linear_ce_fwd's log p and row state; grad_out and
+ * n_items as in ce_bwd. */
+gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const void *weight,
+                          int64_t weight_row_stride, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t dim, const int64_t *labels, int64_t ignore_index,
+                          float temperature, gbce_reduction reduction, const float *grad_out,
+                          const float *saved_logp, const float *row_state, const int64_t *n_items,
+                          void *dhidden, int64_t dhidden_row_stride, void *dweight,
+                          int64_t dweight_row_stride, int accumulate, void *workspace,
+                          size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Loss and both gradients in one call. */
+gbce_status linear_ce_fwd_bwd_fused(
+    const void *hidden, int64_t hidden_row_stride, const void *weight, int64_t weight_row_stride,
+    gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t dim, const int64_t *labels,
+    int64_t ignore_index, float temperature, gbce_reduction reduction, const float *grad_out,
+    float *loss_out, float *logp_out, float *row_state_out, int64_t *n_items_out, void *dhidden,
+    int64_t dhidden_row_stride, void *dweight, int64_t dweight_row_stride, int accumulate,
+    void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The table's other end: rows of a [vocab, dim] table by token, times a
+ * scale (with a tied table, the weight of the calls above), and the
+ * gradient of that lookup, which with accumulate joins the head's gradient
+ * of the same table:
+ *   out[r]    = scale * table[tokens[r]]
+ *   dtable[v] = scale * sum_{r : tokens[r] = v} grad_out[r]   (+ dtable[v])
+ * summed in fp32 in a fixed order and rounded once.  tokens: [rows] int64; a
+ * token equal to ignore_index (padding) gives a row of zeros and no
+ * gradient, whatever its gradient row holds; one outside [0, vocab)
+ * otherwise sets GBCE_DEV_BAD_INDEX, gives a NaN row and no gradient.
+ * Without accumulate every row of dtable is written (zeros where no token
+ * names it); with it only the rows that tokens name are touched.  One type
+ * for table, out, grad_out and dtable; any row strides >= dim, any alignment
+ * of the element type; outputs must not overlap inputs; scale finite.
+ * workspace: gbce_embedding_workspace_size bytes, 16-byte aligned.
+ *
+ * Source: no page has it; it completes the gradient of a tied head (above).
+ */
+size_t gbce_embedding_workspace_size(int64_t rows, int64_t vocab, int64_t dim);
+
+gbce_status embedding_lookup(const void *table, int64_t table_row_stride, gbce_dtype dtype,
+                             int64_t vocab, int64_t dim, const int64_t *tokens, int64_t rows,
+                             int64_t ignore_index, float scale, void *out, int64_t out_row_stride,
+                             int32_t *dev_status, void *stream);
+
+gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, gbce_dtype dtype,
+                                 int64_t rows, int64_t dim, const int64_t *tokens, int64_t vocab,
+                                 int64_t ignore_index, float scale, void *dtable,
+                                 int64_t dtable_row_stride, int accumulate, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * ce_fwd_bwd_fused without a caller workspace and without any allocation.
  *
  * The pages have no counterpart: this exists for callers that cannot provide
