@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libgbce.so")
 
 SOURCES = ["gbce_api.cu", "gbce_reduce.cu", "gbce_kernels_f32.cu", "gbce_kernels_bf16.cu",
            "gbce_noalloc.cu", "gbce_slices.cu", "gbce_linear.cu", "gbce_linear_api.cu",
-           "gbce_embedding.cu"]
+           "gbce_linear_mma.cu", "gbce_embedding.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -88,9 +88,70 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(LinParams p)
     }
 }
 
+// Four elements at a time, or one.
+template <typename T> struct Quad;
+template <> struct Quad<__nv_bfloat16> { using type = uint2; };
+template <> struct Quad<float> { using type = float4; };
+
+// Planes of a value: bf16 x is its own; fp32 x = hi + mid + lo, each the
+// rounding of what is left (24 bits in three times 8).
+template <int PLANES>
+__device__ __forceinline__ void store_planes(float x, __nv_bfloat16 *dst, int64_t plane)
+{
+#pragma unroll
+    for (int z = 0; z < PLANES; ++z) {
+        const __nv_bfloat16 w = __float2bfloat16_rn(x);
+        dst[z * plane] = w;
+        x -= __bfloat162float(w);
+    }
+}
+
+// One row of an operand into its planes; `quads` when both sides allow four
+// elements at a time.
+template <typename T, int PLANES>
+__device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64_t plane,
+                                         int64_t dim, bool quads, bool zero)
+{
+    int64_t done = 0;
+    if (quads) {
+        done = dim / 4 * 4;
+        for (int64_t d = 4 * static_cast<int64_t>(threadIdx.x); d < done; d += 4 * blockDim.x) {
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (!zero) {
+                const auto raw = *reinterpret_cast<const typename Quad<T>::type *>(src + d);
+                const T *e = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = static_cast<float>(e[i]);
+            }
+#pragma unroll
+            for (int z = 0; z < PLANES; ++z) {
+                uint2 w;
+                w.x = float2_to_bf16x2(make_float2(x[0], x[1]));
+                w.y = float2_to_bf16x2(make_float2(x[2], x[3]));
+                *reinterpret_cast<uint2 *>(dst + z * plane + d) = w;
+                const float2 lo = bf16x2_to_float2(w.x), hi = bf16x2_to_float2(w.y);
+                x[0] -= lo.x;
+                x[1] -= lo.y;
+                x[2] -= hi.x;
+                x[3] -= hi.y;
+            }
+        }
+    }
+    for (int64_t d = done + threadIdx.x; d < dim; d += blockDim.x)
+        store_planes<PLANES>(zero ? 0.0f : static_cast<float>(src[d]), dst + d, plane);
+}
+
+template <typename T>
+__device__ __forceinline__ bool quad_rows(const T *base, int64_t stride)
+{
+    constexpr uint64_t bytes = 4 * sizeof(T);
+    return reinterpret_cast<uintptr_t>(base) % bytes == 0 && stride % 4 == 0;
+}
+
 // Packed hidden states and targets of the live rows, one CTA per packed row;
 // the rows up to the next multiple of kLinRowPad are zeros.
-template <typename T>
+template <typename T, int PLANES>
 __global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
 {
     grid_dependency_wait();
@@ -101,10 +162,9 @@ __global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
         return;
     const bool in = i < live;
     const int64_t r = in ? p.row_list[i] : 0;
-    const T *src = static_cast<const T *>(p.hidden) + r * p.hidden_stride;
-    T *dst = static_cast<T *>(p.hpack) + i * p.dim;
-    for (int64_t d = threadIdx.x; d < p.dim; d += blockDim.x)
-        dst[d] = in ? src[d] : T(0.0f);
+    const T *base = static_cast<const T *>(p.hidden);
+    pack_row<T, PLANES>(base + r * p.hidden_stride, static_cast<__nv_bfloat16 *>(p.hpack) + i * p.pitch,
+                        p.hpack_plane, p.dim, quad_rows(base, p.hidden_stride), !in);
     const int K = static_cast<int>(p.k);
     for (int k = threadIdx.x; k < K; k += blockDim.x) {
         const int64_t t = in ? p.targets[r * K + k] : -1;
@@ -112,116 +172,18 @@ __global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
     }
 }
 
-// ------------------------------------------------------------ simple products
-
-constexpr int kSgT = 64, kSgK = 16;
-
-// One 64 x 64 tile of A . B over k: 256 threads, 4 x 4 values each, every
-// product and sum in fp32.  A(m, k) = a[m am + k ak], B(n, k) = b[n bn + k bk].
-template <typename TA, typename TB>
-__device__ void simple_tile(const TA *a, int64_t am, int64_t ak, int64_t m0, int64_t mlim,
-                            const TB *b, int64_t bn, int64_t bk, int64_t n0, int64_t nlim,
-                            int64_t klim, float (&acc)[4][4], float *sm)
+// One piece of a weight that the products cannot read in place: fp32, or rows
+// that do not start on 16 bytes.
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64_t v0)
 {
-    float *sa = sm, *sb = sm + kSgK * (kSgT + 1);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = 0.0f;
-    for (int64_t k0 = 0; k0 < klim; k0 += kSgK) {
-        for (int e = threadIdx.x; e < kSgT * kSgK; e += 256) {
-            const int row = ak == 1 ? e / kSgK : e % kSgT, kk = ak == 1 ? e % kSgK : e / kSgT;
-            const bool in = m0 + row < mlim && k0 + kk < klim;
-            sa[kk * (kSgT + 1) + row] = in ? static_cast<float>(a[(m0 + row) * am + (k0 + kk) * ak])
-                                           : 0.0f;
-        }
-        for (int e = threadIdx.x; e < kSgT * kSgK; e += 256) {
-            const int row = bk == 1 ? e / kSgK : e % kSgT, kk = bk == 1 ? e % kSgK : e / kSgT;
-            const bool in = n0 + row < nlim && k0 + kk < klim;
-            sb[kk * (kSgT + 1) + row] = in ? static_cast<float>(b[(n0 + row) * bn + (k0 + kk) * bk])
-                                           : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kSgK; ++kk) {
-            float x[4], y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = sa[kk * (kSgT + 1) + ty * 4 + i];
-                y[i] = sb[kk * (kSgT + 1) + tx * 4 + i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-}
-
-constexpr int kSgSmem = kSgT * (kSgT + 1);  // floats; holds the operands, then the tile
-
-// Logits of a 64 x 64 tile into shared memory.
-template <typename T>
-__device__ void simple_logits(const LinParams &p, int64_t i0, int64_t v0, int32_t live, float *sm)
-{
-    float acc[4][4];
-    simple_tile(static_cast<const T *>(p.hpack), p.dim, 1, i0, live,
-                static_cast<const T *>(p.weight), p.weight_stride, 1, v0, p.vocab, p.dim, acc, sm);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sm[(ty * 4 + i) * (kSgT + 1) + tx * 4 + j] = acc[i][j];
-    __syncthreads();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) lin_stats_simple(LinParams p)
-{
-    __shared__ float sm[kSgSmem];
-    const int32_t live = p.head->n_live;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kSgT;
-    if (i0 >= live)
-        return;
-    const int K = static_cast<int>(p.k);
-    float m = kNegInf, s = 0.0f;
-    const int64_t i = i0 + threadIdx.x;
-    for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * kLinTileV;
-         v0 < min(p.vocab, (static_cast<int64_t>(blockIdx.x) + 1) * kLinTileV); v0 += kSgT) {
-        simple_logits<T>(p, i0, v0, live, sm);
-        if (threadIdx.x < kSgT && i < live) {
-            float *row = sm + threadIdx.x * (kSgT + 1);
-            const int n = static_cast<int>(min(static_cast<int64_t>(kSgT), p.vocab - v0));
-            // a column gathered twice is read before the first of them masks it
-            for (int k = 0; k < K; ++k) {
-                const int64_t j = p.tgt[i * K + k] - v0;
-                if (j >= 0 && j < n)
-                    p.xt[i * K + k] = row[j];
-            }
-            for (int k = 0; k < K; ++k) {
-                const int64_t j = p.tgt[i * K + k] - v0;
-                if (j >= 0 && j < n)
-                    row[j] = kNegInf;
-            }
-            float tm = kNegInf;
-            for (int j = 0; j < n; ++j)
-                tm = fmaxf(tm, row[j]);
-            const float ref = tm == kNegInf ? 0.0f : tm;
-            float ts = 0.0f;
-            for (int j = 0; j < n; ++j)
-                ts += ex2((row[j] - ref) * p.c);
-            // a tile of NaNs has no max, and keeps its NaN sum
-            merge_max_sum(m, s, ts == ts ? tm : ref, ts, p.c);
-        }
-        __syncthreads();
-    }
-    if (threadIdx.x < kSgT && i < live)
-        p.partials[i * p.tiles + blockIdx.x] = make_float2(m, s);
+    grid_dependency_wait();
+    launch_dependents();
+    const int64_t i = blockIdx.x;
+    const T *base = static_cast<const T *>(p.weight);
+    pack_row<T, PLANES>(base + (v0 + i) * p.weight_stride,
+                        static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch, p.wpack_rows * p.pitch,
+                        p.dim, quad_rows(base, p.weight_stride), false);
 }
 
 // One warp per live row: its tiles' partials merged in a fixed order (lane l
@@ -324,82 +286,6 @@ __global__ void __launch_bounds__(128) lin_prepare_kernel(LinParams p)
     }
 }
 
-// dz of one piece of the vocabulary [v0, v1), in the inputs' type.
-template <typename T>
-__global__ void __launch_bounds__(256) lin_dz_simple(LinParams p, int64_t v0, int64_t v1)
-{
-    __shared__ float sm[kSgSmem];
-    const int32_t live = p.head->n_live;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kSgT;
-    if (i0 >= live)
-        return;
-    const int64_t c0 = v0 + static_cast<int64_t>(blockIdx.x) * kSgT;
-    simple_logits<T>(p, i0, c0, live, sm);
-    T *dz = static_cast<T *>(p.dz);
-    for (int e = threadIdx.x; e < kSgT * kSgT; e += 256) {
-        const int64_t i = i0 + e / kSgT, v = c0 + e % kSgT;
-        if (i < live && v < v1) {
-            const float2 g = p.grow[i];
-            dz[i * p.piece + v - v0] = T(g.y * ex2((sm[e / kSgT * (kSgT + 1) + e % kSgT] - g.x) * p.c));
-        }
-    }
-    __syncthreads();
-    const int64_t i = i0 + threadIdx.x;
-    if (threadIdx.x < kSgT && i < live)
-        for (int k = 0; k < p.k; ++k) {
-            const int64_t v = p.tgt[i * p.k + k];
-            if (v >= c0 && v < min(v1, c0 + kSgT))
-                dz[i * p.piece + v - v0] = T(p.dzt[i * p.k + k]);
-        }
-}
-
-// dh (+)= dz . weight over one piece.
-template <typename T>
-__global__ void __launch_bounds__(256) lin_dh_simple(LinParams p, int64_t v0, int64_t v1)
-{
-    __shared__ float sm[kSgSmem];
-    const int32_t live = p.head->n_live;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kSgT, d0 = static_cast<int64_t>(blockIdx.x) * kSgT;
-    if (i0 >= live)
-        return;
-    float acc[4][4];
-    simple_tile(static_cast<const T *>(p.dz), p.piece, 1, i0, live,
-                static_cast<const T *>(p.weight) + v0 * p.weight_stride, 1, p.weight_stride, d0,
-                p.dim, v1 - v0, acc, sm);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t i = i0 + ty * 4 + a, d = d0 + tx * 4 + b;
-            if (i < live && d < p.dim) {
-                float *o = p.dh + i * p.dim + d;
-                *o = v0 == 0 ? acc[a][b] : *o + acc[a][b];
-            }
-        }
-}
-
-// dweight rows of one piece, (+)= alpha dz^T . hidden.
-template <typename T>
-__global__ void __launch_bounds__(256) lin_dw_simple(LinParams p, int64_t v0, int64_t v1)
-{
-    __shared__ float sm[kSgSmem];
-    const int32_t live = p.head->n_live;
-    const float alpha = p.head->alpha;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kSgT, d0 = static_cast<int64_t>(blockIdx.x) * kSgT;
-    float acc[4][4];
-    simple_tile(static_cast<const T *>(p.dz), 1, p.piece, c0, v1 - v0,
-                static_cast<const T *>(p.hpack), 1, p.dim, d0, p.dim, live, acc, sm);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = v0 + c0 + ty * 4 + a, d = d0 + tx * 4 + b;
-            if (v < v1 && d < p.dim) {
-                T *o = static_cast<T *>(p.dweight) + v * p.dweight_stride + d;
-                const float x = alpha * acc[a][b];
-                *o = T(p.accumulate ? static_cast<float>(*o) + x : x);
-            }
-        }
-}
-
 // dhidden by original row: alpha times the sums, zeros for rows left out,
 // NaN for rows with a target out of range.
 template <typename T>
@@ -411,9 +297,16 @@ __global__ void __launch_bounds__(128) lin_finish_kernel(LinParams p)
     const int32_t i = p.row_map[r];
     const float alpha = p.head->alpha;
     T *out = static_cast<T *>(p.dhidden) + r * p.dhidden_stride;
+    const float fill = i == kLinRowBad ? nan_value() : 0.0f;
+    const float *sums = p.dh + (i >= 0 ? i : 0) * p.dh_pitch;
     for (int64_t d = threadIdx.x; d < p.dim; d += blockDim.x) {
-        const float x = i >= 0 ? alpha * p.dh[i * p.dim + d]
-                               : (i == kLinRowBad ? nan_value() : 0.0f);
+        float x = fill;
+        if (i >= 0) {
+            x = 0.0f;
+            for (int z = 0; z < p.dh_splits; ++z)
+                x += sums[z * p.rows_pad * p.dh_pitch + d];
+            x *= alpha;
+        }
         out[d] = T(x);
     }
 }
@@ -455,19 +348,15 @@ cudaError_t lin_plan(const LinParams &p, cudaStream_t s)
 
 cudaError_t lin_pack(const LinParams &p, cudaStream_t s)
 {
-    return launch_after(p.bf16 ? lin_pack_kernel<__nv_bfloat16> : lin_pack_kernel<float>,
+    return launch_after(p.bf16 ? lin_pack_kernel<__nv_bfloat16, 1> : lin_pack_kernel<float, 3>,
                         dim3(static_cast<unsigned>(p.rows_pad)), dim3(128), 0, s, p);
 }
 
-cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
+cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>(p.tiles), blocks(p.rows, kSgT));
-    if (p.bf16)
-        lin_stats_simple<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else
-        lin_stats_simple<float><<<grid, 256, 0, s>>>(p);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_after(p.bf16 ? lin_pack_weight_kernel<__nv_bfloat16, 1>
+                               : lin_pack_weight_kernel<float, 3>,
+                        dim3(static_cast<unsigned>(v1 - v0)), dim3(128), 0, s, p, v0);
 }
 
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s)
@@ -480,33 +369,10 @@ cudaError_t lin_prepare(const LinParams &p, cudaStream_t s)
     return launch_after(lin_prepare_kernel, dim3(blocks(p.rows, 128)), dim3(128), 0, s, p);
 }
 
-template <typename T>
-static cudaError_t grads(const LinParams &p, cudaStream_t s)
+cudaError_t lin_finish(const LinParams &p, cudaStream_t s)
 {
-    for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
-        const int64_t v1 = v0 + p.piece < p.vocab ? v0 + p.piece : p.vocab;
-        lin_dz_simple<T><<<dim3(blocks(v1 - v0, kSgT), blocks(p.rows, kSgT)), 256, 0, s>>>(p, v0, v1);
-        note_launches(1);
-        if (p.dhidden != nullptr) {
-            lin_dh_simple<T><<<dim3(blocks(p.dim, kSgT), blocks(p.rows, kSgT)), 256, 0, s>>>(p, v0, v1);
-            note_launches(1);
-        }
-        if (p.dweight != nullptr) {
-            lin_dw_simple<T><<<dim3(blocks(p.dim, kSgT), blocks(v1 - v0, kSgT)), 256, 0, s>>>(p, v0, v1);
-            note_launches(1);
-        }
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess)
-            return e;
-    }
-    if (p.dhidden == nullptr)
-        return cudaSuccess;
-    return launch_after(lin_finish_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(128), 0, s, p);
-}
-
-cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
-{
-    return p.bf16 ? grads<__nv_bfloat16>(p, s) : grads<float>(p, s);
+    return launch_after(p.bf16 ? lin_finish_kernel<__nv_bfloat16> : lin_finish_kernel<float>,
+                        dim3(static_cast<unsigned>(p.rows)), dim3(128), 0, s, p);
 }
 
 }  // namespace gbce

@@ -71,9 +71,20 @@ struct LinParams {
     float2 *partials;             // [rows_pad, tiles]
     float2 *grow;                 // [rows_pad] (M, coef / S)
     float *dzt;                   // [rows_pad, k] dz of the gathered columns
-    void *hpack;                  // packed live rows
-    void *dz;                     // [rows_pad, piece]
-    float *dh;                    // [splits, rows_pad, dim]
+    // Operands of the products are bf16 planes: one for bf16 inputs, three
+    // whose sum is the value for fp32 ones.
+    int planes;
+    int64_t pitch;                // elements from row to row of hpack and wpack
+    void *hpack;                  // [planes, rows_pad, pitch] packed live rows
+    int64_t hpack_plane;
+    bool weight_direct;           // the weight is read in place, else through wpack
+    void *wpack;                  // [planes, wpack_rows, pitch] one piece of the weight
+    int64_t wpack_rows;
+    void *dz;                     // [planes, rows_pad, piece]
+    int64_t dz_plane;
+    float *dh;                    // [dh_splits, rows_pad, dh_pitch] sums
+    int64_t dh_pitch;
+    int dh_splits;
     int64_t rows_pad, tiles, piece;
 
     int32_t *dev_status;
@@ -84,6 +95,8 @@ cudaError_t lin_pack(const LinParams &p, cudaStream_t s);
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s);
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s);
 cudaError_t lin_prepare(const LinParams &p, cudaStream_t s);
+cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStream_t s);
 cudaError_t lin_grads(const LinParams &p, cudaStream_t s);
+cudaError_t lin_finish(const LinParams &p, cudaStream_t s);
 
 }  // namespace gbce

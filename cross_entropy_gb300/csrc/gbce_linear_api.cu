@@ -25,14 +25,22 @@ int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 size_t elem_size(gbce_dtype dt) { return dt == GBCE_BF16 ? 2 : 4; }
 
 struct Layout {
-    size_t head, row_list, row_map, tgt, xt, partials, loss, logp, state, grow, dzt, hpack, dz, dh;
+    size_t head, row_list, row_map, tgt, xt, partials, loss, logp, state, grow, dzt, hpack, wpack, dz,
+        dh;
     size_t total;
-    int64_t rows_pad, tiles, piece;
+    int64_t rows_pad, tiles, piece, pitch, wpack_rows, dh_pitch;
+    int planes, dh_splits;
 };
+
+// Pairs of SMs of the GPU, and the most parts that dhidden's sums take.
+constexpr int64_t kPairs = 76, kMaxSplits = 16;
 
 // Where everything lies in the workspace.  With `backward`, the buffers of
 // the gradient (and of the statistics, which a fused call needs too).
-Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt, bool backward)
+// `direct`: the weight is read in place; no layout is larger than a direct
+// one's, whatever the weight's alignment.
+Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt, bool backward,
+              bool direct)
 {
     Layout w{};
     size_t off = 0;
@@ -41,7 +49,6 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
         off += align_up(static_cast<size_t>(n) * bytes, 256);
         return at;
     };
-    const size_t es = elem_size(dt);
     w.rows_pad = round_up(rows, gbce::kLinRowPad);
     w.tiles = (vocab + gbce::kLinTileV - 1) / gbce::kLinTileV;
     w.head = take(1, sizeof(gbce::LinHeader));
@@ -50,19 +57,32 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
     w.tgt = take(w.rows_pad * k, 4);
     w.xt = take(w.rows_pad * k, 4);
     w.loss = take(rows, 4);
-    w.hpack = take(w.rows_pad * dim, es);
+    // bf16 planes, rows on 16 bytes as the tensor maps want them
+    w.planes = dt == GBCE_BF16 ? 1 : 3;
+    w.pitch = round_up(dim, 8);
+    w.hpack = take(w.planes * w.rows_pad * w.pitch, 2);
+    const int64_t full = round_up(vocab, gbce::kLinTileV);
+    w.wpack_rows = gbce::kLinPieceUnit < full ? gbce::kLinPieceUnit : full;
+    w.wpack = take(w.planes * w.wpack_rows * w.pitch, 2);
     w.partials = take(w.rows_pad * w.tiles, 8);
     if (backward) {
         w.logp = take(rows * k, 4);
         w.state = take(rows * 2, 4);
         w.grow = take(w.rows_pad, 8);
         w.dzt = take(w.rows_pad * k, 4);
-        const int64_t full = round_up(vocab, gbce::kLinTileV);
-        int64_t units = kPieceBytes / (w.rows_pad * gbce::kLinPieceUnit * static_cast<int64_t>(es));
-        units = units < 1 ? 1 : units;
+        // pieces of the vocabulary: whole units, as many as kPieceBytes of dz
+        // allow; one where the weight has to be packed piece by piece
+        int64_t units = kPieceBytes / (w.planes * w.rows_pad * gbce::kLinPieceUnit * 2);
+        units = units < 1 || !direct ? 1 : units;
         w.piece = units * gbce::kLinPieceUnit < full ? units * gbce::kLinPieceUnit : full;
-        w.dz = take(w.rows_pad * w.piece, es);
-        w.dh = take(w.rows_pad * dim, 4);
+        w.dz = take(w.planes * w.rows_pad * w.piece, 2);
+        // few row tiles: the sums over the vocabulary are split so that every
+        // pair of SMs has a part
+        const int64_t out_tiles = w.rows_pad / 256 * ((dim + 255) / 256);
+        const int64_t parts = kPairs / out_tiles;
+        w.dh_splits = static_cast<int>(parts < 1 ? 1 : (parts > kMaxSplits ? kMaxSplits : parts));
+        w.dh_pitch = round_up(dim, 4);
+        w.dh = take(w.dh_splits * w.rows_pad * w.dh_pitch, 4);
     }
     w.total = off;
     return w;
@@ -96,6 +116,13 @@ struct Shape {
     int64_t rows, vocab, dim, k;
     float temperature;
 };
+
+// The tensor maps read bf16 rows that start on 16 bytes.
+bool weight_direct(const Shape &a)
+{
+    return a.dtype == GBCE_BF16 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 &&
+           a.weight_stride % 8 == 0;
+}
 
 gbce_status check_shape(const Shape &a)
 {
@@ -180,12 +207,21 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
     p.tgt = at<int32_t>(ws, w.tgt);
     p.xt = at<float>(ws, w.xt);
     p.partials = at<float2>(ws, w.partials);
+    p.planes = w.planes;
+    p.pitch = w.pitch;
     p.hpack = at<void>(ws, w.hpack);
+    p.hpack_plane = w.rows_pad * w.pitch;
+    p.weight_direct = weight_direct(a);
+    p.wpack = at<void>(ws, w.wpack);
+    p.wpack_rows = w.wpack_rows;
     if (backward) {
         p.grow = at<float2>(ws, w.grow);
         p.dzt = at<float>(ws, w.dzt);
         p.dz = at<void>(ws, w.dz);
+        p.dz_plane = w.rows_pad * w.piece;
         p.dh = at<float>(ws, w.dh);
+        p.dh_pitch = w.dh_pitch;
+        p.dh_splits = w.dh_splits;
     }
     p.rows_pad = w.rows_pad;
     p.tiles = w.tiles;
@@ -260,7 +296,7 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
         return GBCE_EINVAL;
     if (g != nullptr && (st = check_grads(a, *g)) != GBCE_OK)
         return st;
-    const Layout w = layout(a.rows, a.vocab, a.dim, 1, a.dtype, g != nullptr);
+    const Layout w = layout(a.rows, a.vocab, a.dim, 1, a.dtype, g != nullptr, weight_direct(a));
     if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
         return st;
     LinParams p = params(a, w, workspace, g != nullptr, dev_status);
@@ -300,7 +336,7 @@ size_t gbce_linear_workspace_size(int64_t rows, int64_t vocab, int64_t dim, int6
     if ((dtype != GBCE_F32 && dtype != GBCE_BF16) || rows <= 0 || rows > kMaxRows || vocab < 1 ||
         vocab > kMaxVocab || dim < 1 || dim > kMaxDim || k < 1 || k > GBCE_MAX_K)
         return 0;
-    return layout(rows, vocab, dim, k, dtype, backward != 0).total;
+    return layout(rows, vocab, dim, k, dtype, backward != 0, dtype == GBCE_BF16).total;
 }
 
 gbce_status linear_selective_logsoftmax(const void *hidden, int64_t hidden_row_stride,
@@ -318,7 +354,7 @@ gbce_status linear_selective_logsoftmax(const void *hidden, int64_t hidden_row_s
         return st;
     if (index == nullptr || logp_out == nullptr)
         return GBCE_EINVAL;
-    const Layout w = layout(rows, vocab, dim, k, dtype, false);
+    const Layout w = layout(rows, vocab, dim, k, dtype, false, weight_direct(a));
     if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
         return st;
     LinParams p = params(a, w, workspace, false, dev_status);
@@ -354,7 +390,7 @@ gbce_status linear_selective_logsoftmax_bwd(
         return GBCE_EINVAL;
     if ((st = check_grads(a, g)) != GBCE_OK)
         return st;
-    const Layout w = layout(rows, vocab, dim, k, dtype, true);
+    const Layout w = layout(rows, vocab, dim, k, dtype, true, weight_direct(a));
     if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
         return st;
     LinParams p = params(a, w, workspace, true, dev_status);
@@ -411,7 +447,7 @@ gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const v
         return GBCE_EINVAL;
     if ((st = check_grads(a, g)) != GBCE_OK)
         return st;
-    const Layout w = layout(rows, vocab, dim, 1, dtype, true);
+    const Layout w = layout(rows, vocab, dim, 1, dtype, true, weight_direct(a));
     if ((st = check_workspace(workspace, workspace_bytes, w)) != GBCE_OK)
         return st;
     LinParams p = params(a, w, workspace, true, dev_status);
