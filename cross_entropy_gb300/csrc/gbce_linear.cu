@@ -186,6 +186,32 @@ __global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64
                         p.dim, quad_rows(base, p.weight_stride), false);
 }
 
+// The factor of both gradients that every row shares: a summed or averaged
+// loss's upstream gradient over T (and the number of items).  It stays out of
+// dz and joins at the end, in fp32, so that it is not rounded with each dz.
+__device__ __forceinline__ float shared_factor(const LinParams &p)
+{
+    if (!p.token_ce || p.reduction == 0)
+        return 1.0f;
+    double a = static_cast<double>(p.grad_out[0]) / static_cast<double>(p.T);
+    if (p.reduction == 2) {
+        const int64_t n = p.n_items != nullptr ? *p.n_items : p.head->n_items;
+        a = n > 0 ? a / static_cast<double>(n) : 0.0;
+    }
+    return static_cast<float>(a);
+}
+
+// What the CE gradient of packed row i takes besides its logits: (M, u / S)
+// for the p_j and the label's u expm1(log p), which keeps 1 - p when p rounds
+// to 1; u = upstream / T where rows have their own.
+__device__ __forceinline__ void ce_row_gradient(const LinParams &p, int64_t i, int64_t r, float M,
+                                                float S, float logp)
+{
+    const float u = p.reduction == 0 ? p.grad_out[r] * (1.0f / p.T) : 1.0f;
+    p.grow[i] = make_float2(M, u / S);
+    p.dzt[i] = u * expm1f(logp);
+}
+
 // One warp per live row: its tiles' partials merged in a fixed order (lane l
 // takes the tiles l, l + 32, ..., then the lanes merge), then the log-probs
 // of its targets, each over the other columns, and the whole row's state.
@@ -207,6 +233,7 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(LinParams p)
     const int64_t r = p.row_list[i];
     const int32_t *tg = p.tgt + i * K;
     const float *xt = p.xt + i * K;
+    float logp = 0.0f;
     if (lane < K) {
         float out;
         if (tg[lane] < 0) {
@@ -215,12 +242,13 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(LinParams p)
         } else {
             out = logp_with_targets<GBCE_MAX_K>(m, s, tg, xt, K, lane, p.c, p.T);
         }
+        logp = out;
         if (p.logp_out != nullptr)
             p.logp_out[r * K + lane] = out;
         if (lane == 0 && p.loss_rows != nullptr)
             p.loss_rows[r] = -out;
     }
-    if (lane == 0 && p.state_out != nullptr) {
+    if (lane == 0 && (p.state_out != nullptr || p.fused)) {
         for (int k = 0; k < K; ++k) {
             bool dup = tg[k] < 0;
             for (int j = 0; j < k; ++j)
@@ -228,34 +256,28 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(LinParams p)
             if (!dup)
                 merge_max_sum(m, s, xt[k], 1.0f, p.c);
         }
-        p.state_out[2 * r] = m;
-        p.state_out[2 * r + 1] = s;
+        if (p.state_out != nullptr) {
+            p.state_out[2 * r] = m;
+            p.state_out[2 * r + 1] = s;
+        }
+        if (p.fused) {
+            if (i == 0)
+                p.head->alpha = shared_factor(p);
+            ce_row_gradient(p, i, r, m, s, logp);
+        }
     }
 }
 
-// What the gradient of a row takes besides its logits: (M, coef / S), and
-// the dz of its gathered columns,
-//   -u_t expm1(log p_t) - (sum of the others' u) p_t,   u = upstream / T,
-// in which 1 - p_t keeps its value when p_t rounds to 1.  The factor that
-// all rows share (a summed or averaged loss's) stays out of dz: it joins at
-// the end, in fp32, so that it is not rounded with each dz.
+// A backward call's rows, from the forward's log-probs and row states.  The
+// selective gradient has (M, -G / (T S)) and, for a gathered column,
+//   (-g_t expm1(log p_t) - (sum of the others' g) p_t) / T.
 __global__ void __launch_bounds__(128) lin_prepare_kernel(LinParams p)
 {
     grid_dependency_wait();
     launch_dependents();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const float inv_t = 1.0f / p.T;
-    if (i == 0) {
-        double a = 1.0;
-        if (p.token_ce && p.reduction != 0) {
-            a = static_cast<double>(p.grad_out[0]) / static_cast<double>(p.T);
-            if (p.reduction == 2) {
-                const int64_t n = p.n_items != nullptr ? *p.n_items : p.head->n_items;
-                a = n > 0 ? a / static_cast<double>(n) : 0.0;
-            }
-        }
-        p.head->alpha = static_cast<float>(a);
-    }
+    if (i == 0)
+        p.head->alpha = shared_factor(p);
     if (i >= p.head->n_live)
         return;
     const int K = static_cast<int>(p.k);
@@ -263,11 +285,10 @@ __global__ void __launch_bounds__(128) lin_prepare_kernel(LinParams p)
     const float M = p.saved_state[2 * r], S = p.saved_state[2 * r + 1];
     const float *lp = p.saved_logp + r * K;
     if (p.token_ce) {
-        const float u = p.reduction == 0 ? p.grad_out[r] * inv_t : 1.0f;
-        p.grow[i] = make_float2(M, u / S);
-        p.dzt[i] = u * expm1f(lp[0]);
+        ce_row_gradient(p, i, r, M, S, lp[0]);
         return;
     }
+    const float inv_t = 1.0f / p.T;
     const float *g = p.grad_out + r * K;
     const int32_t *tg = p.tgt + i * K;
     float sum = 0.0f;

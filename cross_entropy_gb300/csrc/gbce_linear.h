@@ -55,6 +55,7 @@ struct LinParams {
     int64_t *n_items_out; // [1]
 
     // backward
+    bool fused;               // the statistics were taken by the same call
     const float *grad_out;    // CE: [rows] or [1]; selective: [rows, k]
     int reduction;            // CE: 0 none, 1 sum, 2 mean
     const int64_t *n_items;   // CE mean; null: the header's

@@ -25,7 +25,7 @@ int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 size_t elem_size(gbce_dtype dt) { return dt == GBCE_BF16 ? 2 : 4; }
 
 struct Layout {
-    size_t head, row_list, row_map, tgt, xt, partials, loss, logp, state, grow, dzt, hpack, wpack, dz,
+    size_t head, row_list, row_map, tgt, xt, partials, loss, grow, dzt, hpack, wpack, dz,
         dh;
     size_t total;
     int64_t rows_pad, tiles, piece, pitch, wpack_rows, dh_pitch;
@@ -62,18 +62,20 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
     w.pitch = round_up(dim, 8);
     w.hpack = take(w.planes * w.rows_pad * w.pitch, 2);
     const int64_t full = round_up(vocab, gbce::kLinTileV);
-    w.wpack_rows = gbce::kLinPieceUnit < full ? gbce::kLinPieceUnit : full;
+    int64_t wunits = kPieceBytes / (w.planes * w.pitch * gbce::kLinPieceUnit * 2);
+    wunits = wunits < 1 ? 1 : wunits;
+    w.wpack_rows = wunits * gbce::kLinPieceUnit < full ? wunits * gbce::kLinPieceUnit : full;
     w.wpack = take(w.planes * w.wpack_rows * w.pitch, 2);
     w.partials = take(w.rows_pad * w.tiles, 8);
     if (backward) {
-        w.logp = take(rows * k, 4);
-        w.state = take(rows * 2, 4);
         w.grow = take(w.rows_pad, 8);
         w.dzt = take(w.rows_pad * k, 4);
         // pieces of the vocabulary: whole units, as many as kPieceBytes of dz
-        // allow; one where the weight has to be packed piece by piece
+        // allow, and no more than the packed part of the weight holds
         int64_t units = kPieceBytes / (w.planes * w.rows_pad * gbce::kLinPieceUnit * 2);
-        units = units < 1 || !direct ? 1 : units;
+        units = units < 1 ? 1 : units;
+        if (!direct && units > wunits)
+            units = wunits;
         w.piece = units * gbce::kLinPieceUnit < full ? units * gbce::kLinPieceUnit : full;
         w.dz = take(w.planes * w.rows_pad * w.piece, 2);
         // few row tiles: the sums over the vocabulary are split so that every
@@ -306,10 +308,13 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
     p.reduction = static_cast<int>(reduction);
     p.n_items_out = n_items_out;
     p.loss_rows = reduction == GBCE_NONE ? loss_out : at<float>(workspace, w.loss);
-    // the gradient takes the log-probs and the row states, wanted or not
-    p.logp_out = logp_out != nullptr || g == nullptr ? logp_out : at<float>(workspace, w.logp);
-    p.state_out = row_state_out != nullptr || g == nullptr ? row_state_out
-                                                           : at<float>(workspace, w.state);
+    p.logp_out = logp_out;
+    p.state_out = row_state_out;
+    if (g != nullptr) {
+        p.fused = true;
+        p.grad_out = grad_out;
+        set_grads(p, *g);
+    }
     cudaError_t e = select_rows(p, s);
     if (e == cudaSuccess)
         e = forward(p, s);
@@ -319,11 +324,7 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
                                      loss_out, s);
     if (e != cudaSuccess || g == nullptr)
         return cuda_status(e);
-    p.grad_out = grad_out;
-    p.saved_logp = p.logp_out;
-    p.saved_state = p.state_out;
-    set_grads(p, *g);
-    return cuda_status(backward(p, s));
+    return cuda_status(gbce::lin_grads(p, s));
 }
 
 }  // namespace

@@ -591,14 +591,19 @@ struct Weight {
     int64_t row0;                 // the piece's first row in it
 };
 
-cudaError_t piece_weight(const LinParams &p, int64_t v0, int64_t v1, Weight &w, cudaStream_t s)
+// `packed`: an earlier launch of the call has been here.
+cudaError_t piece_weight(const LinParams &p, int64_t v0, int64_t v1, bool packed, Weight &w,
+                         cudaStream_t s)
 {
     if (p.weight_direct) {
         w = {p.weight, p.vocab, p.weight_stride, p.weight_stride, v0};  // one plane
         return cudaSuccess;
     }
-    w = {p.wpack, v1 - v0, p.pitch, p.wpack_rows * p.pitch, 0};
-    return lin_pack_weight(p, v0, v1, s);
+    const bool whole = p.wpack_rows >= p.vocab;  // packed once for every use
+    w = {p.wpack, whole ? p.vocab : v1 - v0, p.pitch, p.wpack_rows * p.pitch, whole ? v0 : 0};
+    if (whole && packed)
+        return cudaSuccess;
+    return whole ? lin_pack_weight(p, 0, p.vocab, s) : lin_pack_weight(p, v0, v1, s);
 }
 
 MmaArgs base_args(const LinParams &p, int64_t v0)
@@ -628,7 +633,7 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
     for (int64_t v0 = 0; v0 < p.vocab; v0 += step) {
         const int64_t v1 = v0 + step < p.vocab ? v0 + step : p.vocab;
         Weight w;
-        cudaError_t e = piece_weight(p, v0, v1, w, s);
+        cudaError_t e = piece_weight(p, v0, v1, v0 > 0, w, s);
         CUtensorMap a, b;
         if (e == cudaSuccess)
             e = make_map(&a, p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, 128);
@@ -655,7 +660,7 @@ cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
     for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
         const int64_t v1 = v0 + p.piece < p.vocab ? v0 + p.piece : p.vocab;
         Weight w;
-        cudaError_t e = piece_weight(p, v0, v1, w, s);
+        cudaError_t e = piece_weight(p, v0, v1, v0 > 0 || p.fused, w, s);
         CUtensorMap h_k, w_k, dz_k, w_mn, dz_mn, h_mn;
         const auto map = [&e](CUtensorMap *m, const void *base, int64_t inner, int64_t rows,
                               int64_t stride, int64_t planes, int64_t plane, uint32_t box) {

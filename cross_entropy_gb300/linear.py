@@ -22,8 +22,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (REDUCTIONS, _check, _check_buffer, _check_status, _dev_int64, _dtype_code, _ptr,
-               _stream_ptr, load_library)
+from . import (REDUCTIONS, _check, _check_buffer, _check_status, _dtype_code, _ptr, _stream_ptr,
+               load_library)
 
 
 class LinearCeForward(NamedTuple):
@@ -41,15 +41,30 @@ class LinearCeFused(NamedTuple):
     n_items: torch.Tensor
 
 
+_HERE = contextlib.nullcontext()
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device, and the stream where one is given."""
+def _elsewhere(device, stream):
     with torch.cuda.device(device):
         if stream is None:
             yield
         else:
             with torch.cuda.stream(stream):
                 yield
+
+
+def _on(device, stream):
+    """The tensors' device, and the stream where one is given."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _HERE
+    return _elsewhere(device, stream)
+
+
+def _int64(x, device) -> torch.Tensor:
+    if not (isinstance(x, torch.Tensor) and x.dtype == torch.int64 and x.device == device):
+        x = torch.as_tensor(x, dtype=torch.int64, device=device)
+    return x.contiguous()
 
 
 def _matrix(t: torch.Tensor, what: str) -> torch.Tensor:
@@ -84,21 +99,30 @@ def _operands(hidden, weight):
     return h, w
 
 
+def _flat(x, *shape):
+    """x with this shape, contiguous; x itself where it is."""
+    return (x if x.shape == shape else x.reshape(shape)).contiguous()
+
+
 def _mask(row_mask, rows, device):
     if row_mask is None:
         return None
-    return row_mask.to(device=device, dtype=torch.uint8).reshape(rows).contiguous()
+    if row_mask.dtype != torch.uint8 or row_mask.device != device:
+        row_mask = row_mask.to(device=device, dtype=torch.uint8)
+    return _flat(row_mask, rows)
 
 
 def _index(index, lead, rows, device):
-    idx = _dev_int64(index, device)
+    idx = _int64(index, device)
     squeeze = idx.dim() == len(lead)
     k = 1 if squeeze else idx.shape[-1]
-    return idx.reshape(rows, k), k, squeeze
+    return _flat(idx, rows, k), k, squeeze
 
 
 def _floats(x, shape, device):
-    return torch.as_tensor(x, dtype=torch.float32, device=device).reshape(shape).contiguous()
+    if not (isinstance(x, torch.Tensor) and x.dtype == torch.float32 and x.device == device):
+        x = torch.as_tensor(x, dtype=torch.float32, device=device)
+    return _flat(x, *shape)
 
 
 def _gradient(buf, like: torch.Tensor, name: str, want: bool):
@@ -234,11 +258,11 @@ def linear_ce_fwd(hidden: torch.Tensor, weight: torch.Tensor, labels, ignore_ind
     rows = h.shape[0]
     red = REDUCTIONS[reduction]
     with _on(h.device, stream):
-        lab = _dev_int64(labels, h.device).reshape(rows)
-        loss = torch.empty((rows,) if red == 0 else (1,), dtype=torch.float32, device=h.device)
+        lab = _flat(_int64(labels, h.device), rows)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=h.device)
         logp = torch.empty(rows, dtype=torch.float32, device=h.device)
         state = torch.empty((rows, 2), dtype=torch.float32, device=h.device)
-        n_items = torch.empty(1, dtype=torch.int64, device=h.device)
+        n_items = torch.empty((), dtype=torch.int64, device=h.device)
         _check_status(dev_status, h.device)
         ws, ws_ptr, ws_bytes = _linear_workspace(workspace, lib, h, w, 1, 0)
         st = lib.linear_ce_fwd(
@@ -247,14 +271,16 @@ def linear_ce_fwd(hidden: torch.Tensor, weight: torch.Tensor, labels, ignore_ind
             loss.data_ptr(), logp.data_ptr(), state.data_ptr(), n_items.data_ptr(), ws_ptr,
             ws_bytes, _ptr(dev_status), _stream_ptr(stream, h.device))
     _check(st, "linear_ce_fwd")
-    return LinearCeForward(loss if red == 0 else loss[0], logp, state, n_items[0])
+    return LinearCeForward(loss, logp, state, n_items)
 
 
 def _upstream(grad_out, rows, red, device):
-    g = torch.as_tensor(grad_out, dtype=torch.float32, device=device).reshape(-1).contiguous()
-    if g.numel() != (rows if red == 0 else 1):
+    n = rows if red == 0 else 1
+    if not isinstance(grad_out, torch.Tensor):
+        grad_out = torch.as_tensor(grad_out, dtype=torch.float32)
+    if grad_out.numel() != n:
         raise ValueError("grad_out must have one entry per row for 'none', one otherwise")
-    return g
+    return _floats(grad_out, (n,), device)
 
 
 def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, labels, grad_out,
@@ -271,9 +297,9 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, labels, grad_out,
     rows = h.shape[0]
     red = REDUCTIONS[reduction]
     with _on(h.device, stream):
-        lab = _dev_int64(labels, h.device).reshape(rows)
+        lab = _flat(_int64(labels, h.device), rows)
         g = _upstream(grad_out, rows, red, h.device)
-        n = None if n_items is None else _dev_int64(n_items, h.device).reshape(1)
+        n = None if n_items is None else _int64(n_items, h.device).reshape(1)
         lp = _floats(saved_logp, (rows,), h.device)
         rs = _floats(row_state, (rows, 2), h.device)
         dhidden, dh = _gradient(dhidden, hidden, "dhidden", want_dhidden)
@@ -306,14 +332,14 @@ def linear_ce_fwd_bwd_fused(hidden: torch.Tensor, weight: torch.Tensor, labels, 
     rows = h.shape[0]
     red = REDUCTIONS[reduction]
     with _on(h.device, stream):
-        lab = _dev_int64(labels, h.device).reshape(rows)
+        lab = _flat(_int64(labels, h.device), rows)
         if grad_out is None:
             g = torch.ones(rows if red == 0 else 1, dtype=torch.float32, device=h.device)
         else:
             g = _upstream(grad_out, rows, red, h.device)
-        loss = torch.empty((rows,) if red == 0 else (1,), dtype=torch.float32, device=h.device)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=h.device)
         logp = torch.empty(rows, dtype=torch.float32, device=h.device) if want_logp else None
-        n_items = torch.empty(1, dtype=torch.int64, device=h.device)
+        n_items = torch.empty((), dtype=torch.int64, device=h.device)
         dhidden, dh = _gradient(dhidden, hidden, "dhidden", want_dhidden)
         dweight, dw = _gradient(dweight, weight, "dweight", want_dweight)
         _check_status(dev_status, h.device)
@@ -325,7 +351,7 @@ def linear_ce_fwd_bwd_fused(hidden: torch.Tensor, weight: torch.Tensor, labels, 
             0 if dh is None else _stride(dh), _ptr(dw), 0 if dw is None else _stride(dw), acc,
             ws_ptr, ws_bytes, _ptr(dev_status), _stream_ptr(stream, h.device))
     _check(st, "linear_ce_fwd_bwd_fused")
-    return LinearCeFused(loss if red == 0 else loss[0], dhidden, dweight, logp, n_items[0])
+    return LinearCeFused(loss, dhidden, dweight, logp, n_items)
 
 
 # ------------------------------------------------------------ the table's lookup
@@ -341,7 +367,7 @@ def embedding_lookup(table: torch.Tensor, tokens, scale: float = 1.0, *, ignore_
         raise ValueError("table must have shape [vocab, dim]")
     code = _dtype_code(t)
     with _on(t.device, stream):
-        tok = _dev_int64(tokens, t.device)
+        tok = _int64(tokens, t.device)
         rows = tok.numel()
         shape = (*tok.shape, t.shape[1])
         if out is None:
@@ -370,7 +396,7 @@ def embedding_lookup_bwd(grad_out: torch.Tensor, tokens, vocab: int, scale: floa
     code = _dtype_code(g)
     rows, dim = g.shape
     with _on(g.device, stream):
-        tok = _dev_int64(tokens, g.device)
+        tok = _int64(tokens, g.device)
         if tok.shape != grad_out.shape[:-1]:
             raise ValueError(f"tokens must have shape {tuple(grad_out.shape[:-1])}")
         if dtable is None:
