@@ -307,28 +307,47 @@ __global__ void __launch_bounds__(128) lin_prepare_kernel(LinParams p)
     }
 }
 
-// dhidden by original row: alpha times the sums, zeros for rows left out,
-// NaN for rows with a target out of range.
+// dhidden by original row: alpha times the sum of its parts, zeros for rows
+// left out, NaN for rows with a target out of range.  Four values a thread.
 template <typename T>
 __global__ void __launch_bounds__(128) lin_finish_kernel(LinParams p)
 {
     grid_dependency_wait();
     launch_dependents();
     const int64_t r = blockIdx.x;
-    const int32_t i = p.row_map[r];
+    const int32_t i = p.row_map[r], parts = p.head->dh_splits;
+    const int32_t m = 128 * p.grads_tile.ctas;
+    const int64_t part = static_cast<int64_t>((p.head->n_live + m - 1) / m) * m * p.dh_pitch;
     const float alpha = p.head->alpha;
     T *out = static_cast<T *>(p.dhidden) + r * p.dhidden_stride;
+    const bool quads = reinterpret_cast<uintptr_t>(p.dhidden) % (4 * sizeof(T)) == 0 && p.dhidden_stride % 4 == 0;
     const float fill = i == kLinRowBad ? nan_value() : 0.0f;
     const float *sums = p.dh + (i >= 0 ? i : 0) * p.dh_pitch;
-    for (int64_t d = threadIdx.x; d < p.dim; d += blockDim.x) {
-        float x = fill;
+    for (int64_t d = 4 * static_cast<int64_t>(threadIdx.x); d < p.dim; d += 4 * blockDim.x) {
+        float4 x = make_float4(fill, fill, fill, fill);
         if (i >= 0) {
-            x = 0.0f;
-            for (int z = 0; z < p.dh_splits; ++z)
-                x += sums[z * p.rows_pad * p.dh_pitch + d];
-            x *= alpha;
+            x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int z = 0; z < parts; ++z) {
+                const float4 y = *reinterpret_cast<const float4 *>(sums + z * part + d);
+                x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            x = make_float4(alpha * x.x, alpha * x.y, alpha * x.z, alpha * x.w);
         }
-        out[d] = T(x);
+        const float f[4] = {x.x, x.y, x.z, x.w};
+        if (quads && d + 4 <= p.dim) {
+            typename Quad<T>::type w;
+            T *e = reinterpret_cast<T *>(&w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                e[j] = T(f[j]);
+            *reinterpret_cast<typename Quad<T>::type *>(out + d) = w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (d + j < p.dim)
+                    out[d + j] = T(f[j]);
+        }
     }
 }
 

@@ -16,12 +16,30 @@
 
 namespace gbce {
 
-// Rows of the packed buffers are padded to this many; one vocabulary tile of
-// the statistics is this wide.
+// Rows of the packed buffers are padded to this many, columns of a piece to
+// as many.
 constexpr int kLinRowPad = 256;
-constexpr int kLinTileV = 256;
-// Vocabulary columns in one piece of the backward: a multiple of this.
-constexpr int64_t kLinPieceUnit = 76 * 256;
+// The GPU's SMs, for choices that the workspace's layout depends on (a pure
+// function of a call's sizes).
+constexpr int64_t kLinSms = 152;
+// Vocabulary columns in one piece of the backward: a multiple of this, a
+// 256-wide tile for each pair of SMs.
+constexpr int64_t kLinPieceUnit = kLinSms / 2 * 256;
+// The most parts that dhidden's sums over a piece are split into.
+constexpr int kMaxSplits = 16;
+
+// A tile shape of the products: 128 rows per CTA, `ctas` CTAs, n columns.
+struct LinTile {
+    int ctas, n;
+};
+
+// One product for choose_tile(): an m x n result, `depth` 64-deep blocks
+// (`split`: which may be split).
+struct LinWork {
+    int64_t m, n, depth;
+    bool split;
+};
+LinTile choose_tile(LinWork a, LinWork b);
 
 // First words of the workspace, written by the plan kernel (n_live, n_items)
 // and the prepare kernel (alpha).
@@ -29,6 +47,7 @@ struct LinHeader {
     int64_t n_items;  // rows that count towards the mean
     int32_t n_live;   // rows packed
     float alpha;      // factor of both gradients that is the same for every row
+    int32_t dh_splits;  // parts that dhidden's sums came in (grads kernel)
 };
 
 // row_map values of rows that are not packed.
@@ -69,7 +88,7 @@ struct LinParams {
     int32_t *row_list, *row_map;  // packed -> original, original -> packed
     int32_t *tgt;                 // [rows_pad, k] packed targets (-1: out of range)
     float *xt;                    // [rows_pad, k] their logits
-    float2 *partials;             // [rows_pad, tiles]
+    float2 *partials;             // [rows_pad, tiles] (max, sum) of each tile
     float2 *grow;                 // [rows_pad] (M, coef / S)
     float *dzt;                   // [rows_pad, k] dz of the gathered columns
     // Operands of the products are bf16 planes: one for bf16 inputs, three
@@ -83,9 +102,9 @@ struct LinParams {
     int64_t wpack_rows;
     void *dz;                     // [planes, rows_pad, piece]
     int64_t dz_plane;
-    float *dh;                    // [dh_splits, rows_pad, dh_pitch] sums
-    int64_t dh_pitch;
-    int dh_splits;
+    float *dh;                    // [parts, rows of whole tiles, dh_pitch] sums
+    int64_t dh_pitch, dh_room;    // elements from row to row, and in all
+    LinTile logits_tile, grads_tile;
     int64_t rows_pad, tiles, piece;
 
     int32_t *dev_status;

@@ -16,9 +16,12 @@ namespace {
 constexpr int64_t kMaxVocab = INT32_MAX - 64;
 constexpr int64_t kMaxRows = int64_t{1} << 24;
 constexpr int64_t kMaxDim = int64_t{1} << 20;
-// Bytes of dz that one piece of the vocabulary may take beyond its smallest
-// width (kLinPieceUnit columns).
+// Bytes that one piece's dz, or a piece of an fp32 weight, may take beyond the
+// smallest width (kLinPieceUnit columns).
 constexpr int64_t kPieceBytes = int64_t{512} << 20;
+// The same for a bf16 weight that has to be packed; most are read in place
+// and leave this room unused.
+constexpr int64_t kWeightBytes = int64_t{128} << 20;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -28,12 +31,13 @@ struct Layout {
     size_t head, row_list, row_map, tgt, xt, partials, loss, grow, dzt, hpack, wpack, dz,
         dh;
     size_t total;
-    int64_t rows_pad, tiles, piece, pitch, wpack_rows, dh_pitch;
-    int planes, dh_splits;
+    int64_t rows_pad, tiles, piece, pitch, wpack_rows, dh_pitch, dh_room;
+    int planes;
+    gbce::LinTile logits_tile, grads_tile;
 };
 
-// Pairs of SMs of the GPU, and the most parts that dhidden's sums take.
-constexpr int64_t kPairs = 76, kMaxSplits = 16;
+// fp32 values that split sums of dhidden may take beyond one part.
+constexpr int64_t kSplitRoom = int64_t{8} << 20;
 
 // Where everything lies in the workspace.  With `backward`, the buffers of
 // the gradient (and of the statistics, which a fused call needs too).
@@ -50,7 +54,10 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
         return at;
     };
     w.rows_pad = round_up(rows, gbce::kLinRowPad);
-    w.tiles = (vocab + gbce::kLinTileV - 1) / gbce::kLinTileV;
+    const int64_t products = dt == GBCE_BF16 ? 1 : 6;
+    const int64_t depth = (dim + 63) / 64 * products;
+    w.logits_tile = gbce::choose_tile({rows, vocab, depth, false}, {0, 0, 0, false});
+    w.tiles = (vocab + w.logits_tile.n - 1) / w.logits_tile.n;
     w.head = take(1, sizeof(gbce::LinHeader));
     w.row_list = take(rows, 4);
     w.row_map = take(rows, 4);
@@ -61,8 +68,8 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
     w.planes = dt == GBCE_BF16 ? 1 : 3;
     w.pitch = round_up(dim, 8);
     w.hpack = take(w.planes * w.rows_pad * w.pitch, 2);
-    const int64_t full = round_up(vocab, gbce::kLinTileV);
-    int64_t wunits = kPieceBytes / (w.planes * w.pitch * gbce::kLinPieceUnit * 2);
+    const int64_t full = round_up(vocab, 256);
+    int64_t wunits = (dt == GBCE_BF16 ? kWeightBytes : kPieceBytes) / (w.planes * w.pitch * gbce::kLinPieceUnit * 2);
     wunits = wunits < 1 ? 1 : wunits;
     w.wpack_rows = wunits * gbce::kLinPieceUnit < full ? wunits * gbce::kLinPieceUnit : full;
     w.wpack = take(w.planes * w.wpack_rows * w.pitch, 2);
@@ -78,13 +85,13 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
             units = wunits;
         w.piece = units * gbce::kLinPieceUnit < full ? units * gbce::kLinPieceUnit : full;
         w.dz = take(w.planes * w.rows_pad * w.piece, 2);
-        // few row tiles: the sums over the vocabulary are split so that every
-        // pair of SMs has a part
-        const int64_t out_tiles = w.rows_pad / 256 * ((dim + 255) / 256);
-        const int64_t parts = kPairs / out_tiles;
-        w.dh_splits = static_cast<int>(parts < 1 ? 1 : (parts > kMaxSplits ? kMaxSplits : parts));
+        const int64_t piece_depth = w.piece / 64 * products, row_depth = (rows + 63) / 64 * products;
+        w.grads_tile = gbce::choose_tile({rows, dim, piece_depth, true}, {w.piece, dim, row_depth, false});
         w.dh_pitch = round_up(dim, 4);
-        w.dh = take(w.dh_splits * w.rows_pad * w.dh_pitch, 4);
+        const int64_t one = w.rows_pad * w.dh_pitch;
+        const int64_t most = one * gbce::kMaxSplits < kSplitRoom ? one * gbce::kMaxSplits : kSplitRoom;
+        w.dh_room = one > most ? one : most;
+        w.dh = take(w.dh_room, 4);
     }
     w.total = off;
     return w;
@@ -223,10 +230,12 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
         p.dz_plane = w.rows_pad * w.piece;
         p.dh = at<float>(ws, w.dh);
         p.dh_pitch = w.dh_pitch;
-        p.dh_splits = w.dh_splits;
+        p.dh_room = w.dh_room;
     }
     p.rows_pad = w.rows_pad;
     p.tiles = w.tiles;
+    p.logits_tile = w.logits_tile;
+    p.grads_tile = w.grads_tile;
     p.piece = w.piece;
     p.dev_status = dev_status;
     return p;

@@ -1,21 +1,27 @@
 // The matrix products of the calls that start from hidden states, on the
-// tensor cores: one kernel, four uses.
+// tensor cores: one kernel, three uses.
 //
-//   stats  logits = hidden . weight^T    -> (max, sum) per row and 256 columns
+//   stats  logits = hidden . weight^T    -> (max, sum) per row and tile
 //   dz     the same logits again         -> dz, in memory for one piece
-//   dh     dz . weight                   -> dhidden sums (fp32)
-//   dw     dz^T . hidden                 -> dweight rows of the piece
+//   grads  dz . weight                   -> dhidden sums (fp32), and in the
+//          dz^T . hidden                 -> same launch dweight rows of the piece
 //
-// A pair of CTAs works on a 256 x 256 tile: TMA brings 64-deep slices of both
-// operands into a six-stage ring (32 KB a stage and CTA), one thread of the
-// pair issues the MMAs (M = 256 across the pair), and the sums lie in TMEM,
-// two tiles' worth (2 x 256 columns), so that four warps turn one tile into
-// outputs while the next is multiplied.  Persistent: one pair per two SMs.
+// TMA brings 64-deep slices of both operands of a tile into a ring, one thread
+// issues the MMAs, and the sums lie in TMEM, two tiles' worth, so that four
+// warps turn one tile into outputs while the next is multiplied.  Persistent:
+// every CTA (or pair of CTAs) takes tiles until there are no more.
+//
+// Tiles.  256 x 256 by a pair of CTAs (M = 256 across the pair, each loads
+// half of both operands) moves the fewest bytes per product and is what large
+// calls run.  128 x {256, 128, 64} by single CTAs is for calls whose 256 x 256
+// tiles would leave SMs idle, and, 256 wide, for up to 128 rows, where the
+// weight's bytes are the work and half of a pair's rows would be empty.
+// choose_tile() takes the shape with the least estimated time.
 //
 // Operands are read in the layout they have: hidden, weight and dz lie with
-// the product's depth innermost for stats and dz (and dz for dh), and with it
-// outermost for dh's weight and both operands of dw; the matrix descriptors
-// take either, so that nothing is ever transposed in memory.
+// the product's depth innermost for the logits (and dz for dhidden), and with
+// it outermost for dhidden's weight and both operands of dweight; the matrix
+// descriptors take either, so that nothing is ever transposed in memory.
 //
 // fp32 inputs come as three bf16 planes, x = hi + mid + lo with 8 more bits
 // in each; six of the nine products (all above 2^-24 of x y) are summed,
@@ -30,25 +36,33 @@ namespace gbce {
 
 namespace {
 
-constexpr int kRing = 6;
-constexpr int kTile = 256;           // rows and columns of a pair's tile
 constexpr int kDepth = 64;           // depth of a stage: 128 bytes of bf16
-constexpr uint32_t kHalfBytes = 128 * kDepth * 2;  // a CTA's half of one operand
-constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kRowBytes = kDepth * 2;
+constexpr uint32_t kBytesA = 128 * kRowBytes;  // a CTA's rows of A in a stage
 constexpr int kMmaThreads = 192;     // TMA warp, MMA warp, four epilogue warps
-constexpr uint32_t kTmemCols = 512;
 
-enum LinMode : int { kLinStats, kLinDz, kLinDh, kLinDw };
+enum LinMode : int { kLinStats, kLinDz, kLinGrads };
+
+template <int CTAS, int NT> struct Tile {
+    static constexpr int kM = 128 * CTAS, kN = NT;
+    static constexpr int kRowsB = NT / CTAS;  // rows of B that a CTA loads
+    static constexpr uint32_t kBytesB = kRowsB * kRowBytes;
+    static constexpr uint32_t kStage = kBytesA + kBytesB;
+    static constexpr int kRing = 196608 / kStage;  // 6, 4, 6 or 8 stages
+    static constexpr uint32_t kTmemCols = 2 * NT;
+};
 
 struct MmaArgs {
-    const LinHeader *head;
+    LinHeader *head;
     int32_t *dev_status;
     int32_t pairs;         // plane products: 1, or 6 for fp32 inputs
-    int32_t depth;         // elements of the depth (dw: the live rows)
-    int32_t tiles_m;       // dw: tiles of the piece; else from the live rows
-    int32_t tiles_n;
-    int32_t splits;        // dh: parts of the depth
-    int32_t b_row0;        // stats, dz, dh: the piece's first row in the weight's map
+    int32_t blocks;        // stats, dz, dhidden: the depth in blocks of kDepth
+    int32_t tiles_n;       // stats, dz: of the piece; grads: of dim
+    int32_t tiles_v;       // grads: tiles of the piece's rows (0: no dweight)
+    int32_t want_dh;
+    int32_t piece_blocks;  // grads: blocks of a whole piece
+    int32_t a_rows;        // stats, dz: rows of A's box
+    int32_t b_row0;        // the piece's first row in the weight's map
     int64_t v0, vocab;     // first column of the piece; end of the vocabulary
     float c;
     int32_t k;
@@ -62,58 +76,115 @@ struct MmaArgs {
     int64_t piece, dz_plane;
     int32_t planes;
     float *dh;
-    int64_t dim, dh_pitch, dh_split;
+    int64_t dim, dh_pitch, dh_room;
     void *dweight;
     int64_t dweight_stride;
     int32_t first, accumulate, bf16, vec;
 };
 
-struct MmaShared {
-    uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2];
+template <int RING> struct MmaShared {
+    uint64_t full[RING], empty[RING], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int32_t failed;
+    float turn[4][32][33];  // a warp's 32 x 32 values, to be stored by rows
 };
 
-constexpr uint32_t kSmemBytes = kRing * kStageBytes + sizeof(MmaShared) + 1024;
-
-struct TileId {
-    int32_t m, n, split;
-};
-
-// Tiles in an order that keeps both operands in L2 while they are needed.
-// stats, dz: all row tiles (hidden stays in L2) before the next columns, so
-// that the table is read once.  dh, dw: bands of 8 tiles high, so that the
-// pairs at work cover a block that is about square.
-template <int MODE>
-__device__ __forceinline__ TileId tile_of(int64_t t, int32_t tm, int32_t tn)
+template <int CTAS, int NT>
+constexpr uint32_t smem_bytes()
 {
-    TileId r;
-    if (MODE == kLinStats || MODE == kLinDz) {
-        r.m = static_cast<int32_t>(t % tm);
-        r.n = static_cast<int32_t>(t / tm);
-        r.split = 0;
-        return r;
-    }
-    const int64_t per = static_cast<int64_t>(tm) * tn;
-    r.split = static_cast<int32_t>(t / per);
-    const int32_t u = static_cast<int32_t>(t % per);
-    const int32_t band = u / (8 * tn), in = u % (8 * tn);
-    const int32_t high = min(8, tm - band * 8);
-    r.m = band * 8 + in % high;
-    r.n = in / high;
-    return r;
+    using S = Tile<CTAS, NT>;
+    return S::kRing * S::kStage + sizeof(MmaShared<S::kRing>) + 1024;
 }
+
+// One tile's work: which operands, where, and how deep.
+struct Job {
+    int32_t m, n, split;
+    int32_t k0, k1;  // depth blocks
+    bool dw;         // grads: a dweight tile, else a dhidden tile
+};
+
+// The tiles of a launch, the same for every role.
+template <int MODE> struct Jobs {
+    int32_t tm, tn, tv, splits, blocks, live_blocks;
+    int64_t dh_tiles, total;
+
+    __device__ Jobs(const MmaArgs &q, int32_t live, int tile_m, int64_t units)
+    {
+        tm = (live + tile_m - 1) / tile_m;
+        tn = q.tiles_n;
+        blocks = q.blocks;
+        splits = 1;
+        tv = 0;
+        live_blocks = (live + kDepth - 1) / kDepth;
+        if (MODE != kLinGrads) {
+            dh_tiles = total = static_cast<int64_t>(tm) * tn;
+            return;
+        }
+        tv = q.tiles_v;
+        dh_tiles = q.want_dh ? static_cast<int64_t>(tm) * tn : 0;
+        // dhidden's depth, the vocabulary, is split until a tile is at most an
+        // eighth of what a CTA has to do in all, so that handing tiles out in
+        // turn comes out even (1024 x 32768 x 1024 fp32: 655 us with halves,
+        // EIGHTH_US with eighths); the same for every piece, whose sums are added
+        const int64_t all = dh_tiles * q.piece_blocks + static_cast<int64_t>(tv) * tn * live_blocks;
+        const int64_t share = max(all / units / 8, static_cast<int64_t>(4));
+        int64_t want = (q.piece_blocks + share - 1) / share;
+        if (dh_tiles > 0)
+            want = min(want, q.dh_room / (static_cast<int64_t>(tm) * tile_m * q.dh_pitch));
+        splits = static_cast<int32_t>(max(static_cast<int64_t>(1), min(want, static_cast<int64_t>(kMaxSplits))));
+        dh_tiles *= splits;
+        total = dh_tiles + static_cast<int64_t>(tv) * tn;
+    }
+
+    // Tiles in an order that keeps both operands in L2 while they are needed.
+    // Logits: all row tiles (hidden stays in L2) before the next columns, so
+    // that the table is read once.  Gradients: bands of 8 tiles high, so that
+    // the CTAs at work cover a block that is about square; dhidden's first,
+    // being the deeper ones.
+    __device__ __forceinline__ Job at(int64_t t) const
+    {
+        Job j;
+        j.split = 0;
+        j.dw = false;
+        j.k0 = 0;
+        j.k1 = blocks;
+        if (MODE != kLinGrads) {
+            j.m = static_cast<int32_t>(t % tm);
+            j.n = static_cast<int32_t>(t / tm);
+            return j;
+        }
+        int32_t high_all = tm;
+        if (t >= dh_tiles) {
+            t -= dh_tiles;
+            j.dw = true;
+            j.k1 = live_blocks;
+            high_all = tv;
+        } else {
+            const int64_t per = static_cast<int64_t>(tm) * tn;
+            j.split = static_cast<int32_t>(t / per);
+            t %= per;
+            j.k0 = static_cast<int32_t>(static_cast<int64_t>(blocks) * j.split / splits);
+            j.k1 = static_cast<int32_t>(static_cast<int64_t>(blocks) * (j.split + 1) / splits);
+        }
+        const int32_t u = static_cast<int32_t>(t);
+        const int32_t band = u / (8 * tn), in = u % (8 * tn);
+        const int32_t high = min(8, high_all - band * 8);
+        j.m = band * 8 + in % high;
+        j.n = in / high;
+        return j;
+    }
+};
 
 // Plane indices of product q of six, smallest first.
 __device__ __forceinline__ int plane_a(int pairs, int q) { return pairs == 1 ? 0 : (0x201100 >> (4 * (5 - q))) & 15; }
 __device__ __forceinline__ int plane_b(int pairs, int q) { return pairs == 1 ? 0 : (0x021010 >> (4 * (5 - q))) & 15; }
 
-__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, MmaShared *sh,
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, int32_t *failed,
                                              int32_t *dev_status)
 {
     if (mbar_wait_cluster(bar, parity))
         return true;
-    *reinterpret_cast<volatile int32_t *>(&sh->failed) = 1;
+    *reinterpret_cast<volatile int32_t *>(failed) = 1;
     report(dev_status, GBCE_DEV_TIMEOUT);
     return false;
 }
@@ -156,16 +227,43 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 }  // namespace
 
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
-    lin_mma_kernel(const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MmaArgs q)
+// Stores of one 32 x 32 block whose rows do not start on 16 bytes: through
+// shared memory, so that a warp writes one row's 32 columns at a time.
+template <typename T>
+__device__ __forceinline__ void store_rows_turned(float (&buf)[32][33], const float (&v)[32], T *out,
+                                                  int64_t stride, int32_t rows, int32_t cols,
+                                                  bool accumulate)
 {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        buf[lane][j] = v[j];
+    __syncwarp();
+    if (lane < cols) {
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+            T *o = out + r * stride + lane;
+            const float x = buf[r][lane];
+            *o = T(accumulate ? static_cast<float>(*o) + x : x);
+        }
+    }
+    __syncwarp();
+}
+
+template <int MODE, int CTAS, int NT>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    lin_mma_kernel(const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_a2,
+                   const __grid_constant__ CUtensorMap map_b2, const __grid_constant__ MmaArgs q)
+{
+    using S = Tile<CTAS, NT>;
+    constexpr int kRing = S::kRing;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-    MmaShared *sh = reinterpret_cast<MmaShared *>(ring + kRing * kStageBytes);
+    MmaShared<kRing> *sh = reinterpret_cast<MmaShared<kRing> *>(ring + kRing * S::kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
     if (threadIdx.x == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
@@ -175,72 +273,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 8);  // four warps of each CTA
+            mbar_init(&sh->acc_empty[i], 4 * CTAS);  // four warps of each CTA
         }
         sh->failed = 0;
         fence_barrier_init();
     }
     if (warp == 1)
-        tmem_alloc_pair(&sh->tmem, kTmemCols);
+        tmem_alloc<CTAS>(&sh->tmem, S::kTmemCols);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers exist before either signals them
+    if (CTAS == 2)
+        cluster_sync();  // both CTAs' barriers exist before either signals them
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
 
     grid_dependency_wait();
     launch_dependents();
     const int32_t live = q.head->n_live;
-    const int32_t tm = MODE == kLinDw ? q.tiles_m : (live + kTile - 1) / kTile;
-    const int32_t tn = q.tiles_n;
-    const int64_t tiles = static_cast<int64_t>(tm) * tn * (MODE == kLinDh ? q.splits : 1);
-    const int64_t pair0 = blockIdx.x >> 1, pairs_at_work = gridDim.x >> 1;
-    const int32_t depth = MODE == kLinDw ? live : q.depth;
-    const int32_t blocks_all = (depth + kDepth - 1) / kDepth;
-
-    // depth blocks [first, last) of a tile
-    const auto depth_first = [&](int32_t split) {
-        return MODE == kLinDh ? static_cast<int32_t>(static_cast<int64_t>(blocks_all) * split / q.splits) : 0;
-    };
-    const auto depth_last = [&](int32_t split) {
-        return MODE == kLinDh ? static_cast<int32_t>(static_cast<int64_t>(blocks_all) * (split + 1) / q.splits)
-                              : blocks_all;
-    };
+    const int64_t units = gridDim.x / CTAS, unit = blockIdx.x / CTAS;
+    const Jobs<MODE> jobs(q, live, S::kM, units);
+    if (MODE == kLinGrads && blockIdx.x == 0 && threadIdx.x == 0)
+        q.head->dh_splits = jobs.splits;
 
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int64_t t = pair0; ok && t < tiles; t += pairs_at_work) {
-                const TileId id = tile_of<MODE>(t, tm, tn);
-                const int32_t k0 = depth_first(id.split), k1 = depth_last(id.split);
-                const int32_t m0 = id.m * kTile + static_cast<int32_t>(rank) * 128;
-                const int32_t n0 = id.n * kTile + static_cast<int32_t>(rank) * 128;
+            for (int64_t t = unit; ok && t < jobs.total; t += units) {
+                const Job job = jobs.at(t);
+                const int32_t m0 = job.m * S::kM + static_cast<int32_t>(rank) * 128;
+                const int32_t n0 = job.n * NT + static_cast<int32_t>(rank) * S::kRowsB;
+                // bytes of a stage: A's box may be lower than the tile
+                const uint32_t bytes = MODE == kLinGrads
+                                           ? S::kStage
+                                           : static_cast<uint32_t>(q.a_rows) * kRowBytes + S::kBytesB;
                 for (int pr = 0; ok && pr < q.pairs; ++pr) {
                     const int za = plane_a(q.pairs, pr), zb = plane_b(q.pairs, pr);
-                    for (int32_t kb = k0; kb < k1; ++kb) {
-                        if (!wait_or_fail(&sh->empty[stage], phase ^ 1u, sh, q.dev_status)) {
+                    for (int32_t kb = job.k0; kb < job.k1; ++kb) {
+                        if (!wait_or_fail(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *a = ring + stage * kStageBytes, *b = a + kHalfBytes;
+                        uint8_t *a = ring + stage * S::kStage, *b = a + kBytesA;
                         if (rank == 0)
-                            mbar_arrive_expect_tx(&sh->full[stage], 2 * kStageBytes);
-                        const uint32_t bar = map_to_rank(smem_addr(&sh->full[stage]), 0);
+                            mbar_arrive_expect_tx(&sh->full[stage], CTAS * bytes);
+                        const uint32_t own = smem_addr(&sh->full[stage]);
+                        const uint32_t bar = CTAS == 2 ? map_to_rank(own, 0) : own;
                         const int32_t k = kb * kDepth;
-                        if (MODE == kLinDw) {
-                            tma_load_3d_pair(a, &map_a, m0, k, za, bar);
-                            tma_load_3d_pair(a + kHalfBytes / 2, &map_a, m0 + 64, k, za, bar);
+                        if (MODE == kLinGrads) {
+                            if (job.dw) {
+                                tma_load_3d<CTAS>(a, &map_a2, m0, k, za, bar);
+                                tma_load_3d<CTAS>(a + kBytesA / 2, &map_a2, m0 + 64, k, za, bar);
+                            } else {
+                                tma_load_3d<CTAS>(a, &map_a, k, m0, za, bar);
+                            }
+                            const CUtensorMap *mb = job.dw ? &map_b2 : &map_b;
+                            const int32_t row = job.dw ? k : q.b_row0 + k;
+#pragma unroll
+                            for (int i = 0; i < S::kRowsB / 64; ++i)
+                                tma_load_3d<CTAS>(b + i * 64 * kRowBytes, mb, n0 + 64 * i, row, zb, bar);
                         } else {
-                            tma_load_3d_pair(a, &map_a, k, m0, za, bar);
-                        }
-                        if (MODE == kLinDw || MODE == kLinDh) {
-                            const int32_t row = MODE == kLinDh ? q.b_row0 + k : k;
-                            tma_load_3d_pair(b, &map_b, n0, row, zb, bar);
-                            tma_load_3d_pair(b + kHalfBytes / 2, &map_b, n0 + 64, row, zb, bar);
-                        } else {
-                            tma_load_3d_pair(b, &map_b, k, q.b_row0 + n0, zb, bar);
+                            tma_load_3d<CTAS>(a, &map_a, k, m0, za, bar);
+                            tma_load_3d<CTAS>(b, &map_b, k, q.b_row0 + n0, zb, bar);
                         }
                         if (++stage == kRing) {
                             stage = 0;
@@ -252,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
             // every stage used is free again: no copy is in flight and no
             // arrival is on its way to this CTA when it ends
             for (int i = 0; ok && i < kRing; ++i) {
-                ok = wait_or_fail(&sh->empty[stage], phase ^ 1u, sh, q.dev_status);
+                ok = wait_or_fail(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status);
                 if (++stage == kRing) {
                     stage = 0;
                     phase ^= 1u;
@@ -262,39 +357,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr bool kAmn = MODE == kLinDw, kBmn = MODE == kLinDw || MODE == kLinDh;
-            constexpr uint32_t idesc = mma_idesc(kTile, kTile, kAmn, kBmn);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t t = pair0; ok && t < tiles; t += pairs_at_work) {
-                const TileId id = tile_of<MODE>(t, tm, tn);
-                const int32_t n_blocks = (depth_last(id.split) - depth_first(id.split)) * q.pairs;
-                ok = wait_or_fail(&sh->acc_empty[acc], acc_phase ^ 1u, sh, q.dev_status);
+            for (int64_t t = unit; ok && t < jobs.total; t += units) {
+                const Job job = jobs.at(t);
+                const bool a_mn = MODE == kLinGrads && job.dw, b_mn = MODE == kLinGrads;
+                const uint32_t idesc = mma_idesc(S::kM, NT, a_mn, b_mn);
+                // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
+                const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
+                const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
+                ok = wait_or_fail(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
                 tc_fence_after();
-                const uint32_t d = tmem + acc * kTile;
+                const uint32_t d = tmem + acc * NT;
                 for (int32_t kb = 0; ok && kb < n_blocks; ++kb) {
-                    ok = wait_or_fail(&sh->full[stage], phase, sh, q.dev_status);
+                    ok = wait_or_fail(&sh->full[stage], phase, &sh->failed, q.dev_status);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t a = smem_addr(ring + stage * kStageBytes), b = a + kHalfBytes;
+                    const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
+                    uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
+                    uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
 #pragma unroll
                     for (int kk = 0; kk < kDepth / 16; ++kk) {
-                        const uint64_t da = kAmn ? mma_desc(a + kk * 2048, kHalfBytes / 2, 1024)
-                                                 : mma_desc(a + kk * 32, 16, 1024);
-                        const uint64_t db = kBmn ? mma_desc(b + kk * 2048, kHalfBytes / 2, 1024)
-                                                 : mma_desc(b + kk * 32, 16, 1024);
-                        mma_bf16_pair(d, da, db, idesc, kb > 0 || kk > 0);
+                        mma_bf16<CTAS>(d, da, db, idesc, kb > 0 || kk > 0);
+                        da += step_a >> 4;
+                        db += step_b >> 4;
                     }
-                    mma_commit_pair(&sh->empty[stage]);
+                    mma_commit<CTAS>(&sh->empty[stage]);
                     if (++stage == kRing) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (ok)
-                    mma_commit_pair(&sh->acc_full[acc]);
+                    mma_commit<CTAS>(&sh->acc_full[acc]);
                 acc ^= 1;
                 acc_phase ^= acc == 0 ? 1u : 0u;
             }
@@ -303,47 +400,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
     } else {
         const int quad = warp & 3;  // the TMEM lanes that this warp may read
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        const int32_t tile_row = static_cast<int32_t>(rank) * 128 + quad * 32 + lane;
-        const float alpha = MODE == kLinDw ? q.head->alpha : 1.0f;
+        const int32_t warp_row = static_cast<int32_t>(rank) * 128 + quad * 32;
+        const float alpha = MODE == kLinGrads ? q.head->alpha : 1.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int64_t t = pair0; t < tiles; t += pairs_at_work) {
-            const TileId id = tile_of<MODE>(t, tm, tn);
-            const bool any = depth_last(id.split) > depth_first(id.split);
-            const int32_t row = id.m * kTile + tile_row;
-            const int64_t col0 = static_cast<int64_t>(id.n) * kTile;
-            // stats, dz: this row's gathered columns, as bits of the tile
-            uint32_t hit[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int64_t t = unit; t < jobs.total; t += units) {
+            const Job job = jobs.at(t);
+            const bool any = job.k1 > job.k0;
+            const int32_t row0 = job.m * S::kM + warp_row, row = row0 + lane;
+            const int64_t col0 = static_cast<int64_t>(job.n) * NT;
+            // logits: this row's gathered columns, as bits of the tile
+            uint32_t hit[NT / 32];
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w)
+                hit[w] = 0;
             bool any_hit = false;
             float2 g = make_float2(0.0f, 0.0f);
-            if ((MODE == kLinStats || MODE == kLinDz) && row < live) {
+            if (MODE != kLinGrads && row < live) {
                 if (MODE == kLinDz)
                     g = q.grow[row];
                 for (int k = 0; k < q.k; ++k) {
                     const int64_t j = q.tgt[static_cast<int64_t>(row) * q.k + k] - (q.v0 + col0);
-                    if (j >= 0 && j < kTile) {
+                    if (j >= 0 && j < NT) {
                         any_hit = true;
 #pragma unroll
-                        for (int w = 0; w < 8; ++w)
+                        for (int w = 0; w < NT / 32; ++w)
                             if (MODE == kLinStats && j >> 5 == w)
                                 hit[w] |= 1u << (j & 31);
                     }
                 }
             }
-            if (!__all_sync(0xffffffffu, wait_or_fail(&sh->acc_full[acc], acc_phase, sh, q.dev_status)))
+            if (!__all_sync(0xffffffffu,
+                            wait_or_fail(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status)))
                 break;
             tc_fence_after();
-            const uint32_t src = tmem + lanes + acc * kTile;
+            const uint32_t src = tmem + lanes + acc * NT;
             RowStats st;
 #pragma unroll 1
-            for (int ch = 0; ch < kTile / 32; ++ch) {
+            for (int ch = 0; ch < NT / 32; ++ch) {
                 float v[32];
                 tmem_load32(src + ch * 32, v);
-                if (ch == kTile / 32 - 1) {  // the sums are read: the tile after next may start
+                if (ch == NT / 32 - 1) {  // the sums are read: the tile after next may start
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_remote(map_to_rank(smem_addr(&sh->acc_empty[acc]), 0));
+                    if (lane == 0) {
+                        if (CTAS == 2)
+                            mbar_arrive_remote(map_to_rank(smem_addr(&sh->acc_empty[acc]), 0));
+                        else
+                            mbar_arrive(&sh->acc_empty[acc]);
+                    }
                 }
                 const int64_t c0 = col0 + ch * 32;
                 if (MODE == kLinStats) {
@@ -355,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
                     }
                     uint32_t mine = 0;
 #pragma unroll
-                    for (int w = 0; w < 8; ++w)
+                    for (int w = 0; w < NT / 32; ++w)
                         mine = ch == w ? hit[w] : mine;
                     if (mine != 0) {
                         for (int k = 0; k < q.k; ++k) {
@@ -400,9 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
                         }
                     }
                 }
-                if (MODE == kLinDh && row < live) {
-                    float *out = q.dh + static_cast<int64_t>(id.split) * q.dh_split +
-                                 static_cast<int64_t>(row) * q.dh_pitch + c0;
+                if (MODE == kLinGrads && !job.dw && row < live) {
+                    float *out = q.dh + (static_cast<int64_t>(job.split) * jobs.tm * S::kM + row) * q.dh_pitch + c0;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         if (c0 + j < q.dim) {
@@ -416,69 +520,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
                             *reinterpret_cast<float4 *>(out + j) = x;
                         }
                 }
-                if (MODE == kLinDw && q.v0 + row < q.vocab) {
+                if (MODE == kLinGrads && job.dw && q.v0 + row0 < q.vocab && c0 < q.dim) {
                     const int64_t at = (q.v0 + row) * q.dweight_stride + c0;
+                    const bool mine = q.v0 + row < q.vocab;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = any ? alpha * v[j] : 0.0f;
-                    const bool whole = q.vec != 0 && c0 + 32 <= q.dim;
-                    if (q.bf16) {
+                    if (q.vec == 0 || c0 + 32 > q.dim) {
+                        const int64_t base = (q.v0 + row0) * q.dweight_stride + c0;
+                        const int32_t rows = static_cast<int32_t>(min(static_cast<int64_t>(32), q.vocab - q.v0 - row0));
+                        const int32_t cols = static_cast<int32_t>(min(static_cast<int64_t>(32), q.dim - c0));
+                        if (q.bf16)
+                            store_rows_turned(sh->turn[quad], v, static_cast<__nv_bfloat16 *>(q.dweight) + base,
+                                              q.dweight_stride, rows, cols, q.accumulate != 0);
+                        else
+                            store_rows_turned(sh->turn[quad], v, static_cast<float *>(q.dweight) + base,
+                                              q.dweight_stride, rows, cols, q.accumulate != 0);
+                    } else if (q.bf16 && mine) {
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.dweight) + at;
-                        if (whole) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint4 *o = reinterpret_cast<uint4 *>(out + j);
-                                if (q.accumulate) {
-                                    const uint4 old = *o;
-                                    const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 *o = reinterpret_cast<uint4 *>(out + j);
+                            if (q.accumulate) {
+                                const uint4 old = *o;
+                                const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float2 f = bf16x2_to_float2(ow[i]);
-                                        v[j + 2 * i] += f.x;
-                                        v[j + 2 * i + 1] += f.y;
-                                    }
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f = bf16x2_to_float2(ow[i]);
+                                    v[j + 2 * i] += f.x;
+                                    v[j + 2 * i + 1] += f.y;
                                 }
-                                *o = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                                                pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c0 + j < q.dim)
-                                    out[j] = __float2bfloat16_rn(
-                                        q.accumulate ? __bfloat162float(out[j]) + v[j] : v[j]);
+                            *o = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                                            pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
                         }
-                    } else {
+                    } else if (mine) {
                         float *out = static_cast<float *>(q.dweight) + at;
-                        if (whole) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                float4 *o = reinterpret_cast<float4 *>(out + j);
-                                float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                                if (q.accumulate) {
-                                    const float4 old = *o;
-                                    x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
-                                }
-                                *o = x;
+                        for (int j = 0; j < 32; j += 4) {
+                            float4 *o = reinterpret_cast<float4 *>(out + j);
+                            float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                            if (q.accumulate) {
+                                const float4 old = *o;
+                                x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c0 + j < q.dim)
-                                    out[j] = q.accumulate ? out[j] + v[j] : v[j];
+                            *o = x;
                         }
                     }
                 }
             }
             if (MODE == kLinStats && row < live)
-                q.partials[static_cast<int64_t>(row) * q.partial_tiles + q.v0 / kTile + id.n] =
+                q.partials[static_cast<int64_t>(row) * q.partial_tiles + q.v0 / NT + job.n] =
                     make_float2(st.s == st.s ? st.m : (st.m == kNegInf ? 0.0f : st.m), st.s);
             if (MODE == kLinDz && any_hit) {
                 // the gathered columns, over what this thread wrote above
                 for (int k = 0; k < q.k; ++k) {
                     const int64_t at = static_cast<int64_t>(row) * q.k + k;
                     const int64_t j = q.tgt[at] - (q.v0 + col0);
-                    if (j >= 0 && j < kTile) {
+                    if (j >= 0 && j < NT) {
                         float x = q.dzt[at];
                         __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + col0 + j;
                         for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
@@ -503,13 +602,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmaThreads, 1)
             __nanosleep(1000);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if (CTAS == 2)
+        cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free_pair(tmem, kTmemCols);
+        tmem_free<CTAS>(tmem, S::kTmemCols);
     }
-    __syncthreads();
-    cluster_sync();
+    if (CTAS == 2) {
+        __syncthreads();
+        cluster_sync();
+    }
 }
 
 // ----------------------------------------------------------------- launches
@@ -557,31 +659,47 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t inner, int64_t 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int MODE>
-cudaError_t launch_mma(const CUtensorMap &a, const CUtensorMap &b, const MmaArgs &q, int64_t max_tiles,
-                       cudaStream_t s)
+template <int MODE, int CTAS, int NT>
+cudaError_t launch_mma(const CUtensorMap *maps, const MmaArgs &q, int64_t tiles, cudaStream_t s)
 {
     const int sms = device_sm_count();
     if (sms < 2)
         return cudaErrorInvalidDevice;
-    cudaError_t e = cudaFuncSetAttribute(lin_mma_kernel<MODE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const auto kernel = lin_mma_kernel<MODE, CTAS, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_bytes<CTAS, NT>());
     if (e != cudaSuccess)
         return e;
-    const int64_t pairs = max_tiles < sms / 2 ? max_tiles : sms / 2;
+    const int64_t units = tiles < sms / CTAS ? tiles : sms / CTAS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.gridDim = dim3(static_cast<unsigned>(CTAS * units));
     cfg.blockDim = dim3(kMmaThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = smem_bytes<CTAS, NT>();
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, lin_mma_kernel<MODE>, a, b, q);
+    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], q);
     note_launches(1);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t launch_shape(LinTile shape, const CUtensorMap *maps, const MmaArgs &q, int64_t tiles,
+                         cudaStream_t s)
+{
+    if (shape.ctas == 2)
+        return launch_mma<MODE, 2, 256>(maps, q, tiles, s);
+    if (shape.n == 256)
+        return launch_mma<MODE, 1, 256>(maps, q, tiles, s);
+    return shape.n == 128 ? launch_mma<MODE, 1, 128>(maps, q, tiles, s)
+                          : launch_mma<MODE, 1, 64>(maps, q, tiles, s);
 }
 
 // What the logits' operands look like to the kernels for one piece.
@@ -613,7 +731,6 @@ MmaArgs base_args(const LinParams &p, int64_t v0)
     q.dev_status = p.dev_status;
     q.planes = p.planes;
     q.pairs = p.planes == 1 ? 1 : 6;
-    q.splits = 1;
     q.v0 = v0;
     q.vocab = p.vocab;
     q.c = p.c;
@@ -623,32 +740,76 @@ MmaArgs base_args(const LinParams &p, int64_t v0)
     return q;
 }
 
-int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// Rows of A's box: no more than the call has, so that a few rows cost a few.
+uint32_t box_rows(const LinParams &p, LinTile shape)
+{
+    return shape.ctas == 1 && p.rows < 128 ? static_cast<uint32_t>(ceil_div(p.rows, 8) * 8) : 128u;
+}
 
 }  // namespace
+
+// Estimated cycles of the candidates and the best of them.  A 64-deep block
+// takes about 640 cycles as 256 x 256 by a pair or 128 x 256 by one CTA, 340
+// as 128 x 128 and 200 as 128 x 64 (whose operands' shared-memory reads set
+// the pace); a tile's start and outputs add about 2000 + 10 per column that
+// only the next tile hides.  `jobs` sums tiles x depth for the tile shape.
+LinTile choose_tile(LinWork a, LinWork b)
+{
+    constexpr LinTile shapes[4] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
+    constexpr int64_t cycles[4] = {640, 640, 340, 200};
+    LinTile best = shapes[0];
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < 4; ++i) {
+        const LinTile t = shapes[i];
+        const int64_t units = kLinSms / t.ctas, m = 128 * t.ctas;
+        int64_t cost = 2000 + 10 * t.n, longest = 0, sum = 0;
+        for (const LinWork &w : {a, b}) {
+            const int64_t tiles = ceil_div(w.m, m) * ceil_div(w.n, t.n);
+            const int64_t depth = w.split ? ceil_div(w.depth, ceil_div(units, tiles > 0 ? tiles : 1)) : w.depth;
+            sum += tiles * (w.depth * cycles[i] + 500);
+            if (tiles > 0 && depth > longest)
+                longest = depth;
+            // whole waves where every tile is as deep
+            if (b.m == 0)
+                cost += ceil_div(tiles, units) * w.depth * cycles[i];
+        }
+        if (b.m != 0)
+            cost += sum / units > longest * cycles[i] ? sum / units : longest * cycles[i];
+        if (cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return best;
+}
 
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
 {
     const int64_t step = p.weight_direct ? p.vocab : p.wpack_rows;
+    const LinTile shape = p.logits_tile;
     for (int64_t v0 = 0; v0 < p.vocab; v0 += step) {
         const int64_t v1 = v0 + step < p.vocab ? v0 + step : p.vocab;
         Weight w;
         cudaError_t e = piece_weight(p, v0, v1, v0 > 0, w, s);
-        CUtensorMap a, b;
+        CUtensorMap maps[4] = {};
+        MmaArgs q = base_args(p, v0);
+        q.a_rows = static_cast<int32_t>(box_rows(p, shape));
         if (e == cudaSuccess)
-            e = make_map(&a, p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, 128);
+            e = make_map(&maps[0], p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, q.a_rows);
         if (e == cudaSuccess)
-            e = make_map(&b, w.base, p.dim, w.rows, w.stride, p.planes, w.plane, 128);
+            e = make_map(&maps[1], w.base, p.dim, w.rows, w.stride, p.planes, w.plane,
+                         static_cast<uint32_t>(shape.n / shape.ctas));
         if (e != cudaSuccess)
             return e;
-        MmaArgs q = base_args(p, v0);
-        q.depth = static_cast<int32_t>(p.dim);
-        q.tiles_n = static_cast<int32_t>(tiles_of(v1 - v0));
+        q.blocks = static_cast<int32_t>(ceil_div(p.dim, kDepth));
+        q.tiles_n = static_cast<int32_t>(ceil_div(v1 - v0, shape.n));
         q.b_row0 = static_cast<int32_t>(w.row0);
         q.xt = p.xt;
         q.partials = p.partials;
         q.partial_tiles = p.tiles;
-        e = launch_mma<kLinStats>(a, b, q, tiles_of(p.rows) * q.tiles_n, s);
+        e = launch_shape<kLinStats>(shape, maps, q, ceil_div(p.rows, 128 * shape.ctas) * q.tiles_n, s);
         if (e != cudaSuccess)
             return e;
     }
@@ -657,56 +818,62 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
 
 cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
 {
+    const LinTile lt = p.logits_tile, gt = p.grads_tile;
     for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
         const int64_t v1 = v0 + p.piece < p.vocab ? v0 + p.piece : p.vocab;
         Weight w;
         cudaError_t e = piece_weight(p, v0, v1, v0 > 0 || p.fused, w, s);
-        CUtensorMap h_k, w_k, dz_k, w_mn, dz_mn, h_mn;
+        CUtensorMap logits[4] = {}, grads[4] = {};
         const auto map = [&e](CUtensorMap *m, const void *base, int64_t inner, int64_t rows,
                               int64_t stride, int64_t planes, int64_t plane, uint32_t box) {
             if (e == cudaSuccess)
                 e = make_map(m, base, inner, rows, stride, planes, plane, box);
         };
-        map(&h_k, p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, 128);
-        map(&h_mn, p.hpack, p.dim, p.rows_pad, p.pitch, p.planes, p.hpack_plane, 64);
-        map(&w_k, w.base, p.dim, w.rows, w.stride, p.planes, w.plane, 128);
-        map(&w_mn, w.base, p.dim, w.rows, w.stride, p.planes, w.plane, 64);
-        map(&dz_k, p.dz, p.piece, p.rows_pad, p.piece, p.planes, p.dz_plane, 128);
-        map(&dz_mn, p.dz, p.piece, p.rows_pad, p.piece, p.planes, p.dz_plane, 64);
+        MmaArgs q = base_args(p, v0);
+        q.a_rows = static_cast<int32_t>(box_rows(p, lt));
+        map(&logits[0], p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, q.a_rows);
+        map(&logits[1], w.base, p.dim, w.rows, w.stride, p.planes, w.plane,
+            static_cast<uint32_t>(lt.n / lt.ctas));
+        map(&grads[0], p.dz, p.piece, p.rows_pad, p.piece, p.planes, p.dz_plane, 128);
+        map(&grads[1], w.base, p.dim, w.rows, w.stride, p.planes, w.plane, 64);
+        map(&grads[2], p.dz, p.piece, p.rows_pad, p.piece, p.planes, p.dz_plane, 64);
+        map(&grads[3], p.hpack, p.dim, p.rows_pad, p.pitch, p.planes, p.hpack_plane, 64);
         if (e != cudaSuccess)
             return e;
-        const int64_t tv = tiles_of(v1 - v0), td = tiles_of(p.dim), tr = tiles_of(p.rows);
-        MmaArgs q = base_args(p, v0);
         q.b_row0 = static_cast<int32_t>(w.row0);
         q.grow = p.grow;
         q.dzt = p.dzt;
         q.dz = static_cast<__nv_bfloat16 *>(p.dz);
         q.piece = p.piece;
         q.dz_plane = p.dz_plane;
-        q.depth = static_cast<int32_t>(p.dim);
-        q.tiles_n = static_cast<int32_t>(tv);
-        e = launch_mma<kLinDz>(h_k, w_k, q, tr * tv, s);
-        q.tiles_n = static_cast<int32_t>(td);
-        if (e == cudaSuccess && p.dhidden != nullptr) {
-            q.depth = static_cast<int32_t>(v1 - v0);
-            q.splits = p.dh_splits;
+        q.blocks = static_cast<int32_t>(ceil_div(p.dim, kDepth));
+        q.tiles_n = static_cast<int32_t>(ceil_div(v1 - v0, lt.n));
+        e = launch_shape<kLinDz>(lt, logits, q, ceil_div(p.rows, 128 * lt.ctas) * q.tiles_n, s);
+        if (e != cudaSuccess)
+            return e;
+        q.blocks = static_cast<int32_t>(ceil_div(v1 - v0, kDepth));
+        q.piece_blocks = static_cast<int32_t>(ceil_div(p.piece, kDepth));
+        q.tiles_n = static_cast<int32_t>(ceil_div(p.dim, gt.n));
+        const int64_t most_splits = p.dhidden != nullptr ? kMaxSplits : 0;
+        if (p.dhidden != nullptr) {
+            q.want_dh = 1;
             q.first = v0 == 0;
             q.dh = p.dh;
             q.dh_pitch = p.dh_pitch;
-            q.dh_split = p.rows_pad * p.dh_pitch;
-            e = launch_mma<kLinDh>(dz_k, w_mn, q, tr * td * p.dh_splits, s);
+            q.dh_room = p.dh_room;
         }
-        if (e == cudaSuccess && p.dweight != nullptr) {
+        if (p.dweight != nullptr) {
             const size_t es = p.bf16 ? 2 : 4;
-            q.tiles_m = static_cast<int32_t>(tv);
+            q.tiles_v = static_cast<int32_t>(ceil_div(v1 - v0, 128 * gt.ctas));
             q.dweight = p.dweight;
             q.dweight_stride = p.dweight_stride;
             q.accumulate = p.accumulate;
             q.bf16 = p.bf16;
             q.vec = reinterpret_cast<uintptr_t>(p.dweight) % 16 == 0 &&
                     static_cast<size_t>(p.dweight_stride) * es % 16 == 0;
-            e = launch_mma<kLinDw>(dz_mn, h_mn, q, tv * td, s);
         }
+        const int64_t tiles = (ceil_div(p.rows, 128 * gt.ctas) * most_splits + q.tiles_v) * q.tiles_n;
+        e = launch_shape<kLinGrads>(gt, grads, q, tiles, s);
         if (e != cudaSuccess)
             return e;
     }

@@ -1,6 +1,7 @@
 // tcgen05 / tensor-map TMA helpers for the matrix kernels, beside the
-// mbarrier helpers of gbce_device.cuh.  Two CTAs of a cluster (a pair) work
-// on one tile: each holds half of A's rows, half of B's and half of D's.
+// mbarrier helpers of gbce_device.cuh.  CTAS = 1: a CTA works on its own tile.
+// CTAS = 2: the two CTAs of a cluster (a pair) work on one tile, each holding
+// half of A's rows, half of B's and half of D's.
 #pragma once
 
 #include <cuda.h>
@@ -12,11 +13,20 @@ namespace gbce {
 // ------------------------------------------------------------- tensor maps
 
 // Box of a 3-D tensor (innermost coordinate first) into this CTA's shared
-// memory; the bytes are counted on `bar`, a shared::cluster address that may
-// lie in the pair's other CTA.
-__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int32_t x,
-                                                 int32_t y, int32_t z, uint32_t bar)
+// memory; the bytes are counted on `bar`, a shared::cluster address that, in
+// a pair, may lie in the other CTA.
+template <int CTAS>
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int32_t x, int32_t y,
+                                            int32_t z, uint32_t bar)
 {
+    if constexpr (CTAS == 1) {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+        return;
+    }
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
@@ -53,20 +63,36 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
 
 // ------------------------------------------------------------------- TMEM
 
-// Both CTAs of the pair call this with one whole warp each.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t columns)
+// One whole warp of the CTA (of each of a pair's) calls these.
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns)
 {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(slot)),
-                 "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if constexpr (CTAS == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
 
-__device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t columns)
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t columns)
 {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(columns)
-                 : "memory");
+    if constexpr (CTAS == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
+                     "r"(columns)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr),
+                     "r"(columns)
+                     : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -115,25 +141,39 @@ __host__ __device__ constexpr uint32_t mma_idesc(uint32_t m, uint32_t n, bool a_
            (static_cast<uint32_t>(b_mn) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                              bool accumulate)
+template <int CTAS>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-        : "memory");
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+            : "memory");
 }
 
-// One arrival on `bar` (same offset in both CTAs of the pair) once every MMA
-// issued so far by this thread is done.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
+// One arrival on `bar` (in a pair: on the barrier at the same offset in both
+// CTAs) once every MMA issued so far by this thread is done.
+template <int CTAS>
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+            " [%0], %1;" ::"r"(smem_addr(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(smem_addr(bar))
+                     : "memory");
 }
 
 }  // namespace gbce
