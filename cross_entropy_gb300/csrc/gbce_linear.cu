@@ -14,47 +14,69 @@ __device__ __forceinline__ float nan_value() { return __int_as_float(0x7fc00000)
 
 }  // namespace
 
+// Whether row r takes part (`live`) and counts (`item`: it was not masked or
+// ignored, though its target may be out of range).
+__device__ __forceinline__ void row_kind(const LinParams &p, int64_t r, bool &live, bool &item)
+{
+    const int K = static_cast<int>(p.k);
+    const bool masked = p.row_mask != nullptr && p.row_mask[r] == 0;
+    item = !masked && !(p.token_ce && p.targets[r] == p.ignore_index);
+    live = item;
+    if (item && (p.token_ce || p.whole_rows))
+        for (int k = 0; k < K; ++k) {
+            const int64_t t = p.targets[r * K + k];
+            live = live && t >= 0 && t < p.vocab;
+        }
+}
+
+// Forward outputs and the map entry of a row that takes no part.
+__device__ __forceinline__ void leave_out(const LinParams &p, int64_t r, bool item)
+{
+    const int K = static_cast<int>(p.k);
+    const float fill = item ? nan_value() : 0.0f;
+    if (item)
+        report(p.dev_status, p.token_ce ? GBCE_DEV_BAD_LABEL : GBCE_DEV_BAD_INDEX);
+    p.row_map[r] = item ? kLinRowBad : kLinRowSkipped;
+    if (p.logp_out != nullptr)
+        for (int k = 0; k < K; ++k)
+            p.logp_out[r * K + k] = fill;
+    if (p.state_out != nullptr) {
+        p.state_out[2 * r] = item ? fill : kNegInf;
+        p.state_out[2 * r + 1] = fill;
+    }
+    if (p.loss_rows != nullptr)
+        p.loss_rows[r] = fill;
+}
+
+__device__ __forceinline__ void write_head(const LinParams &p, int32_t live, int64_t items)
+{
+    p.head->n_live = live;
+    p.head->n_items = items;
+    p.head->alpha = 1.0f;
+    p.head->done = 0;
+    if (p.n_items_out != nullptr)
+        *p.n_items_out = items;
+}
+
 // Which rows take part, as a stable partition: row_list[i] is the i-th live
-// row, row_map[r] its place or why it has none.  Rows that take no part get
-// their forward outputs here (0, or NaN for a target out of range).  One CTA:
-// it reads rows x (k + 1) words, 1024 rows per step by warp ballots and a
-// scan over the warps; every later kernel depends on its count.
+// row, row_map[r] its place or why it has none.  One CTA: it reads rows x
+// (k + 1) words, 1024 rows per step by warp ballots and a scan over the warps;
+// every later kernel depends on its count.
 __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(LinParams p)
 {
     __shared__ int32_t s_live[kPlanWarps], s_item[kPlanWarps];
+    grid_dependency_wait();
     launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int K = static_cast<int>(p.k);
     int32_t base = 0;
     int64_t items = 0;
     for (int64_t r0 = 0; r0 < p.rows; r0 += kPlanThreads) {
         const int64_t r = r0 + threadIdx.x;
         bool live = false, item = false;
         if (r < p.rows) {
-            const bool masked = p.row_mask != nullptr && p.row_mask[r] == 0;
-            item = !masked && !(p.token_ce && p.targets[r] == p.ignore_index);
-            live = item;
-            if (item && (p.token_ce || p.whole_rows)) {
-                for (int k = 0; k < K; ++k) {
-                    const int64_t t = p.targets[r * K + k];
-                    live = live && t >= 0 && t < p.vocab;
-                }
-                if (!live)
-                    report(p.dev_status, p.token_ce ? GBCE_DEV_BAD_LABEL : GBCE_DEV_BAD_INDEX);
-            }
-            if (!live) {
-                const float fill = item ? nan_value() : 0.0f;
-                p.row_map[r] = item ? kLinRowBad : kLinRowSkipped;
-                if (p.logp_out != nullptr)
-                    for (int k = 0; k < K; ++k)
-                        p.logp_out[r * K + k] = fill;
-                if (p.state_out != nullptr) {
-                    p.state_out[2 * r] = item ? fill : kNegInf;
-                    p.state_out[2 * r + 1] = fill;
-                }
-                if (p.loss_rows != nullptr)
-                    p.loss_rows[r] = fill;
-            }
+            row_kind(p, r, live, item);
+            if (!live)
+                leave_out(p, r, item);
         }
         const unsigned bl = __ballot_sync(0xffffffffu, live);
         const unsigned bi = __ballot_sync(0xffffffffu, item);
@@ -79,13 +101,8 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(LinParams p)
         items += titem;
         __syncthreads();  // before the next step overwrites the counts
     }
-    if (threadIdx.x == 0) {
-        p.head->n_live = base;
-        p.head->n_items = items;
-        p.head->alpha = 1.0f;
-        if (p.n_items_out != nullptr)
-            *p.n_items_out = items;
-    }
+    if (threadIdx.x == 0)
+        write_head(p, base, items);
 }
 
 // Four elements at a time, or one.
@@ -149,19 +166,11 @@ __device__ __forceinline__ bool quad_rows(const T *base, int64_t stride)
     return reinterpret_cast<uintptr_t>(base) % bytes == 0 && stride % 4 == 0;
 }
 
-// Packed hidden states and targets of the live rows, one CTA per packed row;
-// the rows up to the next multiple of kLinRowPad are zeros.
+// Packed row i from row r of the hidden states (zeros past the live rows),
+// and its targets.
 template <typename T, int PLANES>
-__global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
+__device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64_t r, bool in)
 {
-    grid_dependency_wait();
-    launch_dependents();
-    const int32_t live = p.head->n_live;
-    const int64_t i = blockIdx.x;
-    if (i >= (static_cast<int64_t>(live) + kLinRowPad - 1) / kLinRowPad * kLinRowPad)
-        return;
-    const bool in = i < live;
-    const int64_t r = in ? p.row_list[i] : 0;
     const T *base = static_cast<const T *>(p.hidden);
     pack_row<T, PLANES>(base + r * p.hidden_stride, static_cast<__nv_bfloat16 *>(p.hpack) + i * p.pitch,
                         p.hpack_plane, p.dim, quad_rows(base, p.hidden_stride), !in);
@@ -172,18 +181,113 @@ __global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
     }
 }
 
-// One piece of a weight that the products cannot read in place: fp32, or rows
-// that do not start on 16 bytes.
+// Row v of a weight that the products cannot read in place (fp32, or rows
+// that do not start on 16 bytes), into row i of the packed piece.
+template <typename T, int PLANES>
+__device__ __forceinline__ void pack_weight(const LinParams &p, int64_t i, int64_t v)
+{
+    const T *base = static_cast<const T *>(p.weight);
+    pack_row<T, PLANES>(base + v * p.weight_stride, static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch,
+                        p.wpack_rows * p.pitch, p.dim, quad_rows(base, p.weight_stride), false);
+}
+
+// One CTA per packed row.  A backward product over the rows reads whole
+// 64-deep blocks of them: the rows up to the next multiple of kLinRowPad are
+// zeros there.
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
+{
+    grid_dependency_wait();
+    launch_dependents();
+    const int32_t live = p.head->n_live;
+    const int64_t i = blockIdx.x;
+    if (i >= (static_cast<int64_t>(live) + kLinRowPad - 1) / kLinRowPad * kLinRowPad)
+        return;
+    pack_hidden<T, PLANES>(p, i, i < live ? p.row_list[i] : 0, i < live);
+}
+
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64_t v0)
 {
     grid_dependency_wait();
     launch_dependents();
+    pack_weight<T, PLANES>(p, blockIdx.x, v0 + blockIdx.x);
+}
+
+// Plan and packing in one launch, for calls of up to kSmallRows rows whose
+// time is launches: every CTA finds its own row by counting all of them, the
+// first writes the plan down.  CTAs from `packed` on pack the weight, where
+// it needs that and fits whole.  (64 rows fp32: three launches' 14 us are
+// one's SMALL_PACK_US.)
+constexpr int kSmallRows = 1024, kSmallTargets = 4096;
+
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_t packed)
+{
+    __shared__ uint32_t s_live[kSmallRows / 32], s_item[kSmallRows / 32];
+    __shared__ int32_t s_row, s_total;
+    grid_dependency_wait();
+    launch_dependents();
+    if (blockIdx.x >= packed) {
+        pack_weight<T, PLANES>(p, blockIdx.x - packed, blockIdx.x - packed);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool first = blockIdx.x == 0;
+#pragma unroll
+    for (int it = 0; it < kSmallRows / 128; ++it) {
+        const int r = it * 128 + static_cast<int>(threadIdx.x);
+        bool live = false, item = false;
+        if (r < p.rows) {
+            row_kind(p, r, live, item);
+            if (first && !live)
+                leave_out(p, r, item);
+        }
+        const unsigned bl = __ballot_sync(0xffffffffu, live);
+        const unsigned bi = __ballot_sync(0xffffffffu, item);
+        if (lane == 0) {
+            s_live[it * 4 + warp] = bl;
+            s_item[it * 4 + warp] = bi;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // lane l has rows [32 l, 32 l + 32); the i-th live row is in the word
+        // whose running count passes i
+        const uint32_t word = s_live[lane];
+        int32_t upto = __popc(word), items = __popc(s_item[lane]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? x : 0;
+        }
+        items = __reduce_add_sync(0xffffffffu, items);
+        const int32_t before = upto - __popc(word), i = static_cast<int32_t>(blockIdx.x);
+        if (before <= i && i < upto) {
+            uint32_t w = word;
+            for (int32_t skip = i - before; skip > 0; --skip)
+                w &= w - 1;
+            s_row = lane * 32 + __ffs(w) - 1;
+        }
+        if (lane == 31)
+            s_total = upto;
+        if (first) {
+            int32_t at = before;
+            for (uint32_t w = word; w != 0; w &= w - 1, ++at) {
+                const int32_t r = lane * 32 + __ffs(w) - 1;
+                p.row_list[at] = r;
+                p.row_map[r] = at;
+            }
+            if (lane == 31)
+                write_head(p, upto, items);
+        }
+    }
+    __syncthreads();
+    const int32_t live = s_total;
     const int64_t i = blockIdx.x;
-    const T *base = static_cast<const T *>(p.weight);
-    pack_row<T, PLANES>(base + (v0 + i) * p.weight_stride,
-                        static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch, p.wpack_rows * p.pitch,
-                        p.dim, quad_rows(base, p.weight_stride), false);
+    if (i >= (static_cast<int64_t>(live) + kLinRowPad - 1) / kLinRowPad * kLinRowPad)
+        return;
+    pack_hidden<T, PLANES>(p, i, i < live ? s_row : 0, i < live);
 }
 
 // The factor of both gradients that every row shares: a summed or averaged
@@ -213,58 +317,107 @@ __device__ __forceinline__ void ce_row_gradient(const LinParams &p, int64_t i, i
 }
 
 // One warp per live row: its tiles' partials merged in a fixed order (lane l
-// takes the tiles l, l + 32, ..., then the lanes merge), then the log-probs
-// of its targets, each over the other columns, and the whole row's state.
-__global__ void __launch_bounds__(128) lin_combine_kernel(LinParams p)
+// takes the tiles l, l + 32, ..., eight at a time, then the lanes merge), then
+// the log-probs of its targets, each over the other columns, and the whole
+// row's state.  Lane k has target k; a target gathered before counts once.
+// The last CTA to finish sums the losses of all rows, in row order per thread
+// and over the threads in a fixed tree: the order does not depend on which CTA
+// that is.
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinParams p)
 {
+    __shared__ int32_t s_last;
+    __shared__ double s_sum[kCombineWarps];
     grid_dependency_wait();
     launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (i >= p.head->n_live)
-        return;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int K = static_cast<int>(p.k);
-    float m = kNegInf, s = 0.0f, unused = 0.0f;
-    for (int64_t t = lane; t < p.tiles; t += 32) {
-        const float2 part = p.partials[i * p.tiles + t];
-        merge_max_sum(m, s, part.x, part.y, p.c);
+    if (i < p.head->n_live) {
+        const int64_t r = p.row_list[i];
+        const int32_t tg = lane < K ? p.tgt[i * K + lane] : -1;
+        const float xt = lane < K ? p.xt[i * K + lane] : 0.0f;
+        float m = kNegInf, s = 0.0f, unused = 0.0f;
+        const float2 *part = p.partials + i * p.tiles;
+        for (int64_t t0 = 0; t0 < p.tiles; t0 += 256) {
+            float2 x[8];
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t t = t0 + u * 32 + lane;
+                x[u] = t < p.tiles ? part[t] : make_float2(kNegInf, 0.0f);
+                top = fmaxf(top, x[u].x);
+            }
+            const float ref = top == kNegInf ? 0.0f : top;
+            s *= ex2((m - ref) * p.c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                s = fmaf(x[u].y, ex2((x[u].x - ref) * p.c), s);
+            m = top;
+        }
+        warp_merge_state<0>(m, s, unused, p.c, 0.0f);
+        // others of target k: (m, s) and the distinct targets that are not k
+        const unsigned same = __match_any_sync(0xffffffffu, tg);
+        const bool counts = tg >= 0 && (same & ((1u << lane) - 1u)) == 0;
+        float om = m, os = s, M = m, S = s;
+        for (int j = 0; j < K; ++j) {
+            const int32_t tj = __shfl_sync(0xffffffffu, tg, j);
+            const float xj = __shfl_sync(0xffffffffu, xt, j);
+            if (__shfl_sync(0xffffffffu, static_cast<int>(counts), j) == 0)
+                continue;
+            merge_max_sum(M, S, xj, 1.0f, p.c);
+            if (tj != tg)
+                merge_max_sum(om, os, xj, 1.0f, p.c);
+        }
+        float logp = 0.0f;
+        if (lane < K) {
+            logp = nan_value();
+            if (tg < 0)
+                report(p.dev_status, GBCE_DEV_BAD_INDEX);
+            else
+                logp = finalize_logp(om, os, xt, p.T);
+            if (p.logp_out != nullptr)
+                p.logp_out[r * K + lane] = logp;
+        }
+        if (lane == 0) {
+            if (p.loss_rows != nullptr)
+                p.loss_rows[r] = -logp;
+            if (p.state_out != nullptr) {
+                p.state_out[2 * r] = M;
+                p.state_out[2 * r + 1] = S;
+            }
+            if (p.fused)
+                ce_row_gradient(p, i, r, M, S, logp);
+        }
     }
-    warp_merge_state<0>(m, s, unused, p.c, 0.0f);
-    const int64_t r = p.row_list[i];
-    const int32_t *tg = p.tgt + i * K;
-    const float *xt = p.xt + i * K;
-    float logp = 0.0f;
-    if (lane < K) {
-        float out;
-        if (tg[lane] < 0) {
-            out = nan_value();
-            report(p.dev_status, GBCE_DEV_BAD_INDEX);
-        } else {
-            out = logp_with_targets<GBCE_MAX_K>(m, s, tg, xt, K, lane, p.c, p.T);
-        }
-        logp = out;
-        if (p.logp_out != nullptr)
-            p.logp_out[r * K + lane] = out;
-        if (lane == 0 && p.loss_rows != nullptr)
-            p.loss_rows[r] = -out;
-    }
-    if (lane == 0 && (p.state_out != nullptr || p.fused)) {
-        for (int k = 0; k < K; ++k) {
-            bool dup = tg[k] < 0;
-            for (int j = 0; j < k; ++j)
-                dup |= tg[j] == tg[k];
-            if (!dup)
-                merge_max_sum(m, s, xt[k], 1.0f, p.c);
-        }
-        if (p.state_out != nullptr) {
-            p.state_out[2 * r] = m;
-            p.state_out[2 * r + 1] = s;
-        }
-        if (p.fused) {
-            if (i == 0)
-                p.head->alpha = shared_factor(p);
-            ce_row_gradient(p, i, r, m, s, logp);
-        }
+    if (p.fused && blockIdx.x == 0 && threadIdx.x == 0)
+        p.head->alpha = shared_factor(p);
+    if (p.loss_out == nullptr)
+        return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atomicAdd(&p.head->done, 1) == static_cast<int32_t>(gridDim.x) - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    __threadfence();
+    double sum = 0.0;
+    for (int64_t r = threadIdx.x; r < p.rows; r += 32 * kCombineWarps)
+        sum += static_cast<double>(__ldcg(p.loss_rows + r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0)
+        s_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < kCombineWarps; ++w)
+            total += s_sum[w];
+        const int64_t n = p.head->n_items;
+        *p.loss_out = static_cast<float>(p.reduction == 2 ? (n > 0 ? total / static_cast<double>(n) : 0.0) : total);
     }
 }
 
@@ -379,17 +532,26 @@ unsigned blocks(int64_t n, int64_t per) { return static_cast<unsigned>((n + per 
 
 }  // namespace
 
-cudaError_t lin_plan(const LinParams &p, cudaStream_t s)
+cudaError_t lin_select(const LinParams &p, cudaStream_t s)
 {
-    lin_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-    note_launches(1);
-    return cudaGetLastError();
+    const int64_t packed = p.backward ? p.rows_pad : p.rows;
+    if (p.rows <= kSmallRows && p.rows * p.k <= kSmallTargets) {
+        const int64_t weight = p.weight_direct || p.wpack_rows < p.vocab ? 0 : p.vocab;
+        return launch_after(p.bf16 ? lin_small_pack_kernel<__nv_bfloat16, 1> : lin_small_pack_kernel<float, 3>,
+                            dim3(static_cast<unsigned>(packed + weight)), dim3(128), 0, s, p,
+                            static_cast<int32_t>(packed));
+    }
+    const cudaError_t e = launch_after(lin_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+    return e != cudaSuccess
+               ? e
+               : launch_after(p.bf16 ? lin_pack_kernel<__nv_bfloat16, 1> : lin_pack_kernel<float, 3>,
+                              dim3(static_cast<unsigned>(packed)), dim3(128), 0, s, p);
 }
 
-cudaError_t lin_pack(const LinParams &p, cudaStream_t s)
+bool lin_weight_packed(const LinParams &p)
 {
-    return launch_after(p.bf16 ? lin_pack_kernel<__nv_bfloat16, 1> : lin_pack_kernel<float, 3>,
-                        dim3(static_cast<unsigned>(p.rows_pad)), dim3(128), 0, s, p);
+    return !p.weight_direct && p.wpack_rows >= p.vocab && p.rows <= kSmallRows &&
+           p.rows * p.k <= kSmallTargets;
 }
 
 cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStream_t s)
@@ -401,7 +563,8 @@ cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStre
 
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s)
 {
-    return launch_after(lin_combine_kernel, dim3(blocks(p.rows, 4)), dim3(128), 0, s, p);
+    return launch_after(lin_combine_kernel, dim3(blocks(p.rows, kCombineWarps)), dim3(32 * kCombineWarps), 0,
+                        s, p);
 }
 
 cudaError_t lin_prepare(const LinParams &p, cudaStream_t s)

@@ -48,6 +48,7 @@ struct LinHeader {
     int32_t n_live;   // rows packed
     float alpha;      // factor of both gradients that is the same for every row
     int32_t dh_splits;  // parts that dhidden's sums came in (grads kernel)
+    int32_t done;     // CTAs of the combine that have finished
 };
 
 // row_map values of rows that are not packed.
@@ -71,9 +72,11 @@ struct LinParams {
     float *logp_out;      // [rows, k]
     float *state_out;     // [rows, 2] max and sum over the row's columns
     float *loss_rows;     // [rows]
+    float *loss_out;      // [1] their sum or mean
     int64_t *n_items_out; // [1]
 
     // backward
+    bool backward;            // the call has gradients
     bool fused;               // the statistics were taken by the same call
     const float *grad_out;    // CE: [rows] or [1]; selective: [rows, k]
     int reduction;            // CE: 0 none, 1 sum, 2 mean
@@ -110,8 +113,8 @@ struct LinParams {
     int32_t *dev_status;
 };
 
-cudaError_t lin_plan(const LinParams &p, cudaStream_t s);
-cudaError_t lin_pack(const LinParams &p, cudaStream_t s);
+cudaError_t lin_select(const LinParams &p, cudaStream_t s);
+bool lin_weight_packed(const LinParams &p);  // lin_select packed the weight too
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s);
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s);
 cudaError_t lin_prepare(const LinParams &p, cudaStream_t s);

@@ -234,6 +234,7 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
     }
     p.rows_pad = w.rows_pad;
     p.tiles = w.tiles;
+    p.backward = backward;
     p.logits_tile = w.logits_tile;
     p.grads_tile = w.grads_tile;
     p.piece = w.piece;
@@ -248,12 +249,6 @@ void set_grads(LinParams &p, const Grads &g)
     p.dhidden_stride = g.dhidden_stride;
     p.dweight_stride = g.dweight_stride;
     p.accumulate = g.accumulate;
-}
-
-cudaError_t select_rows(const LinParams &p, cudaStream_t s)
-{
-    const cudaError_t e = gbce::lin_plan(p, s);
-    return e != cudaSuccess ? e : gbce::lin_pack(p, s);
 }
 
 cudaError_t forward(const LinParams &p, cudaStream_t s)
@@ -317,6 +312,7 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
     p.reduction = static_cast<int>(reduction);
     p.n_items_out = n_items_out;
     p.loss_rows = reduction == GBCE_NONE ? loss_out : at<float>(workspace, w.loss);
+    p.loss_out = reduction == GBCE_NONE ? nullptr : loss_out;
     p.logp_out = logp_out;
     p.state_out = row_state_out;
     if (g != nullptr) {
@@ -324,13 +320,9 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
         p.grad_out = grad_out;
         set_grads(p, *g);
     }
-    cudaError_t e = select_rows(p, s);
+    cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
         e = forward(p, s);
-    if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = gbce::launch_reduce_loss(p.loss_rows, labels, a.rows, ignore_index,
-                                     static_cast<int>(reduction), &p.head->n_items, nullptr,
-                                     loss_out, s);
     if (e != cudaSuccess || g == nullptr)
         return cuda_status(e);
     return cuda_status(gbce::lin_grads(p, s));
@@ -373,7 +365,7 @@ gbce_status linear_selective_logsoftmax(const void *hidden, int64_t hidden_row_s
     p.logp_out = logp_out;
     p.state_out = row_state_out;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = select_rows(p, s);
+    cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
         e = forward(p, s);
     return cuda_status(e);
@@ -411,7 +403,7 @@ gbce_status linear_selective_logsoftmax_bwd(
     p.saved_logp = saved_logp;
     p.saved_state = row_state;
     set_grads(p, g);
-    cudaError_t e = select_rows(p, s);
+    cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
         e = backward(p, s);
     return cuda_status(e);
@@ -470,7 +462,7 @@ gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const v
     p.saved_logp = saved_logp;
     p.saved_state = row_state;
     set_grads(p, g);
-    cudaError_t e = select_rows(p, s);
+    cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
         e = backward(p, s);
     return cuda_status(e);

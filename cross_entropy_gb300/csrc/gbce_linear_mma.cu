@@ -26,6 +26,8 @@
 // fp32 inputs come as three bf16 planes, x = hi + mid + lo with 8 more bits
 // in each; six of the nine products (all above 2^-24 of x y) are summed,
 // smallest first, so that the large ones meet a sum that is still small.
+#include <atomic>
+
 #include <cuda.h>
 
 #include "gbce_kernels.cuh"
@@ -659,6 +661,22 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t inner, int64_t 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Let a kernel use this much shared memory, once per kernel and device.
+template <int MODE, int CTAS, int NT, typename K>
+cudaError_t allow_smem(K *kernel, uint32_t bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit) != 0)
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int MODE, int CTAS, int NT>
 cudaError_t launch_mma(const CUtensorMap *maps, const MmaArgs &q, int64_t tiles, cudaStream_t s)
 {
@@ -666,8 +684,7 @@ cudaError_t launch_mma(const CUtensorMap *maps, const MmaArgs &q, int64_t tiles,
     if (sms < 2)
         return cudaErrorInvalidDevice;
     const auto kernel = lin_mma_kernel<MODE, CTAS, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<CTAS, NT>());
+    cudaError_t e = allow_smem<MODE, CTAS, NT>(kernel, smem_bytes<CTAS, NT>());
     if (e != cudaSuccess)
         return e;
     const int64_t units = tiles < sms / CTAS ? tiles : sms / CTAS;
@@ -792,7 +809,7 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
     for (int64_t v0 = 0; v0 < p.vocab; v0 += step) {
         const int64_t v1 = v0 + step < p.vocab ? v0 + step : p.vocab;
         Weight w;
-        cudaError_t e = piece_weight(p, v0, v1, v0 > 0, w, s);
+        cudaError_t e = piece_weight(p, v0, v1, v0 > 0 || lin_weight_packed(p), w, s);
         CUtensorMap maps[4] = {};
         MmaArgs q = base_args(p, v0);
         q.a_rows = static_cast<int32_t>(box_rows(p, shape));
@@ -822,7 +839,7 @@ cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
     for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
         const int64_t v1 = v0 + p.piece < p.vocab ? v0 + p.piece : p.vocab;
         Weight w;
-        cudaError_t e = piece_weight(p, v0, v1, v0 > 0 || p.fused, w, s);
+        cudaError_t e = piece_weight(p, v0, v1, v0 > 0 || p.fused || lin_weight_packed(p), w, s);
         CUtensorMap logits[4] = {}, grads[4] = {};
         const auto map = [&e](CUtensorMap *m, const void *base, int64_t inner, int64_t rows,
                               int64_t stride, int64_t planes, int64_t plane, uint32_t box) {

@@ -22,8 +22,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (REDUCTIONS, _check, _check_buffer, _check_status, _dtype_code, _ptr, _stream_ptr,
-               load_library)
+from . import REDUCTIONS, _check, _check_buffer, _check_status, _dtype_code, _ptr, load_library
 
 
 class LinearCeForward(NamedTuple):
@@ -59,6 +58,12 @@ def _on(device, stream):
     if stream is None and torch.cuda.current_device() == device.index:
         return _HERE
     return _elsewhere(device, stream)
+
+
+def _stream_ptr(stream, device) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _int64(x, device) -> torch.Tensor:
@@ -191,9 +196,11 @@ def linear_selective_logsoftmax(hidden: torch.Tensor, weight: torch.Tensor, inde
     with _on(h.device, stream):
         idx, k, squeeze = _index(index, lead, rows, h.device)
         mask = _mask(row_mask, rows, h.device)
+        shape = lead if squeeze else (*lead, k)
         if out is None:
-            out = torch.empty((rows, k), dtype=torch.float32, device=h.device)
-        _check_buffer(out, "out", torch.float32, rows * k, h.device)
+            out = torch.empty(shape, dtype=torch.float32, device=h.device)
+        else:
+            _check_buffer(out, "out", torch.float32, rows * k, h.device)
         _check_status(dev_status, h.device)
         state = (torch.empty((rows, 2), dtype=torch.float32, device=h.device)
                  if with_state else None)
@@ -203,7 +210,7 @@ def linear_selective_logsoftmax(hidden: torch.Tensor, weight: torch.Tensor, inde
             h.shape[1], idx.data_ptr(), k, float(temperature), _ptr(mask), out.data_ptr(),
             _ptr(state), ws_ptr, ws_bytes, _ptr(dev_status), _stream_ptr(stream, h.device))
     _check(st, "linear_selective_logsoftmax")
-    res = out.view(lead) if squeeze else out.view(*lead, k)
+    res = out if out.shape == shape else out.view(shape)
     return (res, state) if with_state else res
 
 
