@@ -46,7 +46,7 @@ constexpr int kMmaThreads = 192;     // TMA warp, MMA warp, four epilogue warps
 enum LinMode : int { kLinStats, kLinDz, kLinGrads };
 
 template <int CTAS, int NT> struct Tile {
-    static constexpr int kM = 128 * CTAS, kN = NT;
+    static constexpr int kM = 128 * CTAS;
     static constexpr int kRowsB = NT / CTAS;  // rows of B that a CTA loads
     static constexpr uint32_t kBytesB = kRowsB * kRowBytes;
     static constexpr uint32_t kStage = kBytesA + kBytesB;
@@ -184,11 +184,18 @@ __device__ __forceinline__ int plane_b(int pairs, int q) { return pairs == 1 ? 0
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, int32_t *failed,
                                              int32_t *dev_status)
 {
-    if (mbar_wait_cluster(bar, parity))
+    if (mbar_wait(bar, parity))
         return true;
     *reinterpret_cast<volatile int32_t *>(failed) = 1;
     report(dev_status, GBCE_DEV_TIMEOUT);
     return false;
+}
+
+// The same for a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *failed,
+                                          int32_t *dev_status)
+{
+    return __all_sync(0xffffffffu, wait_or_fail(bar, parity, failed, dev_status));
 }
 
 // ------------------------------------------------------------- epilogues
@@ -297,26 +304,29 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (MODE == kLinGrads && blockIdx.x == 0 && threadIdx.x == 0)
         q.head->dh_splits = jobs.splits;
 
+    // The first two warps run whole, so that addresses and descriptors stay in
+    // uniform registers, and elect the lane that issues: with one lane in the
+    // loop a stage took some 540 cycles to issue, more than a 128-wide tile's
+    // products take.
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int64_t t = unit; ok && t < jobs.total; t += units) {
-                const Job job = jobs.at(t);
-                const int32_t m0 = job.m * S::kM + static_cast<int32_t>(rank) * 128;
-                const int32_t n0 = job.n * NT + static_cast<int32_t>(rank) * S::kRowsB;
-                // bytes of a stage: A's box may be lower than the tile
-                const uint32_t bytes = MODE == kLinGrads
-                                           ? S::kStage
-                                           : static_cast<uint32_t>(q.a_rows) * kRowBytes + S::kBytesB;
-                for (int pr = 0; ok && pr < q.pairs; ++pr) {
-                    const int za = plane_a(q.pairs, pr), zb = plane_b(q.pairs, pr);
-                    for (int32_t kb = job.k0; kb < job.k1; ++kb) {
-                        if (!wait_or_fail(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status)) {
-                            ok = false;
-                            break;
-                        }
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t t = unit; ok && t < jobs.total; t += units) {
+            const Job job = jobs.at(t);
+            const int32_t m0 = job.m * S::kM + static_cast<int32_t>(rank) * 128;
+            const int32_t n0 = job.n * NT + static_cast<int32_t>(rank) * S::kRowsB;
+            // bytes of a stage: A's box may be lower than the tile
+            const uint32_t bytes = MODE == kLinGrads
+                                       ? S::kStage
+                                       : static_cast<uint32_t>(q.a_rows) * kRowBytes + S::kBytesB;
+            for (int pr = 0; ok && pr < q.pairs; ++pr) {
+                const int za = plane_a(q.pairs, pr), zb = plane_b(q.pairs, pr);
+                for (int32_t kb = job.k0; kb < job.k1; ++kb) {
+                    ok = warp_wait(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
                         uint8_t *a = ring + stage * S::kStage, *b = a + kBytesA;
                         if (rank == 0)
                             mbar_arrive_expect_tx(&sh->full[stage], CTAS * bytes);
@@ -339,26 +349,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             tma_load_3d<CTAS>(a, &map_a, k, m0, za, bar);
                             tma_load_3d<CTAS>(b, &map_b, k, q.b_row0 + n0, zb, bar);
                         }
-                        if (++stage == kRing) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    }
+                    __syncwarp();
+                    if (++stage == kRing) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
-            // every stage used is free again: no copy is in flight and no
-            // arrival is on its way to this CTA when it ends
-            for (int i = 0; ok && i < kRing; ++i) {
-                ok = wait_or_fail(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status);
-                if (++stage == kRing) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+        }
+        // every stage used is free again: no copy is in flight and no
+        // arrival is on its way to this CTA when it ends
+        for (int i = 0; ok && i < kRing; ++i) {
+            ok = warp_wait(&sh->empty[stage], phase ^ 1u, &sh->failed, q.dev_status);
+            if (++stage == kRing) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
@@ -369,36 +379,39 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                ok = wait_or_fail(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
+                ok = warp_wait(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
                 tc_fence_after();
                 const uint32_t d = tmem + acc * NT;
                 for (int32_t kb = 0; ok && kb < n_blocks; ++kb) {
-                    ok = wait_or_fail(&sh->full[stage], phase, &sh->failed, q.dev_status);
+                    ok = warp_wait(&sh->full[stage], phase, &sh->failed, q.dev_status);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
-                    uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
-                    uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
+                    if (elect_one()) {
+                        const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
+                        uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
+                        uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
 #pragma unroll
-                    for (int kk = 0; kk < kDepth / 16; ++kk) {
-                        mma_bf16<CTAS>(d, da, db, idesc, kb > 0 || kk > 0);
-                        da += step_a >> 4;
-                        db += step_b >> 4;
+                        for (int kk = 0; kk < kDepth / 16; ++kk) {
+                            mma_bf16<CTAS>(d, da, db, idesc, kb > 0 || kk > 0);
+                            da += step_a >> 4;
+                            db += step_b >> 4;
+                        }
+                        mma_commit<CTAS>(&sh->empty[stage]);
                     }
-                    mma_commit<CTAS>(&sh->empty[stage]);
+                    __syncwarp();
                     if (++stage == kRing) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok)
+                if (ok && elect_one())
                     mma_commit<CTAS>(&sh->acc_full[acc]);
+                __syncwarp();
                 acc ^= 1;
                 acc_phase ^= acc == 0 ? 1u : 0u;
             }
         }
-        __syncwarp();
     } else {
         const int quad = warp & 3;  // the TMEM lanes that this warp may read
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -432,8 +445,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                 }
             }
-            if (!__all_sync(0xffffffffu,
-                            wait_or_fail(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status)))
+            if (!warp_wait(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status))
                 break;
             tc_fence_after();
             const uint32_t src = tmem + lanes + acc * NT;
@@ -767,15 +779,16 @@ uint32_t box_rows(const LinParams &p, LinTile shape)
 
 }  // namespace
 
-// Estimated cycles of the candidates and the best of them.  A 64-deep block
-// takes about 640 cycles as 256 x 256 by a pair or 128 x 256 by one CTA, 340
-// as 128 x 128 and 200 as 128 x 64 (whose operands' shared-memory reads set
-// the pace); a tile's start and outputs add about 2000 + 10 per column that
-// only the next tile hides.  `jobs` sums tiles x depth for the tile shape.
+// The tile shape with the least estimated time.  Measured at 8192 x 76032 x
+// 2560 (forward): 256 x 256 by pairs 2078 TFLOP/s, 128 x 256 1923, 128 x 128
+// 1349, 128 x 64 720, which is 620, 660, 450 and 420 cycles per 64-deep block;
+// the last two are bound by the operands' way from L2 (24 to 32 KB a block).
+// A tile's start and outputs add about 2000 + 10 per column that only the next
+// tile hides.
 LinTile choose_tile(LinWork a, LinWork b)
 {
     constexpr LinTile shapes[4] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
-    constexpr int64_t cycles[4] = {640, 640, 340, 200};
+    constexpr int64_t cycles[4] = {620, 660, 450, 420};
     LinTile best = shapes[0];
     int64_t least = INT64_MAX;
     for (int i = 0; i < 4; ++i) {
