@@ -516,6 +516,15 @@ __global__ void __launch_bounds__(kMoveThreads) embedding_join_kernel(T *dtable,
     const int64_t i0 = c * a.chunk;
     if (a.keys[i0] == key && i0 > 0 && a.keys[i0 - 1] == key)
         return;  // it began earlier
+    // the chunks that go on with it, 32 looked at a time
+    int64_t last = c;
+    for (bool more = true; more;) {
+        const int64_t e = last + 1 + (threadIdx.x & 31);
+        const unsigned on = __ballot_sync(0xffffffffu, e < a.chunks && a.keys[e * a.chunk] == key);
+        const int run = __ffs(~on) - 1;
+        last += run < 0 ? 32 : run;
+        more = run < 0;
+    }
     const int64_t d = (static_cast<int64_t>(blockIdx.x % a.columns) * kMoveThreads + threadIdx.x) * VEC;
     if (d >= a.dim)
         return;
@@ -524,7 +533,8 @@ __global__ void __launch_bounds__(kMoveThreads) embedding_join_kernel(T *dtable,
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
         sum[j] = p[j];
-    for (int64_t e = c + 1; e < a.chunks && a.keys[e * a.chunk] == key; ++e) {
+#pragma unroll 4
+    for (int64_t e = c + 1; e <= last; ++e) {
         const float *q = a.partial + e * 2 * a.dim + d;
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
@@ -660,19 +670,21 @@ cudaError_t lookup_bwd(const void *grad, int64_t gs, int64_t rows, int64_t vocab
     while (vocab >> (8 * a.passes) != 0)  // the keys go up to vocab itself
         ++a.passes;
     a.ctas = w.ctas;
-    // Few tokens for the table's rows: the zeros go out with the sort, which
-    // leaves the memory idle, and the rows that tokens name are written again.
-    // Many: the chunks' launch writes just the zeros that stay.  (8192 tokens,
-    // 152064 x 2560 bf16: see the figures at the end of this file's header.)
+    // Few tokens for the table's rows: the zeros of all rows go out beside the
+    // sort, which leaves the memory idle, and the rows that tokens name are
+    // written again (8192 tokens, 152064 x 2560 bf16: 143 us; a tenth of the
+    // zeros beside the sort and the rest beside the chunks, which look up who
+    // is named: 189 us).  Many: few zeros are left, and the chunks' launch
+    // writes those.
     gbce::ZeroArgs z{};
-    const bool early = !accumulate && w.ctas > 0 && 2 * rows < vocab;
-    if (early) {
+    const int64_t zero_ctas = accumulate ? 0 : (vocab + gbce::kZeroRows - 1) / gbce::kZeroRows;
+    if (zero_ctas > 0 && w.ctas > 0 && 2 * rows < vocab) {
         z.table = dtable;
         z.vocab = vocab;
         z.row_bytes = dim * static_cast<int64_t>(sizeof(T));
         z.stride_bytes = ds * static_cast<int64_t>(sizeof(T));
         z.width = VEC > 1 ? 16 : static_cast<int>(sizeof(T));
-        z.ctas = (vocab + gbce::kZeroRows - 1) / gbce::kZeroRows;
+        z.ctas = zero_ctas;
     }
     cudaError_t e = cudaSuccess;
     if (w.ctas == 1) {
@@ -708,7 +720,7 @@ cudaError_t lookup_bwd(const void *grad, int64_t gs, int64_t rows, int64_t vocab
     g.columns = static_cast<int32_t>((dim + gbce::kMoveThreads * VEC - 1) / (gbce::kMoveThreads * VEC));
     g.partial = reinterpret_cast<float *>(at(w.partial));
     const int64_t walk = static_cast<int64_t>(g.chunks) * g.columns;
-    const int64_t zeros = accumulate || early ? 0 : (vocab + gbce::kZeroRows - 1) / gbce::kZeroRows;
+    const int64_t zeros = zero_ctas - z.ctas;
     if (e == cudaSuccess && walk + zeros > 0)
         e = launch_after(gbce::embedding_grad_kernel<T, VEC>, walk + zeros, gbce::kMoveThreads, 0, s,
                          static_cast<const T *>(grad), static_cast<T *>(dtable), g);

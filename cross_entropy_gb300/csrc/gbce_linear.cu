@@ -105,65 +105,87 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan_kernel(LinParams p)
         write_head(p, base, items);
 }
 
-// Four elements at a time, or one.
+// Four elements at a time.
 template <typename T> struct Quad;
 template <> struct Quad<__nv_bfloat16> { using type = uint2; };
 template <> struct Quad<float> { using type = float4; };
 
-// Planes of a value: bf16 x is its own; fp32 x = hi + mid + lo, each the
-// rounding of what is left (24 bits in three times 8).
-template <int PLANES>
-__device__ __forceinline__ void store_planes(float x, __nv_bfloat16 *dst, int64_t plane)
+// Eight elements of a row from any element on, as fp32.  `aligned`: from 16
+// bytes.  Otherwise bf16 goes by whole 4-byte words, shifted where the row
+// starts between two (in which case the word before the first element and the
+// one after the last are read too: the caller keeps off the row's ends).
+__device__ __forceinline__ void load_eight(const __nv_bfloat16 *p, bool aligned, float (&x)[8])
 {
+    uint32_t w[4];
+    if (aligned) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint32_t between = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2u);
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) - between);
+        uint32_t u[5];
 #pragma unroll
-    for (int z = 0; z < PLANES; ++z) {
-        const __nv_bfloat16 w = __float2bfloat16_rn(x);
-        dst[z * plane] = w;
-        x -= __bfloat162float(w);
+        for (int i = 0; i < 4; ++i)
+            u[i] = __ldg(q + i);
+        u[4] = between != 0 ? __ldg(q + 4) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __funnelshift_r(u[i], u[i + 1], between * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = bf16x2_to_float2(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
     }
 }
 
-// One row of an operand into its planes; `quads` when both sides allow four
-// elements at a time.
-template <typename T, int PLANES>
-__device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64_t plane,
-                                         int64_t dim, bool quads, bool zero)
+__device__ __forceinline__ void load_eight(const float *p, bool aligned, float (&x)[8])
 {
-    int64_t done = 0;
-    if (quads) {
-        done = dim / 4 * 4;
-        for (int64_t d = 4 * static_cast<int64_t>(threadIdx.x); d < done; d += 4 * blockDim.x) {
-            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (!zero) {
-                const auto raw = *reinterpret_cast<const typename Quad<T>::type *>(src + d);
-                const T *e = reinterpret_cast<const T *>(&raw);
+    if (aligned) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = static_cast<float>(e[i]);
-            }
+        for (int i = 0; i < 8; ++i)
+            x[i] = __ldg(p + i);
+    }
+}
+
+// One row of an operand into its planes: bf16 x is its own; fp32 x = hi + mid
+// + lo, each the rounding of what is left (24 bits in three times 8).  The
+// planes' rows start on 16 bytes.
+template <typename T, int PLANES>
+__device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64_t plane, int64_t dim,
+                                         bool zero)
+{
+    const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+    for (int64_t d = 8 * static_cast<int64_t>(threadIdx.x); d < dim; d += 8 * blockDim.x) {
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        const bool whole = d + 8 <= dim;
+        if (!zero) {
+            if (whole && (aligned || (d > 0 && d + 8 < dim))) {
+                load_eight(src + d, aligned, x);
+            } else {
 #pragma unroll
-            for (int z = 0; z < PLANES; ++z) {
-                uint2 w;
-                w.x = float2_to_bf16x2(make_float2(x[0], x[1]));
-                w.y = float2_to_bf16x2(make_float2(x[2], x[3]));
-                *reinterpret_cast<uint2 *>(dst + z * plane + d) = w;
-                const float2 lo = bf16x2_to_float2(w.x), hi = bf16x2_to_float2(w.y);
-                x[0] -= lo.x;
-                x[1] -= lo.y;
-                x[2] -= hi.x;
-                x[3] -= hi.y;
+                for (int i = 0; i < 8; ++i)
+                    x[i] = d + i < dim ? static_cast<float>(src[d + i]) : 0.0f;
             }
         }
+#pragma unroll
+        for (int z = 0; z < PLANES; ++z) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = float2_to_bf16x2(make_float2(x[2 * i], x[2 * i + 1]));
+                const float2 f = bf16x2_to_float2(w[i]);
+                x[2 * i] -= f.x;
+                x[2 * i + 1] -= f.y;
+            }
+            // past the row's end the row's padding takes the rest
+            *reinterpret_cast<uint4 *>(dst + z * plane + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    for (int64_t d = done + threadIdx.x; d < dim; d += blockDim.x)
-        store_planes<PLANES>(zero ? 0.0f : static_cast<float>(src[d]), dst + d, plane);
-}
-
-template <typename T>
-__device__ __forceinline__ bool quad_rows(const T *base, int64_t stride)
-{
-    constexpr uint64_t bytes = 4 * sizeof(T);
-    return reinterpret_cast<uintptr_t>(base) % bytes == 0 && stride % 4 == 0;
 }
 
 // Packed row i from row r of the hidden states (zeros past the live rows),
@@ -173,7 +195,7 @@ __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64
 {
     const T *base = static_cast<const T *>(p.hidden);
     pack_row<T, PLANES>(base + r * p.hidden_stride, static_cast<__nv_bfloat16 *>(p.hpack) + i * p.pitch,
-                        p.hpack_plane, p.dim, quad_rows(base, p.hidden_stride), !in);
+                        p.hpack_plane, p.dim, !in);
     const int K = static_cast<int>(p.k);
     for (int k = threadIdx.x; k < K; k += blockDim.x) {
         const int64_t t = in ? p.targets[r * K + k] : -1;
@@ -188,7 +210,7 @@ __device__ __forceinline__ void pack_weight(const LinParams &p, int64_t i, int64
 {
     const T *base = static_cast<const T *>(p.weight);
     pack_row<T, PLANES>(base + v * p.weight_stride, static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch,
-                        p.wpack_rows * p.pitch, p.dim, quad_rows(base, p.weight_stride), false);
+                        p.wpack_rows * p.pitch, p.dim, false);
 }
 
 // One CTA per packed row.  A backward product over the rows reads whole
@@ -320,7 +342,8 @@ __device__ __forceinline__ void ce_row_gradient(const LinParams &p, int64_t i, i
 // takes the tiles l, l + 32, ..., eight at a time, then the lanes merge), then
 // the log-probs of its targets, each over the other columns, and the whole
 // row's state.  Lane k has target k; a target gathered before counts once.
-// The last CTA to finish sums the losses of all rows, in row order per thread
+// A direct call's rows were not selected: the warp finds out about its row
+// here, and counts it.  The last CTA to finish sums the losses of all rows, in row order per thread
 // and over the threads in a fixed tree: the order does not depend on which CTA
 // that is.
 constexpr int kCombineWarps = 4;
@@ -334,9 +357,24 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int K = static_cast<int>(p.k);
-    if (i < p.head->n_live) {
-        const int64_t r = p.row_list[i];
-        const int32_t tg = lane < K ? p.tgt[i * K + lane] : -1;
+    bool live = i < p.head->n_live;
+    int64_t r = i;
+    int32_t tg = -1;
+    if (live && p.direct) {
+        // nothing was selected or packed: this warp's row is sorted out here
+        bool item;
+        row_kind(p, r, live, item);
+        if (lane == 0 && item && p.token_ce)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&p.head->n_items), 1ull);
+        if (!live && lane == 0)
+            leave_out(p, r, item);
+        const int64_t t = lane < K ? p.targets[i * K + lane] : -1;
+        tg = t >= 0 && t < p.vocab ? static_cast<int32_t>(t) : -1;
+    } else if (live) {
+        r = p.row_list[i];
+        tg = lane < K ? p.tgt[i * K + lane] : -1;
+    }
+    if (live) {
         const float xt = lane < K ? p.xt[i * K + lane] : 0.0f;
         float m = kNegInf, s = 0.0f, unused = 0.0f;
         const float2 *part = p.partials + i * p.tiles;
@@ -393,7 +431,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
     }
     if (p.fused && blockIdx.x == 0 && threadIdx.x == 0)
         p.head->alpha = shared_factor(p);
-    if (p.loss_out == nullptr)
+    if (p.loss_out == nullptr && !(p.direct && p.n_items_out != nullptr))
         return;
     __threadfence();
     __syncthreads();
@@ -403,8 +441,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
     if (!s_last)
         return;
     __threadfence();
+    const int64_t n = *reinterpret_cast<volatile int64_t *>(&p.head->n_items);
+    if (p.direct && threadIdx.x == 0 && p.n_items_out != nullptr)
+        *p.n_items_out = n;
+    if (p.loss_out == nullptr)
+        return;
     double sum = 0.0;
-    for (int64_t r = threadIdx.x; r < p.rows; r += 32 * kCombineWarps)
+    for (r = threadIdx.x; r < p.rows; r += 32 * kCombineWarps)
         sum += static_cast<double>(__ldcg(p.loss_rows + r));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -416,7 +459,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
         double total = 0.0;
         for (int w = 0; w < kCombineWarps; ++w)
             total += s_sum[w];
-        const int64_t n = p.head->n_items;
         *p.loss_out = static_cast<float>(p.reduction == 2 ? (n > 0 ? total / static_cast<double>(n) : 0.0) : total);
     }
 }
@@ -534,6 +576,8 @@ unsigned blocks(int64_t n, int64_t per) { return static_cast<unsigned>((n + per 
 
 cudaError_t lin_select(const LinParams &p, cudaStream_t s)
 {
+    if (p.direct)
+        return cudaSuccess;
     const int64_t packed = p.backward ? p.rows_pad : p.rows;
     if (p.rows <= kSmallRows && p.rows * p.k <= kSmallTargets) {
         const int64_t weight = p.weight_direct || p.wpack_rows < p.vocab ? 0 : p.vocab;
@@ -550,7 +594,7 @@ cudaError_t lin_select(const LinParams &p, cudaStream_t s)
 
 bool lin_weight_packed(const LinParams &p)
 {
-    return !p.weight_direct && p.wpack_rows >= p.vocab && p.rows <= kSmallRows &&
+    return !p.direct && !p.weight_direct && p.wpack_rows >= p.vocab && p.rows <= kSmallRows &&
            p.rows * p.k <= kSmallTargets;
 }
 

@@ -77,6 +77,7 @@ struct LinParams {
 
     // backward
     bool backward;            // the call has gradients
+    bool direct;              // a short forward: rows stay where they are, none is packed
     bool fused;               // the statistics were taken by the same call
     const float *grad_out;    // CE: [rows] or [1]; selective: [rows, k]
     int reduction;            // CE: 0 none, 1 sum, 2 mean

@@ -37,7 +37,7 @@ struct Layout {
 };
 
 // fp32 values that split sums of dhidden may take beyond one part.
-constexpr int64_t kSplitRoom = int64_t{8} << 20;
+constexpr int64_t kSplitRoom = int64_t{32} << 20;
 
 // Where everything lies in the workspace.  With `backward`, the buffers of
 // the gradient (and of the statistics, which a fused call needs too).
@@ -235,6 +235,10 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
     p.rows_pad = w.rows_pad;
     p.tiles = w.tiles;
     p.backward = backward;
+    // a forward of one row tile: nothing to gain from leaving rows out, so
+    // hidden states that the tensor maps can read are read in place
+    p.direct = !backward && a.rows <= 128 && a.dtype == GBCE_BF16 &&
+               reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0 && a.hidden_stride % 8 == 0;
     p.logits_tile = w.logits_tile;
     p.grads_tile = w.grads_tile;
     p.piece = w.piece;

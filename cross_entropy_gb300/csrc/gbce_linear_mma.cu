@@ -69,6 +69,8 @@ struct MmaArgs {
     float c;
     int32_t k;
     const int32_t *tgt;
+    const int64_t *targets;  // stats of a direct call: [direct_rows, k]
+    int32_t direct_rows;     // else 0
     float *xt;
     float2 *partials;
     int64_t partial_tiles;
@@ -124,16 +126,32 @@ template <int MODE> struct Jobs {
         }
         tv = q.tiles_v;
         dh_tiles = q.want_dh ? static_cast<int64_t>(tm) * tn : 0;
-        // dhidden's depth, the vocabulary, is split until a tile is at most an
-        // eighth of what a CTA has to do in all, so that handing tiles out in
-        // turn comes out even (1024 x 32768 x 1024 fp32: 655 us with halves,
-        // EIGHTH_US with eighths); the same for every piece, whose sums are added
-        const int64_t all = dh_tiles * q.piece_blocks + static_cast<int64_t>(tv) * tn * live_blocks;
-        const int64_t share = max(all / units / 8, static_cast<int64_t>(4));
-        int64_t want = (q.piece_blocks + share - 1) / share;
-        if (dh_tiles > 0)
-            want = min(want, q.dh_room / (static_cast<int64_t>(tm) * tile_m * q.dh_pitch));
-        splits = static_cast<int32_t>(max(static_cast<int64_t>(1), min(want, static_cast<int64_t>(kMaxSplits))));
+        // dhidden's depth, the vocabulary, is split where that evens out what
+        // the CTAs have to do: in turns of whole tiles when dhidden is alone
+        // (80 tiles for 76 pairs are two turns, in eight parts 8.4 of 9), else
+        // until the parts are small next to a CTA's share, dweight's tiles
+        // filling the gaps.  A part costs about 24 products of 64 deep (its sums
+        // go to memory).  2048 x 77824 x 2560: 1055 TFLOP/s whole, 1523 split.  The
+        // same for every piece of a call, whose sums are added.
+        if (dh_tiles > 0) {
+            const float room = static_cast<float>(q.dh_room / (static_cast<int64_t>(tm) * tile_m * q.dh_pitch));
+            const float n = static_cast<float>(dh_tiles), u = static_cast<float>(units);
+            const float depth = static_cast<float>(q.piece_blocks);
+            const float dw = static_cast<float>(tv) * static_cast<float>(tn) * static_cast<float>(live_blocks);
+            const float extra = 24.0f / static_cast<float>(q.pairs);
+            float least = 3.0e38f;
+            for (int k = 1; k <= kMaxSplits && static_cast<float>(k) <= fmaxf(room, 1.0f); ++k) {
+                const float part = depth / static_cast<float>(k) + extra;
+                const float even = (n * static_cast<float>(k) * part + dw) / u;
+                const float cost = 0.1f * static_cast<float>(k) +
+                                   (tv == 0 ? ceilf(n * static_cast<float>(k) / u) * part
+                                            : fmaxf(even, part) + 0.5f * part);
+                if (cost < least) {
+                    least = cost;
+                    splits = k;
+                }
+            }
+        }
         dh_tiles *= splits;
         total = dh_tiles + static_cast<int64_t>(tv) * tn;
     }
@@ -176,6 +194,16 @@ template <int MODE> struct Jobs {
         return j;
     }
 };
+
+// Column of a row's k-th target, from column 0 of the tile; out of the tile's
+// range for a target out of the vocabulary's.
+__device__ __forceinline__ int64_t target_column(const MmaArgs &q, int64_t at, int64_t first)
+{
+    if (q.direct_rows == 0)
+        return q.tgt[at] - first;
+    const int64_t t = q.targets[at];
+    return t < 0 || t >= q.vocab ? -1 : t - first;
+}
 
 // Plane indices of product q of six, smallest first.
 __device__ __forceinline__ int plane_a(int pairs, int q) { return pairs == 1 ? 0 : (0x201100 >> (4 * (5 - q))) & 15; }
@@ -298,7 +326,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 
     grid_dependency_wait();
     launch_dependents();
-    const int32_t live = q.head->n_live;
+    const int32_t live = q.direct_rows > 0 ? q.direct_rows : q.head->n_live;
+    if (MODE == kLinStats && q.direct_rows > 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+        q.head->n_live = live;
+        q.head->n_items = 0;  // the combine counts
+        q.head->done = 0;
+    }
     const int64_t units = gridDim.x / CTAS, unit = blockIdx.x / CTAS;
     const Jobs<MODE> jobs(q, live, S::kM, units);
     if (MODE == kLinGrads && blockIdx.x == 0 && threadIdx.x == 0)
@@ -435,7 +468,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (MODE == kLinDz)
                     g = q.grow[row];
                 for (int k = 0; k < q.k; ++k) {
-                    const int64_t j = q.tgt[static_cast<int64_t>(row) * q.k + k] - (q.v0 + col0);
+                    const int64_t j = target_column(q, static_cast<int64_t>(row) * q.k + k, q.v0 + col0);
                     if (j >= 0 && j < NT) {
                         any_hit = true;
 #pragma unroll
@@ -479,7 +512,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     if (mine != 0) {
                         for (int k = 0; k < q.k; ++k) {
                             const int64_t at = static_cast<int64_t>(row) * q.k + k;
-                            const int64_t j = q.tgt[at] - (q.v0 + c0);
+                            const int64_t j = target_column(q, at, q.v0 + c0);
                             if (j >= 0 && j < 32) {
                                 float x = v[0];
 #pragma unroll
@@ -826,8 +859,14 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
         CUtensorMap maps[4] = {};
         MmaArgs q = base_args(p, v0);
         q.a_rows = static_cast<int32_t>(box_rows(p, shape));
-        if (e == cudaSuccess)
+        if (p.direct) {
+            q.direct_rows = static_cast<int32_t>(p.rows);
+            q.targets = p.targets;
+            if (e == cudaSuccess)
+                e = make_map(&maps[0], p.hidden, p.dim, p.rows, p.hidden_stride, 1, p.hidden_stride, q.a_rows);
+        } else if (e == cudaSuccess) {
             e = make_map(&maps[0], p.hpack, p.dim, p.rows, p.pitch, p.planes, p.hpack_plane, q.a_rows);
+        }
         if (e == cudaSuccess)
             e = make_map(&maps[1], w.base, p.dim, w.rows, w.stride, p.planes, w.plane,
                          static_cast<uint32_t>(shape.n / shape.ctas));
