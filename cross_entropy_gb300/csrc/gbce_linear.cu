@@ -152,9 +152,26 @@ __device__ __forceinline__ void load_eight(const float *p, bool aligned, float (
     }
 }
 
-// One row of an operand into its planes: bf16 x is its own; fp32 x = hi + mid
-// + lo, each the rounding of what is left (24 bits in three times 8).  The
-// planes' rows start on 16 bytes.
+// Eight values into their planes: bf16 x is its own; fp32 x = hi + mid + lo,
+// each the rounding of what is left (24 bits in three times 8).
+template <int PLANES>
+__device__ __forceinline__ void store_eight(float (&x)[8], __nv_bfloat16 *dst, int64_t plane)
+{
+#pragma unroll
+    for (int z = 0; z < PLANES; ++z) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = float2_to_bf16x2(make_float2(x[2 * i], x[2 * i + 1]));
+            const float2 f = bf16x2_to_float2(w[i]);
+            x[2 * i] -= f.x;
+            x[2 * i + 1] -= f.y;
+        }
+        *reinterpret_cast<uint4 *>(dst + z * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// One row of an operand into its planes, whose rows start on 16 bytes.
 template <typename T, int PLANES>
 __device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64_t plane, int64_t dim,
                                          bool zero)
@@ -172,19 +189,7 @@ __device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64
                     x[i] = d + i < dim ? static_cast<float>(src[d + i]) : 0.0f;
             }
         }
-#pragma unroll
-        for (int z = 0; z < PLANES; ++z) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = float2_to_bf16x2(make_float2(x[2 * i], x[2 * i + 1]));
-                const float2 f = bf16x2_to_float2(w[i]);
-                x[2 * i] -= f.x;
-                x[2 * i + 1] -= f.y;
-            }
-            // past the row's end the row's padding takes the rest
-            *reinterpret_cast<uint4 *>(dst + z * plane + d) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        store_eight<PLANES>(x, dst + d, plane);  // past the row's end: its padding
     }
 }
 
@@ -463,6 +468,46 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
     }
 }
 
+// dz from kept logits (a fused CE call): one CTA per packed row and stretch of
+// kDzSpan columns; rows up to the next 64 and columns up to the next 64 are
+// zeros, which the products read.  Bound by memory: 4 bytes of logit and 2 (6
+// for fp32 inputs) of dz a column.
+constexpr int kDzThreads = 128, kDzSpan = kDzThreads * 8 * 4;
+
+template <int PLANES> __global__ void __launch_bounds__(kDzThreads) lin_dz_kernel(LinParams p)
+{
+    grid_dependency_wait();
+    launch_dependents();
+    const int32_t live = p.head->n_live;
+    const int64_t i = blockIdx.y;
+    if (i >= (static_cast<int64_t>(live) + 63) / 64 * 64)
+        return;
+    const bool in = i < live;
+    const float2 g = in ? p.grow[i] : make_float2(0.0f, 0.0f);
+    const int64_t t = in ? p.tgt[i] : -1;
+    const float dzt = in ? p.dzt[i] : 0.0f;
+    const int64_t end = (p.vocab + 63) / 64 * 64;
+    const float *z = p.z + i * p.piece;
+    __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + i * p.piece;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kDzSpan + threadIdx.x * 8;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t c = c0 + u * kDzThreads * 8;
+        if (c >= end)
+            return;
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (in) {
+            load_eight(z + c, true, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = c + j < p.vocab ? g.y * ex2((x[j] - g.x) * p.c) : 0.0f;
+                x[j] = c + j == t ? dzt : x[j];
+            }
+        }
+        store_eight<PLANES>(x, dz + c, p.dz_plane);
+    }
+}
+
 // A backward call's rows, from the forward's log-probs and row states.  The
 // selective gradient has (M, -G / (T S)) and, for a gathered column,
 //   (-g_t expm1(log p_t) - (sum of the others' g) p_t) / T.
@@ -614,6 +659,14 @@ cudaError_t lin_combine(const LinParams &p, cudaStream_t s)
 cudaError_t lin_prepare(const LinParams &p, cudaStream_t s)
 {
     return launch_after(lin_prepare_kernel, dim3(blocks(p.rows, 128)), dim3(128), 0, s, p);
+}
+
+cudaError_t lin_dz(const LinParams &p, cudaStream_t s)
+{
+    const int64_t columns = (p.vocab + 63) / 64 * 64;
+    return launch_after(p.planes == 1 ? lin_dz_kernel<1> : lin_dz_kernel<3>,
+                        dim3(blocks(columns, kDzSpan), blocks(p.rows, 64) * 64), dim3(kDzThreads), 0,
+                        s, p);
 }
 
 cudaError_t lin_finish(const LinParams &p, cudaStream_t s)

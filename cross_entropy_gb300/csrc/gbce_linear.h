@@ -104,6 +104,7 @@ struct LinParams {
     bool weight_direct;           // the weight is read in place, else through wpack
     void *wpack;                  // [planes, wpack_rows, pitch] one piece of the weight
     int64_t wpack_rows;
+    float *z;                     // [rows_pad, piece] logits kept for the gradient, or null
     void *dz;                     // [planes, rows_pad, piece]
     int64_t dz_plane;
     float *dh;                    // [parts, rows of whole tiles, dh_pitch] sums
@@ -118,6 +119,7 @@ cudaError_t lin_select(const LinParams &p, cudaStream_t s);
 bool lin_weight_packed(const LinParams &p);  // lin_select packed the weight too
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s);
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s);
+cudaError_t lin_dz(const LinParams &p, cudaStream_t s);
 cudaError_t lin_prepare(const LinParams &p, cudaStream_t s);
 cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStream_t s);
 cudaError_t lin_grads(const LinParams &p, cudaStream_t s);

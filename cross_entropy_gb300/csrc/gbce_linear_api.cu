@@ -28,13 +28,18 @@ int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 size_t elem_size(gbce_dtype dt) { return dt == GBCE_BF16 ? 2 : 4; }
 
 struct Layout {
-    size_t head, row_list, row_map, tgt, xt, partials, loss, grow, dzt, hpack, wpack, dz,
-        dh;
+    size_t head, row_list, row_map, tgt, xt, partials, loss, grow, dzt, hpack, wpack, z,
+        dz, dh;
     size_t total;
     int64_t rows_pad, tiles, piece, pitch, wpack_rows, dh_pitch, dh_room;
     int planes;
+    bool keep;
     gbce::LinTile logits_tile, grads_tile;
 };
+
+// Bytes of fp32 logits that a fused call keeps rather than forming them twice.
+// Measured, formed twice -> kept: KEEP_FIGURES.
+constexpr int64_t kKeepBytes = int64_t{256} << 20;
 
 // fp32 values that split sums of dhidden may take beyond one part.
 constexpr int64_t kSplitRoom = int64_t{32} << 20;
@@ -84,6 +89,10 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
         if (!direct && units > wunits)
             units = wunits;
         w.piece = units * gbce::kLinPieceUnit < full ? units * gbce::kLinPieceUnit : full;
+        // a call whose logits are few keeps them from the statistics to the
+        // gradient (fused calls)
+        w.keep = w.piece >= vocab && w.rows_pad * w.piece * 4 <= kKeepBytes;
+        w.z = w.keep ? take(w.rows_pad * w.piece, 4) : 0;
         w.dz = take(w.planes * w.rows_pad * w.piece, 2);
         const int64_t piece_depth = w.piece / 64 * products, row_depth = (rows + 63) / 64 * products;
         w.grads_tile = gbce::choose_tile({rows, dim, piece_depth, true}, {w.piece, dim, row_depth, false});
@@ -226,6 +235,7 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
     if (backward) {
         p.grow = at<float2>(ws, w.grow);
         p.dzt = at<float>(ws, w.dzt);
+        p.z = w.keep ? at<float>(ws, w.z) : nullptr;
         p.dz = at<void>(ws, w.dz);
         p.dz_plane = w.rows_pad * w.piece;
         p.dh = at<float>(ws, w.dh);

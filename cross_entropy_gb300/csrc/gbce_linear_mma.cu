@@ -63,6 +63,7 @@ struct MmaArgs {
     int32_t tiles_v;       // grads: tiles of the piece's rows (0: no dweight)
     int32_t want_dh;
     int32_t piece_blocks;  // grads: blocks of a whole piece
+    int32_t units;         // grads: CTAs or pairs that the GPU holds
     int32_t a_rows;        // stats, dz: rows of A's box
     int32_t b_row0;        // the piece's first row in the weight's map
     int64_t v0, vocab;     // first column of the piece; end of the vocabulary
@@ -74,6 +75,8 @@ struct MmaArgs {
     float *xt;
     float2 *partials;
     int64_t partial_tiles;
+    float *z;              // stats: keep the logits here, rows z_pitch apart
+    int64_t z_pitch;
     const float2 *grow;
     const float *dzt;
     __nv_bfloat16 *dz;
@@ -112,7 +115,7 @@ template <int MODE> struct Jobs {
     int32_t tm, tn, tv, splits, blocks, live_blocks;
     int64_t dh_tiles, total;
 
-    __device__ Jobs(const MmaArgs &q, int32_t live, int tile_m, int64_t units)
+    __device__ Jobs(const MmaArgs &q, int32_t live, int tile_m)
     {
         tm = (live + tile_m - 1) / tile_m;
         tn = q.tiles_n;
@@ -126,26 +129,22 @@ template <int MODE> struct Jobs {
         }
         tv = q.tiles_v;
         dh_tiles = q.want_dh ? static_cast<int64_t>(tm) * tn : 0;
-        // dhidden's depth, the vocabulary, is split where that evens out what
-        // the CTAs have to do: in turns of whole tiles when dhidden is alone
-        // (80 tiles for 76 pairs are two turns, in eight parts 8.4 of 9), else
-        // until the parts are small next to a CTA's share, dweight's tiles
-        // filling the gaps.  A part costs about 24 products of 64 deep (its sums
-        // go to memory).  2048 x 77824 x 2560: 1055 TFLOP/s whole, 1523 split.  The
-        // same for every piece of a call, whose sums are added.
+        // dhidden's depth, the vocabulary, is split into parts of equal depth
+        // where its tiles would not come out even over the CTAs (80 tiles for
+        // 76 pairs are two turns, in eight parts 8.4 of 9).  A part costs about
+        // 24 products of 64 deep: its sums go to memory.  2048 x 77824 x 2560:
+        // 1055 TFLOP/s whole, 1587 split.  The same for every piece of a call,
+        // whose sums are added, and whether or not dweight is wanted.
         if (dh_tiles > 0) {
             const float room = static_cast<float>(q.dh_room / (static_cast<int64_t>(tm) * tile_m * q.dh_pitch));
-            const float n = static_cast<float>(dh_tiles), u = static_cast<float>(units);
+            const float n = static_cast<float>(dh_tiles), u = static_cast<float>(q.units);
             const float depth = static_cast<float>(q.piece_blocks);
-            const float dw = static_cast<float>(tv) * static_cast<float>(tn) * static_cast<float>(live_blocks);
             const float extra = 24.0f / static_cast<float>(q.pairs);
             float least = 3.0e38f;
             for (int k = 1; k <= kMaxSplits && static_cast<float>(k) <= fmaxf(room, 1.0f); ++k) {
                 const float part = depth / static_cast<float>(k) + extra;
-                const float even = (n * static_cast<float>(k) * part + dw) / u;
-                const float cost = 0.1f * static_cast<float>(k) +
-                                   (tv == 0 ? ceilf(n * static_cast<float>(k) / u) * part
-                                            : fmaxf(even, part) + 0.5f * part);
+                const float cost = ceilf(n * static_cast<float>(k) / u) * part +
+                                   static_cast<float>(k) / static_cast<float>(q.pairs);
                 if (cost < least) {
                     least = cost;
                     splits = k;
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         q.head->done = 0;
     }
     const int64_t units = gridDim.x / CTAS, unit = blockIdx.x / CTAS;
-    const Jobs<MODE> jobs(q, live, S::kM, units);
+    const Jobs<MODE> jobs(q, live, S::kM);
     if (MODE == kLinGrads && blockIdx.x == 0 && threadIdx.x == 0)
         q.head->dh_splits = jobs.splits;
 
@@ -499,6 +498,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
                 const int64_t c0 = col0 + ch * 32;
                 if (MODE == kLinStats) {
+                    if (q.z != nullptr && row < live) {
+                        float4 *o = reinterpret_cast<float4 *>(q.z + row * q.z_pitch + q.v0 + c0);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            o[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
                     const int64_t end = q.vocab - (q.v0 + c0);  // columns of this chunk that exist
                     if (end < 32) {
 #pragma unroll
@@ -876,6 +881,10 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
         q.tiles_n = static_cast<int32_t>(ceil_div(v1 - v0, shape.n));
         q.b_row0 = static_cast<int32_t>(w.row0);
         q.xt = p.xt;
+        if (p.fused) {
+            q.z = p.z;
+            q.z_pitch = p.piece;
+        }
         q.partials = p.partials;
         q.partial_tiles = p.tiles;
         e = launch_shape<kLinStats>(shape, maps, q, ceil_div(p.rows, 128 * shape.ctas) * q.tiles_n, s);
@@ -917,10 +926,14 @@ cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
         q.dz_plane = p.dz_plane;
         q.blocks = static_cast<int32_t>(ceil_div(p.dim, kDepth));
         q.tiles_n = static_cast<int32_t>(ceil_div(v1 - v0, lt.n));
-        e = launch_shape<kLinDz>(lt, logits, q, ceil_div(p.rows, 128 * lt.ctas) * q.tiles_n, s);
+        if (p.fused && p.z != nullptr)
+            e = lin_dz(p, s);
+        else
+            e = launch_shape<kLinDz>(lt, logits, q, ceil_div(p.rows, 128 * lt.ctas) * q.tiles_n, s);
         if (e != cudaSuccess)
             return e;
         q.blocks = static_cast<int32_t>(ceil_div(v1 - v0, kDepth));
+        q.units = device_sm_count() / gt.ctas;
         q.piece_blocks = static_cast<int32_t>(ceil_div(p.piece, kDepth));
         q.tiles_n = static_cast<int32_t>(ceil_div(p.dim, gt.n));
         const int64_t most_splits = p.dhidden != nullptr ? kMaxSplits : 0;
