@@ -672,10 +672,9 @@ cudaError_t lookup_bwd(const void *grad, int64_t gs, int64_t rows, int64_t vocab
     a.ctas = w.ctas;
     // Few tokens for the table's rows: the zeros of all rows go out beside the
     // sort, which leaves the memory idle, and the rows that tokens name are
-    // written again (8192 tokens, 152064 x 2560 bf16: 143 us; a tenth of the
-    // zeros beside the sort and the rest beside the chunks, which look up who
-    // is named: 189 us).  Many: few zeros are left, and the chunks' launch
-    // writes those.
+    // written again (8192 tokens, 152064 x 2560 bf16: 143 us; with every zero
+    // beside the chunks, where it takes a search to know who is named, 156 us).
+    // Many: few zeros are left, and the chunks' launch writes just those.
     gbce::ZeroArgs z{};
     const int64_t zero_ctas = accumulate ? 0 : (vocab + gbce::kZeroRows - 1) / gbce::kZeroRows;
     if (zero_ctas > 0 && w.ctas > 0 && 2 * rows < vocab) {
