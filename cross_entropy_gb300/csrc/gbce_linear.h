@@ -92,7 +92,7 @@ struct LinParams {
     int32_t *row_list, *row_map;  // packed -> original, original -> packed
     int32_t *tgt;                 // [rows_pad, k] packed targets (-1: out of range)
     float *xt;                    // [rows_pad, k] their logits
-    float2 *partials;             // [rows_pad, tiles] (max, sum) of each tile
+    float2 *partials;             // [rows_pad, tiles] (max, sum) of each half tile
     float2 *grow;                 // [rows_pad] (M, coef / S)
     float *dzt;                   // [rows_pad, k] dz of the gathered columns
     // Operands of the products are bf16 planes: one for bf16 inputs, three

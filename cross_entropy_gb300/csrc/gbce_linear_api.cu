@@ -62,7 +62,9 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
     const int64_t products = dt == GBCE_BF16 ? 1 : 6;
     const int64_t depth = (dim + 63) / 64 * products;
     w.logits_tile = gbce::choose_tile({rows, vocab, depth, false}, {0, 0, 0, false});
-    w.tiles = (vocab + w.logits_tile.n - 1) / w.logits_tile.n;
+    // two halves of a tile leave their own (max, sum)
+    const int64_t half = w.logits_tile.n / 2;
+    w.tiles = (vocab + half - 1) / half;
     w.head = take(1, sizeof(gbce::LinHeader));
     w.row_list = take(rows, 4);
     w.row_map = take(rows, 4);

@@ -7,7 +7,7 @@
 //          dz^T . hidden                 -> same launch dweight rows of the piece
 //
 // TMA brings 64-deep slices of both operands of a tile into a ring, one thread
-// issues the MMAs, and the sums lie in TMEM, two tiles' worth, so that four
+// issues the MMAs, and the sums lie in TMEM, two tiles' worth, so that eight
 // warps turn one tile into outputs while the next is multiplied.  Persistent:
 // every CTA (or pair of CTAs) takes tiles until there are no more.
 //
@@ -41,7 +41,14 @@ namespace {
 constexpr int kDepth = 64;           // depth of a stage: 128 bytes of bf16
 constexpr uint32_t kRowBytes = kDepth * 2;
 constexpr uint32_t kBytesA = 128 * kRowBytes;  // a CTA's rows of A in a stage
-constexpr int kMmaThreads = 192;     // TMA warp, MMA warp, four epilogue warps
+constexpr int kMmaThreads = 320;     // TMA warp, MMA warp, eight epilogue warps
+// The tensor cores cut each partial sum's last bits rather than round them, so
+// a sum of many steps comes out small by a part that grows with their number.
+// Logits are therefore summed 1024 deep at a time and these sums added in fp32
+// registers, rounded to nearest.  Log-probs of 7000 x 76032 x 2560, relative
+// error: 1.2e-6 in one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (fp32 products
+// throughout: 2e-7 to 4e-7); forward 1377, 1383 and 1495 us.
+constexpr int kSegBlocks = 16;
 
 enum LinMode : int { kLinStats, kLinDz, kLinGrads };
 
@@ -93,7 +100,7 @@ template <int RING> struct MmaShared {
     uint64_t full[RING], empty[RING], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int32_t failed;
-    float turn[4][32][33];  // a warp's 32 x 32 values, to be stored by rows
+    float turn[8][32][33];  // a warp's 32 x 32 values, to be stored by rows
 };
 
 template <int CTAS, int NT>
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 4 * CTAS);  // four warps of each CTA
+            mbar_init(&sh->acc_empty[i], 8 * CTAS);  // eight warps of each CTA
         }
         sh->failed = 0;
         fence_barrier_init();
@@ -411,41 +418,49 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                ok = warp_wait(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
-                tc_fence_after();
-                const uint32_t d = tmem + acc * NT;
-                for (int32_t kb = 0; ok && kb < n_blocks; ++kb) {
-                    ok = warp_wait(&sh->full[stage], phase, &sh->failed, q.dev_status);
-                    if (!ok)
-                        break;
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : kSegBlocks;
+                int32_t kb = 0;
+                do {  // one sum in TMEM for each segment
+                    ok = warp_wait(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
-                        uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
-                        uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
-#pragma unroll
-                        for (int kk = 0; kk < kDepth / 16; ++kk) {
-                            mma_bf16<CTAS>(d, da, db, idesc, kb > 0 || kk > 0);
-                            da += step_a >> 4;
-                            db += step_b >> 4;
+                    const uint32_t d = tmem + acc * NT;
+                    const int32_t k_end = min(n_blocks, kb + seg);
+                    for (bool begun = false; ok && kb < k_end; ++kb, begun = true) {
+                        ok = warp_wait(&sh->full[stage], phase, &sh->failed, q.dev_status);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
+                            uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
+                            uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
+    #pragma unroll
+                            for (int kk = 0; kk < kDepth / 16; ++kk) {
+                                mma_bf16<CTAS>(d, da, db, idesc, begun || kk > 0);
+                                da += step_a >> 4;
+                                db += step_b >> 4;
+                            }
+                            mma_commit<CTAS>(&sh->empty[stage]);
                         }
-                        mma_commit<CTAS>(&sh->empty[stage]);
+                        __syncwarp();
+                        if (++stage == kRing) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
+                    if (ok && elect_one())
+                        mma_commit<CTAS>(&sh->acc_full[acc]);
                     __syncwarp();
-                    if (++stage == kRing) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (ok && elect_one())
-                    mma_commit<CTAS>(&sh->acc_full[acc]);
-                __syncwarp();
-                acc ^= 1;
-                acc_phase ^= acc == 0 ? 1u : 0u;
+                    acc ^= 1;
+                    acc_phase ^= acc == 0 ? 1u : 0u;
+                } while (ok && kb < n_blocks);
             }
         }
     } else {
-        const int quad = warp & 3;  // the TMEM lanes that this warp may read
+        // A warp may read the 32 TMEM lanes that its number says; two share
+        // them, each with half of the tile's columns.
+        constexpr int kHalf = NT / 2, kChunks = kHalf / 32;
+        const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const int32_t warp_row = static_cast<int32_t>(rank) * 128 + quad * 32;
         const float alpha = MODE == kLinGrads ? q.head->alpha : 1.0f;
@@ -455,124 +470,172 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const Job job = jobs.at(t);
             const bool any = job.k1 > job.k0;
             const int32_t row0 = job.m * S::kM + warp_row, row = row0 + lane;
-            const int64_t col0 = static_cast<int64_t>(job.n) * NT;
-            // logits: this row's gathered columns, as bits of the tile
-            uint32_t hit[NT / 32];
+            const int64_t col0 = static_cast<int64_t>(job.n) * NT + half * kHalf;
+            bool ok;
+            // next sum in TMEM, and its release once this warp has read it
+            const auto wait_sum = [&] {
+                ok = warp_wait(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status);
+                tc_fence_after();
+                return tmem + lanes + acc * NT + half * kHalf;
+            };
+            const auto sum_read = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CTAS == 2)
+                        mbar_arrive_remote(map_to_rank(smem_addr(&sh->acc_empty[acc]), 0));
+                    else
+                        mbar_arrive(&sh->acc_empty[acc]);
+                }
+                acc ^= 1;
+                acc_phase ^= acc == 0 ? 1u : 0u;
+            };
+            if constexpr (MODE != kLinGrads) {
+                // this row's gathered columns, as bits of this half
+                uint32_t hit[kChunks];
 #pragma unroll
-            for (int w = 0; w < NT / 32; ++w)
-                hit[w] = 0;
-            bool any_hit = false;
-            float2 g = make_float2(0.0f, 0.0f);
-            if (MODE != kLinGrads && row < live) {
-                if (MODE == kLinDz)
-                    g = q.grow[row];
-                for (int k = 0; k < q.k; ++k) {
-                    const int64_t j = target_column(q, static_cast<int64_t>(row) * q.k + k, q.v0 + col0);
-                    if (j >= 0 && j < NT) {
-                        any_hit = true;
+                for (int w = 0; w < kChunks; ++w)
+                    hit[w] = 0;
+                bool any_hit = false;
+                float2 g = make_float2(0.0f, 0.0f);
+                if (row < live) {
+                    if (MODE == kLinDz)
+                        g = q.grow[row];
+                    for (int k = 0; k < q.k; ++k) {
+                        const int64_t j = target_column(q, static_cast<int64_t>(row) * q.k + k, q.v0 + col0);
+                        if (j >= 0 && j < kHalf) {
+                            any_hit = true;
 #pragma unroll
-                        for (int w = 0; w < NT / 32; ++w)
-                            if (MODE == kLinStats && j >> 5 == w)
-                                hit[w] |= 1u << (j & 31);
+                            for (int w = 0; w < kChunks; ++w)
+                                if (MODE == kLinStats && j >> 5 == w)
+                                    hit[w] |= 1u << (j & 31);
+                        }
                     }
                 }
-            }
-            if (!warp_wait(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status))
-                break;
-            tc_fence_after();
-            const uint32_t src = tmem + lanes + acc * NT;
-            RowStats st;
+                float sums[kChunks][32];
+                const int32_t segments = ((job.k1 - job.k0) * q.pairs + kSegBlocks - 1) / kSegBlocks;
+                for (int32_t sg = 0; sg < segments; ++sg) {
+                    const uint32_t src = wait_sum();
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16)
+                        tmem_add16(src + c, &sums[c / 32][c % 32], sg == 0);
+                    sum_read();
+                }
+                if (!ok)
+                    break;
+                RowStats st;
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    float(&v)[32] = sums[ch];
+                    const int64_t c0 = col0 + ch * 32;
+                    const int64_t end = q.vocab - (q.v0 + c0);  // columns of this chunk that exist
+                    if (MODE == kLinStats) {
+                        if (q.z != nullptr && row < live) {
+                            float4 *o = reinterpret_cast<float4 *>(q.z + row * q.z_pitch + q.v0 + c0);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                o[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        }
+                        if (end < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = j < end ? v[j] : kNegInf;
+                        }
+                        const uint32_t mine = hit[ch];
+                        if (mine != 0) {
+                            for (int k = 0; k < q.k; ++k) {
+                                const int64_t at = static_cast<int64_t>(row) * q.k + k;
+                                const int64_t j = target_column(q, at, q.v0 + c0);
+                                if (j >= 0 && j < 32) {
+                                    float x = v[0];
+#pragma unroll
+                                    for (int i = 1; i < 32; ++i)
+                                        x = j == i ? v[i] : x;
+                                    q.xt[at] = x;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = mine >> j & 1u ? kNegInf : v[j];
+                        }
+                        st.add(v, q.c);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = row < live && j < end ? g.y * ex2((v[j] - g.x) * q.c) : 0.0f;
+                        __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + c0;
+                        for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint4 w;
+                                w.x = pack_bf16(v[j], v[j + 1]);
+                                w.y = pack_bf16(v[j + 2], v[j + 3]);
+                                w.z = pack_bf16(v[j + 4], v[j + 5]);
+                                w.w = pack_bf16(v[j + 6], v[j + 7]);
+                                *reinterpret_cast<uint4 *>(out + j) = w;
+                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f = bf16x2_to_float2(ws[i]);
+                                    v[j + 2 * i] -= f.x;
+                                    v[j + 2 * i + 1] -= f.y;
+                                }
+                            }
+                        }
+                    }
+                }
+                if (MODE == kLinStats && row < live && q.v0 + col0 < q.vocab)
+                    q.partials[static_cast<int64_t>(row) * q.partial_tiles + (q.v0 + col0) / kHalf] =
+                        make_float2(st.s == st.s ? st.m : (st.m == kNegInf ? 0.0f : st.m), st.s);
+                if (MODE == kLinDz && any_hit) {
+                    // the gathered columns, over what this thread wrote above
+                    for (int k = 0; k < q.k; ++k) {
+                        const int64_t at = static_cast<int64_t>(row) * q.k + k;
+                        const int64_t j = q.tgt[at] - (q.v0 + col0);
+                        if (j >= 0 && j < kHalf) {
+                            float x = q.dzt[at];
+                            __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + col0 + j;
+                            for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
+                                const __nv_bfloat16 w = __float2bfloat16_rn(x);
+                                *out = w;
+                                x -= __bfloat162float(w);
+                            }
+                        }
+                    }
+                }
+            } else {
+                const uint32_t src = wait_sum();
+                if (!ok)
+                    break;
 #pragma unroll 1
-            for (int ch = 0; ch < NT / 32; ++ch) {
-                float v[32];
-                tmem_load32(src + ch * 32, v);
-                if (ch == NT / 32 - 1) {  // the sums are read: the tile after next may start
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CTAS == 2)
-                            mbar_arrive_remote(map_to_rank(smem_addr(&sh->acc_empty[acc]), 0));
-                        else
-                            mbar_arrive(&sh->acc_empty[acc]);
-                    }
-                }
-                const int64_t c0 = col0 + ch * 32;
-                if (MODE == kLinStats) {
-                    if (q.z != nullptr && row < live) {
-                        float4 *o = reinterpret_cast<float4 *>(q.z + row * q.z_pitch + q.v0 + c0);
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    float v[32];
+                    tmem_load32(src + ch * 32, v);
+                    if (ch == kChunks - 1)  // the tile after next may start
+                        sum_read();
+                    const int64_t c0 = col0 + ch * 32;
+                    if (!job.dw) {
+                        if (row >= live)
+                            continue;
+                        float *out = q.dh + (static_cast<int64_t>(job.split) * jobs.tm * S::kM + row) * q.dh_pitch + c0;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            o[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                    }
-                    const int64_t end = q.vocab - (q.v0 + c0);  // columns of this chunk that exist
-                    if (end < 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = j < end ? v[j] : kNegInf;
-                    }
-                    uint32_t mine = 0;
-#pragma unroll
-                    for (int w = 0; w < NT / 32; ++w)
-                        mine = ch == w ? hit[w] : mine;
-                    if (mine != 0) {
-                        for (int k = 0; k < q.k; ++k) {
-                            const int64_t at = static_cast<int64_t>(row) * q.k + k;
-                            const int64_t j = target_column(q, at, q.v0 + c0);
-                            if (j >= 0 && j < 32) {
-                                float x = v[0];
-#pragma unroll
-                                for (int i = 1; i < 32; ++i)
-                                    x = j == i ? v[i] : x;
-                                q.xt[at] = x;
+                            if (c0 + j < q.dim) {
+                                float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                                if (!any)
+                                    x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (!q.first) {
+                                    const float4 old = *reinterpret_cast<const float4 *>(out + j);
+                                    x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
+                                }
+                                *reinterpret_cast<float4 *>(out + j) = x;
                             }
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = mine >> j & 1u ? kNegInf : v[j];
+                        continue;
                     }
-                    st.add(v, q.c);
-                }
-                if (MODE == kLinDz) {
-                    const int64_t end = q.vocab - (q.v0 + c0);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = row < live && j < end ? g.y * ex2((v[j] - g.x) * q.c) : 0.0f;
-                    __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + c0;
-                    for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 w;
-                            w.x = pack_bf16(v[j], v[j + 1]);
-                            w.y = pack_bf16(v[j + 2], v[j + 3]);
-                            w.z = pack_bf16(v[j + 4], v[j + 5]);
-                            w.w = pack_bf16(v[j + 6], v[j + 7]);
-                            *reinterpret_cast<uint4 *>(out + j) = w;
-                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 f = bf16x2_to_float2(ws[i]);
-                                v[j + 2 * i] -= f.x;
-                                v[j + 2 * i + 1] -= f.y;
-                            }
-                        }
-                    }
-                }
-                if (MODE == kLinGrads && !job.dw && row < live) {
-                    float *out = q.dh + (static_cast<int64_t>(job.split) * jobs.tm * S::kM + row) * q.dh_pitch + c0;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        if (c0 + j < q.dim) {
-                            float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            if (!any)
-                                x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (!q.first) {
-                                const float4 old = *reinterpret_cast<const float4 *>(out + j);
-                                x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
-                            }
-                            *reinterpret_cast<float4 *>(out + j) = x;
-                        }
-                }
-                if (MODE == kLinGrads && job.dw && q.v0 + row0 < q.vocab && c0 < q.dim) {
+                    if (q.v0 + row0 >= q.vocab || c0 >= q.dim)
+                        continue;
                     const int64_t at = (q.v0 + row) * q.dweight_stride + c0;
                     const bool mine = q.v0 + row < q.vocab;
 #pragma unroll
@@ -583,10 +646,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         const int32_t rows = static_cast<int32_t>(min(static_cast<int64_t>(32), q.vocab - q.v0 - row0));
                         const int32_t cols = static_cast<int32_t>(min(static_cast<int64_t>(32), q.dim - c0));
                         if (q.bf16)
-                            store_rows_turned(sh->turn[quad], v, static_cast<__nv_bfloat16 *>(q.dweight) + base,
+                            store_rows_turned(sh->turn[warp - 2], v, static_cast<__nv_bfloat16 *>(q.dweight) + base,
                                               q.dweight_stride, rows, cols, q.accumulate != 0);
                         else
-                            store_rows_turned(sh->turn[quad], v, static_cast<float *>(q.dweight) + base,
+                            store_rows_turned(sh->turn[warp - 2], v, static_cast<float *>(q.dweight) + base,
                                               q.dweight_stride, rows, cols, q.accumulate != 0);
                     } else if (q.bf16 && mine) {
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.dweight) + at;
@@ -621,27 +684,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                 }
             }
-            if (MODE == kLinStats && row < live)
-                q.partials[static_cast<int64_t>(row) * q.partial_tiles + q.v0 / NT + job.n] =
-                    make_float2(st.s == st.s ? st.m : (st.m == kNegInf ? 0.0f : st.m), st.s);
-            if (MODE == kLinDz && any_hit) {
-                // the gathered columns, over what this thread wrote above
-                for (int k = 0; k < q.k; ++k) {
-                    const int64_t at = static_cast<int64_t>(row) * q.k + k;
-                    const int64_t j = q.tgt[at] - (q.v0 + col0);
-                    if (j >= 0 && j < NT) {
-                        float x = q.dzt[at];
-                        __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + col0 + j;
-                        for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
-                            const __nv_bfloat16 w = __float2bfloat16_rn(x);
-                            *out = w;
-                            x -= __bfloat162float(w);
-                        }
-                    }
-                }
-            }
-            acc ^= 1;
-            acc_phase ^= acc == 0 ? 1u : 0u;
         }
         __syncwarp();
     }

@@ -131,6 +131,28 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32])
         v[i] = __uint_as_float(r[i]);
 }
 
+// The same 16 columns wide, added to what v holds (`fresh`: instead of it).
+__device__ __forceinline__ void tmem_add16(uint32_t taddr, float *v, bool fresh)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const float2 x = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+        const float2 y = fresh ? x : fadd2(make_float2(v[i], v[i + 1]), x);
+        v[i] = y.x;
+        v[i + 1] = y.y;
+    }
+}
+
 // -------------------------------------------------------------------- MMA
 
 // Shared-memory matrix descriptor, 128-byte swizzle.  Offsets in bytes.
