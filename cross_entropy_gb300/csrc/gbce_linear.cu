@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64
 // Plan and packing in one launch, for calls of up to kSmallRows rows whose
 // time is launches: every CTA finds its own row by counting all of them, the
 // first writes the plan down.  CTAs from `packed` on pack the weight, where
-// it needs that and fits whole.  (64 rows fp32: three launches' 14 us are
-// one's SMALL_PACK_US.)
+// it needs that and fits whole.  (64 x 4096 x 256 fp32: three launches' 14
+// us became one's 6.6.)
 constexpr int kSmallRows = 1024, kSmallTargets = 4096;
 
 template <typename T, int PLANES>
@@ -479,7 +479,7 @@ template <int PLANES> __global__ void __launch_bounds__(kDzThreads) lin_dz_kerne
     grid_dependency_wait();
     launch_dependents();
     const int32_t live = p.head->n_live;
-    const int64_t i = blockIdx.y;
+    const int64_t i = blockIdx.x;
     if (i >= (static_cast<int64_t>(live) + 63) / 64 * 64)
         return;
     const bool in = i < live;
@@ -489,7 +489,7 @@ template <int PLANES> __global__ void __launch_bounds__(kDzThreads) lin_dz_kerne
     const int64_t end = (p.vocab + 63) / 64 * 64;
     const float *z = p.z + i * p.piece;
     __nv_bfloat16 *dz = static_cast<__nv_bfloat16 *>(p.dz) + i * p.piece;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kDzSpan + threadIdx.x * 8;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kDzSpan + threadIdx.x * 8;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int64_t c = c0 + u * kDzThreads * 8;
@@ -665,7 +665,7 @@ cudaError_t lin_dz(const LinParams &p, cudaStream_t s)
 {
     const int64_t columns = (p.vocab + 63) / 64 * 64;
     return launch_after(p.planes == 1 ? lin_dz_kernel<1> : lin_dz_kernel<3>,
-                        dim3(blocks(columns, kDzSpan), blocks(p.rows, 64) * 64), dim3(kDzThreads), 0,
+                        dim3(blocks(p.rows, 64) * 64, blocks(columns, kDzSpan)), dim3(kDzThreads), 0,
                         s, p);
 }
 

@@ -400,8 +400,11 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
 /*
  * The calls that start from hidden states: the logits are
  *   logits[r, v] = sum_d hidden[r, d] weight[v, d]
- * (the language-model head), and no more of them than a tile is ever kept.
- * Log-probs, losses and gradients are those of the calls above on these
+ * (the language-model head).  They are formed tile by tile and not kept: the
+ * gradients form them again, a piece of the vocabulary at a time, and hold
+ * that piece's gradient (in the inputs' type).  Only a fused call whose fp32
+ * logits take at most 256 MB keeps them in its workspace instead of forming
+ * them twice.  Log-probs, losses and gradients are those of the calls above on these
  * logits, the gradients with respect to hidden and weight:
  *   dhidden = dlogits . weight          dweight = dlogits^T . hidden.
  *

@@ -176,6 +176,60 @@ def test_strided_and_misaligned_operands_and_outputs(dtype, pads):
         assert torch.isnan(whole).all()
 
 
+@pytest.mark.parametrize("rows", [1, 5, 128, 129])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_short_forwards_in_place_and_packed_agree(rows, pad):
+    # up to 128 rows that start on 16 bytes are read where they are: the same
+    # bits as from a packed copy, with masked, ignored and bad targets sorted out
+    h, w, t, mask, up = problem(rows, 777, 96, 3, torch.bfloat16, rows)
+    if rows > 2:
+        mask[1] = 0
+        h[1] = math.nan
+    logp, state = gbce.linear_selective_logsoftmax(strided(h, pad), w, t, 0.9, mask, with_state=True)
+    base, bstate = gbce.linear_selective_logsoftmax(strided(h, 3), w, t, 0.9, mask, with_state=True)
+    assert torch.equal(logp, base) and torch.equal(state, bstate)
+    check_selective(torch.nan_to_num(h), w, t, mask, None, 0.9, logp)
+    lab = t[:, 0].clone()
+    lab[0] = 777 if rows > 4 else lab[0]
+    if rows > 2:
+        lab[2] = -100
+    for red in ("none", "sum", "mean"):
+        st = torch.zeros(2, dtype=torch.int32, device=DEV)
+        a = gbce.linear_ce_fwd(strided(h, pad), w, lab, reduction=red, dev_status=st[:1])
+        b = gbce.linear_ce_fwd(strided(h, 3), w, lab, reduction=red, dev_status=st[1:])
+        for x, y in zip(a, b):
+            assert torch.equal(torch.nan_to_num(x, 7.0), torch.nan_to_num(y, 7.0))
+        assert int(st[0]) == int(st[1]) == (gbce.DEV_BAD_LABEL if rows > 4 else 0)
+
+
+def test_more_rows_than_a_grid_axis_takes():
+    # kept logits of 70000 rows
+    h, w, t, mask, up = problem(70000, 64, 16, 1, torch.bfloat16, 31)
+    lab = torch.where(mask.bool(), t[:, 0], torch.full_like(t[:, 0], -100))
+    out = gbce.linear_ce_fwd_bwd_fused(h, w, lab, reduction="sum", want_logp=True)
+    f = gbce.linear_ce_fwd(h, w, lab, reduction="sum")
+    dh, dw = gbce.linear_ce_bwd(h, w, lab, torch.ones(1), f.logp, f.row_state, f.n_items, reduction="sum")
+    assert torch.equal(out.dhidden, dh) and torch.equal(out.dweight, dw) and torch.equal(out.logp, f.logp)
+    check_selective(h, w, lab[:, None].clamp(min=0), mask, -torch.ones((70000, 1), device=DEV), 1.0,
+                    f.logp[:, None], dh, dw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_exact_workspace_for_any_alignment_of_the_weight(dtype, shift):
+    h, w, t, mask, up = problem(260, 20011, 88, 1, dtype, 33)
+    x = strided(w, 1 if shift else 0, shift)
+    n = gbce.linear_workspace_size(260, 20011, 88, 1, dtype)
+    guard = torch.full((n + 4096,), 173, dtype=torch.uint8, device=DEV)
+    out = gbce.linear_ce_fwd_bwd_fused(h, x, t[:, 0], workspace=guard[:n])
+    again = gbce.linear_ce_fwd_bwd_fused(h, w, t[:, 0])
+    for a, b in zip(again[:3], out[:3]):
+        assert torch.equal(a, b)
+    assert (guard[n:] == 173).all()
+    with pytest.raises(gbce.GbceError):
+        gbce.linear_ce_fwd_bwd_fused(h, x, t[:, 0], workspace=guard[:n - 256])
+
+
 def test_three_dimensional_hidden_and_single_index():
     h, w, t, mask, up = problem(24, 300, 64, 1, torch.bfloat16, 9)
     flat, st = gbce.linear_selective_logsoftmax(h, w, t[:, 0], with_state=True)
