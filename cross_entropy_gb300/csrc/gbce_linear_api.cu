@@ -101,7 +101,7 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
         w.dz = take(w.planes * w.rows_pad * w.piece, 2);
         const int64_t piece_depth = w.piece / 64 * products, row_depth = (rows + 63) / 64 * products;
         w.grads_tile = gbce::choose_tile({rows, dim, piece_depth, true}, {w.piece, dim, row_depth, false});
-        w.dh_pitch = round_up(dim, 4);
+        w.dh_pitch = round_up(dim, 8);
         const int64_t one = w.rows_pad * w.dh_pitch;
         const int64_t most = one * gbce::kMaxSplits < kSplitRoom ? one * gbce::kMaxSplits : kSplitRoom;
         w.dh_room = one > most ? one : most;

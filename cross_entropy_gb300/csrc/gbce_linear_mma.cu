@@ -93,7 +93,8 @@ struct MmaArgs {
     int64_t dim, dh_pitch, dh_room;
     void *dweight;
     int64_t dweight_stride;
-    int32_t first, accumulate, bf16, vec;
+    int32_t first, accumulate, bf16;
+    int32_t vec;           // dweight's rows start on so many bytes: 32, 16 or 0 (fewer)
 };
 
 template <int RING> struct MmaShared {
@@ -269,6 +270,57 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 }  // namespace
+
+// One thread's 32 columns of a row, which starts on 16 bytes (`wide`: on 32).
+__device__ __forceinline__ void store_row(__nv_bfloat16 *out, float (&v)[32], bool accumulate, bool wide)
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 16) {
+        uint4 *o = reinterpret_cast<uint4 *>(out + j);
+        if (accumulate) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 old = o[h];
+                const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = bf16x2_to_float2(ow[i]);
+                    v[j + 8 * h + 2 * i] += f.x;
+                    v[j + 8 * h + 2 * i + 1] += f.y;
+                }
+            }
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = pack_bf16(v[j + 2 * i], v[j + 2 * i + 1]);
+        if (wide) {
+            st_v8(static_cast<void *>(o), w);
+        } else {
+            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_row(float *out, float (&v)[32], bool accumulate, bool wide)
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        float4 *o = reinterpret_cast<float4 *>(out + j);
+        if (accumulate) {
+            const float4 a = o[0], b = o[1];
+            v[j] += a.x, v[j + 1] += a.y, v[j + 2] += a.z, v[j + 3] += a.w;
+            v[j + 4] += b.x, v[j + 5] += b.y, v[j + 6] += b.z, v[j + 7] += b.w;
+        }
+        if (wide) {
+            st_v8(out + j, v + j);
+        } else {
+            o[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            o[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+        }
+    }
+}
 
 // Stores of one 32 x 32 block whose rows do not start on 16 bytes: through
 // shared memory, so that a warp writes one row's 32 columns at a time.
@@ -533,10 +585,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     const int64_t end = q.vocab - (q.v0 + c0);  // columns of this chunk that exist
                     if (MODE == kLinStats) {
                         if (q.z != nullptr && row < live) {
-                            float4 *o = reinterpret_cast<float4 *>(q.z + row * q.z_pitch + q.v0 + c0);
+                            float *o = q.z + row * q.z_pitch + q.v0 + c0;
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                o[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                            for (int j = 0; j < 32; j += 8)
+                                st_v8(o + j, v + j);
                         }
                         if (end < 32) {
 #pragma unroll
@@ -568,20 +620,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + c0;
                         for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint4 w;
-                                w.x = pack_bf16(v[j], v[j + 1]);
-                                w.y = pack_bf16(v[j + 2], v[j + 3]);
-                                w.z = pack_bf16(v[j + 4], v[j + 5]);
-                                w.w = pack_bf16(v[j + 6], v[j + 7]);
-                                *reinterpret_cast<uint4 *>(out + j) = w;
-                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                            for (int j = 0; j < 32; j += 16) {
+                                uint32_t w[8];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 f = bf16x2_to_float2(ws[i]);
+                                for (int i = 0; i < 8; ++i) {
+                                    w[i] = pack_bf16(v[j + 2 * i], v[j + 2 * i + 1]);
+                                    const float2 f = bf16x2_to_float2(w[i]);
                                     v[j + 2 * i] -= f.x;
                                     v[j + 2 * i + 1] -= f.y;
                                 }
+                                st_v8(out + j, w);
                             }
                         }
                     }
@@ -621,16 +669,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             continue;
                         float *out = q.dh + (static_cast<int64_t>(job.split) * jobs.tm * S::kM + row) * q.dh_pitch + c0;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
+                        for (int j = 0; j < 32; j += 8)
                             if (c0 + j < q.dim) {
-                                float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                                if (!any)
-                                    x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                float x[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    x[i] = any ? v[j + i] : 0.0f;
                                 if (!q.first) {
-                                    const float4 old = *reinterpret_cast<const float4 *>(out + j);
-                                    x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
+#pragma unroll
+                                    for (int i = 0; i < 8; i += 4) {
+                                        const float4 old = *reinterpret_cast<const float4 *>(out + j + i);
+                                        x[i] += old.x;
+                                        x[i + 1] += old.y;
+                                        x[i + 2] += old.z;
+                                        x[i + 3] += old.w;
+                                    }
                                 }
-                                *reinterpret_cast<float4 *>(out + j) = x;
+                                st_v8(out + j, x);
                             }
                         continue;
                     }
@@ -651,36 +706,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         else
                             store_rows_turned(sh->turn[warp - 2], v, static_cast<float *>(q.dweight) + base,
                                               q.dweight_stride, rows, cols, q.accumulate != 0);
-                    } else if (q.bf16 && mine) {
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.dweight) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 *o = reinterpret_cast<uint4 *>(out + j);
-                            if (q.accumulate) {
-                                const uint4 old = *o;
-                                const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 f = bf16x2_to_float2(ow[i]);
-                                    v[j + 2 * i] += f.x;
-                                    v[j + 2 * i + 1] += f.y;
-                                }
-                            }
-                            *o = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                                            pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-                        }
                     } else if (mine) {
-                        float *out = static_cast<float *>(q.dweight) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            float4 *o = reinterpret_cast<float4 *>(out + j);
-                            float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            if (q.accumulate) {
-                                const float4 old = *o;
-                                x = make_float4(old.x + x.x, old.y + x.y, old.z + x.z, old.w + x.w);
-                            }
-                            *o = x;
-                        }
+                        if (q.bf16)
+                            store_row(static_cast<__nv_bfloat16 *>(q.dweight) + at, v, q.accumulate != 0, q.vec == 32);
+                        else
+                            store_row(static_cast<float *>(q.dweight) + at, v, q.accumulate != 0, q.vec == 32);
                     }
                 }
             }
@@ -993,8 +1023,9 @@ cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
             q.dweight_stride = p.dweight_stride;
             q.accumulate = p.accumulate;
             q.bf16 = p.bf16;
-            q.vec = reinterpret_cast<uintptr_t>(p.dweight) % 16 == 0 &&
-                    static_cast<size_t>(p.dweight_stride) * es % 16 == 0;
+            const uintptr_t rows = reinterpret_cast<uintptr_t>(p.dweight) |
+                                   static_cast<uintptr_t>(p.dweight_stride) * es;
+            q.vec = rows % 32 == 0 ? 32 : (rows % 16 == 0 ? 16 : 0);
         }
         const int64_t tiles = (ceil_div(p.rows, 128 * gt.ctas) * most_splits + q.tiles_v) * q.tiles_n;
         e = launch_shape<kLinGrads>(gt, grads, q, tiles, s);

@@ -50,6 +50,24 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// 32-byte store: a whole sector per thread.  Rows of a tile lie far apart, one
+// thread each, so a warp's store costs a cycle per row whatever its width.
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_v8(float *p, const float *v)
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = __float_as_uint(v[i]);
+    st_v8(static_cast<void *>(p), w);
+}
+
 // ------------------------------------------------------------ cluster sync
 
 __device__ __forceinline__ uint32_t cluster_rank()

@@ -214,6 +214,19 @@ def test_more_rows_than_a_grid_axis_takes():
                     f.logp[:, None], dh, dw)
 
 
+@pytest.mark.parametrize("rows,V,D,K,dtype", [
+    (4000, 60001, 64, 2, torch.bfloat16),    # two pieces, the last one ragged
+    (3900, 40001, 40, 1, torch.float32),     # three pieces
+    (8, 40001, 4600, 1, torch.float32),      # a weight packed in parts
+    (100, 40001, 4601, 3, torch.bfloat16),   # the same, rows that do not start on 16 bytes
+])
+def test_vocabularies_of_several_pieces(rows, V, D, K, dtype):
+    h, w, t, mask, up = problem(rows, V, D, K, dtype, V + D)
+    logp, state = gbce.linear_selective_logsoftmax(h, w, t, 0.9, mask, with_state=True)
+    dh, dw = gbce.linear_selective_logsoftmax_bwd(h, w, t, up, logp, state, 0.9, mask)
+    check_selective(h, w, t, mask, up, 0.9, logp, dh, dw)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_exact_workspace_for_any_alignment_of_the_weight(dtype, shift):
