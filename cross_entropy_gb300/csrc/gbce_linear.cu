@@ -252,7 +252,7 @@ template <typename T, int PLANES>
 __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_t packed)
 {
     __shared__ uint32_t s_live[kSmallRows / 32], s_item[kSmallRows / 32];
-    __shared__ int32_t s_row, s_total;
+    __shared__ int32_t s_before[kSmallRows / 32], s_row, s_total;
     grid_dependency_wait();
     launch_dependents();
     if (blockIdx.x >= packed) {
@@ -298,18 +298,23 @@ __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_
         }
         if (lane == 31)
             s_total = upto;
-        if (first) {
-            int32_t at = before;
-            for (uint32_t w = word; w != 0; w &= w - 1, ++at) {
-                const int32_t r = lane * 32 + __ffs(w) - 1;
+        s_before[lane] = before;
+        if (first && lane == 31)
+            write_head(p, upto, items);
+    }
+    __syncthreads();
+    if (first) {
+#pragma unroll
+        for (int it = 0; it < kSmallRows / 128; ++it) {
+            const uint32_t w = s_live[it * 4 + warp];
+            const int32_t r = it * 128 + static_cast<int32_t>(threadIdx.x);
+            const int32_t at = s_before[it * 4 + warp] + __popc(w & ((1u << lane) - 1u));
+            if (w >> lane & 1u) {
                 p.row_list[at] = r;
                 p.row_map[r] = at;
             }
-            if (lane == 31)
-                write_head(p, upto, items);
         }
     }
-    __syncthreads();
     const int32_t live = s_total;
     const int64_t i = blockIdx.x;
     if (i >= (static_cast<int64_t>(live) + kLinRowPad - 1) / kLinRowPad * kLinRowPad)
