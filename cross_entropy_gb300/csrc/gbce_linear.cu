@@ -48,11 +48,69 @@ __device__ __forceinline__ void leave_out(const LinParams &p, int64_t r, bool it
         p.loss_rows[r] = fill;
 }
 
+// The factor of both gradients that every row shares: a summed or averaged
+// loss's upstream gradient over T (and the number of items).  It stays out of
+// dz and joins at the end, in fp32, so that it is not rounded with each dz.
+__device__ __forceinline__ float shared_factor(const LinParams &p)
+{
+    if (!p.token_ce || p.reduction == 0)
+        return 1.0f;
+    double a = static_cast<double>(p.grad_out[0]) / static_cast<double>(p.T);
+    if (p.reduction == 2) {
+        const int64_t n = p.n_items != nullptr ? *p.n_items : p.head->n_items;
+        a = n > 0 ? a / static_cast<double>(n) : 0.0;
+    }
+    return static_cast<float>(a);
+}
+
+// What the CE gradient of packed row i takes besides its logits: (M, u / S)
+// for the p_j and the label's u expm1(log p), which keeps 1 - p when p rounds
+// to 1; u = upstream / T where rows have their own.
+__device__ __forceinline__ void ce_row_gradient(const LinParams &p, int64_t i, int64_t r, float M,
+                                                float S, float logp)
+{
+    const float u = p.reduction == 0 ? p.grad_out[r] * (1.0f / p.T) : 1.0f;
+    p.grow[i] = make_float2(M, u / S);
+    p.dzt[i] = u * expm1f(logp);
+}
+
+// A backward call's row, from the forward's log-probs and row state; thread k
+// of the CTA has target k.  The selective gradient has (M, -G / (T S)) and, for
+// a gathered column,
+//   (-g_t expm1(log p_t) - (sum of the others' g) p_t) / T.
+__device__ __forceinline__ void saved_row_gradient(const LinParams &p, int64_t i, int64_t r)
+{
+    const int K = static_cast<int>(p.k), k = static_cast<int>(threadIdx.x);
+    if (k >= K)
+        return;
+    const float M = p.saved_state[2 * r], S = p.saved_state[2 * r + 1];
+    const float logp = p.saved_logp[r * K + k];
+    if (p.token_ce) {
+        ce_row_gradient(p, i, r, M, S, logp);
+        return;
+    }
+    const float inv_t = 1.0f / p.T;
+    const float *g = p.grad_out + r * K;
+    const int64_t *t = p.targets + r * K;
+    const int64_t own = t[k];
+    float sum = 0.0f, mine = 0.0f, other = 0.0f;
+    for (int j = 0; j < K; ++j) {
+        sum += g[j];
+        if (t[j] == own)
+            mine += g[j];
+        else
+            other += g[j];
+    }
+    if (k == 0)
+        p.grow[i] = make_float2(M, -(sum * inv_t) / S);
+    p.dzt[i * K + k] = (-mine * expm1f(logp) - other * expf(logp)) * inv_t;
+}
+
 __device__ __forceinline__ void write_head(const LinParams &p, int32_t live, int64_t items)
 {
     p.head->n_live = live;
     p.head->n_items = items;
-    p.head->alpha = 1.0f;
+    p.head->alpha = p.backward && !p.fused ? shared_factor(p) : 1.0f;
     p.head->done = 0;
     if (p.n_items_out != nullptr)
         *p.n_items_out = items;
@@ -193,8 +251,8 @@ __device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64
     }
 }
 
-// Packed row i from row r of the hidden states (zeros past the live rows),
-// and its targets.
+// Packed row i from row r of the hidden states (zeros past the live rows), its
+// targets, and in a backward call what its gradient takes.
 template <typename T, int PLANES>
 __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64_t r, bool in)
 {
@@ -206,6 +264,8 @@ __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64
         const int64_t t = in ? p.targets[r * K + k] : -1;
         p.tgt[i * K + k] = t >= 0 && t < p.vocab ? static_cast<int32_t>(t) : -1;
     }
+    if (in && p.backward && !p.fused)
+        saved_row_gradient(p, i, r);
 }
 
 // Row v of a weight that the products cannot read in place (fp32, or rows
@@ -320,32 +380,6 @@ __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_
     if (i >= (static_cast<int64_t>(live) + kLinRowPad - 1) / kLinRowPad * kLinRowPad)
         return;
     pack_hidden<T, PLANES>(p, i, i < live ? s_row : 0, i < live);
-}
-
-// The factor of both gradients that every row shares: a summed or averaged
-// loss's upstream gradient over T (and the number of items).  It stays out of
-// dz and joins at the end, in fp32, so that it is not rounded with each dz.
-__device__ __forceinline__ float shared_factor(const LinParams &p)
-{
-    if (!p.token_ce || p.reduction == 0)
-        return 1.0f;
-    double a = static_cast<double>(p.grad_out[0]) / static_cast<double>(p.T);
-    if (p.reduction == 2) {
-        const int64_t n = p.n_items != nullptr ? *p.n_items : p.head->n_items;
-        a = n > 0 ? a / static_cast<double>(n) : 0.0;
-    }
-    return static_cast<float>(a);
-}
-
-// What the CE gradient of packed row i takes besides its logits: (M, u / S)
-// for the p_j and the label's u expm1(log p), which keeps 1 - p when p rounds
-// to 1; u = upstream / T where rows have their own.
-__device__ __forceinline__ void ce_row_gradient(const LinParams &p, int64_t i, int64_t r, float M,
-                                                float S, float logp)
-{
-    const float u = p.reduction == 0 ? p.grad_out[r] * (1.0f / p.T) : 1.0f;
-    p.grow[i] = make_float2(M, u / S);
-    p.dzt[i] = u * expm1f(logp);
 }
 
 // One warp per live row: its tiles' partials merged in a fixed order (lane l
@@ -513,45 +547,6 @@ template <int PLANES> __global__ void __launch_bounds__(kDzThreads) lin_dz_kerne
     }
 }
 
-// A backward call's rows, from the forward's log-probs and row states.  The
-// selective gradient has (M, -G / (T S)) and, for a gathered column,
-//   (-g_t expm1(log p_t) - (sum of the others' g) p_t) / T.
-__global__ void __launch_bounds__(128) lin_prepare_kernel(LinParams p)
-{
-    grid_dependency_wait();
-    launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i == 0)
-        p.head->alpha = shared_factor(p);
-    if (i >= p.head->n_live)
-        return;
-    const int K = static_cast<int>(p.k);
-    const int64_t r = p.row_list[i];
-    const float M = p.saved_state[2 * r], S = p.saved_state[2 * r + 1];
-    const float *lp = p.saved_logp + r * K;
-    if (p.token_ce) {
-        ce_row_gradient(p, i, r, M, S, lp[0]);
-        return;
-    }
-    const float inv_t = 1.0f / p.T;
-    const float *g = p.grad_out + r * K;
-    const int32_t *tg = p.tgt + i * K;
-    float sum = 0.0f;
-    for (int k = 0; k < K; ++k)
-        sum += g[k];
-    p.grow[i] = make_float2(M, -(sum * inv_t) / S);
-    for (int k = 0; k < K; ++k) {
-        float mine = 0.0f, other = 0.0f;
-        for (int j = 0; j < K; ++j) {
-            if (tg[j] == tg[k])
-                mine += g[j];
-            else
-                other += g[j];
-        }
-        p.dzt[i * K + k] = (-mine * expm1f(lp[k]) - other * expf(lp[k])) * inv_t;
-    }
-}
-
 // dhidden by original row: alpha times the sum of its parts, zeros for rows
 // left out, NaN for rows with a target out of range.  Four values a thread.
 template <typename T>
@@ -659,11 +654,6 @@ cudaError_t lin_combine(const LinParams &p, cudaStream_t s)
 {
     return launch_after(lin_combine_kernel, dim3(blocks(p.rows, kCombineWarps)), dim3(32 * kCombineWarps), 0,
                         s, p);
-}
-
-cudaError_t lin_prepare(const LinParams &p, cudaStream_t s)
-{
-    return launch_after(lin_prepare_kernel, dim3(blocks(p.rows, 128)), dim3(128), 0, s, p);
 }
 
 cudaError_t lin_dz(const LinParams &p, cudaStream_t s)

@@ -41,8 +41,7 @@ struct LinWork {
 };
 LinTile choose_tile(LinWork a, LinWork b);
 
-// First words of the workspace, written by the plan kernel (n_live, n_items)
-// and the prepare kernel (alpha).
+// First words of the workspace, written by the row selection and the combine.
 struct LinHeader {
     int64_t n_items;  // rows that count towards the mean
     int32_t n_live;   // rows packed
@@ -120,7 +119,6 @@ bool lin_weight_packed(const LinParams &p);  // lin_select packed the weight too
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s);
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s);
 cudaError_t lin_dz(const LinParams &p, cudaStream_t s);
-cudaError_t lin_prepare(const LinParams &p, cudaStream_t s);
 cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStream_t s);
 cudaError_t lin_grads(const LinParams &p, cudaStream_t s);
 cudaError_t lin_finish(const LinParams &p, cudaStream_t s);

@@ -276,12 +276,6 @@ cudaError_t forward(const LinParams &p, cudaStream_t s)
     return e != cudaSuccess ? e : gbce::lin_combine(p, s);
 }
 
-cudaError_t backward(const LinParams &p, cudaStream_t s)
-{
-    const cudaError_t e = gbce::lin_prepare(p, s);
-    return e != cudaSuccess ? e : gbce::lin_grads(p, s);
-}
-
 bool valid_reduction(gbce_reduction r) { return r == GBCE_NONE || r == GBCE_SUM || r == GBCE_MEAN; }
 
 gbce_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GBCE_OK : GBCE_ECUDA; }
@@ -424,7 +418,7 @@ gbce_status linear_selective_logsoftmax_bwd(
     set_grads(p, g);
     cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
-        e = backward(p, s);
+        e = gbce::lin_grads(p, s);
     return cuda_status(e);
 }
 
@@ -483,7 +477,7 @@ gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const v
     set_grads(p, g);
     cudaError_t e = gbce::lin_select(p, s);
     if (e == cudaSuccess)
-        e = backward(p, s);
+        e = gbce::lin_grads(p, s);
     return cuda_status(e);
 }
 
