@@ -44,13 +44,17 @@ constexpr uint32_t kBytesA = 128 * kRowBytes;  // a CTA's rows of A in a stage
 constexpr int kMmaThreads = 320;     // TMA warp, MMA warp, eight epilogue warps
 // The tensor cores cut each partial sum's last bits rather than round them, so
 // a sum of many steps comes out small by a part that grows with their number.
-// Logits are therefore summed 1024 deep at a time and these sums added in fp32
-// registers, rounded to nearest.  Log-probs of 7000 x 76032 x 2560, relative
+// Logits, and the gradients of fp32 inputs, are therefore summed 1024 deep at a
+// time and these sums added in fp32 registers, rounded to nearest (the sums of
+// bf16 gradients are rounded to 8 bits in the end).  Log-probs of 7000 x 76032 x 2560, relative
 // error: 1.2e-6 in one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (fp32 products
 // throughout: 2e-7 to 4e-7); forward 1377, 1383 and 1495 us.
 constexpr int kSegBlocks = 16;
 
-enum LinMode : int { kLinStats, kLinDz, kLinGrads };
+// kLinGradsSplit: grads of operands in planes (fp32), summed in segments.
+enum LinMode : int { kLinStats, kLinDz, kLinGrads, kLinGradsSplit };
+
+__host__ __device__ constexpr bool is_grads(int mode) { return mode >= kLinGrads; }
 
 template <int CTAS, int NT> struct Tile {
     static constexpr int kM = 128 * CTAS;
@@ -131,7 +135,7 @@ template <int MODE> struct Jobs {
         splits = 1;
         tv = 0;
         live_blocks = (live + kDepth - 1) / kDepth;
-        if (MODE != kLinGrads) {
+        if (!is_grads(MODE)) {
             dh_tiles = total = static_cast<int64_t>(tm) * tn;
             return;
         }
@@ -175,7 +179,7 @@ template <int MODE> struct Jobs {
         j.dw = false;
         j.k0 = 0;
         j.k1 = blocks;
-        if (MODE != kLinGrads) {
+        if (!is_grads(MODE)) {
             j.m = static_cast<int32_t>(t % tm);
             j.n = static_cast<int32_t>(t / tm);
             return j;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     const int64_t units = gridDim.x / CTAS, unit = blockIdx.x / CTAS;
     const Jobs<MODE> jobs(q, live, S::kM);
-    if (MODE == kLinGrads && blockIdx.x == 0 && threadIdx.x == 0)
+    if (is_grads(MODE) && blockIdx.x == 0 && threadIdx.x == 0)
         q.head->dh_splits = jobs.splits;
 
     // The first two warps run whole, so that addresses and descriptors stay in
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int32_t m0 = job.m * S::kM + static_cast<int32_t>(rank) * 128;
             const int32_t n0 = job.n * NT + static_cast<int32_t>(rank) * S::kRowsB;
             // bytes of a stage: A's box may be lower than the tile
-            const uint32_t bytes = MODE == kLinGrads
+            const uint32_t bytes = is_grads(MODE)
                                        ? S::kStage
                                        : static_cast<uint32_t>(q.a_rows) * kRowBytes + S::kBytesB;
             for (int pr = 0; ok && pr < q.pairs; ++pr) {
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         const uint32_t own = smem_addr(&sh->full[stage]);
                         const uint32_t bar = CTAS == 2 ? map_to_rank(own, 0) : own;
                         const int32_t k = kb * kDepth;
-                        if (MODE == kLinGrads) {
+                        if (is_grads(MODE)) {
                             if (job.dw) {
                                 tma_load_3d<CTAS>(a, &map_a2, m0, k, za, bar);
                                 tma_load_3d<CTAS>(a + kBytesA / 2, &map_a2, m0 + 64, k, za, bar);
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             bool ok = true;
             for (int64_t t = unit; ok && t < jobs.total; t += units) {
                 const Job job = jobs.at(t);
-                const bool a_mn = MODE == kLinGrads && job.dw, b_mn = MODE == kLinGrads;
+                const bool a_mn = is_grads(MODE) && job.dw, b_mn = is_grads(MODE);
                 const uint32_t idesc = mma_idesc(S::kM, NT, a_mn, b_mn);
                 // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const int32_t warp_row = static_cast<int32_t>(rank) * 128 + quad * 32;
-        const float alpha = MODE == kLinGrads ? q.head->alpha : 1.0f;
+        const float alpha = is_grads(MODE) ? q.head->alpha : 1.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int64_t t = unit; t < jobs.total; t += units) {
@@ -542,7 +546,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 acc ^= 1;
                 acc_phase ^= acc == 0 ? 1u : 0u;
             };
-            if constexpr (MODE != kLinGrads) {
+            // the tile's sums, segment by segment
+            float sums[kChunks][32];
+            const auto add_segments = [&] {
+                const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : kSegBlocks;
+                for (int32_t kb = 0; kb == 0 || kb < n_blocks; kb += seg) {
+                    const uint32_t src = wait_sum();
+                    if (!ok)
+                        return false;
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16)
+                        tmem_add16(src + c, &sums[c / 32][c % 32], kb == 0);
+                    sum_read();
+                }
+                return true;
+            };
+            if constexpr (!is_grads(MODE)) {
                 // this row's gathered columns, as bits of this half
                 uint32_t hit[kChunks];
 #pragma unroll
@@ -564,18 +584,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         }
                     }
                 }
-                float sums[kChunks][32];
-                const int32_t segments = ((job.k1 - job.k0) * q.pairs + kSegBlocks - 1) / kSegBlocks;
-                for (int32_t sg = 0; sg < segments; ++sg) {
-                    const uint32_t src = wait_sum();
-                    if (!ok)
-                        break;
-#pragma unroll
-                    for (int c = 0; c < kHalf; c += 16)
-                        tmem_add16(src + c, &sums[c / 32][c % 32], sg == 0);
-                    sum_read();
-                }
-                if (!ok)
+                if (!add_segments())
                     break;
                 RowStats st;
 #pragma unroll
@@ -654,19 +663,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     }
                 }
             } else {
-                const uint32_t src = wait_sum();
-                if (!ok)
-                    break;
-#pragma unroll 1
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    float v[32];
-                    tmem_load32(src + ch * 32, v);
-                    if (ch == kChunks - 1)  // the tile after next may start
-                        sum_read();
+                // 32 of this row's columns into dhidden's sums or dweight
+                const auto put = [&](int ch, float(&v)[32]) {
                     const int64_t c0 = col0 + ch * 32;
                     if (!job.dw) {
                         if (row >= live)
-                            continue;
+                            return;
                         float *out = q.dh + (static_cast<int64_t>(job.split) * jobs.tm * S::kM + row) * q.dh_pitch + c0;
 #pragma unroll
                         for (int j = 0; j < 32; j += 8)
@@ -687,10 +689,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                 }
                                 st_v8(out + j, x);
                             }
-                        continue;
+                        return;
                     }
                     if (q.v0 + row0 >= q.vocab || c0 >= q.dim)
-                        continue;
+                        return;
                     const int64_t at = (q.v0 + row) * q.dweight_stride + c0;
                     const bool mine = q.v0 + row < q.vocab;
 #pragma unroll
@@ -712,6 +714,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         else
                             store_row(static_cast<float *>(q.dweight) + at, v, q.accumulate != 0, q.vec == 32);
                     }
+                };
+                if constexpr (MODE == kLinGrads) {
+                    const uint32_t src = wait_sum();
+                    if (!ok)
+                        break;
+#pragma unroll 1
+                    for (int ch = 0; ch < kChunks; ++ch) {
+                        float v[32];
+                        tmem_add16(src + ch * 32, v, true);
+                        tmem_add16(src + ch * 32 + 16, v + 16, true);
+                        if (ch == kChunks - 1)  // the tile after next may start
+                            sum_read();
+                        put(ch, v);
+                    }
+                } else {
+                    if (!add_segments())
+                        break;
+#pragma unroll
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        put(ch, sums[ch]);
                 }
             }
         }
@@ -1028,7 +1050,8 @@ cudaError_t lin_grads(const LinParams &p, cudaStream_t s)
             q.vec = rows % 32 == 0 ? 32 : (rows % 16 == 0 ? 16 : 0);
         }
         const int64_t tiles = (ceil_div(p.rows, 128 * gt.ctas) * most_splits + q.tiles_v) * q.tiles_n;
-        e = launch_shape<kLinGrads>(gt, grads, q, tiles, s);
+        e = p.planes == 1 ? launch_shape<kLinGrads>(gt, grads, q, tiles, s)
+                          : launch_shape<kLinGradsSplit>(gt, grads, q, tiles, s);
         if (e != cudaSuccess)
             return e;
     }

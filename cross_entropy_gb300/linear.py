@@ -137,7 +137,8 @@ def _gradient(buf, like: torch.Tensor, name: str, want: bool):
             raise ValueError(f"{name} was given although it is not wanted")
         return None, None
     if buf is None:
-        buf = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        buf = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return buf, buf if buf.dim() == 2 else buf.view(-1, buf.shape[-1])
     d = _matrix(buf, name)
     if d.device != like.device or d.dtype != like.dtype or buf.shape != like.shape:
         raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on "
@@ -156,9 +157,10 @@ def linear_workspace_size(rows: int, vocab: int, dim: int, k: int = 1, dtype=tor
 def _workspace(ws, need: int, device):
     if ws is None:
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        return ws, ws.data_ptr(), need
+    if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return ws, int(ws.data_ptr()), int(ws.numel() * ws.element_size())
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _linear_workspace(ws, lib, h, w, k, backward):
