@@ -42,19 +42,22 @@ constexpr int kDepth = 64;           // depth of a stage: 128 bytes of bf16
 constexpr uint32_t kRowBytes = kDepth * 2;
 constexpr uint32_t kBytesA = 128 * kRowBytes;  // a CTA's rows of A in a stage
 constexpr int kMmaThreads = 320;     // TMA warp, MMA warp, eight epilogue warps
-// The tensor cores cut each partial sum's last bits rather than round them, so
-// a sum of many steps comes out small by a part that grows with their number.
-// Logits, and the gradients of fp32 inputs, are therefore summed 1024 deep at a
-// time and these sums added in fp32 registers, rounded to nearest (the sums of
-// bf16 gradients are rounded to 8 bits in the end).  Log-probs of 7000 x 76032 x 2560, relative
-// error: 1.2e-6 in one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (fp32 products
-// throughout: 2e-7 to 4e-7); forward 1377, 1383 and 1495 us.
-constexpr int kSegBlocks = 16;
 
 // kLinGradsSplit: grads of operands in planes (fp32), summed in segments.
 enum LinMode : int { kLinStats, kLinDz, kLinGrads, kLinGradsSplit };
 
 __host__ __device__ constexpr bool is_grads(int mode) { return mode >= kLinGrads; }
+
+// Blocks of depth in one sum of the tensor cores.  They cut each partial sum's
+// last bits rather than round them, so a sum of many steps comes out small by
+// a part that grows with their number.  Logits are therefore summed 1024 deep
+// at a time, the gradients of fp32 inputs 512 deep, and these sums added in
+// fp32 registers, rounded to nearest; those of bf16 gradients, which end in 8
+// bits, are one sum.  Log-probs of 7000 x 76032 x 2560, relative error: 1.2e-6
+// in one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (in fp32 products 2e-7 to
+// 4e-7); forward 1377, 1383 and 1495 us.  dhidden of 2000 x 60000 x 512 fp32:
+// 1.1e-6 1024 deep, 6.4e-7 512 deep (fp32 products 5.1e-6); 5% of the time.
+__host__ __device__ constexpr int segment_blocks(int mode) { return mode == kLinGradsSplit ? 8 : 16; }
 
 template <int CTAS, int NT> struct Tile {
     static constexpr int kM = 128 * CTAS;
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : kSegBlocks;
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : segment_blocks(MODE);
                 int32_t kb = 0;
                 do {  // one sum in TMEM for each segment
                     ok = warp_wait(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             float sums[kChunks][32];
             const auto add_segments = [&] {
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : kSegBlocks;
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : segment_blocks(MODE);
                 for (int32_t kb = 0; kb == 0 || kb < n_blocks; kb += seg) {
                     const uint32_t src = wait_sum();
                     if (!ok)
