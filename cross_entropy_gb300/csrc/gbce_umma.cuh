@@ -83,11 +83,13 @@ __device__ __forceinline__ void cluster_sync()
                  ::: "memory");
 }
 
-// Arrive on an mbarrier at a shared::cluster address.
+// Arrive on an mbarrier at a shared::cluster address.  What it tells the other
+// CTA is that TMEM has been read (ordered by the tcgen05 fence before it), no
+// memory that this CTA wrote: at cluster scope the release would wait for the
+// thread's global stores, which are a tile's outputs.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------- TMEM
