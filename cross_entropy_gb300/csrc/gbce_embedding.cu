@@ -12,8 +12,10 @@
 // walks the sorted list in chunks: a chunk sums each run of one token and
 // writes the table rows whose run it holds whole; runs that cross chunks
 // leave partial sums, which a last kernel joins in chunk order.  So a very
-// common token is spread over many CTAs.  The same launch that walks the
-// chunks writes the zeros of the rows nobody names.
+// common token is spread over many CTAs.  The zeros of rows that nobody names
+// go out beside the sort or beside the chunks (see lookup_bwd).  8192 tokens,
+// 152064 x 2560 bf16: 141 us where the bytes alone take 120; the sort (12 us
+// of one CTA) hides behind the zeros, the named rows (20 us) come after them.
 #include <cmath>
 #include <cstdint>
 
@@ -50,8 +52,8 @@ __device__ __forceinline__ uint32_t token_key(const int64_t *tokens, int64_t r, 
     return static_cast<uint32_t>(t);
 }
 
-// Digit counts of this CTA's keys, each warp over its own
-// run of them; rank[it] is the key's place among its warp's of that digit.
+// Digit counts of this CTA's keys, each warp over its own run of them;
+// rank[it] is the key's place among its warp's of that digit.
 __device__ __forceinline__ void sort_count(SortShared &sh, const uint32_t (&key)[kSortSteps],
                                            const bool (&in)[kSortSteps], uint32_t (&rank)[kSortSteps],
                                            int shift)

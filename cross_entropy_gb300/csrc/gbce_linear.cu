@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_
 // the log-probs of its targets, each over the other columns, and the whole
 // row's state.  Lane k has target k; a target gathered before counts once.
 // A direct call's rows were not selected: the warp finds out about its row
-// here, and counts it.  The last CTA to finish sums the losses of all rows, in row order per thread
-// and over the threads in a fixed tree: the order does not depend on which CTA
-// that is.
+// here, and counts it.  The last CTA to finish sums the losses of all rows, in
+// row order per thread and over the threads in a fixed tree: the order does
+// not depend on which CTA that is.
 constexpr int kCombineWarps = 4;
 
 __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinParams p)

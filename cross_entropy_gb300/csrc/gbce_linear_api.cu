@@ -199,7 +199,8 @@ gbce_status check_grads(const Shape &a, const Grads &g)
 
 gbce_status check_workspace(const void *ws, size_t bytes, const Layout &w)
 {
-    if (ws == nullptr || bytes < w.total || reinterpret_cast<uintptr_t>(ws) % 16 != 0)
+    // tiles are stored 32 bytes at a time
+    if (ws == nullptr || bytes < w.total || reinterpret_cast<uintptr_t>(ws) % 32 != 0)
         return GBCE_EWORKSPACE;
     return GBCE_OK;
 }

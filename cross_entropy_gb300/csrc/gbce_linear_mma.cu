@@ -241,8 +241,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_
 }
 
 // ------------------------------------------------------------- epilogues
-// One thread has one row of the tile; `col` is its first column in the tile.
 
+// Running (max, sum) over the columns that one thread has of its row.
 struct RowStats {
     float m = kNegInf, s = 0.0f;
 
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             const uint32_t a = smem_addr(ring + stage * S::kStage), b = a + kBytesA;
                             uint64_t da = mma_desc(a, 64 * kRowBytes, 8 * kRowBytes);
                             uint64_t db = mma_desc(b, 64 * kRowBytes, 8 * kRowBytes);
-    #pragma unroll
+#pragma unroll
                             for (int kk = 0; kk < kDepth / 16; ++kk) {
                                 mma_bf16<CTAS>(d, da, db, idesc, begun || kk > 0);
                                 da += step_a >> 4;

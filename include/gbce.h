@@ -424,9 +424,10 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
  *    and weight_row_stride elements apart (>= dim), any alignment of the
  *    element type; likewise dhidden and dweight.  Rows of 16-byte multiples
  *    are read in place, others are laid out anew in the workspace.
- *  - Rows left out (row_mask[r] == 0, or label == ignore_index) are neither
- *    read nor multiplied, whatever they hold: log p 0, loss 0, row state
- *    (-inf, 0), dhidden 0, no part in dweight.
+ *  - Rows left out (row_mask[r] == 0, or label == ignore_index) have no part
+ *    in anything, whatever they hold (NaN included): log p 0, loss 0, row
+ *    state (-inf, 0), dhidden 0, nothing in dweight.  Calls with gradients and
+ *    longer forwards do no work for them.
  *  - A label outside [0, vocab), or in the backward an index outside it,
  *    sets its dev_status bit, makes the row's log p, loss and dhidden NaN
  *    and leaves the row out of dweight.  In the selective forward an index
@@ -439,7 +440,7 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
  *    fp32, rounded once), else dweight = the gradient, rows of the table
  *    that get none being zeros.  dhidden or dweight may be NULL: it is not
  *    computed.
- *  - workspace: gbce_linear_workspace_size bytes, 16-byte aligned, of one
+ *  - workspace: gbce_linear_workspace_size bytes, 32-byte aligned, of one
  *    call at a time (a captured graph keeps its own).
  *  - Sums are in a fixed order: the same call gives the same bits.
  * Errors: GBCE_EINVAL for rows outside [0, 2^24], dim outside [1, 2^20],

@@ -51,7 +51,7 @@ SHAPE = [
     (dict(w=None), 1), (dict(hs=63), 1), (dict(ws=63), 1), (dict(rows=-1), 1),
     (dict(rows=(1 << 24) + 1), 1), (dict(vocab=0), 1), (dict(vocab=1 << 31), 1), (dict(dim=0), 1),
     (dict(dim=(1 << 20) + 1), 1), (dict(T=0.0), 1), (dict(T=float("nan")), 1),
-    (dict(wk=None), 4), (dict(wk=far(4) + 8), 4), (dict(wb=64), 4),
+    (dict(wk=None), 4), (dict(wk=far(4) + 8), 4), (dict(wk=far(4) + 16), 4), (dict(wb=64), 4),
 ]
 
 
