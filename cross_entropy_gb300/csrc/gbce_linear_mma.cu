@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                 for (int w = 0; w < kChunks; ++w)
                     hit[w] = 0;
-                bool any_hit = false;
+                uint32_t hits = 0;  // bit k: target k is among them
                 float2 g = make_float2(0.0f, 0.0f);
                 if (row < live) {
                     if (MODE == kLinDz)
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     for (int k = 0; k < q.k; ++k) {
                         const int64_t j = target_column(q, static_cast<int64_t>(row) * q.k + k, q.v0 + col0);
                         if (j >= 0 && j < kHalf) {
-                            any_hit = true;
+                            hits |= 1u << k;
 #pragma unroll
                             for (int w = 0; w < kChunks; ++w)
                                 if (MODE == kLinStats && j >> 5 == w)
@@ -609,8 +609,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         }
                         const uint32_t mine = hit[ch];
                         if (mine != 0) {
-                            for (int k = 0; k < q.k; ++k) {
-                                const int64_t at = static_cast<int64_t>(row) * q.k + k;
+                            for (uint32_t left = hits; left != 0; left &= left - 1) {
+                                const int64_t at = static_cast<int64_t>(row) * q.k + __ffs(left) - 1;
                                 const int64_t j = target_column(q, at, q.v0 + c0);
                                 if (j >= 0 && j < 32) {
                                     float x = v[0];
@@ -649,19 +649,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if (MODE == kLinStats && row < live && q.v0 + col0 < q.vocab)
                     q.partials[static_cast<int64_t>(row) * q.partial_tiles + (q.v0 + col0) / kHalf] =
                         make_float2(st.s == st.s ? st.m : (st.m == kNegInf ? 0.0f : st.m), st.s);
-                if (MODE == kLinDz && any_hit) {
+                if (MODE == kLinDz) {
                     // the gathered columns, over what this thread wrote above
-                    for (int k = 0; k < q.k; ++k) {
-                        const int64_t at = static_cast<int64_t>(row) * q.k + k;
-                        const int64_t j = q.tgt[at] - (q.v0 + col0);
-                        if (j >= 0 && j < kHalf) {
-                            float x = q.dzt[at];
-                            __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + col0 + j;
-                            for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
-                                const __nv_bfloat16 w = __float2bfloat16_rn(x);
-                                *out = w;
-                                x -= __bfloat162float(w);
-                            }
+                    for (; hits != 0; hits &= hits - 1) {
+                        const int64_t at = static_cast<int64_t>(row) * q.k + __ffs(hits) - 1;
+                        float x = q.dzt[at];
+                        __nv_bfloat16 *out = q.dz + static_cast<int64_t>(row) * q.piece + (q.tgt[at] - q.v0);
+                        for (int z = 0; z < q.planes; ++z, out += q.dz_plane) {
+                            const __nv_bfloat16 w = __float2bfloat16_rn(x);
+                            *out = w;
+                            x -= __bfloat162float(w);
                         }
                     }
                 }
