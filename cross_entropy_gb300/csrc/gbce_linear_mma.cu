@@ -913,20 +913,22 @@ uint32_t box_rows(const LinParams &p, LinTile shape)
 
 // The tile shape with the least estimated time.  Measured at 8192 x 76032 x
 // 2560 (forward): 256 x 256 by pairs 2078 TFLOP/s, 128 x 256 1923, 128 x 128
-// 1349, 128 x 64 720, which is 620, 660, 450 and 420 cycles per 64-deep block;
+// 1349, 128 x 64 720, which is 620, 670, 450 and 420 cycles per 64-deep block;
 // the last two are bound by the operands' way from L2 (24 to 32 KB a block).
-// A tile's start and outputs add about 2000 + 10 per column that only the next
-// tile hides.
+// A launch's first and last tile add about 2000 + 10 per column that no other
+// tile hides, a launch of pairs 4 us (8000) more.  Forward times, pairs and
+// 128 x 256: 1843 x 151936 x 2560 804 and 850 us, 2048 x 32768 x 1024 112 and
+// 117, 1500 x 8192 x 1024 47 and 42, 384 x 152064 x 4096 361 and 341.
 LinTile choose_tile(LinWork a, LinWork b)
 {
     constexpr LinTile shapes[4] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};
-    constexpr int64_t cycles[4] = {620, 660, 450, 420};
+    constexpr int64_t cycles[4] = {620, 680, 450, 420};
     LinTile best = shapes[0];
     int64_t least = INT64_MAX;
     for (int i = 0; i < 4; ++i) {
         const LinTile t = shapes[i];
         const int64_t units = kLinSms / t.ctas, m = 128 * t.ctas;
-        int64_t cost = 2000 + 10 * t.n, longest = 0, sum = 0;
+        int64_t cost = 2000 + 10 * t.n + (t.ctas == 2 ? 8000 : 0), longest = 0, sum = 0;
         for (const LinWork &w : {a, b}) {
             const int64_t tiles = ceil_div(w.m, m) * ceil_div(w.n, t.n);
             const int64_t depth = w.split ? ceil_div(w.depth, ceil_div(units, tiles > 0 ? tiles : 1)) : w.depth;
