@@ -443,6 +443,8 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
  *  - workspace: gbce_linear_workspace_size bytes, 32-byte aligned, of one
  *    call at a time (a captured graph keeps its own).
  *  - Sums are in a fixed order: the same call gives the same bits.
+ *  - A pipeline wait that gives up sets GBCE_DEV_TIMEOUT; the call's outputs
+ *    are then invalid.
  * Errors: GBCE_EINVAL for rows outside [0, 2^24], dim outside [1, 2^20],
  * vocab < 1, strides below dim, k, temperature and NULL pointers as above,
  * outputs that overlap an input or each other, no gradient wanted at all;
