@@ -137,24 +137,35 @@ struct ZeroArgs {
     int64_t ctas;                            // 0: nothing to write
 };
 
+// `bytes` of zeros from `at` by the CTA's threads, `width` bytes a store.
+__device__ __forceinline__ void zero_bytes(char *at, int64_t bytes, int width)
+{
+    for (int64_t b = static_cast<int64_t>(threadIdx.x) * width; b < bytes;
+         b += static_cast<int64_t>(blockDim.x) * width) {
+        if (width == 16)
+            *reinterpret_cast<uint4 *>(at + b) = make_uint4(0, 0, 0, 0);
+        else if (width == 4)
+            *reinterpret_cast<uint32_t *>(at + b) = 0;
+        else
+            *reinterpret_cast<uint16_t *>(at + b) = 0;
+    }
+}
+
 __device__ __forceinline__ void zero_rows(const ZeroArgs &z, int64_t cta)
 {
     const int64_t v0 = cta * kZeroRows, v1 = min(z.vocab, v0 + kZeroRows);
-    // rows without gaps are one run of bytes
-    const bool flat = z.row_bytes == z.stride_bytes;
-    const int64_t bytes = flat ? (v1 - v0) * z.row_bytes : z.row_bytes;
-    for (int64_t v = v0; v < (flat ? v0 + 1 : v1); ++v) {
-        char *row = static_cast<char *>(z.table) + v * z.stride_bytes;
-        for (int64_t b = static_cast<int64_t>(threadIdx.x) * z.width; b < bytes;
-             b += static_cast<int64_t>(blockDim.x) * z.width) {
-            if (z.width == 16)
-                *reinterpret_cast<uint4 *>(row + b) = make_uint4(0, 0, 0, 0);
-            else if (z.width == 4)
-                *reinterpret_cast<uint32_t *>(row + b) = 0;
-            else
-                *reinterpret_cast<uint16_t *>(row + b) = 0;
-        }
+    char *first = static_cast<char *>(z.table) + v0 * z.stride_bytes;
+    if (z.row_bytes == z.stride_bytes) {
+        // rows without gaps are one run of bytes, which starts on 16 where the
+        // table does (16 rows of 2-byte elements are 32 bytes or a multiple)
+        const int64_t bytes = (v1 - v0) * z.row_bytes;
+        const int64_t wide = reinterpret_cast<uintptr_t>(z.table) % 16 == 0 ? bytes / 16 * 16 : 0;
+        zero_bytes(first, wide, 16);
+        zero_bytes(first + wide, bytes - wide, z.width);
+        return;
     }
+    for (int64_t v = v0; v < v1; ++v, first += z.stride_bytes)
+        zero_bytes(first, z.row_bytes, z.width);
 }
 
 // Few tokens (one chunk): every pass in one CTA, the list in shared memory,

@@ -140,6 +140,31 @@ def test_bad_tokens_empty_calls_and_shapes():
     assert not z[0].any() and torch.equal(z[1], table[4])
 
 
+def test_offsets_past_32_bits():
+    V, D = 540000, 4096
+    table = torch.zeros((V, D), dtype=torch.bfloat16, device=DEV)
+    t = torch.tensor([0, V - 1, V // 2, V - 1, -100], device=DEV)
+    table[V - 1] = 3.0
+    out = gbce.embedding_lookup(table, t, 0.5)
+    assert (out[[1, 3]] == 1.5).all() and not out[[0, 2, 4]].any()
+    d = gbce.embedding_lookup_bwd(torch.ones((5, D), dtype=torch.bfloat16, device=DEV), t, V, 2.0,
+                                  dtable=table.fill_(7.0))
+    assert (d[V - 1] == 4.0).all() and (d[0] == 2.0).all() and (d[V // 2] == 2.0).all()
+    assert float(d.sum(dtype=torch.float64)) == 8.0 * D
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,D", [(1000, 31), (1003, 7), (999, 130), (17, 1), (5, 3)])
+def test_zeros_reach_every_element_of_odd_tables(dtype, V, D):
+    for shift in (0, 1):
+        buf = torch.full((V * D + shift + 1,), 7.0, dtype=dtype, device=DEV)
+        d = buf[shift:shift + V * D].view(V, D)
+        gbce.embedding_lookup_bwd(torch.ones((1, D), dtype=dtype, device=DEV),
+                                  torch.tensor([V // 2], device=DEV), V, dtable=d)
+        assert float(d.double().sum()) == D and (d[V // 2] == 1).all()
+        assert float(buf[-1]) == 7.0 and (shift == 0 or float(buf[0]) == 7.0)
+
+
 def test_streams_and_a_captured_graph():
     g = torch.Generator(device=DEV).manual_seed(8)
     t = tokens_of("common", 5000, 2000, g)
