@@ -229,26 +229,24 @@ __device__ __forceinline__ void store_eight(float (&x)[8], __nv_bfloat16 *dst, i
     }
 }
 
-// One row of an operand into its planes, whose rows start on 16 bytes.
+// Elements [d, d + 8) of a row into its planes, whose rows start on 16 bytes;
+// past the row's end its padding takes the rest.
 template <typename T, int PLANES>
-__device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64_t plane, int64_t dim,
-                                         bool zero)
+__device__ __forceinline__ void pack_eight(const T *src, __nv_bfloat16 *dst, int64_t plane, int64_t d,
+                                           int64_t dim, bool zero)
 {
-    const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0;
-    for (int64_t d = 8 * static_cast<int64_t>(threadIdx.x); d < dim; d += 8 * blockDim.x) {
-        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        const bool whole = d + 8 <= dim;
-        if (!zero) {
-            if (whole && (aligned || (d > 0 && d + 8 < dim))) {
-                load_eight(src + d, aligned, x);
-            } else {
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (!zero) {
+        const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+        if (d + 8 <= dim && (aligned || (d > 0 && d + 8 < dim))) {
+            load_eight(src + d, aligned, x);
+        } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = d + i < dim ? static_cast<float>(src[d + i]) : 0.0f;
-            }
+            for (int i = 0; i < 8; ++i)
+                x[i] = d + i < dim ? static_cast<float>(src[d + i]) : 0.0f;
         }
-        store_eight<PLANES>(x, dst + d, plane);  // past the row's end: its padding
     }
+    store_eight<PLANES>(x, dst + d, plane);
 }
 
 // Packed row i from row r of the hidden states (zeros past the live rows), its
@@ -256,9 +254,10 @@ __device__ __forceinline__ void pack_row(const T *src, __nv_bfloat16 *dst, int64
 template <typename T, int PLANES>
 __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64_t r, bool in)
 {
-    const T *base = static_cast<const T *>(p.hidden);
-    pack_row<T, PLANES>(base + r * p.hidden_stride, static_cast<__nv_bfloat16 *>(p.hpack) + i * p.pitch,
-                        p.hpack_plane, p.dim, !in);
+    const T *src = static_cast<const T *>(p.hidden) + r * p.hidden_stride;
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.hpack) + i * p.pitch;
+    for (int64_t d = 8 * static_cast<int64_t>(threadIdx.x); d < p.dim; d += 8 * blockDim.x)
+        pack_eight<T, PLANES>(src, dst, p.hpack_plane, d, p.dim, !in);
     const int K = static_cast<int>(p.k);
     for (int k = threadIdx.x; k < K; k += blockDim.x) {
         const int64_t t = in ? p.targets[r * K + k] : -1;
@@ -268,14 +267,27 @@ __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64
         saved_row_gradient(p, i, r);
 }
 
-// Row v of a weight that the products cannot read in place (fp32, or rows
-// that do not start on 16 bytes), into row i of the packed piece.
-template <typename T, int PLANES>
-__device__ __forceinline__ void pack_weight(const LinParams &p, int64_t i, int64_t v)
+// Rows of a weight that the products cannot read in place (fp32, or rows that
+// do not start on 16 bytes): rows [v0, v0 + rows) into the packed piece from
+// its start, weight_rows_per_cta of them by CTA `cta`, enough to keep its
+// threads busy when rows are short.
+__host__ __device__ __forceinline__ int64_t weight_rows_per_cta(int64_t dim)
 {
-    const T *base = static_cast<const T *>(p.weight);
-    pack_row<T, PLANES>(base + v * p.weight_stride, static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch,
-                        p.wpack_rows * p.pitch, p.dim, false);
+    return dim >= 2048 ? 1 : (dim <= 64 ? 32 : 2048 / dim);
+}
+
+template <typename T, int PLANES>
+__device__ __forceinline__ void pack_weight(const LinParams &p, int64_t cta, int64_t v0, int64_t rows)
+{
+    const int64_t per = weight_rows_per_cta(p.dim), i0 = cta * per;
+    const uint32_t parts = static_cast<uint32_t>((p.dim + 7) / 8);
+    const uint32_t all = static_cast<uint32_t>(min(per, rows - i0)) * parts;
+    for (uint32_t e = threadIdx.x; e < all; e += blockDim.x) {
+        const int64_t i = i0 + e / parts;
+        pack_eight<T, PLANES>(static_cast<const T *>(p.weight) + (v0 + i) * p.weight_stride,
+                              static_cast<__nv_bfloat16 *>(p.wpack) + i * p.pitch, p.wpack_rows * p.pitch,
+                              8 * static_cast<int64_t>(e % parts), p.dim, false);
+    }
 }
 
 // One CTA per packed row.  A backward product over the rows reads whole
@@ -294,11 +306,11 @@ __global__ void __launch_bounds__(128) lin_pack_kernel(LinParams p)
 }
 
 template <typename T, int PLANES>
-__global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64_t v0)
+__global__ void __launch_bounds__(128) lin_pack_weight_kernel(LinParams p, int64_t v0, int64_t rows)
 {
     grid_dependency_wait();
     launch_dependents();
-    pack_weight<T, PLANES>(p, blockIdx.x, v0 + blockIdx.x);
+    pack_weight<T, PLANES>(p, blockIdx.x, v0, rows);
 }
 
 // Plan and packing in one launch, for calls of up to kSmallRows rows whose
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_
     grid_dependency_wait();
     launch_dependents();
     if (blockIdx.x >= packed) {
-        pack_weight<T, PLANES>(p, blockIdx.x - packed, blockIdx.x - packed);
+        pack_weight<T, PLANES>(p, static_cast<int64_t>(blockIdx.x) - packed, 0, p.vocab);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -625,7 +637,9 @@ cudaError_t lin_select(const LinParams &p, cudaStream_t s)
         return cudaSuccess;
     const int64_t packed = p.backward ? p.rows_pad : p.rows;
     if (p.rows <= kSmallRows && p.rows * p.k <= kSmallTargets) {
-        const int64_t weight = p.weight_direct || p.wpack_rows < p.vocab ? 0 : p.vocab;
+        const int64_t weight = p.weight_direct || p.wpack_rows < p.vocab
+                                   ? 0
+                                   : blocks(p.vocab, weight_rows_per_cta(p.dim));
         return launch_after(p.bf16 ? lin_small_pack_kernel<__nv_bfloat16, 1> : lin_small_pack_kernel<float, 3>,
                             dim3(static_cast<unsigned>(packed + weight)), dim3(128), 0, s, p,
                             static_cast<int32_t>(packed));
@@ -647,7 +661,7 @@ cudaError_t lin_pack_weight(const LinParams &p, int64_t v0, int64_t v1, cudaStre
 {
     return launch_after(p.bf16 ? lin_pack_weight_kernel<__nv_bfloat16, 1>
                                : lin_pack_weight_kernel<float, 3>,
-                        dim3(static_cast<unsigned>(v1 - v0)), dim3(128), 0, s, p, v0);
+                        dim3(blocks(v1 - v0, weight_rows_per_cta(p.dim))), dim3(128), 0, s, p, v0, v1 - v0);
 }
 
 cudaError_t lin_combine(const LinParams &p, cudaStream_t s)
