@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(128) lin_finish_kernel(LinParams p)
         float4 x = make_float4(fill, fill, fill, fill);
         if (i >= 0) {
             x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
             for (int z = 0; z < parts; ++z) {
                 const float4 y = *reinterpret_cast<const float4 *>(sums + z * part + d);
                 x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);

@@ -26,7 +26,7 @@ constexpr int64_t kLinSms = 152;
 // 256-wide tile for each pair of SMs.
 constexpr int64_t kLinPieceUnit = kLinSms / 2 * 256;
 // The most parts that dhidden's sums over a piece are split into.
-constexpr int kMaxSplits = 16;
+constexpr uint32_t kMaxSplits = 64;
 
 // A tile shape of the products: 128 rows per CTA, `ctas` CTAs, n columns.
 struct LinTile {

@@ -150,21 +150,24 @@ template <int MODE> struct Jobs {
         // 24 products of 64 deep: its sums go to memory.  2048 x 77824 x 2560:
         // 1055 TFLOP/s whole, 1587 split.  The same for every piece of a call,
         // whose sums are added, and whether or not dweight is wanted.
+        // Each lane looks at two numbers of parts.
         if (dh_tiles > 0) {
             const float room = static_cast<float>(q.dh_room / (static_cast<int64_t>(tm) * tile_m * q.dh_pitch));
             const float n = static_cast<float>(dh_tiles), u = static_cast<float>(q.units);
             const float depth = static_cast<float>(q.piece_blocks);
             const float extra = 24.0f / static_cast<float>(q.pairs);
-            float least = 3.0e38f;
-            for (int k = 1; k <= kMaxSplits && static_cast<float>(k) <= fmaxf(room, 1.0f); ++k) {
-                const float part = depth / static_cast<float>(k) + extra;
-                const float cost = ceilf(n * static_cast<float>(k) / u) * part +
-                                   static_cast<float>(k) / static_cast<float>(q.pairs);
-                if (cost < least) {
+            uint32_t least = 0xffffffffu, mine = 1;  // costs are positive: their bits compare alike
+#pragma unroll
+            for (uint32_t k = (threadIdx.x & 31) + 1; k <= kMaxSplits; k += 32) {
+                const float parts = static_cast<float>(k), part = depth / parts + extra;
+                const uint32_t cost = __float_as_uint(ceilf(n * parts / u) * part + parts / static_cast<float>(q.pairs));
+                if (cost < least && (k == 1 || parts <= room)) {
                     least = cost;
-                    splits = k;
+                    mine = k;
                 }
             }
+            const uint32_t best = __reduce_min_sync(0xffffffffu, least);
+            splits = static_cast<int32_t>(__reduce_min_sync(0xffffffffu, least == best ? mine : kMaxSplits));
         }
         dh_tiles *= splits;
         total = dh_tiles + static_cast<int64_t>(tv) * tn;
