@@ -2,6 +2,7 @@
 // calls that start from hidden states (see gbce_linear.h).
 #include "gbce_kernels.cuh"
 #include "gbce_linear.h"
+#include "gbce_linear_rows.cuh"
 
 namespace gbce {
 
@@ -168,48 +169,6 @@ template <typename T> struct Quad;
 template <> struct Quad<__nv_bfloat16> { using type = uint2; };
 template <> struct Quad<float> { using type = float4; };
 
-// Eight elements of a row from any element on, as fp32.  `aligned`: from 16
-// bytes.  Otherwise bf16 goes by whole 4-byte words, shifted where the row
-// starts between two (in which case the word before the first element and the
-// one after the last are read too: the caller keeps off the row's ends).
-__device__ __forceinline__ void load_eight(const __nv_bfloat16 *p, bool aligned, float (&x)[8])
-{
-    uint32_t w[4];
-    if (aligned) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-        const uint32_t between = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 2u);
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) - between);
-        uint32_t u[5];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = __ldg(q + i);
-        u[4] = between != 0 ? __ldg(q + 4) : 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __funnelshift_r(u[i], u[i + 1], between * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = bf16x2_to_float2(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
-__device__ __forceinline__ void load_eight(const float *p, bool aligned, float (&x)[8])
-{
-    if (aligned) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = __ldg(p + i);
-    }
-}
-
 // Eight values into their planes: bf16 x is its own; fp32 x = hi + mid + lo,
 // each the rounding of what is left (24 bits in three times 8).
 template <int PLANES>
@@ -236,16 +195,8 @@ __device__ __forceinline__ void pack_eight(const T *src, __nv_bfloat16 *dst, int
                                            int64_t dim, bool zero)
 {
     float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (!zero) {
-        const bool aligned = reinterpret_cast<uintptr_t>(src) % 16 == 0;
-        if (d + 8 <= dim && (aligned || (d > 0 && d + 8 < dim))) {
-            load_eight(src + d, aligned, x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = d + i < dim ? static_cast<float>(src[d + i]) : 0.0f;
-        }
-    }
+    if (!zero)
+        read_eight(src, d, dim, x);
     store_eight<PLANES>(x, dst + d, plane);
 }
 

@@ -32,6 +32,7 @@
 
 #include "gbce_kernels.cuh"
 #include "gbce_linear.h"
+#include "gbce_linear_rows.cuh"
 #include "gbce_umma.cuh"
 
 namespace gbce {
@@ -51,13 +52,21 @@ __host__ __device__ constexpr bool is_grads(int mode) { return mode >= kLinGrads
 // Blocks of depth in one sum of the tensor cores.  They cut each partial sum's
 // last bits rather than round them, so a sum of many steps comes out small by
 // a part that grows with their number.  Logits are therefore summed 1024 deep
-// at a time, the gradients of fp32 inputs 512 deep, and these sums added in
-// fp32 registers, rounded to nearest; those of bf16 gradients, which end in 8
-// bits, are one sum.  Log-probs of 7000 x 76032 x 2560, relative error: 1.2e-6
-// in one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (in fp32 products 2e-7 to
-// 4e-7); forward 1377, 1383 and 1495 us.  dhidden of 2000 x 60000 x 512 fp32:
-// 1.1e-6 1024 deep, 6.4e-7 512 deep (fp32 products 5.1e-6); 5% of the time.
-__host__ __device__ constexpr int segment_blocks(int mode) { return mode == kLinGradsSplit ? 8 : 16; }
+// at a time (256 for up to 128 rows, where the table's bytes leave the time),
+// the gradients of fp32 inputs 512 deep, and these sums added in fp32
+// registers, rounded to nearest; those of bf16 gradients, which end in 8 bits,
+// are one sum.  Log-probs of 7000 x 76032 x 2560, relative error: 1.2e-6 in
+// one sum, 3.9e-7 1024 deep, 2.1e-7 512 deep (in fp32 products 2e-7 to 4e-7);
+// loss and gradients 5.87 ms 1024 deep, 6.22 512 deep.  dhidden of 2000 x 60000
+// x 512 fp32: 1.1e-6 1024 deep, 6.4e-7 512 deep (fp32 products 5.1e-6); 5% of
+// the time.
+//
+// The gathered columns' own logits are not taken from these sums: a row whose
+// target leads by 45 has a log p of e^-45 whose relative error is the absolute
+// error of that logit, and a logit of 50 summed 1024 deep came out 4e-5 too
+// small.  They are fp32 products of their two rows (row_dot), made by the
+// epilogue's warps: such rows' log p is then within 2e-7 (1 x 152064 x 4096).
+constexpr int kSegLogits = 16, kSegShort = 4, kSegGrads = 8;
 
 template <int CTAS, int NT> struct Tile {
     static constexpr int kM = 128 * CTAS;
@@ -86,6 +95,10 @@ struct MmaArgs {
     const int32_t *tgt;
     const int64_t *targets;  // stats of a direct call: [direct_rows, k]
     int32_t direct_rows;     // else 0
+    int32_t seg;                  // stats, dz: blocks of a segment
+    const void *hidden, *weight;  // stats: for the gathered columns' logits
+    int64_t hidden_stride, weight_stride;
+    const int32_t *row_list;
     float *xt;
     float2 *partials;
     int64_t partial_tiles;
@@ -220,6 +233,24 @@ __device__ __forceinline__ int64_t target_column(const MmaArgs &q, int64_t at, i
         return q.tgt[at] - first;
     const int64_t t = q.targets[at];
     return t < 0 || t >= q.vocab ? -1 : t - first;
+}
+
+// Logit of gathered column `at` (row x k + target), by a warp.
+__device__ __forceinline__ void target_logit(const MmaArgs &q, int64_t at)
+{
+    const int64_t t = target_column(q, at, 0), i = at / q.k;
+    if (t < 0)
+        return;
+    const int64_t r = q.direct_rows == 0 ? q.row_list[i] : i;
+    float x;
+    if (q.planes == 1)
+        x = row_dot(static_cast<const __nv_bfloat16 *>(q.hidden) + r * q.hidden_stride,
+                    static_cast<const __nv_bfloat16 *>(q.weight) + t * q.weight_stride, q.dim);
+    else
+        x = row_dot(static_cast<const float *>(q.hidden) + r * q.hidden_stride,
+                    static_cast<const float *>(q.weight) + t * q.weight_stride, q.dim);
+    if ((threadIdx.x & 31) == 0)
+        q.xt[at] = x;
 }
 
 // Plane indices of product q of six, smallest first.
@@ -480,7 +511,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 // 16 deep: 32 bytes along a row, or two groups of 8 k-rows
                 const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : segment_blocks(MODE);
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : (is_grads(MODE) ? kSegGrads : q.seg);
                 int32_t kb = 0;
                 do {  // one sum in TMEM for each segment
                     ok = warp_wait(&sh->acc_empty[acc], acc_phase ^ 1u, &sh->failed, q.dev_status);
@@ -528,6 +559,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const float alpha = is_grads(MODE) ? q.head->alpha : 1.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
+        // stats: this warp's share of the gathered columns' logits.  One each
+        // at most: made while the first tile's blocks are on their way (48
+        // rows x 4: 34.6 us, after the tiles 36.0), the first ones by
+        // different CTAs.  More: after the tiles (7000 rows x 1: 1510 us,
+        // before them 1570, where they hold up the tiles that CTAs share in L2).
+        const int64_t all_dots = MODE == kLinStats && q.xt != nullptr ? static_cast<int64_t>(live) * q.k : 0;
+        const int64_t dot_step = static_cast<int64_t>(gridDim.x) * 8;
+        int64_t dot = static_cast<int64_t>(warp - 2) * gridDim.x + blockIdx.x;
+        const auto make_dots = [&] {
+            for (; dot < all_dots; dot += dot_step)
+                target_logit(q, dot);
+        };
+        if (MODE == kLinStats && all_dots <= dot_step)
+            make_dots();
         for (int64_t t = unit; t < jobs.total; t += units) {
             const Job job = jobs.at(t);
             const bool any = job.k1 > job.k0;
@@ -556,7 +601,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             float sums[kChunks][32];
             const auto add_segments = [&] {
                 const int32_t n_blocks = (job.k1 - job.k0) * q.pairs;
-                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : segment_blocks(MODE);
+                const int32_t seg = MODE == kLinGrads ? max(n_blocks, 1) : (is_grads(MODE) ? kSegGrads : q.seg);
                 for (int32_t kb = 0; kb == 0 || kb < n_blocks; kb += seg) {
                     const uint32_t src = wait_sum();
                     if (!ok)
@@ -574,7 +619,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                 for (int w = 0; w < kChunks; ++w)
                     hit[w] = 0;
-                uint32_t hits = 0;  // bit k: target k is among them
+                uint32_t hits = 0;  // dz, bit k: target k is among them
                 float2 g = make_float2(0.0f, 0.0f);
                 if (row < live) {
                     if (MODE == kLinDz)
@@ -582,7 +627,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     for (int k = 0; k < q.k; ++k) {
                         const int64_t j = target_column(q, static_cast<int64_t>(row) * q.k + k, q.v0 + col0);
                         if (j >= 0 && j < kHalf) {
-                            hits |= 1u << k;
+                            hits |= MODE == kLinDz ? 1u << k : 0u;
 #pragma unroll
                             for (int w = 0; w < kChunks; ++w)
                                 if (MODE == kLinStats && j >> 5 == w)
@@ -612,17 +657,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         }
                         const uint32_t mine = hit[ch];
                         if (mine != 0) {
-                            for (uint32_t left = hits; left != 0; left &= left - 1) {
-                                const int64_t at = static_cast<int64_t>(row) * q.k + __ffs(left) - 1;
-                                const int64_t j = target_column(q, at, q.v0 + c0);
-                                if (j >= 0 && j < 32) {
-                                    float x = v[0];
-#pragma unroll
-                                    for (int i = 1; i < 32; ++i)
-                                        x = j == i ? v[i] : x;
-                                    q.xt[at] = x;
-                                }
-                            }
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 v[j] = mine >> j & 1u ? kNegInf : v[j];
@@ -740,6 +774,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
             }
         }
+        if (MODE == kLinStats)
+            make_dots();
         __syncwarp();
     }
 
@@ -901,6 +937,7 @@ MmaArgs base_args(const LinParams &p, int64_t v0)
     q.k = static_cast<int32_t>(p.k);
     q.tgt = p.tgt;
     q.dim = p.dim;
+    q.seg = p.rows <= 128 ? kSegShort : kSegLogits;
     return q;
 }
 
@@ -979,7 +1016,14 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
         q.blocks = static_cast<int32_t>(ceil_div(p.dim, kDepth));
         q.tiles_n = static_cast<int32_t>(ceil_div(v1 - v0, shape.n));
         q.b_row0 = static_cast<int32_t>(w.row0);
-        q.xt = p.xt;
+        // of the launches over parts of the table the first makes all the
+        // gathered columns' logits
+        q.hidden = p.hidden;
+        q.weight = p.weight;
+        q.hidden_stride = p.hidden_stride;
+        q.weight_stride = p.weight_stride;
+        q.row_list = p.row_list;
+        q.xt = v0 == 0 ? p.xt : nullptr;
         if (p.fused) {
             q.z = p.z;
             q.z_pitch = p.piece;

@@ -202,6 +202,33 @@ def test_short_forwards_in_place_and_packed_agree(rows, pad):
         assert int(st[0]) == int(st[1]) == (gbce.DEV_BAD_LABEL if rows > 4 else 0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D,pad", [(1, 4096, 0), (48, 4096, 8), (300, 4096, 0), (300, 4095, 0), (700, 2561, 3)])
+def test_confident_rows_keep_their_digits(rows, D, pad, dtype):
+    # One column of weight, the others zero: their logits are exactly 0 and log p
+    # = -softplus(log(V - 1) - z), whose relative error is what z and the steps
+    # after it are off by.  All products of z are positive, so in 256 running
+    # sums of D / 256 terms and a tree of 8 levels it carries at most
+    # (D / 512 + 1 + 8) u z (half a sum on average, one half ulp a term); the
+    # temperature, the log, the differences and exp2's argument 6 u (z + 12)
+    # more, exp2 and log1p 16 u.  Sums that are cut instead of rounded, 64
+    # steps long and more, are off by 64 u z and more.
+    g = torch.Generator(device=DEV).manual_seed(D + rows)
+    V, at = 513, 300
+    w = torch.zeros((V, D), dtype=dtype, device=DEV)
+    w[at] = (torch.rand(D, generator=g, device=DEV) + 0.5).to(dtype)
+    lead = 20.0 + 40.0 * torch.rand(rows, 1, generator=g, device=DEV)
+    h = (lead * w[at].float() / w[at].float().square().sum()).to(dtype)
+    lab = torch.full((rows,), at, dtype=torch.int64, device=DEV)
+    z = h.double() @ w[at].double()
+    exp = -torch.nn.functional.softplus(math.log(V - 1) - z, threshold=1e9)
+    bound = exp.abs() * (ref.U * ((D / 512 + 9) * z + 6 * (z + 12) + 16))
+    logp, _ = gbce.linear_selective_logsoftmax(strided(h, pad), strided(w, pad), lab[:, None], 1.0, with_state=True)
+    ref.assert_within(logp[:, 0], exp, bound, "log p")
+    both = gbce.linear_ce_fwd_bwd_fused(strided(h, pad), strided(w, pad), lab, want_logp=True)
+    assert torch.equal(both.logp.reshape(-1), logp[:, 0])
+
+
 def test_more_rows_than_a_grid_axis_takes():
     # kept logits of 70000 rows
     h, w, t, mask, up = problem(70000, 64, 16, 1, torch.bfloat16, 31)
