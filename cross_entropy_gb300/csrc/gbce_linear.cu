@@ -201,7 +201,8 @@ __device__ __forceinline__ void pack_eight(const T *src, __nv_bfloat16 *dst, int
 }
 
 // Packed row i from row r of the hidden states (zeros past the live rows), its
-// targets, and in a backward call what its gradient takes.
+// targets, their logits where there are many, and in a backward call what its
+// gradient takes.
 template <typename T, int PLANES>
 __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64_t r, bool in)
 {
@@ -214,6 +215,15 @@ __device__ __forceinline__ void pack_hidden(const LinParams &p, int64_t i, int64
         const int64_t t = in ? p.targets[r * K + k] : -1;
         p.tgt[i * K + k] = t >= 0 && t < p.vocab ? static_cast<int32_t>(t) : -1;
     }
+    if (in && lin_dots_in_pack(p))
+        for (int k = threadIdx.x >> 5; k < K; k += blockDim.x >> 5) {
+            const int64_t t = p.targets[r * K + k];
+            if (t < 0 || t >= p.vocab)
+                continue;
+            const float x = row_dot(src, static_cast<const T *>(p.weight) + t * p.weight_stride, p.dim);
+            if ((threadIdx.x & 31) == 0)
+                p.xt[i * K + k] = x;
+        }
     if (in && p.backward && !p.fused)
         saved_row_gradient(p, i, r);
 }

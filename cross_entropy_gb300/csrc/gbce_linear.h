@@ -114,6 +114,18 @@ struct LinParams {
     int32_t *dev_status;
 };
 
+// Who makes the gathered columns' logits, fp32 products of two rows each.
+// Few: the statistics kernel's epilogue, at most one a warp, while its first
+// tile is on its way (48 rows x 4: 34.6 us; after its tiles 36.0).  More: the
+// packing before it, a warp each with the memory to itself (2000 x 4096 x 512,
+// four targets: 34.6 us; after the tiles 43.5; 7000 x 76032 x 2560, one: 1525
+// us either way, before the tiles, behind whose loads they wait, 1569).
+constexpr int64_t kLinStatsDots = 1216;
+inline __host__ __device__ bool lin_dots_in_pack(const LinParams &p)
+{
+    return !p.direct && (p.fused || !p.backward) && p.rows * p.k > kLinStatsDots;
+}
+
 cudaError_t lin_select(const LinParams &p, cudaStream_t s);
 bool lin_weight_packed(const LinParams &p);  // lin_select packed the weight too
 cudaError_t lin_stats(const LinParams &p, cudaStream_t s);

@@ -64,8 +64,9 @@ __host__ __device__ constexpr bool is_grads(int mode) { return mode >= kLinGrads
 // The gathered columns' own logits are not taken from these sums: a row whose
 // target leads by 45 has a log p of e^-45 whose relative error is the absolute
 // error of that logit, and a logit of 50 summed 1024 deep came out 4e-5 too
-// small.  They are fp32 products of their two rows (row_dot), made by the
-// epilogue's warps: such rows' log p is then within 2e-7 (1 x 152064 x 4096).
+// small.  They are fp32 products of their two rows (row_dot), made apart: such
+// rows' log p is then within 2e-7 (1 x 152064 x 4096).  What that costs: 2048
+// x 32768 x 1024 92 -> 98 us, 7000 x 76032 x 2560 nothing.
 constexpr int kSegLogits = 16, kSegShort = 4, kSegGrads = 8;
 
 template <int CTAS, int NT> struct Tile {
@@ -559,11 +560,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const float alpha = is_grads(MODE) ? q.head->alpha : 1.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
-        // stats: this warp's share of the gathered columns' logits.  One each
-        // at most: made while the first tile's blocks are on their way (48
-        // rows x 4: 34.6 us, after the tiles 36.0), the first ones by
-        // different CTAs.  More: after the tiles (7000 rows x 1: 1510 us,
-        // before them 1570, where they hold up the tiles that CTAs share in L2).
+        // stats: this warp's share of the gathered columns' logits, the first
+        // ones by different CTAs, before its tiles (more than one a warp,
+        // which only a call in place can have: after them)
         const int64_t all_dots = MODE == kLinStats && q.xt != nullptr ? static_cast<int64_t>(live) * q.k : 0;
         const int64_t dot_step = static_cast<int64_t>(gridDim.x) * 8;
         int64_t dot = static_cast<int64_t>(warp - 2) * gridDim.x + blockIdx.x;
@@ -1023,7 +1022,7 @@ cudaError_t lin_stats(const LinParams &p, cudaStream_t s)
         q.hidden_stride = p.hidden_stride;
         q.weight_stride = p.weight_stride;
         q.row_list = p.row_list;
-        q.xt = v0 == 0 ? p.xt : nullptr;
+        q.xt = v0 == 0 && !lin_dots_in_pack(p) ? p.xt : nullptr;
         if (p.fused) {
             q.z = p.z;
             q.z_pitch = p.piece;
