@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             // next sum in TMEM, and its release once this warp has read it
             const auto wait_sum = [&] {
                 ok = warp_wait(&sh->acc_full[acc], acc_phase, &sh->failed, q.dev_status);
+                __syncwarp();
                 tc_fence_after();
                 return tmem + lanes + acc * NT + half * kHalf;
             };
@@ -763,6 +764,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         if (ch == kChunks - 1)  // the tile after next may start
                             sum_read();
                         put(ch, v);
+                        // the lanes of a tile's last rows part in there, and
+                        // the next loads from TMEM are the whole warp's
+                        __syncwarp();
                     }
                 } else {
                     if (!add_segments())
