@@ -63,3 +63,45 @@ def test_gradients_of_tiles_that_end_inside_a_warp(rows, V, D, dtype):
     both = start.double() + rdw
     # the sum's addition and rounding on top
     ref.assert_within(acc, both, bw + (ref.HALF[dtype] + ref.U) * both.abs(), "dweight +=")
+
+
+def elapsed(call, n=10):
+    for _ in range(3):
+        call()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    a.record()
+    for _ in range(n):
+        call()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) / n
+
+
+def test_lookup_gradient_takes_no_longer_for_one_token_than_for_many():
+    # 2 rows >= vocab: the zeros of a fresh table are written by CTAs that find
+    # out which of their rows are named.  Walking the run of a token that every
+    # row names cost one of them 8192 loads in a row (ten times the call).
+    rows, V, D = 262144, 400000, 8
+    g = torch.Generator(device=DEV).manual_seed(2)
+    go = torch.randn((rows, D), generator=g, device=DEV)
+    spread = torch.randint(0, V, (rows,), generator=g, device=DEV)
+    one = torch.full((rows,), 5, device=DEV)
+    t = [elapsed(lambda: gbce.embedding_lookup_bwd(go, tok, V)) for tok in (spread, one)]
+    assert t[1] <= 3.0 * t[0], t
+
+
+@pytest.mark.parametrize("rows,V", [(64, 100), (700, 47), (4000, 600), (9000, 33), (30000, 17)])
+def test_rows_beside_long_runs_get_their_zeros(rows, V):
+    # runs of one token from 1 to all the rows, on every place of a block of 16
+    # table rows, among neighbours that nobody names and that somebody does
+    go = torch.ones((rows, 3), device=DEV)
+    for at in range(min(V, 17)):
+        for other in (at, (at + 1) % V, (at + 5) % V, V - 1):
+            for n in (1, 31, 33, rows - 2):
+                tok = torch.full((rows,), at, device=DEV)
+                tok[:max(0, rows - 1 - n)] = -100
+                tok[rows // 2] = other
+                d = gbce.embedding_lookup_bwd(go, tok, V, dtable=torch.full((V, 3), 7.0, device=DEV))
+                want = torch.bincount(tok[tok >= 0], minlength=V).float()  # whole numbers: exact
+                assert torch.equal(d, want[:, None].expand(V, 3)), (at, other, n)
