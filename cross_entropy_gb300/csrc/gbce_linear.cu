@@ -90,21 +90,25 @@ __device__ __forceinline__ void saved_row_gradient(const LinParams &p, int64_t i
         ce_row_gradient(p, i, r, M, S, logp);
         return;
     }
-    const float inv_t = 1.0f / p.T;
+    // sums of upstream in fp64 (in fp32 one that cancels keeps only its terms'
+    // rounding), the others' from their own terms rather than as a difference,
+    // and over T before they meet the probabilities
     const float *g = p.grad_out + r * K;
     const int64_t *t = p.targets + r * K;
     const int64_t own = t[k];
-    float sum = 0.0f, mine = 0.0f, other = 0.0f;
+    double sum = 0.0, mine = 0.0, other = 0.0;
     for (int j = 0; j < K; ++j) {
-        sum += g[j];
+        const double gj = g[j];
+        sum += gj;
         if (t[j] == own)
-            mine += g[j];
+            mine += gj;
         else
-            other += g[j];
+            other += gj;
     }
     if (k == 0)
-        p.grow[i] = make_float2(M, -(sum * inv_t) / S);
-    p.dzt[i * K + k] = (-mine * expm1f(logp) - other * expf(logp)) * inv_t;
+        p.grow[i] = make_float2(M, -static_cast<float>(sum / p.T) / S);
+    p.dzt[i * K + k] = fmaf(-static_cast<float>(mine / p.T), expm1f(logp),
+                            -static_cast<float>(other / p.T) * expf(logp));
 }
 
 __device__ __forceinline__ void write_head(const LinParams &p, int32_t live, int64_t items)

@@ -105,3 +105,46 @@ def test_rows_beside_long_runs_get_their_zeros(rows, V):
                 d = gbce.embedding_lookup_bwd(go, tok, V, dtable=torch.full((V, 3), 7.0, device=DEV))
                 want = torch.bincount(tok[tok >= 0], minlength=V).float()  # whole numbers: exact
                 assert torch.equal(d, want[:, None].expand(V, 3)), (at, other, n)
+
+
+@pytest.mark.parametrize("rows,V,D", [(256, 3, 8), (300, 40, 64)])
+def test_upstream_sums_that_cancel(rows, V, D):
+    # K = 16: indices 8..15 repeat 0..7 with each upstream negated to within
+    # 1e-4, so that every column's summed upstream (and every element of the
+    # gradients) is a sum of terms about 1 that cancels to about 1e-4.
+    #
+    # A gathered column's dz is g_t (1 - p_t) / T - g_o p_t / T with g_t and g_o
+    # the exact sums.  Sums of 16 fp32 values in fp64 and their one rounding are
+    # within 2 u of them; 1 - p_t and p_t come from the saved log p, off by
+    # comp (2 ez + 2 u (|log p| + 64)) + 4 u |log p| at most, which relative to
+    # either is at most 2 ez + 2 u (|log p| + 64) + 4 u (|log p| + 1) (for |log
+    # p| p <= 1 - p); expm1, exp, two products and the sum 8 u; the other
+    # columns 2 ez + 16 u of |G| p_j / T.  Sums in fp32 are off by up to 16 u
+    # of the terms, a thousand times as much of what is left.
+    T, K = 0.8, 16
+    h, w, t, _ = draw(rows, V, D, K, torch.float32, rows)
+    g = torch.Generator(device=DEV).manual_seed(92)
+    up = torch.randn((rows, K), generator=g, device=DEV)
+    t[:, 8:] = t[:, :8]
+    up[:, 8:] = -up[:, :8] + 1e-4 * torch.randn((rows, 8), generator=g, device=DEV)
+    logp, state = gbce.linear_selective_logsoftmax(h, w, t, T, with_state=True)
+    dh, dw = gbce.linear_selective_logsoftmax_bwd(h, w, t, up, logp, state, T)
+
+    live = torch.ones(rows, dtype=torch.bool, device=DEV)
+    p, lp, comp, ez = ref.rows_of(h, w, t, T, live)
+    u64 = up.double()
+    total = u64.sum(1, keepdim=True)
+    dz, off = -total * p, total.abs() * p * (2 * ez + 16 * ref.U)
+    for k in range(K):
+        own = t[:, k:k + 1]
+        mine = torch.where(t == own, u64, 0.0).sum(1, keepdim=True)
+        other = torch.where(t == own, 0.0, u64).sum(1, keepdim=True)
+        pt, ct, size = p.gather(1, own), comp[:, k:k + 1], lp[:, k:k + 1].abs()
+        rel = 2 * ez + 2 * ref.U * (size + 64) + 4 * ref.U * (size + 1) + 10 * ref.U
+        dz.scatter_(1, own, mine * ct - other * pt)
+        off.scatter_(1, own, (mine.abs() * ct + other.abs() * pt) * rel)
+    dz, off = dz / T, off / T + 4 * ref.U * dz.abs() / T  # and what three bf16 planes leave
+    for got, want, size, err, n, what in (
+            (dh, dz @ w.double(), dz.abs() @ w.double().abs(), off @ w.double().abs(), V, "dhidden"),
+            (dw, dz.t() @ h.double(), dz.abs().t() @ h.double().abs(), off.t() @ h.double().abs(), rows, "dweight")):
+        ref.assert_within(got, want, 1.01 * err + (n / 8 + 16) * ref.U * size + ref.U * want.abs(), what)
