@@ -114,15 +114,16 @@ Layout layout(int64_t rows, int64_t vocab, int64_t dim, int64_t k, gbce_dtype dt
 bool overlap(const void *a, size_t an, const void *b, size_t bn)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bn && y < x + an;
+    return an > 0 && bn > 0 && x < y + bn && y < x + an;
 }
 
 size_t span(int64_t rows, int64_t stride, int64_t dim, gbce_dtype dt)
 {
-    return static_cast<size_t>((rows - 1) * stride + dim) * elem_size(dt);
+    return rows == 0 ? 0 : static_cast<size_t>((rows - 1) * stride + dim) * elem_size(dt);
 }
 
-// A [n, dim] matrix of rows `stride` apart: addressable and of its type's alignment.
+// A [n, dim] matrix of rows `stride` apart: addressable and of its type's
+// alignment.  One without rows has any address; null is no matrix at all.
 gbce_status check_matrix(const void *p, int64_t n, int64_t stride, int64_t dim, gbce_dtype dt)
 {
     if (p == nullptr || stride < dim || stride > (INT64_MAX / 16) / (n > 0 ? n : 1))
@@ -152,7 +153,8 @@ gbce_status check_shape(const Shape &a)
     if (a.dtype != GBCE_F32 && a.dtype != GBCE_BF16)
         return GBCE_EDTYPE;
     if (a.rows < 0 || a.rows > kMaxRows || a.vocab < 1 || a.vocab > kMaxVocab || a.dim < 1 ||
-        a.dim > kMaxDim || a.k < 1 || a.k > GBCE_MAX_K)
+        a.dim > kMaxDim || a.k < 1 || a.k > GBCE_MAX_K || a.hidden_stride < a.dim ||
+        a.weight_stride < a.dim)
         return GBCE_EINVAL;
     if (!(std::isfinite(a.temperature) && a.temperature > 0.0f))
         return GBCE_EINVAL;
@@ -281,14 +283,18 @@ bool valid_reduction(gbce_reduction r) { return r == GBCE_NONE || r == GBCE_SUM 
 
 gbce_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GBCE_OK : GBCE_ECUDA; }
 
-// dweight of a call without rows: zeros, unless it accumulates.
-cudaError_t zero_dweight(const Shape &a, const Grads &g, cudaStream_t s)
+// The gradients of a call without rows: zeros in dweight, unless it
+// accumulates.  What is written, and next to what, is checked as in any call.
+gbce_status no_rows(const Shape &a, const Grads &g, cudaStream_t s)
 {
+    gbce_status st = check_matrix(a.weight, a.vocab, a.weight_stride, a.dim, a.dtype);
+    if (st != GBCE_OK || (st = check_grads(a, g)) != GBCE_OK)
+        return st;
     if (g.dweight == nullptr || g.accumulate)
-        return cudaSuccess;
+        return GBCE_OK;
     const size_t es = elem_size(a.dtype);
-    return cudaMemset2DAsync(g.dweight, static_cast<size_t>(g.dweight_stride) * es, 0,
-                             static_cast<size_t>(a.dim) * es, static_cast<size_t>(a.vocab), s);
+    return cuda_status(cudaMemset2DAsync(g.dweight, static_cast<size_t>(g.dweight_stride) * es, 0,
+                                         static_cast<size_t>(a.dim) * es, static_cast<size_t>(a.vocab), s));
 }
 
 // The loss, and with `g` both gradients after it.
@@ -305,8 +311,10 @@ gbce_status ce_call(const Shape &a, const int64_t *labels, int64_t ignore_index,
     if (a.rows == 0) {
         if (reduction != GBCE_NONE && loss_out == nullptr)
             return GBCE_EINVAL;
-        cudaError_t e = g != nullptr ? zero_dweight(a, *g, s) : cudaSuccess;
-        if (e == cudaSuccess && reduction != GBCE_NONE)
+        if (g != nullptr && (st = no_rows(a, *g, s)) != GBCE_OK)
+            return st;
+        cudaError_t e = cudaSuccess;
+        if (reduction != GBCE_NONE)
             e = cudaMemsetAsync(loss_out, 0, sizeof(float), s);
         if (e == cudaSuccess && n_items_out != nullptr)
             e = cudaMemsetAsync(n_items_out, 0, sizeof(int64_t), s);
@@ -401,7 +409,7 @@ gbce_status linear_selective_logsoftmax_bwd(
     if (st != GBCE_OK)
         return st;
     if (rows == 0)
-        return cuda_status(zero_dweight(a, g, s));
+        return no_rows(a, g, s);
     if (index == nullptr || grad_logp == nullptr || saved_logp == nullptr || row_state == nullptr)
         return GBCE_EINVAL;
     if ((st = check_grads(a, g)) != GBCE_OK)
@@ -457,7 +465,7 @@ gbce_status linear_ce_bwd(const void *hidden, int64_t hidden_row_stride, const v
     if (!valid_reduction(reduction))
         return GBCE_EINVAL;
     if (rows == 0)
-        return cuda_status(zero_dweight(a, g, s));
+        return no_rows(a, g, s);
     if (labels == nullptr || grad_out == nullptr || saved_logp == nullptr || row_state == nullptr ||
         (reduction == GBCE_MEAN && n_items == nullptr))
         return GBCE_EINVAL;

@@ -146,6 +146,12 @@ def _gradient(buf, like: torch.Tensor, name: str, want: bool):
     return buf, d
 
 
+def _wanted(d: Optional[torch.Tensor], weight: torch.Tensor) -> Optional[int]:
+    """Address of a wanted gradient.  An empty tensor has none, which the library would read as
+    not wanted: any address does for it, the weight's for one."""
+    return None if d is None else d.data_ptr() or weight.data_ptr()
+
+
 def linear_workspace_size(rows: int, vocab: int, dim: int, k: int = 1, dtype=torch.bfloat16,
                           backward: bool = True) -> int:
     """Bytes of workspace of a linear_* call of these sizes."""
@@ -249,7 +255,7 @@ def linear_selective_logsoftmax_bwd(hidden: torch.Tensor, weight: torch.Tensor, 
         st = lib.linear_selective_logsoftmax_bwd(
             h.data_ptr(), _stride(h), w.data_ptr(), _stride(w), _dtype_code(h), rows, w.shape[0],
             h.shape[1], idx.data_ptr(), k, float(temperature), _ptr(mask), g.data_ptr(),
-            lp.data_ptr(), rs.data_ptr(), _ptr(dh), 0 if dh is None else _stride(dh), _ptr(dw),
+            lp.data_ptr(), rs.data_ptr(), _wanted(dh, w), 0 if dh is None else _stride(dh), _ptr(dw),
             0 if dw is None else _stride(dw), acc, ws_ptr, ws_bytes, _ptr(dev_status),
             _stream_ptr(stream, h.device))
     _check(st, "linear_selective_logsoftmax_bwd")
@@ -318,7 +324,7 @@ def linear_ce_bwd(hidden: torch.Tensor, weight: torch.Tensor, labels, grad_out,
         st = lib.linear_ce_bwd(
             h.data_ptr(), _stride(h), w.data_ptr(), _stride(w), _dtype_code(h), rows, w.shape[0],
             h.shape[1], lab.data_ptr(), int(ignore_index), float(temperature), red, g.data_ptr(),
-            lp.data_ptr(), rs.data_ptr(), _ptr(n), _ptr(dh), 0 if dh is None else _stride(dh),
+            lp.data_ptr(), rs.data_ptr(), _ptr(n), _wanted(dh, w), 0 if dh is None else _stride(dh),
             _ptr(dw), 0 if dw is None else _stride(dw), acc, ws_ptr, ws_bytes, _ptr(dev_status),
             _stream_ptr(stream, h.device))
     _check(st, "linear_ce_bwd")
@@ -356,7 +362,7 @@ def linear_ce_fwd_bwd_fused(hidden: torch.Tensor, weight: torch.Tensor, labels, 
         st = lib.linear_ce_fwd_bwd_fused(
             h.data_ptr(), _stride(h), w.data_ptr(), _stride(w), _dtype_code(h), rows, w.shape[0],
             h.shape[1], lab.data_ptr(), int(ignore_index), float(temperature), red, g.data_ptr(),
-            loss.data_ptr(), _ptr(logp), None, n_items.data_ptr(), _ptr(dh),
+            loss.data_ptr(), _ptr(logp), None, n_items.data_ptr(), _wanted(dh, w),
             0 if dh is None else _stride(dh), _ptr(dw), 0 if dw is None else _stride(dw), acc,
             ws_ptr, ws_bytes, _ptr(dev_status), _stream_ptr(stream, h.device))
     _check(st, "linear_ce_fwd_bwd_fused")

@@ -447,9 +447,11 @@ gbce_status vocab_slice_grad(const void *logits, gbce_dtype dtype, int64_t rows,
  *    are then invalid.
  * Errors: GBCE_EINVAL for rows outside [0, 2^24], dim outside [1, 2^20],
  * vocab < 1, strides below dim, k, temperature and NULL pointers as above,
- * outputs that overlap an input or each other, no gradient wanted at all;
- * GBCE_EDTYPE; GBCE_EWORKSPACE.  Label smoothing, DFT, soft-capping and the
- * entropy are not available on this path.
+ * outputs that overlap an input or each other, no gradient wanted at all
+ * (a call without rows is refused for the same, but takes NULL for its empty
+ * inputs; a dhidden that is wanted has an address there too); GBCE_EDTYPE;
+ * GBCE_EWORKSPACE.  Label smoothing, DFT, soft-capping and the entropy are not
+ * available on this path.
  */
 
 /* Bytes of workspace of a call; backward: 0 for the two forward calls.

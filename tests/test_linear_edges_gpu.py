@@ -148,3 +148,29 @@ def test_upstream_sums_that_cancel(rows, V, D):
             (dh, dz @ w.double(), dz.abs() @ w.double().abs(), off @ w.double().abs(), V, "dhidden"),
             (dw, dz.t() @ h.double(), dz.abs().t() @ h.double().abs(), off.t() @ h.double().abs(), rows, "dweight")):
         ref.assert_within(got, want, 1.01 * err + (n / 8 + 16) * ref.U * size + ref.U * want.abs(), what)
+
+
+def test_gradients_without_rows():
+    w = torch.randn((300, 64), device=DEV, dtype=torch.bfloat16)
+    h = torch.empty((0, 64), device=DEV, dtype=torch.bfloat16)
+    lab = torch.empty((0,), device=DEV, dtype=torch.int64)
+    logp, state = torch.empty((0,), device=DEV), torch.empty((0, 2), device=DEV)
+    calls = [lambda **kw: gbce.linear_ce_fwd_bwd_fused(h, w, lab, **kw)[1:3],
+             lambda **kw: gbce.linear_ce_bwd(h, w, lab, 1.0, logp, state, torch.zeros((), dtype=torch.int64), **kw),
+             lambda **kw: gbce.linear_selective_logsoftmax_bwd(h, w, lab, logp, logp, state, **kw)]
+    for call in calls:
+        before = w.clone()
+        with pytest.raises(gbce.GbceError):
+            call(dweight=w)
+        with pytest.raises(gbce.GbceError):
+            call(want_dhidden=False, want_dweight=False)
+        assert torch.equal(w, before)
+        dh, dw = call(want_dweight=False)
+        assert dh.shape == (0, 64) and dw is None
+        dh, dw = call(want_dhidden=False, dweight=torch.full_like(w, 7.0))
+        assert dh is None and not dw.any()
+        wide = torch.full((300, 70), 7.0, device=DEV, dtype=torch.bfloat16)
+        dh, dw = call(dweight=wide[:, :64])
+        assert dh.shape == (0, 64) and not dw.any() and (wide[:, 64:] == 7.0).all()
+        dh, dw = call(dweight=torch.full_like(w, 7.0), accumulate=True)
+        assert (dw == 7.0).all()
