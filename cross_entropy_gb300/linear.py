@@ -389,7 +389,7 @@ def embedding_lookup(table: torch.Tensor, tokens, scale: float = 1.0, *, ignore_
             out = torch.empty(shape, dtype=t.dtype, device=t.device)
         elif out.shape != torch.Size(shape) or out.dtype != t.dtype or out.device != t.device:
             raise ValueError(f"out must be a {t.dtype} tensor of shape {shape} on {t.device}")
-        o = out.view(1, -1) if out.dim() == 1 else _matrix(out, "out")
+        o = _matrix(out.unsqueeze(0) if out.dim() == 1 else out, "out")
         _check_status(dev_status, t.device)
         st = lib.embedding_lookup(t.data_ptr(), _stride(t), code, t.shape[0], t.shape[1],
                                   tok.data_ptr(), rows, int(ignore_index), float(scale),

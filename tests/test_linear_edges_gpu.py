@@ -174,3 +174,17 @@ def test_gradients_without_rows():
         assert dh.shape == (0, 64) and not dw.any() and (wide[:, 64:] == 7.0).all()
         dh, dw = call(dweight=torch.full_like(w, 7.0), accumulate=True)
         assert (dw == 7.0).all()
+
+
+def test_lookup_of_a_scalar_token_into_a_part_of_another_tensor():
+    # one row of `dim` elements: its own unit stride counts, like any row's
+    table = torch.randn((10, 16), device=DEV)
+    buf = torch.full((64,), 7.0, device=DEV)
+    with pytest.raises(ValueError, match="unit stride"):
+        gbce.embedding_lookup(table, torch.tensor(3), out=buf[0:32:2])
+    assert (buf == 7.0).all()
+    out = gbce.embedding_lookup(table, torch.tensor(3), out=buf[5:21])
+    assert torch.equal(out, table[3]) and (buf[:5] == 7.0).all() and (buf[21:] == 7.0).all()
+    one = torch.randn((4, 1), device=DEV)
+    out = gbce.embedding_lookup(one, torch.tensor(2), out=buf[0:64:64])
+    assert torch.equal(out, one[2]) and (buf[22:] == 7.0).all()
