@@ -407,7 +407,7 @@ def embedding_lookup_bwd(grad_out: torch.Tensor, tokens, vocab: int, scale: floa
     ``accumulate`` added to the given ``dtable``."""
     lib = load_library()
     acc = _accumulates(accumulate, dtable, "dtable")
-    g = _matrix(grad_out, "grad_out")
+    g = _matrix(grad_out.unsqueeze(0) if grad_out.dim() == 1 else grad_out, "grad_out")
     code = _dtype_code(g)
     rows, dim = g.shape
     with _on(g.device, stream):

@@ -188,3 +188,21 @@ def test_lookup_of_a_scalar_token_into_a_part_of_another_tensor():
     one = torch.randn((4, 1), device=DEV)
     out = gbce.embedding_lookup(one, torch.tensor(2), out=buf[0:64:64])
     assert torch.equal(out, one[2]) and (buf[22:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_of_a_scalar_tokens_lookup(dtype):
+    # tokens of any shape have rows of shape [*tokens.shape, dim], [dim] for a scalar
+    table = torch.randn((10, 16), device=DEV).to(dtype)
+    tok = torch.tensor(3, device=DEV)
+    row = gbce.embedding_lookup(table, tok, 2.0)
+    d = gbce.embedding_lookup_bwd(row, tok, 10, 2.0)
+    want = torch.zeros_like(table)
+    want[3] = 2.0 * row  # a power of two: exact
+    assert torch.equal(d, want)
+    acc = gbce.embedding_lookup_bwd(row, tok, 10, 2.0, dtable=d, accumulate=True)
+    assert acc is d and torch.equal(d, 2.0 * want)
+    with pytest.raises(ValueError, match="unit stride"):
+        gbce.embedding_lookup_bwd(torch.zeros(32, device=DEV, dtype=dtype)[::2], tok, 10)
+    with pytest.raises(ValueError, match="shape"):
+        gbce.embedding_lookup_bwd(row, tok[None], 10)
