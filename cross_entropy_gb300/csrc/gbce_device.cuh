@@ -726,11 +726,12 @@ __device__ __forceinline__ void warp_merge_state(float &m, float &s, float &h, f
 // units: a = log s + (m - x_t) / T, log p = -softplus(a).  The margin
 // (m - x_t) / T is one IEEE division of an exact (bf16) or once-rounded
 // (fp32) difference, taken from the same values the sweep read, so log p
-// is never positive.  s == 0 (no other column, V == 1) gives log p = 0.
+// is never positive.  s == 0 (no other column, V == 1) gives log p = 0, unless
+// x_t is NaN: in a row of NaN logits the merges find no max and leave s at 0.
 __device__ __forceinline__ float finalize_logp(float m, float s, float xt, float T)
 {
     if (!(s > 0.0f))
-        return (s == 0.0f) ? 0.0f : __int_as_float(0x7fc00000);
+        return (s == 0.0f && xt == xt) ? 0.0f : __int_as_float(0x7fc00000);
     const float a = logf(s) + (m - xt) / T;
     return -softplus(a);
 }
@@ -747,11 +748,11 @@ __device__ __forceinline__ float finalize_logp(float m, float s, float xt, float
 // and fall below fp32's normal range, while H = e^a (1 + L - mean) may not:
 // there e^a is carried times 2^64 (the square of e^{a/2} 2^32, both normal
 // down to a = -174) and the product is scaled back in one rounding, so an
-// entropy down to fp32's smallest subnormal keeps its value.
+// entropy down to fp32's smallest subnormal keeps its value.  s == 0: as above.
 __device__ __forceinline__ float finalize_entropy(float m, float s, float h, float xt, float T)
 {
     if (!(s > 0.0f))
-        return (s == 0.0f) ? 0.0f : __int_as_float(0x7fc00000);
+        return (s == 0.0f && xt == xt) ? 0.0f : __int_as_float(0x7fc00000);
     const float ls = logf(s);
     const float a = ls + (m - xt) / T;
     const float mean_u = (h / s) * 0.69314718055994531f;  // <= 0
