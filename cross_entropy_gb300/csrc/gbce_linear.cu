@@ -359,6 +359,17 @@ __global__ void __launch_bounds__(128) lin_small_pack_kernel(LinParams p, int32_
     pack_hidden<T, PLANES>(p, i, i < live ? s_row : 0, i < live);
 }
 
+// One gathered logit into a (max, sum).  A NaN stays one: merge_max_sum would
+// take it for nothing where nothing else is (its max is then -inf).
+__device__ __forceinline__ void add_logit(float &m, float &s, float x, float c)
+{
+    merge_max_sum(m, s, x, 1.0f, c);
+    if (x != x) {
+        m = m == kNegInf ? 0.0f : m;
+        s = x;
+    }
+}
+
 // One warp per live row: its tiles' partials merged in a fixed order (lane l
 // takes the tiles l, l + 32, ..., eight at a time, then the lanes merge), then
 // the log-probs of its targets, each over the other columns, and the whole
@@ -425,9 +436,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) lin_combine_kernel(LinPara
             const float xj = __shfl_sync(0xffffffffu, xt, j);
             if (__shfl_sync(0xffffffffu, static_cast<int>(counts), j) == 0)
                 continue;
-            merge_max_sum(M, S, xj, 1.0f, p.c);
+            add_logit(M, S, xj, p.c);
             if (tj != tg)
-                merge_max_sum(om, os, xj, 1.0f, p.c);
+                add_logit(om, os, xj, p.c);
         }
         float logp = 0.0f;
         if (lane < K) {

@@ -206,3 +206,29 @@ def test_gradient_of_a_scalar_tokens_lookup(dtype):
         gbce.embedding_lookup_bwd(torch.zeros(32, device=DEV, dtype=dtype)[::2], tok, 10)
     with pytest.raises(ValueError, match="shape"):
         gbce.embedding_lookup_bwd(row, tok[None], 10)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,K", [(1, 1), (2, 2), (3, 5), (16, 16)])
+def test_nan_where_every_column_is_gathered(V, K, dtype):
+    # no column is left for the tiles' sums, so the NaN is in gathered logits alone
+    nan = float("nan")
+    g = torch.Generator(device=DEV).manual_seed(V)
+    h = torch.randn((3, 8), generator=g, device=DEV).to(dtype)
+    w = torch.randn((V, 8), generator=g, device=DEV).to(dtype)
+    t = (torch.arange(K, device=DEV) % V).expand(3, K).contiguous()
+    clean, cstate = gbce.linear_selective_logsoftmax(h, w, t, with_state=True)
+    assert torch.isfinite(clean).all()
+    hn = h.clone()
+    hn[1] = nan  # a NaN row: its log-probs, its state and its gradients, nobody else's
+    logp, state = gbce.linear_selective_logsoftmax(hn, w, t, with_state=True)
+    assert torch.isnan(logp[1]).all() and torch.isnan(state[1, 1])
+    assert torch.equal(logp[[0, 2]], clean[[0, 2]]) and torch.equal(state[[0, 2]], cstate[[0, 2]])
+    dh, _ = gbce.linear_selective_logsoftmax_bwd(hn, w, t, torch.ones_like(logp), logp, state)
+    assert torch.isnan(dh[1]).all() and torch.isfinite(dh[[0, 2]]).all()
+    out = gbce.linear_ce_fwd_bwd_fused(hn, w, t[:, 0], reduction="none", want_logp=True)
+    assert torch.isnan(out.loss[1]) and torch.isnan(out.logp[1]) and torch.isfinite(out.loss[[0, 2]]).all()
+    wn = w.clone()
+    wn[V - 1] = nan  # a NaN column: every row has it among its others
+    logp, state = gbce.linear_selective_logsoftmax(h, wn, t, with_state=True)
+    assert torch.isnan(logp).all() and torch.isnan(state[:, 1]).all()
