@@ -110,6 +110,7 @@ struct LinParams {
     int64_t dh_pitch, dh_room;    // elements from row to row, and in all
     LinTile logits_tile, grads_tile;
     int64_t rows_pad, tiles, piece;
+    int64_t stats_warps;          // epilogue warps of the (first) statistics launch
 
     int32_t *dev_status;
 };
@@ -119,11 +120,13 @@ struct LinParams {
 // tile is on its way (48 rows x 4: 34.6 us; after its tiles 36.0).  More: the
 // packing before it, a warp each with the memory to itself (2000 x 4096 x 512,
 // four targets: 34.6 us; after the tiles 43.5; 7000 x 76032 x 2560, one: 1525
-// us either way, before the tiles, behind whose loads they wait, 1569).
-constexpr int64_t kLinStatsDots = 1216;
+// us either way, before the tiles, behind whose loads they wait, 1569).  The
+// warps are those of the CTAs that the launch has, few where tiles are few:
+// 300 x 128 x 4096, four targets, six CTAs: in the packing 26 us, after the
+// tiles 68; 1000 x 64 x 512, one: 12.6 and 30.6.
 inline __host__ __device__ bool lin_dots_in_pack(const LinParams &p)
 {
-    return !p.direct && (p.fused || !p.backward) && p.rows * p.k > kLinStatsDots;
+    return !p.direct && (p.fused || !p.backward) && p.rows * p.k > p.stats_warps;
 }
 
 cudaError_t lin_select(const LinParams &p, cudaStream_t s);

@@ -260,6 +260,10 @@ LinParams params(const Shape &a, const Layout &w, void *ws, bool backward, int32
     p.logits_tile = w.logits_tile;
     p.grads_tile = w.grads_tile;
     p.piece = w.piece;
+    const int64_t m = 128 * w.logits_tile.ctas, n = w.logits_tile.n;
+    const int64_t columns = p.weight_direct || w.wpack_rows > a.vocab ? a.vocab : w.wpack_rows;
+    const int64_t tiles = (a.rows + m - 1) / m * ((columns + n - 1) / n), units = gbce::kLinSms / w.logits_tile.ctas;
+    p.stats_warps = 8 * w.logits_tile.ctas * (tiles < units ? tiles : units);
     p.dev_status = dev_status;
     return p;
 }

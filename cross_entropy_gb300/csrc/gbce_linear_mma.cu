@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         // stats: this warp's share of the gathered columns' logits, the first
-        // ones by different CTAs, before its tiles (more than one a warp,
-        // which only a call in place can have: after them)
+        // ones by different CTAs, before its tiles (more than one a warp, which
+        // calls in place have where tiles are few: after them)
         const int64_t all_dots = MODE == kLinStats && q.xt != nullptr ? static_cast<int64_t>(live) * q.k : 0;
         const int64_t dot_step = static_cast<int64_t>(gridDim.x) * 8;
         int64_t dot = static_cast<int64_t>(warp - 2) * gridDim.x + blockIdx.x;

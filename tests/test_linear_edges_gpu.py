@@ -232,3 +232,36 @@ def test_nan_where_every_column_is_gathered(V, K, dtype):
     wn[V - 1] = nan  # a NaN column: every row has it among its others
     logp, state = gbce.linear_selective_logsoftmax(h, wn, t, with_state=True)
     assert torch.isnan(logp).all() and torch.isnan(state[:, 1]).all()
+
+
+def graph_of(call, n=10):
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    return graph
+
+
+def test_fewer_targets_take_no_longer_than_more():
+    # six CTAs make the logits of 300 x 128: with the 1200 gathered ones of four
+    # targets left to their warps a call took over twice as long as with 16
+    # targets, whose logits the packing makes
+    h, w, t, _ = draw(300, 128, 4096, 16, torch.bfloat16, 5)
+    four = t[:, :4].contiguous()
+    ms = [elapsed(graph_of(lambda: gbce.linear_selective_logsoftmax(h, w, x)).replay) for x in (four, t)]
+    assert ms[0] <= 1.5 * ms[1], ms
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V,D,K", [(1000, 64, 200, 1), (600, 130, 72, 2), (129, 65, 264, 4), (200, 40, 64, 6)])
+def test_many_rows_of_few_columns(rows, V, D, K, dtype):
+    h, w, t, _ = draw(rows, V, D, K, dtype, rows)
+    logp, state = gbce.linear_selective_logsoftmax(h, w, t, 0.8, with_state=True)
+    live = torch.ones(rows, dtype=torch.bool, device=DEV)
+    p, lp, comp, ez = ref.rows_of(h, w, t, 0.8, live)
+    ref.assert_within(logp, lp, ref.logp_bound(lp, comp, ez), "log p")
+    lab = t[:, 0].contiguous()
+    both = gbce.linear_ce_fwd_bwd_fused(h, w, lab, want_logp=True)
+    f = gbce.linear_ce_fwd(h, w, lab)
+    assert torch.equal(both.logp, f.logp) and torch.equal(both.loss, f.loss)
