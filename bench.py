@@ -80,24 +80,36 @@ def measured_peak():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# The translation units of the calls over given logits, which this file times.
+TIMED_SOURCES = ("gbce_api.cu", "gbce_kernels_bf16.cu", "gbce_kernels_f32.cu", "gbce_noalloc.cu",
+                 "gbce_reduce.cu", "gbce_slices.cu")
+
+
 def kernel_source_hash():
-    """Hash of the CUDA sources' code: comments and blank space left out,
-    so that a comment edit does not void counters taken on the same code
-    (a string literal holding a comment marker would be cut too: there is
-    none that matters in these sources)."""
+    """Hash of the timed calls' CUDA sources, those units and what they
+    include: other calls' files do not void counters taken on the same code,
+    nor does a comment or blank space, which are left out (a string literal
+    holding a comment marker would be cut too: there is none that matters in
+    these sources)."""
     import hashlib
     import re
 
-    h = hashlib.sha256()
     csrc = os.path.join(ROOT, "cross_entropy_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(csrc, name), encoding="utf-8") as f:
-                text = f.read()
-            text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
-            text = re.sub(r"//[^\n]*", " ", text)
-            h.update(name.encode())
-            h.update(" ".join(text.split()).encode())
+    code, todo = {}, list(TIMED_SOURCES)
+    while todo:
+        name = todo.pop()
+        if name in code or not os.path.exists(os.path.join(csrc, name)):
+            continue  # (the public header, outside this folder, has no code)
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            text = f.read()
+        text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
+        text = re.sub(r"//[^\n]*", " ", text)
+        todo += re.findall(r'#include "([^"/]+)"', text)
+        code[name] = " ".join(text.split())
+    h = hashlib.sha256()
+    for name in sorted(code):
+        h.update(name.encode())
+        h.update(code[name].encode())
     return h.hexdigest()[:16]
 
 
