@@ -14,7 +14,7 @@
 // leave partial sums, which a last kernel joins in chunk order.  So a very
 // common token is spread over many CTAs.  The zeros of rows that nobody names
 // go out beside the sort or beside the chunks (see lookup_bwd).  8192 tokens,
-// 152064 x 2560 bf16: 141 us where the bytes alone take 120; the sort (12 us
+// 152064 x 2560 bf16: 146 us where the bytes alone take 120; the sort (12 us
 // of one CTA) hides behind the zeros, the named rows (20 us) come after them.
 #include <cmath>
 #include <cstdint>
@@ -700,8 +700,8 @@ cudaError_t lookup_bwd(const void *grad, int64_t gs, int64_t rows, int64_t vocab
     a.ctas = w.ctas;
     // Few tokens for the table's rows: the zeros of all rows go out beside the
     // sort, which leaves the memory idle, and the rows that tokens name are
-    // written again (8192 tokens, 152064 x 2560 bf16: 143 us; with every zero
-    // beside the chunks, where it takes a search to know who is named, 156 us).
+    // written again (8192 tokens, 152064 x 2560 bf16: 146 us; with every zero
+    // beside the chunks, where it takes a search to know who is named, 154 us).
     // Many: few zeros are left, and the chunks' launch writes just those.
     gbce::ZeroArgs z{};
     const int64_t zero_ctas = accumulate ? 0 : (vocab + gbce::kZeroRows - 1) / gbce::kZeroRows;

@@ -26,6 +26,14 @@
 // fp32 inputs come as three bf16 planes, x = hi + mid + lo with 8 more bits
 // in each; six of the nine products (all above 2^-24 of x y) are summed,
 // smallest first, so that the large ones meet a sum that is still small.
+//
+// dz of bf16 inputs is one bf16 plane, rounded once, as dlogits of bf16 logits
+// are.  In two planes (16 bits) the gradients' error against 64 bits is that of
+// their own rounding, 1.66e-3 in norm; in one it is 1.68e-3 to 1.71e-3 where
+// many rows' dz meet (losses of 256 to 613 rows) and 2.4e-3 where one gathered
+// column leads each row's (log-probs of 2048 x 151936).  The second plane
+// doubles both gradients' products: 8192 x 152064 x 4096 23.4 -> 35.6 ms, 2048
+// x 151936 x 2560 with its forward 3.5 -> 5.4, 613 x 40001 x 1001 256 -> 326 us.
 #include <atomic>
 
 #include <cuda.h>
@@ -955,13 +963,15 @@ uint32_t box_rows(const LinParams &p, LinTile shape)
 }  // namespace
 
 // The tile shape with the least estimated time.  Measured at 8192 x 76032 x
-// 2560 (forward): 256 x 256 by pairs 2078 TFLOP/s, 128 x 256 1923, 128 x 128
-// 1349, 128 x 64 720, which is 620, 670, 450 and 420 cycles per 64-deep block;
-// the last two are bound by the operands' way from L2 (24 to 32 KB a block).
-// A launch's first and last tile add about 2000 + 10 per column that no other
-// tile hides, a launch of pairs 4 us (8000) more.  Forward times, pairs and
-// 128 x 256: 1843 x 151936 x 2560 804 and 850 us, 2048 x 32768 x 1024 112 and
-// 117, 1500 x 8192 x 1024 47 and 42, 384 x 152064 x 4096 361 and 341.
+// 2560 (forward): 256 x 256 by pairs 2002 TFLOP/s, 128 x 256 1697, 128 x 128
+// 1271, 128 x 64 683; the last two are bound by the operands' way from L2 (24
+// to 32 KB a block).  Taking pairs as 620 cycles per 64-deep block the others
+// are 731, 489 and 455.  The table's 450 and 420 are those less 8% (the choice
+// between the two is the same), its 680 and the 4 us (8000) that a launch of
+// pairs costs more are fitted to forwards of fewer rows, pairs and 128 x 256:
+// 1843 x 151936 x 2560 804 and 850 us, 2048 x 32768 x 1024 112 and 117, 1500 x
+// 8192 x 1024 47 and 42, 384 x 152064 x 4096 361 and 341.  A launch's first and
+// last tile add about 2000 + 10 per column that no other tile hides.
 LinTile choose_tile(LinWork a, LinWork b)
 {
     constexpr LinTile shapes[4] = {{2, 256}, {1, 256}, {1, 128}, {1, 64}};

@@ -193,8 +193,8 @@ def linear_selective_logsoftmax(hidden: torch.Tensor, weight: torch.Tensor, inde
 
     ``hidden`` [..., dim] and ``weight`` [vocab, dim] are both fp32 or both
     bf16; ``index`` is [..., K] (or [...] for K = 1).  fp32, shape
-    index.shape; masked-out rows are not read and give 0.  ``with_state``:
-    returns ``(logp, row_state)``, row_state [rows, 2] being what the backward
+    index.shape; masked-out rows give 0 whatever they hold (a bf16 call of up
+    to 128 rows may read them).  ``with_state``: returns ``(logp, row_state)``, row_state [rows, 2] being what the backward
     takes.
     """
     lib = load_library()
