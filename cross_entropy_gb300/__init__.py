@@ -31,6 +31,12 @@ Functions (same names as the C ABI):
   hidden states and the head's weight, without keeping the logits; and
   :func:`embedding_lookup` (and ``_bwd``), the same table's lookup (module
   ``linear``).
+* :func:`distill_fwd`, :func:`distill_bwd`, :func:`distill_fwd_bwd_fused`,
+  :func:`policy_loss` and :func:`policy_loss_fwd_bwd_fused`,
+  :func:`preference_loss` and :func:`preference_loss_fwd_bwd_fused` -- the
+  losses of post-training with their gradients: distillation from a teacher's
+  top logits, the clipped policy loss with a KL term, the preference loss of
+  paired sequences (module ``losses``).
 
 Caller-supplied output, scratch and status tensors are checked for device,
 dtype and size before any GPU work: the kernels write through their data
@@ -98,8 +104,26 @@ _SIGNATURES = {
                                 _vp, _vp]),
     "embedding_lookup_bwd": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i64,
                                     _i32, _vp, _sz, _vp, _vp]),
+    "distill_fwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i32, _vp,
+                           _vp, _vp, _vp, _sz, _vp, _vp]),
+    "distill_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i32, _vp,
+                           _vp, _vp, _vp, _i64, _vp, _vp]),
+    "distill_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp,
+                                     _i32, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp, _vp]),
+    "policy_loss": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz,
+                           _vp]),
+    "policy_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _vp, _vp,
+                                         _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz,
+                                         _vp, _vp]),
+    "gbce_preference_workspace_size": (_sz, [_i64, _i64]),
+    "preference_loss": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                               _sz, _vp, _vp]),
+    "preference_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _vp,
+                                             _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64,
+                                             _vp, _sz, _vp, _vp]),
 }
 MAX_SLICES = 64
+MAX_TEACHER_K = 256
 
 _lib = None
 
@@ -629,3 +653,10 @@ from .linear import (LinearCeForward, LinearCeFused, embedding_lookup,  # noqa: 
                      embedding_lookup_bwd, linear_ce_bwd, linear_ce_fwd,
                      linear_ce_fwd_bwd_fused, linear_selective_logsoftmax,
                      linear_selective_logsoftmax_bwd, linear_workspace_size)
+
+# ------------------------------------------------ the losses of post-training
+
+from .losses import (DistillForward, DistillFused, PolicyFused, PolicyLoss,  # noqa: E402,F401
+                     PreferenceFused, PreferenceLoss, distill_bwd, distill_fwd,
+                     distill_fwd_bwd_fused, policy_loss, policy_loss_fwd_bwd_fused,
+                     preference_loss, preference_loss_fwd_bwd_fused, preference_workspace_size)

@@ -1,0 +1,63 @@
+// Internal interface between the C-ABI layer of the post-training losses
+// (gbce_post_api.cu) and their row kernels (one translation unit per logit
+// type).  Not installed, not part of the ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gbce {
+
+constexpr int kMaxListed = 256;  // teacher entries of a row (GBCE_MAX_TEACHER_K)
+
+// Which loss a row kernel computes, and how much of it.
+enum PostOp : int { kOpDistill = 0, kOpPolicy = 1 };
+enum PostPass : int { kPassFwd = 0, kPassBwd = 1, kPassFused = 2 };
+
+// The clipped policy loss of one row (see policy_row).
+struct PolicyTerms {
+    const float *advantages;  // [rows]
+    const float *old_logp;    // [rows] or null (the current log p, held constant)
+    const float *ref_logp;    // [rows] or null (no KL term)
+    float clip_low, clip_high, kl_beta;
+};
+
+struct PostParams {
+    const void *logits;
+    int64_t rows, vocab, row_stride;  // row_stride in elements
+    float T, c;                       // temperature, log2(e) / T
+
+    // distillation: the teacher's entries
+    const int64_t *index;       // [rows, k] columns, -1: no entry
+    const float *teacher;       // [rows, k] logits
+    const float *teacher_rest;  // [rows] log-sum-exp of its other logits / T, or null
+    int64_t k;
+    const uint8_t *row_mask;  // [rows] or null
+
+    // policy loss
+    const int64_t *labels;  // [rows]
+    int64_t ignore_index;
+    PolicyTerms policy;
+
+    float *loss_rows;         // [rows] (null in the backward pass)
+    float *logp_out;          // policy: [rows] or null
+    float *rest_state_out;    // distill forward: [rows, 2] (m, s) of the unlisted columns, or null
+    const float *rest_state;  // distill backward: the forward's
+
+    void *dlogits;
+    int64_t d_stride;
+    int vec_store;          // dlogits rows share the logits rows' 16-byte phase
+    const float *grad_out;  // [rows] or [1]
+    int reduction;          // 0 none, 1 sum, 2 mean
+    const int64_t *n_items;
+    int32_t *dev_status;
+};
+
+template <typename T>
+cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stream);
+
+// n_items = number of rows with mask != 0 (rows when mask is null) into *n_out.
+cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
+                              cudaStream_t stream);
+
+}  // namespace gbce

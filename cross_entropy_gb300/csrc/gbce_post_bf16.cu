@@ -1,0 +1,6 @@
+// bf16-logit instantiations of the post-training losses' row kernels.
+#include "gbce_post.cuh"
+
+namespace gbce {
+template cudaError_t launch_post<__nv_bfloat16>(const PostParams &, int, int, cudaStream_t);
+}  // namespace gbce

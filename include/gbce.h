@@ -544,6 +544,195 @@ gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, 
                                  size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * The losses of post-training, from the same [rows, vocab] logits: z = x / T,
+ * q = softmax(z) over the row's vocab columns.  A row that is left out
+ * (row_mask[r] == 0, or label == ignore_index) has loss 0 and a zero gradient
+ * row whatever it holds; its logits are not read.  Sums over rows are taken
+ * in fp64 in a fixed order; row losses and gradients are fp32 throughout,
+ * dlogits rounded once.  workspace: gbce_workspace_size(rows, vocab, 1) bytes
+ * unless stated, 16-byte aligned, of one call at a time (a captured graph
+ * keeps its own); nothing in it needs zeroing.
+ *
+ * Source: the calls that the pages' log-probs and cross-entropies serve are
+ * the RL and preference trainers of "perf(rlhf): chunk selective_log_softmax
+ * instead of looping per token", "PR information", and the distillation
+ * losses of "Fix softmax collapse in CE, GRPO, KL/JSD and softmax",
+ * "Summary"; the formulas are written out here.
+ */
+
+/* Largest number of teacher entries per row. */
+#define GBCE_MAX_TEACHER_K 256
+
+/*
+ * Distillation from a teacher's top logits.  Row r lists the teacher's
+ * columns index[r, k] (-1: no entry, its teacher logit unread) and its logits
+ * t[r, k] there; teacher_rest[r], where given, is log sum_j e^{t_j / T} over
+ * the teacher's other columns (-inf: none).  With p the softmax over t / T of
+ * the entries and the rest,
+ *   loss_r = sum_k p_k (log p_k - log q_k) + p_rest (log p_rest - log q_rest),
+ *   q_rest = the sum of q over the columns not listed,
+ *   dz_k = q_k - p_k (listed),   dz_j = (q_rest - p_rest) q_j / q_rest (others),
+ *   dlogits = g_r dz / T,
+ * 0 log 0 = 0, g_r = grad_out[r] (NONE), grad_out[0] (SUM) or grad_out[0] /
+ * n_items (MEAN, n_items the rows not masked out).  Without teacher_rest the
+ * teacher is its listed entries renormalised and dz = q - p.  The loss is
+ * evaluated as sum p (q / p - 1 - log (q / p)), whose terms are not negative,
+ * and q - p as p expm1(log q - log p): a student close to its teacher keeps
+ * both.  A column listed twice counts once, with the sum of both
+ * probabilities.  A row without entries, or whose entries are all -inf,
+ * and without a rest has loss 0 and a zero gradient (it is still counted).  A
+ * teacher logit of -inf has p = 0; a NaN or +inf one, or such a teacher_rest,
+ * makes the row's loss and gradient NaN.  (The conventional factor T^2 of
+ * softened teachers belongs in grad_out.)
+ *
+ *   index          [rows, k] int64, 1 <= k <= GBCE_MAX_TEACHER_K
+ *   teacher_logits [rows, k] fp32
+ *   teacher_rest   [rows] fp32 or NULL
+ *   loss_out       [rows] (NONE) or [1]
+ *   rest_state_out [rows, 2] fp32 or NULL: the max m over the row's unlisted
+ *                  columns (raw logits) and sum e^{(x_j - m) / T}; distill_bwd
+ *                  takes it back (a row left out: -inf, 0)
+ *   n_items_out    [1] int64 or NULL
+ * Errors: as the cross-entropy calls; an index other than -1 outside
+ * [0, vocab) sets GBCE_DEV_BAD_INDEX and makes the row's loss and gradient
+ * NaN.
+ */
+gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                        int64_t row_stride, const int64_t *index, int64_t k,
+                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const uint8_t *row_mask, gbce_reduction reduction, float *loss_out,
+                        float *rest_state_out, int64_t *n_items_out, void *workspace,
+                        size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* The gradient from distill_fwd's rest state (same logits, teacher and T). */
+gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
+                        int64_t row_stride, const int64_t *index, int64_t k,
+                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const uint8_t *row_mask, gbce_reduction reduction, const float *grad_out,
+                        const float *rest_state, const int64_t *n_items, void *dlogits,
+                        int64_t dlogits_row_stride, int32_t *dev_status, void *stream);
+
+/* Loss and gradient in one call, each row read from HBM once. */
+gbce_status distill_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
+                                  int64_t vocab, int64_t row_stride, const int64_t *index,
+                                  int64_t k, const float *teacher_logits,
+                                  const float *teacher_rest, float temperature,
+                                  const uint8_t *row_mask, gbce_reduction reduction,
+                                  const float *grad_out, float *loss_out, int64_t *n_items_out,
+                                  void *dlogits, int64_t dlogits_row_stride, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The clipped policy loss with a KL term.  With lp = log q_y of the row's
+ * token, A its advantage, rho = e^{lp - old_logp} (1 without old_logp: the
+ * current policy is the old one) and d = ref_logp - lp:
+ *   loss_r = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *            + kl_beta (e^d - 1 - d),
+ *   dloss_r/dlp = -rho A (0 where the clip holds) - kl_beta (e^d - 1);
+ * at a clip's border itself the gradient is the unclipped one, and a row with
+ * A = 0 has no surrogate, however large its ratio.
+ *   clip_low in [0, 1], clip_high >= 0 (may be +inf: no clip),
+ *   kl_beta >= 0; ref_logp may be NULL only when kl_beta is 0.
+ */
+typedef struct gbce_policy_options {
+    float clip_low;
+    float clip_high;
+    float kl_beta;
+} gbce_policy_options;
+
+/*
+ * From log-probs (of selective_logsoftmax, linear_selective_logsoftmax or
+ * vocab_slice_combine with k = 1): loss, and dlogp_out[r] = the derivative by
+ * logp[r] times the upstream gradient, which those calls' backward takes as
+ * grad_logp.  All of logp, advantages, old_logp, ref_logp and dlogp_out are
+ * [rows] fp32; rows with row_mask[r] == 0 are not read and give 0.  dlogp_out
+ * may be NULL (then grad_out too).  workspace: gbce_workspace_size(rows, 1, 1).
+ */
+gbce_status policy_loss(const float *logp, int64_t rows, const uint8_t *row_mask,
+                        const float *advantages, const float *old_logp, const float *ref_logp,
+                        const gbce_policy_options *options, gbce_reduction reduction,
+                        const float *grad_out, float *loss_out, float *dlogp_out,
+                        int64_t *n_items_out, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/*
+ * From logits, loss and dlogits in one call (each row read from HBM once):
+ * lp = log q_{labels[r]}, rows with label == ignore_index left out; reductions
+ * as in ce_fwd; logp_out [rows] or NULL.  Errors as ce_fwd_bwd_fused.
+ */
+gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
+                                      int64_t vocab, int64_t row_stride, const int64_t *labels,
+                                      int64_t ignore_index, float temperature,
+                                      const float *advantages, const float *old_logp,
+                                      const float *ref_logp, const gbce_policy_options *options,
+                                      gbce_reduction reduction, const float *grad_out,
+                                      float *loss_out, float *logp_out, int64_t *n_items_out,
+                                      void *dlogits, int64_t dlogits_row_stride, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The preference loss of paired sequences.  The rows are the tokens of 2 pairs
+ * sequences laid end to end: sequence s has rows [seq_offsets[s],
+ * seq_offsets[s + 1]), the chosen answers first (s < pairs), then the rejected
+ * ones in the same order.  A sequence's score is
+ *   score_s = sum over its live rows of (lp_r - ref_logp_r)
+ * (ref_logp NULL: 0; `average`: divided by the number of live rows, at least
+ * 1), h_i = score_i - score_{pairs + i}, and with sigma the logistic function
+ *   GBCE_PREFERENCE_SIGMOID: loss_i = -(1 - eps) log sigma(u) - eps log sigma(-u),
+ *                            u = beta (h_i - margin), eps = label_smoothing,
+ *   GBCE_PREFERENCE_SQUARED: loss_i = (h_i - 1 / (2 beta))^2.
+ * A sequence may be empty, or all of its rows left out (score 0).  Rows before
+ * the first sequence or behind the last have no part in anything (log p 0, a
+ * zero gradient).  Scores, losses and their derivatives are taken in fp64.
+ * Reductions are over pairs (MEAN: / pairs).  Offsets are device memory:
+ * ones that decrease or leave [0, rows] set GBCE_DEV_BAD_INDEX and make the
+ * losses of the pairs they belong to NaN (an end of the whole range: of all
+ * pairs); no access leaves the rows.
+ *   beta > 0; label_smoothing in [0, 0.5); margin and label_smoothing 0 with
+ *   GBCE_PREFERENCE_SQUARED.
+ */
+typedef enum {
+    GBCE_PREFERENCE_SIGMOID = 0,
+    GBCE_PREFERENCE_SQUARED = 1
+} gbce_preference_kind;
+
+typedef struct gbce_preference_options {
+    float beta;
+    float margin;
+    float label_smoothing;
+    int32_t kind;
+    int32_t average;
+} gbce_preference_options;
+
+/* Workspace of the two preference calls, a pure function of its arguments;
+ * 0 for arguments that no call takes. */
+size_t gbce_preference_workspace_size(int64_t rows, int64_t pairs);
+
+/*
+ * From log-probs, as policy_loss.  seq_offsets [2 pairs + 1] int64, grad_out
+ * [pairs] (NONE) or [1], seq_score_out [2 pairs] or NULL, dlogp_out [rows] or
+ * NULL (then grad_out may be NULL too).
+ */
+gbce_status preference_loss(const float *logp, int64_t rows, const uint8_t *row_mask,
+                            const int64_t *seq_offsets, int64_t pairs, const float *ref_logp,
+                            const gbce_preference_options *options, gbce_reduction reduction,
+                            const float *grad_out, float *loss_out, float *dlogp_out,
+                            float *seq_score_out, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * From logits, loss and dlogits in one call.  A row's gradient needs its whole
+ * pair's scores, so the logits are read twice.
+ */
+gbce_status preference_loss_fwd_bwd_fused(
+    const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+    const int64_t *labels, int64_t ignore_index, float temperature, const int64_t *seq_offsets,
+    int64_t pairs, const float *ref_logp, const gbce_preference_options *options,
+    gbce_reduction reduction, const float *grad_out, float *loss_out, float *logp_out,
+    float *seq_score_out, void *dlogits, int64_t dlogits_row_stride, void *workspace,
+    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * ce_fwd_bwd_fused without a caller workspace and without any allocation.
  *
  * The pages have no counterpart: this exists for callers that cannot provide
