@@ -64,6 +64,7 @@ DEV_BAD_LABEL, DEV_BAD_INDEX, DEV_TIMEOUT = 1, 2, 4
 # The C entry points and their argument types, in header order.
 _vp, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _i32 = ctypes.c_int
+_f64 = ctypes.c_double
 _SIGNATURES = {
     "gbce_workspace_size": (_sz, [_i64, _i64, _i64]),
     "gbce_status_string": (ctypes.c_char_p, [_i32]),
@@ -104,21 +105,21 @@ _SIGNATURES = {
                                 _vp, _vp]),
     "embedding_lookup_bwd": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i64,
                                     _i32, _vp, _sz, _vp, _vp]),
-    "distill_fwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i32, _vp,
+    "distill_fwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f64, _vp, _i32, _vp,
                            _vp, _vp, _vp, _sz, _vp, _vp]),
-    "distill_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i32, _vp,
+    "distill_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f64, _vp, _i32, _vp,
                            _vp, _vp, _vp, _i64, _vp, _vp]),
-    "distill_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp,
+    "distill_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _f64, _vp,
                                      _i32, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp, _vp]),
     "policy_loss": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz,
                            _vp]),
-    "policy_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _vp, _vp,
+    "policy_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f64, _vp, _vp,
                                          _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz,
                                          _vp, _vp]),
     "gbce_preference_workspace_size": (_sz, [_i64, _i64]),
     "preference_loss": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                _sz, _vp, _vp]),
-    "preference_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f32, _vp,
+    "preference_loss_fwd_bwd_fused": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _f64, _vp,
                                              _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64,
                                              _vp, _sz, _vp, _vp]),
 }

@@ -1,16 +1,22 @@
 // Row kernels of the post-training losses over [rows, vocab] logits (sm_103a):
-// distillation from a teacher's top logits, and the clipped policy loss.
+// distillation from a teacher's top logits, and the losses of one token's log
+// p per row (the clipped policy loss; the sweeps around the preference loss).
 //
-// Both losses see a row as a few LISTED columns (the teacher's entries; the
-// sampled token) and the REST.  One sweep takes the online (max m, sum s) of
-// the rest with the listed columns left out; the listed logits are gathered on
-// the side, so that 1 - p never comes from a difference with 1 (the form of
-// the cross-entropy kernels).  The loss and every gradient then follow from
-// (m, s) and the listed logits:
+// All of them see a row as a few LISTED columns (the teacher's entries; the
+// row's token) and the REST.  One sweep takes the online (max m, sum s) of the
+// rest with the listed columns left out; the listed logits are gathered on the
+// side, so that 1 - p never comes from a difference with 1 (the form of the
+// cross-entropy kernels).  The loss and every gradient then follow from (m, s)
+// and the listed logits:
 //   unlisted j:  dx_j = gs 2^{(x_j - m) c - log2 s}, gs = (g / T) times the
 //                rest's whole share of the gradient,
-//   listed k:    a value of its own, stored over the sweep's by the thread
-//                that owns the column's vector.
+//   listed k:    a value of its own.
+//
+// A CTA is a ring of bulk copies (one producer thread), NCW consumer warps
+// that sweep the copied vectors, and one list warp that runs ahead: it takes
+// the next row, gathers its listed columns while the consumers still sweep the
+// row before, and finishes the loss of each swept row.  What bounds it is HBM:
+// logits once in, gradients once out; the gradient pass reads its row from L2.
 #pragma once
 
 #include "gbce_kernels.cuh"
@@ -20,34 +26,147 @@ namespace gbce {
 
 constexpr float kQuietNan = __builtin_nanf("");
 
-// ------------------------------------------------------------ listed columns
-
-// The listed columns of one row, in shared memory.  Column col of a row is
-// owned by one consumer thread (the one whose sweep reads it); the entries of
-// an owner form a chain head[owner] -> next -> ... of which a thread walks only
-// its own, so the sweep and the patches need no barrier between threads.
-template <int NC>
-struct ListBuf {
-    int32_t col[kMaxListed];  // column; -1: no entry (or a repeat of an earlier one)
-    float x[kMaxListed];      // student logit
-    float lp[kMaxListed];     // teacher's log p
-    int32_t next[kMaxListed];
-    int32_t head[NC];
-    float ml, sl;   // listed logits: max, and sum of 2^{(x - ml) c} without one holder of the max
-    float lp_rest;  // teacher's log p of the unlisted columns (-inf: none)
-    int state;      // RowState
+// A value of the problem in two floats (c = log2(e) / T, 1 / T), the first of 14
+// bits: products with it do not carry the constant's own rounding.  With c in
+// one float log p is off by up to 2e-7 in one direction in every row, and the
+// preference loss sums hundreds of them.  Both parts are positive, so that -inf
+// times either is -inf.
+struct TwoFloat {
+    float hi, lo;
 };
+
+__device__ __forceinline__ float scaled(float x, TwoFloat k) { return fmaf(x, k.hi, x * k.lo); }
+
+// -------------------------------------------------------------- the rest's sum
+
+// Online (max, sum) of the unlisted logits in the exp2 domain, as OnlineStats
+// but with exponents from both parts of c (one more packed multiply-add per
+// pair; the sweep has issue slots to spare).
+struct RestStats {
+    float m = kNegInf;
+    float nmc = __builtin_huge_valf();  // -m c, the shift added to every x c
+    float2 sa = make_float2(0.0f, 0.0f);
+    float2 sb = make_float2(0.0f, 0.0f);
+
+    __device__ __forceinline__ void raise_to(float vmax, TwoFloat c)
+    {
+        if (vmax > m) {
+            const float nmc_new = -scaled(vmax, c);
+            const float f = ex2(nmc_new - nmc);
+            const float2 ff = make_float2(f, f);
+            sa = fmul2(sa, ff);
+            sb = fmul2(sb, ff);
+            m = vmax;
+            nmc = nmc_new;
+        }
+    }
+    // (x c_lo spans many steps of nmc, so what rounding takes from it differs
+    // from logit to logit and leaves the sum alone)
+    __device__ __forceinline__ float2 terms(float2 x, TwoFloat c) const
+    {
+        const float2 hi = make_float2(c.hi, c.hi), lo = make_float2(c.lo, c.lo);
+        const float2 z = ffma2(x, hi, ffma2(x, lo, make_float2(nmc, nmc)));
+        return make_float2(ex2(z.x), ex2(z.y));
+    }
+    __device__ __forceinline__ void add(float2 p, float2 q, TwoFloat c)
+    {
+        sa = fadd2(sa, terms(p, c));
+        sb = fadd2(sb, terms(q, c));
+    }
+    __device__ __forceinline__ void add1(float x, TwoFloat c)
+    {
+        raise_to(x, c);
+        if (x != kNegInf)
+            sa.x += ex2(fmaf(x, c.hi, fmaf(x, c.lo, nmc)));
+    }
+    __device__ __forceinline__ float sum() const
+    {
+        return __fadd_rn(__fadd_rn(sa.x, sa.y), __fadd_rn(sb.x, sb.y));
+    }
+    // what every exponent carries of the shift's rounding (OnlineStats::residual)
+    __device__ __forceinline__ float residual(TwoFloat c) const
+    {
+        return isfinite(m) ? fmaf(m, c.lo, fmaf(m, c.hi, nmc)) : 0.0f;
+    }
+};
+
+// Merge the (m, s) of the 32 lanes into one, on every lane, in a fixed order.
+__device__ __forceinline__ void warp_merge_rest(float &m, float &s, TwoFloat c, float r = 0.0f)
+{
+    float M;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
+    float v = 0.0f;
+    if (M != kNegInf && m != kNegInf)
+        v = __fmul_rn(s, ex2(__fsub_rn(scaled(m - M, c), r)));
+    m = M;
+    s = warp_sum(v);
+}
+
+// ... and of two states (the slices of a row, in slice order).
+__device__ __forceinline__ void merge_rest(float &m, float &s, float m2, float s2, TwoFloat c)
+{
+    const float M = fmaxf(m, m2);
+    if (M != kNegInf)
+        s = __fadd_rn(m == kNegInf ? 0.0f : __fmul_rn(s, ex2(scaled(m - M, c))),
+                      m2 == kNegInf ? 0.0f : __fmul_rn(s2, ex2(scaled(m2 - M, c))));
+    m = M;
+}
+
+// ------------------------------------------------------------ listed columns
 
 enum RowState : int {
     kRowLive = 0,
     kRowSkip = 1,     // left out, or a teacher without mass: loss 0, gradient 0
     kRowInvalid = 2,  // NaN outputs (a bad index or label, a NaN teacher logit)
+    kRowEnd = 3,      // no more rows
 };
 
-// Which slice of a row a CTA sweeps, and which of its threads owns a column.
+// One row on its way through a CTA: what the list warp found out about it.
+struct RowSlot {
+    int64_t r;
+    int state;     // RowState
+    int streamed;  // the producer copies the row (its state may turn out otherwise)
+    float m, s;    // the rest's state: from the consumers (or, backward, for them)
+    float gt;      // upstream gradient / T
+    // distill: listed logits' max, and sum of 2^{(x - ml) c} without one holder of the
+    // max; teacher's log p of the unlisted columns (-inf: none)
+    float ml, sl, lp_rest;
+    // token: column, logit; advantage, old and reference log p
+    int y;
+    float xy, adv, old_lp, ref_lp;
+};
+
+// The listed columns of a row, in shared memory.  Column col of a row is owned
+// by one consumer thread (the one whose sweep reads it); the entries of an owner
+// form a chain head[owner] -> next -> ... of which a thread walks only its own,
+// so that neither the sweep nor the patches need a barrier between threads.
+struct ListRef {
+    int32_t *head;  // [NC]
+    int32_t *col;   // [k] column; -1: no entry (or a repeat of an earlier one)
+    int32_t *next;  // [k]
+    float *x;       // [k] student logit
+    float *lp;      // [k] teacher's log p
+    float *sum;     // [k] for repeats: log of the summed teacher terms
+};
+
+__host__ __device__ __forceinline__ int list_words(int nc, int k) { return nc + 5 * k; }
+
+__device__ __forceinline__ ListRef list_at(int32_t *words, int nc, int k)
+{
+    ListRef L;
+    L.head = words;
+    L.col = words + nc;
+    L.next = L.col + k;
+    L.x = reinterpret_cast<float *>(L.next + k);
+    L.lp = L.x + k;
+    L.sum = L.lp + k;
+    return L;
+}
+
+// Which part of a row a CTA sweeps.
 struct Slice {
     RowGeom g;
-    int64_t v0, v1;  // body vectors of the slice
+    int64_t v0, v1;    // body vectors
     bool first, last;  // the slice holds the row's scalar head / tail
 };
 
@@ -58,20 +177,11 @@ __device__ __forceinline__ int column_owner(const Slice &sl, int32_t col)
         return col;
     if (col >= sl.g.tail0)
         return static_cast<int>(col - sl.g.tail0);
-    const int64_t v = (col - sl.g.head) / VEC - sl.v0;
-    return static_cast<int>((v % NC + NC) % NC);
-}
-
-// Whether the slice sweeps this column.
-template <int VEC>
-__device__ __forceinline__ bool in_slice(const Slice &sl, int32_t col)
-{
-    if (col < sl.g.head)
-        return sl.first;
-    if (col >= sl.g.tail0)
-        return sl.last;
-    const int64_t v = (col - sl.g.head) / VEC;
-    return v >= sl.v0 && v < sl.v1;
+    // (a column of another slice has an owner too: its entry is found there by
+    // the search for repeats, and its vector lies outside [v0, v1))
+    const int32_t v = (col - static_cast<int32_t>(sl.g.head)) / VEC - static_cast<int32_t>(sl.v0);
+    const int32_t o = v % NC;
+    return o < 0 ? o + NC : o;
 }
 
 // (this lane's value, its entry) -> the warp's largest value and the lowest
@@ -89,30 +199,32 @@ __device__ __forceinline__ void warp_argmax(float &v, int32_t &k)
     }
 }
 
-// Read the teacher's entries of row r into L (one warp).  An index listed
-// twice is one column with the sum of both probabilities.  The teacher's
-// distribution is the softmax over its logits / T and teacher_rest.
+// Read the teacher's entries of row r into L (one warp).  An index listed twice
+// is one column with the sum of both probabilities.  The teacher's distribution
+// is the softmax over its logits / T and teacher_rest.
 template <typename T, int NC>
 __device__ void build_list(const PostParams &p, int64_t r, const T *row, const Slice &sl,
-                           ListBuf<NC> &L, int lane)
+                           const ListRef &L, RowSlot &slot, int lane)
 {
     constexpr int VEC = Elem<T>::kVec;
-    constexpr int kPer = kMaxListed / 32;
     const int K = static_cast<int>(p.k);
-    const float c = p.c;
+    const TwoFloat c = {p.c_hi, p.c_lo}, inv_t = {p.it_hi, p.it_lo};
+    const float inf = __builtin_huge_valf();
     const float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
-    bool bad = false, nan_t = !(rest < __builtin_huge_valf());
+    bool bad = false, nan_t = !(rest < inf);
     for (int i = lane; i < NC; i += 32)
         L.head[i] = -1;
+#pragma unroll 2
     for (int k = lane; k < K; k += 32) {
         const int64_t t = p.index[r * K + k];
+        const float raw = p.teacher[r * K + k];
         const bool here = t >= 0 && t < p.vocab;
         bad |= !here && t != -1;
         float tau = kNegInf, x = kNegInf;
         if (here) {
-            tau = p.teacher[r * K + k] / p.T;
             x = Elem<T>::load(row + t);
-            nan_t |= !(tau < __builtin_huge_valf());
+            tau = raw == kNegInf ? kNegInf : scaled(raw, inv_t);
+            nan_t |= !(raw < inf);
         }
         L.col[k] = here ? static_cast<int32_t>(t) : -1;
         L.x[k] = x;
@@ -127,23 +239,19 @@ __device__ void build_list(const PostParams &p, int64_t r, const T *row, const S
     __syncwarp();
     // repeats: equal columns share an owner, so its chain shows them all
     uint32_t repeat = 0, repeated = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int k = lane + 32 * i;
-        if (k >= K || L.col[k] < 0)
+    for (int k = lane, i = 0; k < K; k += 32, ++i) {
+        const int32_t col = L.col[k];
+        if (col < 0)
             continue;
-        for (int j = L.head[column_owner<VEC, NC>(sl, L.col[k])]; j >= 0; j = L.next[j]) {
-            if (j != k && L.col[j] == L.col[k])
+        for (int j = L.head[column_owner<VEC, NC>(sl, col)]; j >= 0; j = L.next[j])
+            if (j != k && L.col[j] == col)
                 (j < k ? repeat : repeated) |= 1u << i;
-        }
     }
-    // the first of several takes their sum, in entry order
-    float tsum[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int k = lane + 32 * i;
-        tsum[i] = k < K ? L.lp[k] : kNegInf;
-        if ((repeated >> i & 1u) && !(repeat >> i & 1u)) {
+    if (__any_sync(0xffffffffu, repeat != 0)) {
+        // the first of several takes their sum, in entry order
+        for (int k = lane, i = 0; k < K; k += 32, ++i) {
+            if (!(repeated >> i & 1u) || (repeat >> i & 1u))
+                continue;
             float m = kNegInf, s = 0.0f;
             for (int j = k; j < K; ++j)
                 if (L.col[j] == L.col[k])
@@ -151,30 +259,29 @@ __device__ void build_list(const PostParams &p, int64_t r, const T *row, const S
             for (int j = k; j < K; ++j)
                 if (L.col[j] == L.col[k] && L.lp[j] != kNegInf)
                     s += expf(L.lp[j] - m);
-            tsum[i] = s > 0.0f ? m + logf(s) : kNegInf;
+            L.sum[k] = s > 0.0f ? m + logf(s) : kNegInf;
+        }
+        __syncwarp();
+        for (int k = lane, i = 0; k < K; k += 32, ++i) {
+            if (repeat >> i & 1u)
+                L.col[k] = -1;
+            else if (repeated >> i & 1u)
+                L.lp[k] = L.sum[k];
         }
     }
-    __syncwarp();
     // maxima: the teacher's over the entries and the rest, the student's
     float mt = kNegInf, ml = kNegInf;
     int32_t at = INT32_MAX, al = INT32_MAX;
     bool nan_x = false;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int k = lane + 32 * i;
-        if (k >= K || L.col[k] < 0)
+    for (int k = lane; k < K; k += 32) {
+        if (L.col[k] < 0)
             continue;
-        if (repeat >> i & 1u) {
-            L.col[k] = -1;
-            continue;
-        }
-        L.lp[k] = tsum[i];
-        if (tsum[i] > mt) {
-            mt = tsum[i];
+        const float tau = L.lp[k], x = L.x[k];
+        if (tau > mt) {
+            mt = tau;
             at = k;
         }
-        const float x = L.x[k];
-        nan_x |= x != x || x == __builtin_huge_valf();
+        nan_x |= x != x || x == inf;
         if (x > ml) {
             ml = x;
             al = k;
@@ -188,36 +295,30 @@ __device__ void build_list(const PostParams &p, int64_t r, const T *row, const S
         at = -1;
     }
     // the sums without one holder of the maximum, whose own term is 1
-    float st = (at != -1 && rest != kNegInf) ? expf(rest - mt) : 0.0f, sx = 0.0f;
-    st = lane == 0 ? st : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int k = lane + 32 * i;
-        if (k >= K || L.col[k] < 0)
+    float st = (lane == 0 && at != -1 && rest != kNegInf) ? expf(rest - mt) : 0.0f, sx = 0.0f;
+    for (int k = lane; k < K; k += 32) {
+        if (L.col[k] < 0)
             continue;
         if (k != at && L.lp[k] != kNegInf)
             st += expf(L.lp[k] - mt);
         if (k != al && L.x[k] != kNegInf)
-            sx += ex2((L.x[k] - ml) * c);
+            sx += ex2(scaled(L.x[k] - ml, c));
     }
     st = warp_sum(st);
     sx = warp_sum(sx);
     const float lt = log1pf(st);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int k = lane + 32 * i;
-        if (k < K && L.col[k] >= 0)
+    for (int k = lane; k < K; k += 32)
+        if (L.col[k] >= 0)
             L.lp[k] = (L.lp[k] - mt) - lt;
-    }
     if (lane == 0) {
         // a row with a NaN (or +inf) listed logit has no softmax
-        L.ml = nan_x ? 0.0f : ml;
-        L.sl = nan_x ? kQuietNan : sx;
-        L.lp_rest = rest == kNegInf ? kNegInf : (rest - mt) - lt;
-        L.state = (bad || nan_t) ? kRowInvalid : (mt == kNegInf ? kRowSkip : kRowLive);
+        slot.ml = nan_x ? 0.0f : ml;
+        slot.sl = nan_x ? kQuietNan : sx;
+        slot.lp_rest = rest == kNegInf ? kNegInf : (rest - mt) - lt;
+        slot.state = (bad || nan_t) ? kRowInvalid : (mt == kNegInf ? kRowSkip : kRowLive);
+        if (bad && sl.first)
+            report(p.dev_status, GBCE_DEV_BAD_INDEX);
     }
-    if (bad && lane == 0 && sl.first)
-        report(p.dev_status, GBCE_DEV_BAD_INDEX);
 }
 
 // ------------------------------------------------------- distillation of a row
@@ -228,23 +329,39 @@ struct StudentRow {
     float M, log_s, log_rest;
 };
 
-__device__ __forceinline__ StudentRow student_row(float m, float s, float ml, float sl, float c,
-                                                  float T)
+__device__ __forceinline__ StudentRow student_row(float m, float s, float ml, float sl, TwoFloat c,
+                                                  TwoFloat inv_t)
 {
     StudentRow q;
     q.M = fmaxf(m, ml);
-    const float rest = m == kNegInf ? s : s * ex2((m - q.M) * c);
-    const float listed = ml == kNegInf ? 0.0f : (1.0f + sl) * ex2((ml - q.M) * c);
+    const float rest = m == kNegInf ? s : s * ex2(scaled(m - q.M, c));
+    const float listed = ml == kNegInf ? 0.0f : (1.0f + sl) * ex2(scaled(ml - q.M, c));
     // log of the whole sum: past its own largest term where that is listed
     q.log_s = ml >= m ? log1pf(sl + rest) : logf(rest + listed);
     // log of the rest's share, by whichever of the two does not cancel
-    q.log_rest = rest >= listed ? -log1pf(listed / rest)
-                                : (s > 0.0f ? (logf(s) + (m - q.M) / T) - q.log_s : kNegInf);
-    if (q.M == kNegInf || listed != listed || rest != rest) {
-        q.log_s = kQuietNan;
-        q.log_rest = kQuietNan;
-    }
+    q.log_rest = rest >= listed
+                     ? -log1pf(listed / rest)
+                     : (s > 0.0f ? (logf(s) + scaled(m - q.M, inv_t)) - q.log_s : kNegInf);
+    if (q.M == kNegInf || listed != listed || rest != rest)
+        q.log_s = q.log_rest = kQuietNan;
     return q;
+}
+
+__device__ __forceinline__ float student_logp(const StudentRow &q, float x, TwoFloat inv_t)
+{
+    return scaled(x - q.M, inv_t) - q.log_s;
+}
+
+// (e^u - 1 - u) / u^2 for |u| < 1/4, by its series: the next term is below
+// 2^-24 of the sum.
+__device__ __forceinline__ float phi_series(float u)
+{
+    float h = 1.0f / 5040.0f;
+    h = fmaf(h, u, 1.0f / 720.0f);
+    h = fmaf(h, u, 1.0f / 120.0f);
+    h = fmaf(h, u, 1.0f / 24.0f);
+    h = fmaf(h, u, 1.0f / 6.0f);
+    return fmaf(h, u, 0.5f);
 }
 
 // p phi(u), u = log q - log p, phi(u) = e^u - 1 - u >= 0: one term of
@@ -257,16 +374,8 @@ __device__ __forceinline__ float kl_term(float lp, float lq)
     if (lp == kNegInf)
         return q;
     const float p = expf(lp), u = lq - lp;
-    if (fabsf(u) < 0.25f) {
-        // u^2 / 2 + u^3 / 6 + ...: the next term is below 2^-24 of the sum
-        float h = 1.0f / 5040.0f;
-        h = fmaf(h, u, 1.0f / 720.0f);
-        h = fmaf(h, u, 1.0f / 120.0f);
-        h = fmaf(h, u, 1.0f / 24.0f);
-        h = fmaf(h, u, 1.0f / 6.0f);
-        h = fmaf(h, u, 0.5f);
-        return p * u * u * h;
-    }
+    if (fabsf(u) < 0.25f)
+        return p * u * u * phi_series(u);
     if (u > 1.0f)
         return (q - p) - p * u;
     return p > 0.0f ? p * (expm1f(u) - u) : 0.0f;
@@ -281,19 +390,36 @@ __device__ __forceinline__ float share_gap(float lp, float lq)
     return fabsf(u) < 1.0f ? expf(lp) * expm1f(u) : expf(lq) - expf(lp);
 }
 
-// ---------------------------------------------------------- policy of a row
+// ----------------------------------------------------- one token's log p
+
+// The SFU's 2^x is low by 8e-8 of its value on the average of a row's exponents
+// (measured: log p of 2048 rows of 152064 logits, T 0.7 to 1.3, lies 8.1e-8 to
+// 1.1e-7 above fp64's), and so is the rest's sum.
+constexpr float kEx2Low = 8e-8f;
+
+// finalize_logp with 1 / T in two floats.
+__device__ __forceinline__ float token_logp(float m, float s, float xy, TwoFloat inv_t)
+{
+    if (!(s > 0.0f))
+        return (s == 0.0f && xy == xy) ? 0.0f : kQuietNan;
+    // the sum's rounding error joins kEx2Low, or a term below half its step would
+    // vanish in every row
+    const float ls = logf(s), d = scaled(m - xy, inv_t), a = __fadd_rn(ls, d);
+    const float b = __fsub_rn(a, ls);
+    const float err = __fadd_rn(__fsub_rn(ls, __fsub_rn(a, b)), __fsub_rn(d, b));
+    return -softplus(isfinite(a) ? a + (err + kEx2Low) : a);
+}
 
 // The clipped policy loss of one row from its log p, and its derivative:
 //   rho = e^{lp - old},  loss = -min(rho A, clip(rho) A) + beta (e^d - 1 - d),
 //   d = ref - lp;  d loss / d lp = -rho A [not clipped] - beta (e^d - 1).
 // At a clip's border the unclipped side is taken.
-__device__ __forceinline__ void policy_row(const PolicyTerms &t, int64_t r, float lp, float &loss,
-                                           float &dlp)
+__device__ __forceinline__ void policy_row(const PolicyTerms &t, float A, float old_lp,
+                                           float ref_lp, float lp, float &loss, float &dlp)
 {
-    const float A = t.advantages[r];
     loss = dlp = lp != lp ? kQuietNan : 0.0f;
     if (A != 0.0f && lp == lp) {  // (no advantage: no surrogate, however large the ratio)
-        const float rho = t.old_logp != nullptr ? expf(lp - t.old_logp[r]) : 1.0f;
+        const float rho = t.old_logp != nullptr ? expf(lp - old_lp) : 1.0f;
         const float edge = A > 0.0f ? 1.0f + t.clip_high : 1.0f - t.clip_low;
         const bool held = A > 0.0f ? rho > edge : rho < edge;
         loss = -A * (held ? edge : rho);
@@ -302,17 +428,8 @@ __device__ __forceinline__ void policy_row(const PolicyTerms &t, int64_t r, floa
             loss = dlp = kQuietNan;
     }
     if (t.ref_logp != nullptr && t.kl_beta != 0.0f) {
-        const float d = t.ref_logp[r] - lp, e = expm1f(d);
-        float k3 = e - d;
-        if (fabsf(d) < 0.25f) {
-            float h = 1.0f / 5040.0f;
-            h = fmaf(h, d, 1.0f / 720.0f);
-            h = fmaf(h, d, 1.0f / 120.0f);
-            h = fmaf(h, d, 1.0f / 24.0f);
-            h = fmaf(h, d, 1.0f / 6.0f);
-            h = fmaf(h, d, 0.5f);
-            k3 = d * d * h;
-        }
+        const float d = ref_lp - lp, e = expm1f(d);
+        const float k3 = fabsf(d) < 0.25f ? d * d * phi_series(d) : e - d;
         loss = fmaf(t.kl_beta, k3, loss);
         dlp = fmaf(-t.kl_beta, e, dlp);
     }
@@ -339,183 +456,806 @@ __device__ __forceinline__ GradConsts rest_consts(float m, float s, float c, flo
     return k;
 }
 
-__device__ __forceinline__ float post_upstream(const PostParams &p, int64_t r)
+__device__ __forceinline__ float post_upstream(const PostParams &p, int64_t r, int64_t n)
 {
     if (p.reduction == 0)
         return p.grad_out[r];
     if (p.reduction == 1)
         return p.grad_out[0];
-    const int64_t n = *p.n_items;
     return n > 0 ? p.grad_out[0] / static_cast<float>(n) : 0.0f;
 }
 
 // ------------------------------------------------------------ the row kernel
 
-constexpr int kPostWarps = 8;
+// Consumer warps, ring, and how many rows may be between the list warp and the
+// consumers, of the three CTA shapes (see launch_post).
+template <int SHAPE> struct PostShape;
+template <> struct PostShape<kShapeLong> {
+    static constexpr int kWarps = 24, kChunk = 49152, kStages = 4, kSlots = 2, kCtasPerSm = 1;
+};
+template <> struct PostShape<kShapeMid> {
+    static constexpr int kWarps = 8, kChunk = 16384, kStages = 4, kSlots = 2, kCtasPerSm = 3;
+};
+template <> struct PostShape<kShapeShort> {
+    static constexpr int kWarps = 4, kChunk = 8192, kStages = 2, kSlots = 2, kCtasPerSm = 5;
+};
 
-// One CTA per row: warp 0 gathers the listed columns, every thread sweeps its
-// vectors of the row for (m, s), and sweeps them again for the gradient.
-template <typename T, int OP, int PASS>
-__global__ void __launch_bounds__(kPostWarps * 32) post_row_kernel(const PostParams p)
+template <int SHAPE> constexpr int post_threads() { return (PostShape<SHAPE>::kWarps + 2) * 32; }
+
+template <int SHAPE> constexpr int post_smem(int op, int64_t k)
+{
+    using S = PostShape<SHAPE>;
+    return S::kStages * (S::kChunk + kRingAlign) + kRingAlign +
+           (op == kOpDistill
+                ? S::kSlots * 4 * list_words(S::kWarps * 32, static_cast<int>(k))
+                : 0);
+}
+
+// Fold one vector into a thread's rest state.
+__device__ __forceinline__ void rest_add(RestStats &st, const uint4 &a, TwoFloat c,
+                                         const __nv_bfloat16 *)
+{
+    st.add(bf16x2_to_float2(a.x), bf16x2_to_float2(a.y), c);
+    st.add(bf16x2_to_float2(a.z), bf16x2_to_float2(a.w), c);
+}
+
+__device__ __forceinline__ void rest_add(RestStats &st, const uint4 &a, TwoFloat c, const float *)
+{
+    st.add(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)),
+           make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), c);
+}
+
+// Orders this thread's writes to shared memory before the bulk copies that
+// refill it (issued by another thread once this one has released the stage).
+__device__ __forceinline__ void fence_before_refill()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ float neg_inf_as(float) { return kNegInf; }
+__device__ __forceinline__ __nv_bfloat16 neg_inf_as(__nv_bfloat16)
+{
+    return __ushort_as_bfloat16(0xff80);
+}
+
+// The VEC elements that begin `sh` elements into the pair (a, b).
+template <typename T>
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int sh)
+{
+    const int words = sizeof(T) == 2 ? sh >> 1 : sh;
+    if (words & 1) {
+        a = make_uint4(a.y, a.z, a.w, b.x);
+        b = make_uint4(b.y, b.z, b.w, b.w);
+    }
+    if (words & 2) {
+        a = make_uint4(a.z, a.w, b.x, b.y);
+        b.x = b.z;
+    }
+    if (sizeof(T) == 2 && (sh & 1))
+        a = make_uint4(__funnelshift_r(a.x, a.y, 16), __funnelshift_r(a.y, a.z, 16),
+                       __funnelshift_r(a.z, a.w, 16), __funnelshift_r(a.w, b.x, 16));
+    return a;
+}
+
+// How a gradient row is stored: 16-byte vectors from element `begin` on, whose
+// elements begin `sh` elements into a logits vector.  sh = 0: the two rows share
+// their phase, and vector v of the one is vector v of the other.  Otherwise
+// vector v is made of the logits vectors v and v + 1, and the elements before
+// the first and behind the last such pair are stored one by one.
+struct StoreGeom {
+    int sh;
+    int64_t begin, vecs, end;  // scalars [0, begin) and [end, V)
+};
+
+template <typename T>
+__device__ __forceinline__ StoreGeom store_geom(const T *drow, const RowGeom &g, int64_t V)
+{
+    constexpr int VEC = Elem<T>::kVec;
+    const int dhead = static_cast<int>(
+        ((16u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(drow) & 15u)) & 15u) / sizeof(T));
+    StoreGeom d;
+    d.sh = static_cast<int>(dhead - g.head) & (VEC - 1);
+    if (d.sh == 0) {
+        d.begin = g.head;
+        d.vecs = g.nvec;
+    } else {
+        d.vecs = g.nvec > 1 ? g.nvec - 1 : 0;
+        d.begin = d.vecs > 0 ? g.head + d.sh : V;
+    }
+    d.end = d.begin + d.vecs * VEC;
+    return d;
+}
+
+template <typename T, int OP, int PASS, int SHAPE>
+__global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtasPerSm)
+    post_kernel(const PostParams p)
 {
     using E = Elem<T>;
+    using Shape = PostShape<SHAPE>;
     constexpr int VEC = E::kVec;
-    constexpr int NCW = kPostWarps, NC = NCW * 32;
-    __shared__ ListBuf<NC> L;
-    __shared__ float red_m[NCW], red_s[NCW];
+    constexpr int NCW = Shape::kWarps, NC = NCW * 32;
+    constexpr int S = Shape::kStages, CHUNK = Shape::kChunk, CV = CHUNK / 16;
+    constexpr int PITCH = CHUNK + kRingAlign;  // of the stages: a chunk and one vector more
+    constexpr int PER_THREAD = CV / NC, Q = Shape::kSlots;
+    static_assert(CV % NC == 0 && PER_THREAD % 2 == 0, "a chunk splits into pairs of vectors");
+    constexpr bool kStats = PASS != kPassBwd, kGrad = PASS != kPassFwd;
+    constexpr int kPasses = (kStats ? 1 : 0) + (kGrad ? 1 : 0);
+    constexpr bool kList = OP == kOpDistill;
+
+    extern __shared__ __align__(128) uint8_t dyn_smem[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(dyn_smem) + (kRingAlign - 1)) & ~uintptr_t(kRingAlign - 1));
+    int32_t *lists = reinterpret_cast<int32_t *>(ring + S * PITCH);
+    __shared__ uint64_t full_bar[S], empty_bar[S];
+    // rows: known (to the producer), list built (to the consumers), statistics
+    // done (to the list warp), slot free again
+    __shared__ uint64_t row_bar[Q], list_bar[Q], stat_bar[Q], free_bar[Q];
+    __shared__ RowSlot slots[Q];
+    // per-warp partials, double-buffered by row (a warp may be a row ahead)
+    __shared__ float red_m[2][NCW], red_s[2][NCW];
+    __shared__ uint64_t xbar;  // cluster of CTAs per row: every slice's partial
+    __shared__ __align__(16) float4 xchg[kMaxClusterCtas];
+
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t r = blockIdx.x, V = p.vocab;
-    const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
-    T *drow = PASS == kPassFwd ? nullptr : static_cast<T *>(p.dlogits) + r * p.d_stride;
-    const float c = p.c;
+    const int64_t V = p.vocab;
+    const TwoFloat c = {p.c_hi, p.c_lo}, inv_t = {p.it_hi, p.it_lo};
+    const int C = p.splits;
+    const int64_t cluster = C > 1 ? blockIdx.x / C : blockIdx.x;
+    const int split = C > 1 ? static_cast<int>(blockIdx.x - cluster * C) : 0;
+    const int64_t clusters = gridDim.x / C;
 
-    int state = kRowLive;
-    int32_t y = -1;
-    if (OP == kOpPolicy) {
-        const int64_t lab = p.labels[r];
-        state = lab == p.ignore_index ? kRowSkip : (lab < 0 || lab >= V ? kRowInvalid : kRowLive);
-        y = state == kRowLive ? static_cast<int32_t>(lab) : -1;
-        if (state == kRowInvalid && tid == 0)
-            report(p.dev_status, GBCE_DEV_BAD_LABEL);
-    } else if (p.row_mask != nullptr && p.row_mask[r] == 0) {
-        state = kRowSkip;
-    }
-    const RowGeom g = row_geom<T>(row, V);
-    const Slice sl = {g, 0, g.nvec, true, true};
-    if (OP == kOpDistill && state == kRowLive) {
-        if (warp == 0)
-            build_list<T, NC>(p, r, row, sl, L, lane);
-        __syncthreads();
-        state = L.state;
-    }
-    if (state != kRowLive) {
-        const float fill = state == kRowSkip ? 0.0f : kQuietNan;
-        if (tid == 0) {
-            if (PASS != kPassBwd)
-                p.loss_rows[r] = fill;
-            if (OP == kOpPolicy && p.logp_out != nullptr)
-                p.logp_out[r] = fill;
-            if (OP == kOpDistill && p.rest_state_out != nullptr) {
-                p.rest_state_out[2 * r] = kNegInf;
-                p.rest_state_out[2 * r + 1] = 0.0f;
-            }
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full_bar[i], 1);
+            mbar_init(&empty_bar[i], NCW);
         }
-        if (PASS != kPassFwd)
-            fill_row_slice<T>(drow, V, 0, 1, fill);
-        return;
+        for (int i = 0; i < Q; ++i) {
+            mbar_init(&row_bar[i], 1);
+            mbar_init(&list_bar[i], 1);
+            mbar_init(&stat_bar[i], 1);
+            mbar_init(&free_bar[i], NCW + 1);
+        }
+        mbar_init(&xbar, 1);
+        fence_barrier_init();
     }
+    __syncthreads();
+    if (C > 1)
+        cluster_arrive_relaxed();
+    grid_dependency_wait();
 
-    // whether this thread's column col is listed
-    const auto listed = [&](int32_t col) {
-        if (OP == kOpPolicy)
-            return col == y;
-        for (int j = L.head[tid]; j >= 0; j = L.next[j])
-            if (L.col[j] == col)
-                return true;
-        return false;
+    const auto slice_of = [&](const T *row) {
+        Slice sl;
+        sl.g = row_geom<T>(row, V);
+        sl.v0 = C == 1 ? 0 : sl.g.nvec * split / C;
+        sl.v1 = C == 1 ? sl.g.nvec : sl.g.nvec * (split + 1) / C;
+        sl.first = split == 0;
+        sl.last = split == C - 1;
+        return sl;
     };
-    float m, s;
-    if (PASS == kPassBwd) {
-        m = p.rest_state[2 * r];
-        s = p.rest_state[2 * r + 1];
-    } else {
-        OnlineStats<false> st;
-        for_each_own_column<T>(row, g, V, tid, NC, [&](float x, int64_t col) {
-            st.add1(listed(static_cast<int32_t>(col)) ? kNegInf : x, c);
-        });
-        float h = 0.0f;
-        m = st.m;
-        s = st.sum();
-        if (s != s)  // (a thread that met only NaN has no max: its NaN must still count)
-            m = fmaxf(m, 0.0f);
-        warp_merge_state<kHNone>(m, s, h, c, st.residual(c));
-        if (lane == 0) {
-            red_m[warp] = m;
-            red_s[warp] = s;
-        }
-        __syncthreads();
-        m = lane < NCW ? red_m[lane] : kNegInf;
-        s = lane < NCW ? red_s[lane] : 0.0f;
-        warp_merge_state<kHNone>(m, s, h, c);
-    }
 
-    float gs = 0.0f, gt = 0.0f;  // the rest's share of the gradient; g / T
-    float dy = 0.0f;             // policy: the gradient at the label
-    StudentRow q;
-    if (OP == kOpPolicy) {
-        const float lp = finalize_logp(m, s, E::load(row + y), p.T);
-        float loss, dlp;
-        policy_row(p.policy, r, lp, loss, dlp);
-        if (tid == 0) {
-            p.loss_rows[r] = loss;
-            if (p.logp_out != nullptr)
-                p.logp_out[r] = lp;
-        }
-        dy = -(post_upstream(p, r) / p.T * dlp) * expm1f(lp);
-        gs = -dy;
-    } else {
-        q = student_row(m, s, L.ml, L.sl, c, p.T);
-        if (PASS != kPassBwd && warp == 0) {
-            float kl = lane == 0 ? kl_term(L.lp_rest, q.log_rest) : 0.0f;
-            for (int k = lane; k < p.k; k += 32)
-                if (L.col[k] >= 0)
-                    kl += kl_term(L.lp[k], (L.x[k] - q.M) / p.T - q.log_s);
-            kl = warp_sum(kl);
-            if (lane == 0) {
-                p.loss_rows[r] = kl;
-                if (p.rest_state_out != nullptr) {
-                    p.rest_state_out[2 * r] = m;
-                    p.rest_state_out[2 * r + 1] = s;
+    // ------------------------------------------------------------ list warp
+    if (warp == NCW + 1) {
+        bool ok = true;
+        // a swept row's loss and statistics (by the first slice's CTA)
+        const auto finish = [&](uint32_t i) {
+            const int q = i % Q;
+            const RowSlot &w = slots[q];
+            if (!kStats || w.state == kRowEnd)
+                return;
+            if (w.state != kRowLive) {
+                if (lane == 0 && split == 0) {
+                    const float fill = w.state == kRowSkip ? 0.0f : kQuietNan;
+                    if (p.loss_rows != nullptr)
+                        p.loss_rows[w.r] = fill;
+                    if (p.logp_out != nullptr)
+                        p.logp_out[w.r] = fill;
+                    if (p.rest_state_out != nullptr) {
+                        p.rest_state_out[2 * w.r] = kNegInf;
+                        p.rest_state_out[2 * w.r + 1] = 0.0f;
+                    }
+                }
+                return;
+            }
+            if (!mbar_wait(&stat_bar[q], (i / Q) & 1)) {
+                ok = false;
+                return;
+            }
+            if (split != 0)
+                return;
+            const float m = w.m, s = w.s;
+            if (p.rest_state_out != nullptr && lane == 0) {
+                p.rest_state_out[2 * w.r] = m;
+                p.rest_state_out[2 * w.r + 1] = s;
+            }
+            if (kList) {
+                const ListRef L = list_at(lists + q * list_words(NC, p.k), NC, p.k);
+                const StudentRow st = student_row(m, s, w.ml, w.sl, c, inv_t);
+                float kl = lane == 0 ? kl_term(w.lp_rest, st.log_rest) : 0.0f;
+                for (int k = lane; k < p.k; k += 32)
+                    if (L.col[k] >= 0)
+                        kl += kl_term(L.lp[k], student_logp(st, L.x[k], inv_t));
+                kl = warp_sum(kl);
+                if (lane == 0)
+                    p.loss_rows[w.r] = kl;
+            } else if (lane == 0) {
+                const float lp = token_logp(m, s, w.xy, inv_t);
+                if (p.logp_out != nullptr)
+                    p.logp_out[w.r] = lp;
+                if (OP == kOpPolicy) {
+                    float loss, dlp;
+                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
+                    p.loss_rows[w.r] = loss;
                 }
             }
-        }
-        if (PASS != kPassFwd) {
-            gt = post_upstream(p, r) / p.T;
-            gs = gt * share_gap(L.lp_rest, q.log_rest);
-        }
-    }
-    if (PASS == kPassFwd)
-        return;
-
-    const GradConsts gk = rest_consts(m, s, c, gs);
-    for (int64_t e = tid; e < g.head; e += NC)
-        E::store(drow + e, grad_scalar(E::load(row + e), gk));
-    for (int64_t e = g.tail0 + tid; e < V; e += NC)
-        E::store(drow + e, grad_scalar(E::load(row + e), gk));
-    const uint4 *body = reinterpret_cast<const uint4 *>(row + g.head);
-    constexpr int32_t kNoLabel = 0x7fffffff;
-    for (int64_t v = tid; v < g.nvec; v += NC) {
-        const uint4 raw = body[v];
-        T *d = drow + g.head + v * VEC;
-        if (p.vec_store) {
-            st_cs_v4(d, GradVec<T>::run(raw, kNoLabel, gk));
-        } else {
-            float f[VEC];
-            GradVec<T>::run_unpacked(raw, kNoLabel, gk, f);
+        };
+        const int64_t lo = p.row_range != nullptr ? p.row_range[0] : 0;
+        const int64_t hi = p.row_range != nullptr ? p.row_range[p.row_range_end] : p.rows;
+        int64_t t = cluster;
+        int64_t n_items = 0;
+        uint32_t i = 0;
+        for (;; ++i) {
+            const int q = i % Q;
+            if (i >= Q) {
+                finish(i - Q);
+                if (!ok || !mbar_wait(&free_bar[q], (i / Q - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+            }
+            RowSlot &w = slots[q];
+            __syncwarp();
+            const bool end = t >= p.rows;
+            const int64_t r = p.reverse ? p.rows - 1 - t : t;
+            int state = end ? kRowEnd : kRowLive;
+            int64_t lab = 0;
+            if (!end) {
+                if (kList) {
+                    if (p.row_mask != nullptr && p.row_mask[r] == 0)
+                        state = kRowSkip;
+                } else {
+                    lab = p.labels[r];
+                    if (lab == p.ignore_index || r < lo || r >= hi)
+                        state = kRowSkip;
+                    else if (lab < 0 || lab >= V)
+                        state = kRowInvalid;
+                }
+            }
+            if (lane == 0) {
+                w.r = r;
+                w.state = state;
+                w.streamed = state == kRowLive;
+                mbar_arrive(&row_bar[q]);
+            }
+            if (i == 0 && kGrad && p.n_items != nullptr && p.reduction == GBCE_MEAN)
+                n_items = *p.n_items;
+            if (i == 0 && p.n_items_out != nullptr &&
+                (blockIdx.x == 0 || (kGrad && p.reduction == GBCE_MEAN))) {
+                // one row per CTA at most: every CTA counts the rows that are kept
+                for (int64_t j = lane; j < p.rows; j += 32)
+                    n_items += kList ? (p.row_mask == nullptr || p.row_mask[j] != 0)
+                                     : p.labels[j] != p.ignore_index;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                E::store(d + e, f[e]);
+                for (int off = 16; off > 0; off >>= 1)
+                    n_items += __shfl_xor_sync(0xffffffffu, n_items, off);
+                if (blockIdx.x == 0 && lane == 0)
+                    *p.n_items_out = n_items;
+            }
+            if (i == 0 && p.zero_out != nullptr && blockIdx.x == 0 && lane == 0)
+                *p.zero_out = 0;
+            // the next row: a ticket where CTAs take more than one row each
+            int64_t next = t + clusters;
+            if (!end && p.ticket != nullptr) {
+                int32_t n = 0;
+                if (lane == 0)
+                    n = atomicAdd(p.ticket, 1);
+                next = clusters + __shfl_sync(0xffffffffu, n, 0);
+            }
+            if (state == kRowLive) {
+                const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
+                if (lane == 0) {
+                    if (kGrad)
+                        w.gt = scaled(post_upstream(p, r, n_items), inv_t);
+                    if (!kStats) {
+                        w.m = p.rest_state[2 * r];
+                        w.s = p.rest_state[2 * r + 1];
+                    }
+                    if (!kList) {
+                        w.y = static_cast<int>(lab);
+                        w.xy = E::load(row + lab);
+                    }
+                    if (OP == kOpPolicy) {
+                        w.adv = p.policy.advantages[r];
+                        w.old_lp = p.policy.old_logp != nullptr ? p.policy.old_logp[r] : 0.0f;
+                        w.ref_lp = p.policy.ref_logp != nullptr ? p.policy.ref_logp[r] : 0.0f;
+                    }
+                }
+                if (kList) {
+                    const ListRef L = list_at(lists + q * list_words(NC, p.k), NC, p.k);
+                    build_list<T, NC>(p, r, row, slice_of(row), L, w, lane);
+                }
+            } else if (state == kRowInvalid && lane == 0 && split == 0) {
+                report(p.dev_status, GBCE_DEV_BAD_LABEL);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&list_bar[q]);
+            if (end)
+                break;
+            t = next;
         }
+        if (ok)
+            for (uint32_t j = i > Q - 1 ? i - (Q - 1) : 0; j < i && ok; ++j)
+                finish(j);
+        if (!ok && lane == 0)
+            report(p.dev_status, GBCE_DEV_TIMEOUT);
+        return;
     }
-    // the listed columns, over this thread's own stores
-    if (OP == kOpPolicy) {
-        if (column_owner<VEC, NC>(sl, y) == tid)
-            E::store(drow + y, dy);
-    } else {
-        for (int j = L.head[tid]; j >= 0; j = L.next[j])
-            if (L.col[j] >= 0)
-                E::store(drow + L.col[j],
-                         gt * share_gap(L.lp[j], (L.x[j] - q.M) / p.T - q.log_s));
+
+    // ------------------------------------------------------------ producer
+    if (warp == NCW) {
+        if (lane != 0)
+            return;
+        const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+        uint32_t seq = 0, pos = 0, lap = 0;  // chunks issued; ring position and its lap
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+            const int q = i % Q;
+            if (!mbar_wait(&row_bar[q], (i / Q) & 1)) {
+                ok = false;
+                break;
+            }
+            const int64_t r = slots[q].r;
+            const bool streamed = slots[q].streamed != 0;
+            // (the state that the list warp may change later is not read here)
+            const bool end = r >= p.rows || r < 0;
+            mbar_arrive(&free_bar[q]);
+            if (end)
+                break;
+            if (!streamed)
+                continue;
+            const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
+            const Slice sl = slice_of(row);
+            const char *body = reinterpret_cast<const char *>(row + sl.g.head) + sl.v0 * 16;
+            const int64_t total = (sl.v1 - sl.v0) * 16;
+            // gradient rows of another phase need the vector behind each chunk too
+            int64_t more = 0;
+            if (kGrad &&
+                store_geom<T>(static_cast<const T *>(p.dlogits) + r * p.d_stride, sl.g, V).sh != 0)
+                more = 16;
+            const int64_t total_grad = more != 0 && sl.v1 < sl.g.nvec ? total + 16 : total;
+            for (int pass = 0; pass < kPasses && ok; ++pass)
+                for (int64_t off = 0; off < total; off += CHUNK, ++seq) {
+                    if (lap > 0 && !mbar_wait(&empty_bar[pos], (lap - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool grad = kGrad && pass == kPasses - 1;
+                    const int64_t left = (grad ? total_grad : total) - off;
+                    const int64_t most = CHUNK + (grad ? more : 0);
+                    const uint32_t bytes = static_cast<uint32_t>(left < most ? left : most);
+                    mbar_arrive_expect_tx(&full_bar[pos], bytes);
+                    bulk_load(ring + pos * PITCH, body + off, bytes, &full_bar[pos],
+                              pass + 1 < kPasses || p.keep_rows ? keep : stream);
+                    if (++pos == S) {
+                        pos = 0;
+                        ++lap;
+                    }
+                }
+        }
+        if (!ok)
+            report(p.dev_status, GBCE_DEV_TIMEOUT);
+        // no copy may still be in flight when the CTA exits
+        for (uint32_t j = (seq > S ? seq - S : 0); j < seq; ++j)
+            mbar_wait(&full_bar[j % S], (j / S) & 1);
+        return;
+    }
+
+    // ------------------------------------------------------------ consumers
+    uint32_t pos = 0, lap = 0;
+    bool alive = true;
+    for (uint32_t i = 0;; ++i) {
+        const int q = i % Q;
+        if (!mbar_wait(&list_bar[q], (i / Q) & 1)) {
+            report(p.dev_status, GBCE_DEV_TIMEOUT);
+            break;
+        }
+        RowSlot &w = slots[q];
+        const int state = w.state;
+        if (state == kRowEnd)
+            break;
+        const int64_t r = w.r;
+        const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
+        T *drow = kGrad ? static_cast<T *>(p.dlogits) + r * p.d_stride : nullptr;
+        const Slice sl = slice_of(row);
+        const int32_t nvec = static_cast<int32_t>(sl.v1 - sl.v0);
+        const int32_t nchunks = (nvec + CV - 1) / CV;
+        const int32_t head = static_cast<int32_t>(sl.g.head);
+        const auto wait_chunk = [&] {
+            if (alive && !mbar_wait(&full_bar[pos], lap & 1)) {
+                alive = false;
+                report(p.dev_status, GBCE_DEV_TIMEOUT);
+            }
+            return reinterpret_cast<uint4 *>(ring + pos * PITCH);
+        };
+        const auto done_chunk = [&] {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty_bar[pos]);
+            if (++pos == S) {
+                pos = 0;
+                ++lap;
+            }
+        };
+        if (state != kRowLive) {
+            if (w.streamed)  // (found out after its copies began)
+                for (int32_t j = 0; j < nchunks * kPasses; ++j) {
+                    wait_chunk();
+                    done_chunk();
+                }
+            if (kStats && tid == 0)
+                mbar_arrive(&stat_bar[q]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&free_bar[q]);
+            if (kGrad) {
+                const float fill = state == kRowSkip ? 0.0f : kQuietNan;
+                const RowGeom gd = row_geom<T>(drow, V);
+                const int64_t d0 = gd.nvec * split / C, d1 = gd.nvec * (split + 1) / C;
+                float f[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    f[e] = fill;
+                const uint4 pat = E::pack(f);
+                uint4 *body = reinterpret_cast<uint4 *>(drow + gd.head);
+                for (int64_t v = d0 + tid; v < d1; v += NC)
+                    st_cs_v4(body + v, pat);
+                if (sl.first && tid < gd.head)
+                    E::store(drow + tid, fill);
+                if (sl.last && gd.tail0 + tid < V)
+                    E::store(drow + gd.tail0 + tid, fill);
+            }
+            continue;
+        }
+
+        const ListRef L = kList ? list_at(lists + q * list_words(NC, p.k), NC, p.k) : ListRef{};
+        const int32_t y = kList ? -1 : w.y;
+        const int first_own = kList ? L.head[tid] : -1;
+        const int32_t col0 = head + static_cast<int32_t>(sl.v0) * VEC;  // of the slice's vector 0
+        // calls f(column, entry) for the listed columns this thread owns
+        const auto each_own = [&](auto &&f) {
+            if constexpr (kList) {
+                for (int j = first_own; j >= 0; j = L.next[j])
+                    if (L.col[j] >= 0)
+                        f(L.col[j], j);
+            } else {
+                if (column_owner<VEC, NC>(sl, y) == tid)
+                    f(y, 0);
+            }
+        };
+        bool own_any = false;  // in this slice's vectors
+        each_own([&](int32_t col, int) { own_any |= col >= col0 && col < col0 + nvec * VEC; });
+        const auto is_listed = [&](int32_t at) {
+            bool hit = false;
+            each_own([&](int32_t col, int) { hit |= col == at; });
+            return hit;
+        };
+
+        float m, s;
+        if (kStats) {
+            RestStats st;
+            if (sl.first && tid < sl.g.head)
+                st.add1(is_listed(tid) ? kNegInf : E::load(row + tid), c);
+            if (sl.last && sl.g.tail0 + tid < V)
+                st.add1(is_listed(static_cast<int32_t>(sl.g.tail0) + tid)
+                            ? kNegInf
+                            : E::load(row + sl.g.tail0 + tid),
+                        c);
+            for (int32_t j = 0; j < nchunks; ++j) {
+                uint4 *chunk = wait_chunk();
+                const int32_t vb0 = j * CV;
+                const int32_t nv = nvec - vb0 < CV ? nvec - vb0 : CV;
+                if (own_any && alive) {
+                    // listed columns leave the sum: -inf in the copied row, written
+                    // by the thread that alone reads their vector
+                    bool wrote = false;
+                    each_own([&](int32_t col, int) {
+                        const int32_t e = col - col0 - vb0 * VEC;
+                        if (col >= col0 && e >= 0 && e < nv * VEC) {
+                            reinterpret_cast<T *>(chunk)[e] = neg_inf_as(T());
+                            wrote = true;
+                        }
+                    });
+                    if (wrote)
+                        fence_before_refill();
+                }
+                if (alive && nv == CV) {
+                    uint4 raw[PER_THREAD];
+#pragma unroll
+                    for (int u = 0; u < PER_THREAD; ++u)
+                        raw[u] = chunk[tid + u * NC];
+#pragma unroll
+                    for (int u = 0; u < PER_THREAD; u += 2) {
+                        const float own = FastVec<T>::vmax(raw[u], raw[u + 1]);
+                        // (many warps: the running max rises for the whole warp at once)
+                        st.raise_to(NCW > 8 ? warp_max_active(own) : own, c);
+                        if (own != kNegInf) {
+                            rest_add(st, raw[u], c, static_cast<const T *>(nullptr));
+                            rest_add(st, raw[u + 1], c, static_cast<const T *>(nullptr));
+                        }
+                    }
+                } else if (alive) {
+                    for (int32_t v = tid; v < nv; v += NC) {
+                        const uint4 raw = chunk[v];
+                        const float own = FastVec<T>::vmax(raw);
+                        st.raise_to(own, c);
+                        if (own != kNegInf)
+                            rest_add(st, raw, c, static_cast<const T *>(nullptr));
+                    }
+                }
+                done_chunk();
+            }
+            // each warp's state, one barrier, then every warp merges them all
+            const int rb = i & 1;
+            m = st.m;
+            s = st.sum();
+            if (s != s)  // (a thread that met only NaN has no max: its NaN must still count)
+                m = fmaxf(m, 0.0f);
+            warp_merge_rest(m, s, c, st.residual(c));
+            if (lane == 0) {
+                red_m[rb][warp] = m;
+                red_s[rb][warp] = s;
+            }
+            named_sync(1, NC);
+            m = lane < NCW ? red_m[rb][lane] : kNegInf;
+            s = lane < NCW ? red_s[rb][lane] : 0.0f;
+            warp_merge_rest(m, s, c);
+            if (C > 1) {
+                // the slices' partials, to every CTA of the row
+                if (warp == 0) {
+                    cluster_wait();  // every peer's mbarriers exist
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&xbar, C * static_cast<uint32_t>(sizeof(float4)));
+                        const uint32_t at = smem_addr(&xchg[split]), bar = smem_addr(&xbar);
+                        for (int t = 0; t < C; ++t)
+                            st_async_v4(map_to_rank(at, t), make_float4(m, s, 0.0f, 0.0f),
+                                        map_to_rank(bar, t));
+                    }
+                    __syncwarp();
+                }
+                if (!mbar_wait_cluster(&xbar, 0)) {
+                    alive = false;
+                    report(p.dev_status, GBCE_DEV_TIMEOUT);
+                }
+                m = kNegInf;
+                s = 0.0f;
+                for (int t = 0; t < C; ++t)
+                    merge_rest(m, s, xchg[t].x, xchg[t].y, c);
+            }
+            if (tid == 0) {
+                w.m = m;
+                w.s = s;
+                mbar_arrive(&stat_bar[q]);
+            }
+        } else {
+            m = w.m;
+            s = w.s;
+        }
+
+        if (kGrad) {
+            const float gt = w.gt;
+            float gs, dy = 0.0f;
+            if (kList) {
+                gs = gt * share_gap(w.lp_rest,
+                                    student_row(m, s, w.ml, w.sl, c, inv_t).log_rest);
+            } else {
+                const float lp = token_logp(m, s, w.xy, inv_t);
+                float slope = gt;  // (g / T) dloss / dlog p
+                if (OP == kOpPolicy) {
+                    float loss, dlp;
+                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
+                    slope *= dlp;
+                }
+                dy = -slope * expm1f(lp);
+                gs = -dy;
+            }
+            const GradConsts gk = rest_consts(m, s, c.hi + c.lo, gs);
+            constexpr int32_t kNoLabel = 0x7fffffff;
+            const StoreGeom dg = store_geom<T>(drow, sl.g, V);
+            const int sh = dg.sh;
+            if (sl.first && tid < dg.begin)
+                E::store(drow + tid, grad_scalar(E::load(row + tid), gk));
+            if (sl.last && dg.end + tid < V)
+                E::store(drow + dg.end + tid, grad_scalar(E::load(row + dg.end + tid), gk));
+            // this slice's stored vectors: [0, stored) from drow + dbase on
+            const int64_t here = dg.vecs - sl.v0;
+            const int32_t stored = static_cast<int32_t>(here < nvec ? (here > 0 ? here : 0) : nvec);
+            T *dbase = drow + col0 + sh;
+            for (int32_t j = 0; j < nchunks; ++j) {
+                const uint4 *chunk = wait_chunk();
+                const int32_t vb0 = j * CV;
+                const int32_t nv = stored - vb0 < CV ? stored - vb0 : CV;
+                T *d = dbase + vb0 * VEC;
+                if (alive && nv == CV) {
+                    uint4 raw[PER_THREAD];
+                    if (sh == 0) {
+#pragma unroll
+                        for (int u = 0; u < PER_THREAD; ++u)
+                            raw[u] = chunk[tid + u * NC];
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < PER_THREAD; ++u)
+                            raw[u] = shifted<T>(chunk[tid + u * NC], chunk[tid + u * NC + 1], sh);
+                    }
+#pragma unroll
+                    for (int u = 0; u < PER_THREAD; ++u)
+                        st_cs_v4(d + (tid + u * NC) * VEC,
+                                 GradVec<T>::run(raw[u], kNoLabel, gk));
+                } else if (alive) {
+                    for (int32_t v = tid; v < nv; v += NC) {
+                        const uint4 raw =
+                            sh == 0 ? chunk[v] : shifted<T>(chunk[v], chunk[v + 1], sh);
+                        st_cs_v4(d + v * VEC, GradVec<T>::run(raw, kNoLabel, gk));
+                    }
+                }
+                done_chunk();
+            }
+            // the listed columns, over what the sweep stored there: by the same
+            // thread, or (rows of another phase: other threads' vectors) once
+            // every thread of this CTA has stored
+            if (sh != 0)
+                named_sync(2, NC);
+            const int32_t s0 = sl.first ? 0 : col0 + sh;
+            const int64_t s1 = sl.last ? V : static_cast<int64_t>(col0) + sh + stored * VEC;
+            each_own([&](int32_t col, int j) {
+                if (col < s0 || col >= s1)
+                    return;  // (stored by another slice's CTA)
+                float v = dy;
+                if constexpr (kList)
+                    v = w.gt * share_gap(L.lp[j],
+                                         student_logp(student_row(m, s, w.ml, w.sl, c, inv_t),
+                                                      L.x[j], inv_t));
+                E::store(drow + col, v);
+            });
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&free_bar[q]);
     }
 }
 
-template <typename T, int OP, int PASS>
-cudaError_t launch_post_as(const PostParams &p, cudaStream_t stream)
+// ------------------------------------------------------------------- launches
+
+// Shared memory of an SM, and what a CTA's static arrays and the system take of it.
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 2048 + 1024;
+// Bytes of rows that may wait in L2 for their gradient pass.
+constexpr int64_t kPostL2Budget = int64_t(76) << 20;
+// The least columns a slice of a split row has.
+constexpr int64_t kPostSliceElems = 8192;
+
+struct PostLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    PostLaunch(int64_t ctas, int threads, int smem, int splits, cudaStream_t stream)
+    {
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (splits > 1) {
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+            attr[1].val.clusterDim.y = 1;
+            attr[1].val.clusterDim.z = 1;
+            cfg.numAttrs = 2;
+        }
+    }
+};
+
+template <typename T, int OP, int PASS, int SHAPE>
+cudaError_t launch_post_shape(const PostParams &params, int sms, cudaStream_t stream)
 {
-    post_row_kernel<T, OP, PASS>
-        <<<static_cast<unsigned>(p.rows), kPostWarps * 32, 0, stream>>>(p);
+    using Shape = PostShape<SHAPE>;
+    static std::atomic<uint64_t> attr_done{0};
+    static std::atomic<int> most_clusters[64][kMaxClusterCtas + 1] = {};
+    auto kernel = post_kernel<T, OP, PASS, SHAPE>;
+    cudaError_t err = ensure_smem_attr(kernel, post_smem<SHAPE>(OP, kMaxListed), attr_done);
+    if (err != cudaSuccess)
+        return err;
+    constexpr int threads = post_threads<SHAPE>();
+    const int smem = post_smem<SHAPE>(OP, params.k);
+    PostParams p = params;
+    const int fit = kSmemPerSm / (smem + kSmemPerCta);
+    int64_t slots = static_cast<int64_t>(sms) * (fit < Shape::kCtasPerSm ? fit : Shape::kCtasPerSm);
+    if (p.splits > 1) {
+        // the largest cluster for which every row's is resident at once (a
+        // cluster must fit one GPC); the query runs once per device and size
+        int dev = 0;
+        if ((err = cudaGetDevice(&dev)) != cudaSuccess)
+            return err;
+        int C = p.splits;
+        for (; C > 1 && dev < 64; --C) {
+            int n = most_clusters[dev][C].load(std::memory_order_relaxed);
+            if (n == 0) {
+                PostLaunch probe(C * p.rows, threads, post_smem<SHAPE>(OP, kMaxListed), C, nullptr);
+                probe.cfg.attrs = &probe.attr[1];  // (the cluster alone)
+                probe.cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &probe.cfg) != cudaSuccess || n < 1) {
+                    (void)cudaGetLastError();
+                    n = -1;  // no answer: no split of this size
+                }
+                most_clusters[dev][C].store(n, std::memory_order_relaxed);
+            }
+            if (n >= p.rows)
+                break;
+        }
+        p.splits = C;
+    }
+    int64_t grid = p.rows * p.splits;
+    if (p.splits == 1) {
+        if (PASS == kPassFused && SHAPE == kShapeLong) {
+            // a row stays in L2 from its first read to its second: fewer CTAs
+            // where the rows are long, but not below half the SMs
+            const int64_t fit_l2 = kPostL2Budget / (p.vocab * static_cast<int64_t>(sizeof(T)) + 1);
+            const int64_t least = sms / 2 > 0 ? sms / 2 : 1;
+            if (fit_l2 < slots)
+                slots = fit_l2 > least ? fit_l2 : least;
+        }
+        if (p.rows > slots) {
+            // rows beyond the first wave go by ticket: zeroed, and the items
+            // counted, by a kernel before this one
+            grid = slots;
+            if (p.ticket == nullptr)
+                err = cudaSuccess;  // (no workspace: a static walk)
+            else if (p.n_items_out == nullptr)
+                err = cudaMemsetAsync(p.ticket, 0, sizeof(int32_t), stream);
+            else if (OP == kOpDistill)
+                err = launch_count_mask(p.row_mask, p.rows, p.n_items_out, p.ticket, stream);
+            else
+                err = launch_count_items(p.labels, p.rows, p.ignore_index, p.n_items_out, p.ticket,
+                                         nullptr, nullptr, stream);
+            if (err != cudaSuccess)
+                return err;
+            if (p.n_items_out != nullptr)
+                p.n_items = p.n_items_out;
+            p.n_items_out = nullptr;
+        } else {
+            p.ticket = nullptr;
+        }
+    }
+    if (grid == p.rows * p.splits)
+        p.ticket = nullptr;
+    const PostLaunch l(grid, threads, smem, p.splits, stream);
+    err = cudaLaunchKernelEx(&l.cfg, kernel, p);
     note_launches(1);
-    return cudaGetLastError();
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <typename T, int OP, int PASS>
+cudaError_t launch_post_as(PostParams p, cudaStream_t stream)
+{
+    const int sms = device_sm_count();
+    if (sms <= 0)
+        return cudaErrorInvalidDevice;
+    const int64_t row_bytes = p.vocab * static_cast<int64_t>(sizeof(T));
+    p.splits = 1;
+    // few rows: each one's slices on the CTAs of a cluster
+    const int64_t slots = static_cast<int64_t>(sms) * PostShape<kShapeMid>::kCtasPerSm;
+    if (p.rows * 2 <= slots && p.vocab >= 2 * kPostSliceElems) {
+        int64_t n = slots / p.rows;
+        if (n > p.vocab / kPostSliceElems)
+            n = p.vocab / kPostSliceElems;
+        p.splits = static_cast<int>(n < kMaxClusterCtas ? n : kMaxClusterCtas);
+        return launch_post_shape<T, OP, PASS, kShapeMid>(p, sms, stream);
+    }
+    if (row_bytes >= 96 * 1024)
+        return launch_post_shape<T, OP, PASS, kShapeLong>(p, sms, stream);
+    if (row_bytes >= 24 * 1024)
+        return launch_post_shape<T, OP, PASS, kShapeMid>(p, sms, stream);
+    return launch_post_shape<T, OP, PASS, kShapeShort>(p, sms, stream);
 }
 
 template <typename T>
@@ -525,6 +1265,9 @@ cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stre
         return cudaSuccess;
     if (op == kOpPolicy)
         return launch_post_as<T, kOpPolicy, kPassFused>(p, stream);
+    if (op == kOpToken)
+        return pass == kPassFwd ? launch_post_as<T, kOpToken, kPassFwd>(p, stream)
+                                : launch_post_as<T, kOpToken, kPassBwd>(p, stream);
     if (pass == kPassFwd)
         return launch_post_as<T, kOpDistill, kPassFwd>(p, stream);
     if (pass == kPassBwd)

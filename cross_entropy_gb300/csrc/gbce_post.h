@@ -10,9 +10,14 @@ namespace gbce {
 
 constexpr int kMaxListed = 256;  // teacher entries of a row (GBCE_MAX_TEACHER_K)
 
-// Which loss a row kernel computes, and how much of it.
-enum PostOp : int { kOpDistill = 0, kOpPolicy = 1 };
+// Which loss a row kernel computes, how much of it, and by CTAs of which shape.
+enum PostOp : int {
+    kOpDistill = 0,
+    kOpPolicy = 1,
+    kOpToken = 2,  // log p of one column and its gradient (around the preference loss)
+};
 enum PostPass : int { kPassFwd = 0, kPassBwd = 1, kPassFused = 2 };
+enum ShapeOfCta : int { kShapeShort = 0, kShapeMid = 1, kShapeLong = 2 };
 
 // The clipped policy loss of one row (see policy_row).
 struct PolicyTerms {
@@ -25,7 +30,8 @@ struct PolicyTerms {
 struct PostParams {
     const void *logits;
     int64_t rows, vocab, row_stride;  // row_stride in elements
-    float T, c;                       // temperature, log2(e) / T
+    float c_hi, c_lo;                 // log2(e) / T in two floats
+    float it_hi, it_lo;               // 1 / T in two floats
 
     // distillation: the teacher's entries
     const int64_t *index;       // [rows, k] columns, -1: no entry
@@ -34,30 +40,39 @@ struct PostParams {
     int64_t k;
     const uint8_t *row_mask;  // [rows] or null
 
-    // policy loss
+    // policy, token
     const int64_t *labels;  // [rows]
     int64_t ignore_index;
     PolicyTerms policy;
+    // token: rows outside [row_range[0], row_range[row_range_end]) are left out; null: none
+    const int64_t *row_range;
+    int64_t row_range_end;
 
-    float *loss_rows;         // [rows] (null in the backward pass)
-    float *logp_out;          // policy: [rows] or null
-    float *rest_state_out;    // distill forward: [rows, 2] (m, s) of the unlisted columns, or null
-    const float *rest_state;  // distill backward: the forward's
+    float *loss_rows;         // distill, policy: [rows] (null in the backward pass)
+    float *logp_out;          // policy, token: [rows] or null
+    float *rest_state_out;    // forward: [rows, 2] (m, s) of the unlisted columns, or null
+    const float *rest_state;  // backward: the forward's
 
     void *dlogits;
     int64_t d_stride;
-    int vec_store;          // dlogits rows share the logits rows' 16-byte phase
     const float *grad_out;  // [rows] or [1]
     int reduction;          // 0 none, 1 sum, 2 mean
-    const int64_t *n_items;
+    const int64_t *n_items;   // backward: the forward's count
+    int64_t *n_items_out;     // else: the count goes here (null: not wanted)
     int32_t *dev_status;
+    int32_t *ticket;    // hands out the rows beyond the first wave
+    int32_t *zero_out;  // zeroed on the way, nullable
+    int splits;       // CTAs (a cluster) per row
+    int keep_rows;    // forward: leave the rows in L2 for a backward pass that follows
+    int reverse;      // walk the rows from the last to the first
 };
 
 template <typename T>
 cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stream);
 
-// n_items = number of rows with mask != 0 (rows when mask is null) into *n_out.
+// n_items = number of rows with mask != 0 (rows when mask is null) into *n_out;
+// *zero_out (nullable) is zeroed.
 cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
-                              cudaStream_t stream);
+                              int32_t *zero_out, cudaStream_t stream);
 
 }  // namespace gbce

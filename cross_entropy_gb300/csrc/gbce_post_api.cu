@@ -18,9 +18,14 @@ namespace gbce {
 constexpr int kCountThreads = 256;
 
 __global__ void __launch_bounds__(kCountThreads)
-    count_mask_kernel(const uint8_t *mask, int64_t rows, int64_t *n_out)
+    count_mask_kernel(const uint8_t *mask, int64_t rows, int64_t *n_out, int32_t *zero_out)
 {
     __shared__ int64_t part[kCountThreads / 32];
+    // the row kernel after this one may start its prologue now: it waits for
+    // this kernel's outputs before it reads them
+    launch_dependents();
+    if (threadIdx.x == 0 && zero_out != nullptr)
+        *zero_out = 0;
     int64_t n = 0;
     if (mask == nullptr)
         n = threadIdx.x == 0 ? rows : 0;
@@ -42,38 +47,253 @@ __global__ void __launch_bounds__(kCountThreads)
 }
 
 cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
-                              cudaStream_t stream)
+                              int32_t *zero_out, cudaStream_t stream)
 {
-    count_mask_kernel<<<1, kCountThreads, 0, stream>>>(mask, rows, n_out);
+    count_mask_kernel<<<1, kCountThreads, 0, stream>>>(mask, rows, n_out, zero_out);
     note_launches(1);
     return cudaGetLastError();
 }
 
 // ------------------------------------------- policy loss of given log-probs
 
-// One thread per row: 17 to 21 bytes of traffic and some twenty operations.
-__global__ void __launch_bounds__(256)
-    policy_logp_kernel(const float *logp, int64_t rows, const uint8_t *mask, PolicyTerms t,
-                       int reduction, const float *grad_out, const int64_t *n_items,
-                       float *loss_rows, float *dlogp)
+struct PolicyRows {
+    const float *logp;  // [rows]
+    int64_t rows;
+    const uint8_t *mask;
+    PolicyTerms terms;
+    int reduction;
+    const float *grad_out;  // [rows] or [1] or null
+    float *loss_rows;       // NONE: [rows]
+    float *loss_out;        // else: [1]
+    float *dlogp;           // [rows] or null
+    int64_t *n_items;
+};
+
+// A row's loss (0 where it is left out) and, from the upstream gradient, its
+// derivative.
+__device__ __forceinline__ float policy_one_row(const PolicyRows &q, int64_t r, bool live, float g)
 {
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (r >= rows)
-        return;
     float loss = 0.0f, d = 0.0f;
-    if (mask == nullptr || mask[r] != 0) {
-        policy_row(t, r, logp[r], loss, d);
-        if (dlogp != nullptr) {
-            float g = reduction == 0 ? grad_out[r] : grad_out[0];
-            if (reduction == 2)
-                g /= static_cast<float>(*n_items);  // (this row is live: the count is not 0)
-            d *= g;
+    if (live) {
+        const PolicyTerms &t = q.terms;
+        policy_row(t, t.advantages[r], t.old_logp != nullptr ? t.old_logp[r] : 0.0f,
+                   t.ref_logp != nullptr ? t.ref_logp[r] : 0.0f, q.logp[r], loss, d);
+        if (q.reduction == GBCE_NONE && q.dlogp != nullptr)
+            g = q.grad_out[r];
+        d *= g;
+    }
+    if (q.dlogp != nullptr)
+        q.dlogp[r] = d;
+    if (q.reduction == GBCE_NONE)
+        q.loss_rows[r] = loss;
+    return loss;
+}
+
+constexpr int kPolicyThreads = 1024, kPolicyWarps = kPolicyThreads / 32;
+constexpr int kPolicyCtas = 8;  // of the cluster
+
+// Sums of a count and a loss over the cluster in a fixed order, to every thread:
+// over the CTA's warps, then over the CTAs' parts in rank order.
+struct ClusterSum {
+    double loss[kPolicyWarps];
+    int64_t count[kPolicyWarps];
+    double cta_loss;
+    int64_t cta_count;
+};
+
+__device__ __forceinline__ void warp_sums(double &s, int64_t &n)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+    }
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+__device__ void cluster_sums(ClusterSum &own, double &s, int64_t &n)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    warp_sums(s, n);
+    if (lane == 0) {
+        own.loss[warp] = s;
+        own.count[warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        s = own.loss[lane];
+        n = own.count[lane];
+        warp_sums(s, n);
+        if (lane == 0) {
+            own.cta_loss = s;
+            own.cta_count = n;
         }
     }
-    if (loss_rows != nullptr)
-        loss_rows[r] = loss;
-    if (dlogp != nullptr)
-        dlogp[r] = d;
+    cluster_barrier();
+    const uint32_t a = smem_addr(&own.cta_loss), b = smem_addr(&own.cta_count);
+    s = 0.0;
+    n = 0;
+    for (uint32_t i = 0; i < kPolicyCtas; ++i) {
+        double v;
+        int64_t k;
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(a, i)));
+        asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(k) : "r"(map_to_rank(b, i)));
+        s += v;
+        n += k;
+    }
+    cluster_barrier();  // (no CTA leaves, or writes its sums anew, before all have read them)
+}
+
+// One cluster for all rows: the count, the rows, the reduced loss, in one
+// launch.  Latency is what such a call costs (17 to 21 bytes and some twenty
+// operations a row): three launches of one CTA, one CTA and a grid took 48 us at
+// 65536 rows.
+__global__ void __cluster_dims__(kPolicyCtas, 1, 1) __launch_bounds__(kPolicyThreads)
+    policy_cluster_kernel(const PolicyRows q)
+{
+    __shared__ ClusterSum sums;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPolicyThreads + threadIdx.x;
+    constexpr int64_t kStep = static_cast<int64_t>(kPolicyCtas) * kPolicyThreads;
+    double s = 0.0;
+    int64_t n = 0;
+    if (q.mask == nullptr)
+        n = first == 0 ? q.rows : 0;
+    else
+#pragma unroll 4
+        for (int64_t r = first; r < q.rows; r += kStep)
+            n += q.mask[r] != 0;
+    cluster_sums(sums, s, n);
+    float g = 1.0f;
+    if (q.dlogp != nullptr && q.reduction != GBCE_NONE)
+        g = q.reduction == GBCE_MEAN && n > 0 ? q.grad_out[0] / static_cast<float>(n)
+                                              : q.grad_out[0];
+    s = 0.0;
+#pragma unroll 2
+    for (int64_t r = first; r < q.rows; r += kStep)
+        s += policy_one_row(q, r, q.mask == nullptr || q.mask[r] != 0, g);
+    if (first == 0)
+        *q.n_items = n;
+    if (q.reduction == GBCE_NONE)
+        return;
+    const int64_t kept = n;
+    cluster_sums(sums, s, n);
+    if (first == 0)
+        *q.loss_out = static_cast<float>(
+            q.reduction == GBCE_MEAN ? (kept > 0 ? s / static_cast<double>(kept) : 0.0) : s);
+}
+
+// Many rows: a grid counts the rows of each CTA's part, a grid takes them (every
+// CTA summing the parts' counts itself), one CTA sums the parts' losses.
+constexpr int kPolicyPartRows = 4096, kPolicyMaxParts = 65536;
+
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_count_kernel(const uint8_t *mask, int64_t rows, int64_t part, int64_t *counts)
+{
+    __shared__ ClusterSum sums;
+    const int64_t lo = blockIdx.x * part, hi = lo + part < rows ? lo + part : rows;
+    double s = 0.0;
+    int64_t n = 0;
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kPolicyThreads)
+        n += mask == nullptr || mask[r] != 0;
+    warp_sums(s, n);
+    if ((threadIdx.x & 31) == 0)
+        sums.count[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        n = sums.count[threadIdx.x];
+        warp_sums(s, n);
+        if (threadIdx.x == 0)
+            counts[blockIdx.x] = n;
+    }
+}
+
+// The CTA's sums of (a thread's) loss and count, to every thread.
+__device__ void cta_sums(ClusterSum &own, double &s, int64_t &n)
+{
+    warp_sums(s, n);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        own.loss[threadIdx.x >> 5] = s;
+        own.count[threadIdx.x >> 5] = n;
+    }
+    __syncthreads();
+    s = own.loss[threadIdx.x & 31];
+    n = own.count[threadIdx.x & 31];
+    warp_sums(s, n);
+}
+
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_part_kernel(const PolicyRows q, int64_t part, const int64_t *counts, double *losses)
+{
+    __shared__ ClusterSum sums;
+    double s = 0.0;
+    int64_t n = 0;
+    for (int64_t i = threadIdx.x; i < gridDim.x; i += kPolicyThreads)
+        n += counts[i];
+    cta_sums(sums, s, n);
+    float g = 1.0f;
+    if (q.dlogp != nullptr && q.reduction != GBCE_NONE)
+        g = q.reduction == GBCE_MEAN && n > 0 ? q.grad_out[0] / static_cast<float>(n)
+                                              : q.grad_out[0];
+    const int64_t lo = blockIdx.x * part, hi = lo + part < q.rows ? lo + part : q.rows;
+    s = 0.0;
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kPolicyThreads)
+        s += policy_one_row(q, r, q.mask == nullptr || q.mask[r] != 0, g);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *q.n_items = n;
+    n = 0;
+    cta_sums(sums, s, n);
+    if (threadIdx.x == 0)
+        losses[blockIdx.x] = s;
+}
+
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_sum_kernel(const double *losses, int64_t parts, int mean, const int64_t *n_items,
+                      float *loss_out)
+{
+    __shared__ ClusterSum sums;
+    double s = 0.0;
+    int64_t n = 0;
+    for (int64_t i = threadIdx.x; i < parts; i += kPolicyThreads)
+        s += losses[i];
+    cta_sums(sums, s, n);
+    const int64_t kept = *n_items;
+    if (threadIdx.x == 0)
+        *loss_out = static_cast<float>(mean ? (kept > 0 ? s / static_cast<double>(kept) : 0.0) : s);
+}
+
+// Up to this many rows go to the one cluster.
+constexpr int64_t kPolicyClusterRows = 131072;
+
+cudaError_t launch_policy_rows(const PolicyRows &q, void *parts, cudaStream_t stream)
+{
+    if (q.rows <= kPolicyClusterRows) {
+        policy_cluster_kernel<<<kPolicyCtas, kPolicyThreads, 0, stream>>>(q);
+        note_launches(1);
+        return cudaGetLastError();
+    }
+    int64_t part = kPolicyPartRows;
+    if ((q.rows + part - 1) / part > kPolicyMaxParts)
+        part = (q.rows + kPolicyMaxParts - 1) / kPolicyMaxParts;
+    const int64_t n = (q.rows + part - 1) / part;
+    double *losses = static_cast<double *>(parts);
+    int64_t *counts = reinterpret_cast<int64_t *>(losses + n);
+    policy_count_kernel<<<static_cast<unsigned>(n), kPolicyThreads, 0, stream>>>(q.mask, q.rows,
+                                                                                 part, counts);
+    policy_part_kernel<<<static_cast<unsigned>(n), kPolicyThreads, 0, stream>>>(q, part, counts,
+                                                                                losses);
+    note_launches(2);
+    if (q.reduction != GBCE_NONE) {
+        policy_sum_kernel<<<1, kPolicyThreads, 0, stream>>>(losses, n, q.reduction == GBCE_MEAN,
+                                                            q.n_items, q.loss_out);
+        note_launches(1);
+    }
+    return cudaGetLastError();
 }
 
 // -------------------------------------------------------------- preference
@@ -93,18 +313,6 @@ __device__ __forceinline__ SeqRows seq_rows(const int64_t *offsets, int64_t s, i
     return q;
 }
 
-// The labels as the sweeps take them: ignore_index for rows of no sequence.
-// Offsets that decrease or leave [0, rows] are reported (bad_offsets is also
-// left for the pair kernel, which then makes the losses NaN).
-__global__ void __launch_bounds__(256)
-    preference_labels_kernel(const int64_t *labels, int64_t rows, int64_t ignore_index,
-                             const int64_t *offsets, int64_t sequences, int64_t *out)
-{
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (r < rows)
-        out[r] = r >= offsets[0] && r < offsets[sequences] ? labels[r] : ignore_index;
-}
-
 struct PreferenceTerms {
     const float *logp;      // [rows]
     const float *ref_logp;  // [rows] or null
@@ -118,10 +326,11 @@ struct PreferenceTerms {
     int squared, average;
     int reduction;
     const float *grad_out;  // [pairs] or [1]
-    float sign;             // of the rows' gradients: +1 d/dlogp, -1 as token CE's upstream
     float *loss_pairs;      // [pairs]
     float *seq_score;       // [2 pairs] or null
     float *drow;            // [rows] or null
+    float *loss_out;        // reduced loss, by the last pair's CTA (null: not reduced)
+    int32_t *done;          // pairs done so far: 0 at the start
     int32_t *dev_status;
 };
 
@@ -197,11 +406,31 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
         if (tid == 0)
             report(t.dev_status, GBCE_DEV_BAD_INDEX);
     }
+    __shared__ int s_last;
     if (tid == 0) {
         t.loss_pairs[i] = static_cast<float>(loss);
         if (t.seq_score != nullptr) {
             t.seq_score[i] = static_cast<float>(score[0]);
             t.seq_score[i + t.pairs] = static_cast<float>(score[1]);
+        }
+        s_last = 0;
+        if (t.loss_out != nullptr) {
+            __threadfence();  // the loss before the count
+            s_last = atomicAdd(t.done, 1) == static_cast<int32_t>(t.pairs) - 1;
+        }
+    }
+    if (t.loss_out != nullptr) {
+        __syncthreads();
+        if (s_last) {
+            // the last pair to finish sums them all, in pair order
+            __threadfence();
+            double sum = 0.0;
+            for (int64_t j = tid; j < t.pairs; j += kPairThreads)
+                sum += static_cast<double>(__ldcg(t.loss_pairs + j));
+            sum = cta_sum(sum, scratch);
+            if (tid == 0)
+                *t.loss_out = static_cast<float>(
+                    t.reduction == GBCE_MEAN ? sum / static_cast<double>(t.pairs) : sum);
         }
     }
     if (t.drow == nullptr)
@@ -210,31 +439,22 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
     if (t.reduction == 2)
         g /= static_cast<double>(t.pairs);
     for (int side = 0; side < 2; ++side) {
-        const double d = (side == 0 ? dh : -dh) * weight[side] * g * t.sign;
+        const double d = (side == 0 ? dh : -dh) * weight[side] * g;
         for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
             t.drow[r] = preference_live(t, r) ? static_cast<float>(d) : 0.0f;
     }
 }
 
-// loss_out[0] = sum of n losses, or their mean, in fp64 and a fixed order.
-__global__ void __launch_bounds__(kPairThreads)
-    pair_reduce_kernel(const float *loss, int64_t n, int mean, float *loss_out)
-{
-    __shared__ double scratch[kPairThreads / 32];
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kPairThreads)
-        sum += static_cast<double>(loss[i]);
-    sum = cta_sum(sum, scratch);
-    if (threadIdx.x == 0)
-        *loss_out = static_cast<float>(mean ? sum / static_cast<double>(n) : sum);
-}
-
-// Zeros for the rows of no sequence (a preference call from log-probs).
+// Zeros for the rows of no sequence (a preference call from log-probs), and
+// for the count of pairs done.
 __global__ void __launch_bounds__(256)
-    preference_outside_kernel(int64_t rows, const int64_t *offsets, int64_t sequences, float *drow)
+    preference_outside_kernel(int64_t rows, const int64_t *offsets, int64_t sequences, float *drow,
+                              int32_t *zero_out)
 {
     const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (r < rows && (r < offsets[0] || r >= offsets[sequences]))
+    if (r == 0)
+        *zero_out = 0;
+    if (drow != nullptr && r < rows && (r < offsets[0] || r >= offsets[sequences]))
         drow[r] = 0.0f;
 }
 
@@ -255,13 +475,13 @@ gbce_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GBCE_OK : GBC
 bool good_reduction(gbce_reduction r) { return r == GBCE_NONE || r == GBCE_SUM || r == GBCE_MEAN; }
 
 gbce_status check_logits(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
-                         int64_t row_stride, float temperature)
+                         int64_t row_stride, double temperature)
 {
     if (dtype != GBCE_F32 && dtype != GBCE_BF16)
         return GBCE_EDTYPE;
     if (rows < 0 || rows > kMaxRows || vocab < 1 || vocab > kMaxVocab || row_stride < vocab)
         return GBCE_EINVAL;
-    if (!(std::isfinite(temperature) && temperature > 0.0f))
+    if (!(temperature >= 1e-30 && temperature <= 1e30))
         return GBCE_EINVAL;
     if (rows == 0)
         return GBCE_OK;
@@ -296,31 +516,33 @@ gbce_status check_workspace(const void *ws, size_t bytes, size_t need)
     return GBCE_OK;
 }
 
-PostParams post_params(const void *logits, int64_t rows, int64_t vocab, int64_t row_stride,
-                       float temperature, int32_t *dev_status)
+// v > 0 as hi + lo, hi of 14 bits, both positive: a logit of -inf times either
+// part is -inf, where a lo of 0 or below would make its exponent NaN.
+void two_floats(double v, float &hi, float &lo)
 {
+    int exponent = 0;
+    const double mantissa = std::frexp(v, &exponent);
+    hi = static_cast<float>(std::ldexp(std::floor(std::ldexp(mantissa, 14)), exponent - 14));
+    lo = static_cast<float>(v - static_cast<double>(hi));
+    if (!(lo > 0.0f))
+        lo = hi * 0x1p-60f > 0.0f ? hi * 0x1p-60f : 0x1p-149f;
+}
+
+PostParams post_params(const void *logits, int64_t rows, int64_t vocab, int64_t row_stride,
+                       double temperature, int32_t *dev_status)
+{
+    const double c = 1.4426950408889634 / temperature, it = 1.0 / temperature;
     PostParams p{};
     p.logits = logits;
     p.rows = rows;
     p.vocab = vocab;
     p.row_stride = row_stride;
-    p.T = temperature;
-    // log2(e) / T rounded once from the fp64 quotient
-    p.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+    two_floats(c, p.c_hi, p.c_lo);
+    two_floats(it, p.it_hi, p.it_lo);
+    p.k = 1;
+    p.splits = 1;
     p.dev_status = dev_status;
     return p;
-}
-
-void set_dlogits(PostParams &p, gbce_dtype dt, void *dlogits, int64_t d_stride)
-{
-    const uint64_t es = elem_size(dt);
-    p.dlogits = dlogits;
-    p.d_stride = d_stride;
-    // every dlogits row at its logits row's offset modulo 16 bytes
-    p.vec_store = ((reinterpret_cast<uintptr_t>(p.logits) ^ reinterpret_cast<uintptr_t>(dlogits)) &
-                   15u) == 0 &&
-                  ((static_cast<uint64_t>(p.row_stride) * es) & 15u) ==
-                      ((static_cast<uint64_t>(d_stride) * es) & 15u);
 }
 
 cudaError_t launch_post(const PostParams &p, gbce_dtype dt, int op, int pass, cudaStream_t s)
@@ -329,7 +551,9 @@ cudaError_t launch_post(const PostParams &p, gbce_dtype dt, int op, int pass, cu
                            : gbce::launch_post<float>(p, op, pass, s);
 }
 
-// Workspace of the per-row losses: the item count, then [rows] floats.
+// Workspace of the calls with one loss per row: the item count (8 bytes), the
+// row ticket, then at 256 [rows] floats of losses (or 16 bytes for each of the
+// at most rows / 4096 + 1 parts of a long vector of log-probs).
 size_t loss_workspace(int64_t rows)
 {
     return rows <= 0 ? 0 : 256 + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
@@ -348,7 +572,7 @@ cudaError_t empty_loss(gbce_reduction reduction, float *loss_out, int64_t *n_ite
     if (reduction != GBCE_NONE)
         return gbce::launch_reduce_loss(nullptr, nullptr, 0, 0, static_cast<int>(reduction),
                                         nullptr, n_items_out, loss_out, s);
-    return n_items_out != nullptr ? gbce::launch_count_mask(nullptr, 0, n_items_out, s)
+    return n_items_out != nullptr ? gbce::launch_count_mask(nullptr, 0, n_items_out, nullptr, s)
                                   : cudaSuccess;
 }
 
@@ -390,28 +614,19 @@ void set_preference_options(PreferenceTerms &t, const gbce_preference_options *o
 }
 
 struct PreferenceLayout {
-    size_t labels, logp, grad, loss, total;
+    size_t loss, state, logp, grad, total;
 };
 
 PreferenceLayout preference_layout(int64_t rows, int64_t pairs)
 {
     const size_t r = static_cast<size_t>(rows), n = static_cast<size_t>(pairs);
     PreferenceLayout w{};
-    w.loss = 0;  // (and more than the workspace that ce_fwd asks for in all)
-    w.labels = 256 + align_up(n * sizeof(float), 256);
-    w.logp = w.labels + align_up(r * sizeof(int64_t), 256);
+    w.loss = 256;  // (the two sweeps' row tickets before it)
+    w.state = w.loss + align_up(n * sizeof(float), 256);
+    w.logp = w.state + align_up(2 * r * sizeof(float), 256);
     w.grad = w.logp + align_up(r * sizeof(float), 256);
     w.total = w.grad + align_up(r * sizeof(float), 256);
     return w;
-}
-
-cudaError_t reduce_pairs(const float *loss, int64_t n, gbce_reduction reduction, float *loss_out,
-                         cudaStream_t s)
-{
-    gbce::pair_reduce_kernel<<<1, gbce::kPairThreads, 0, s>>>(loss, n, reduction == GBCE_MEAN,
-                                                              loss_out);
-    gbce::note_launches(1);
-    return cudaGetLastError();
 }
 
 constexpr int64_t kMaxPairs = int64_t(1) << 30;
@@ -424,7 +639,7 @@ extern "C" {
 
 gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const int64_t *index, int64_t k,
-                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const float *teacher_logits, const float *teacher_rest, double temperature,
                         const uint8_t *row_mask, gbce_reduction reduction, float *loss_out,
                         float *rest_state_out, int64_t *n_items_out, void *workspace,
                         size_t workspace_bytes, int32_t *dev_status, void *stream)
@@ -453,11 +668,9 @@ gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
     p.row_mask = row_mask;
     p.loss_rows = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, 256);
     p.rest_state_out = rest_state_out;
-    cudaError_t e = cudaSuccess;
-    if (reduction == GBCE_MEAN || n_items_out != nullptr)
-        e = gbce::launch_count_mask(row_mask, rows, n_ptr, s);
-    if (e == cudaSuccess)
-        e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFwd, s);
+    p.ticket = ws_at<int32_t>(workspace, 8);
+    p.n_items_out = n_ptr;
+    cudaError_t e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFwd, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
         e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
                                      n_ptr, nullptr, loss_out, s);
@@ -466,7 +679,7 @@ gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
 
 gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const int64_t *index, int64_t k,
-                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const float *teacher_logits, const float *teacher_rest, double temperature,
                         const uint8_t *row_mask, gbce_reduction reduction, const float *grad_out,
                         const float *rest_state, const int64_t *n_items, void *dlogits,
                         int64_t dlogits_row_stride, int32_t *dev_status, void *stream)
@@ -494,7 +707,8 @@ gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
     p.grad_out = grad_out;
     p.reduction = static_cast<int>(reduction);
     p.n_items = n_items;
-    set_dlogits(p, dtype, dlogits, dlogits_row_stride);
+    p.dlogits = dlogits;
+    p.d_stride = dlogits_row_stride;
     return cuda_status(launch_post(p, dtype, gbce::kOpDistill, gbce::kPassBwd,
                                    static_cast<cudaStream_t>(stream)));
 }
@@ -502,7 +716,7 @@ gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
 gbce_status distill_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
                                   int64_t vocab, int64_t row_stride, const int64_t *index,
                                   int64_t k, const float *teacher_logits,
-                                  const float *teacher_rest, float temperature,
+                                  const float *teacher_rest, double temperature,
                                   const uint8_t *row_mask, gbce_reduction reduction,
                                   const float *grad_out, float *loss_out, int64_t *n_items_out,
                                   void *dlogits, int64_t dlogits_row_stride, void *workspace,
@@ -537,13 +751,11 @@ gbce_status distill_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t 
     p.loss_rows = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, 256);
     p.grad_out = grad_out;
     p.reduction = static_cast<int>(reduction);
-    p.n_items = n_ptr;
-    set_dlogits(p, dtype, dlogits, dlogits_row_stride);
-    cudaError_t e = cudaSuccess;
-    if (reduction == GBCE_MEAN || n_items_out != nullptr)
-        e = gbce::launch_count_mask(row_mask, rows, n_ptr, s);
-    if (e == cudaSuccess)
-        e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFused, s);
+    p.dlogits = dlogits;
+    p.d_stride = dlogits_row_stride;
+    p.ticket = ws_at<int32_t>(workspace, 8);
+    p.n_items_out = n_ptr;
+    cudaError_t e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFused, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
         e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
                                      n_ptr, nullptr, loss_out, s);
@@ -576,27 +788,23 @@ gbce_status policy_loss(const float *logp, int64_t rows, const uint8_t *row_mask
         return GBCE_EINVAL;
     if ((st = check_workspace(workspace, workspace_bytes, loss_workspace(rows))) != GBCE_OK)
         return st;
-    int64_t *n_ptr = n_items_out != nullptr ? n_items_out : ws_at<int64_t>(workspace, 0);
-    float *loss_rows = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, 256);
-    cudaError_t e = cudaSuccess;
-    if (reduction == GBCE_MEAN || n_items_out != nullptr)
-        e = gbce::launch_count_mask(row_mask, rows, n_ptr, s);
-    if (e == cudaSuccess) {
-        gbce::policy_logp_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(
-            logp, rows, row_mask, policy_terms(options, advantages, old_logp, ref_logp),
-            static_cast<int>(reduction), grad_out, n_ptr, loss_rows, dlogp_out);
-        gbce::note_launches(1);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = gbce::launch_reduce_loss(loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
-                                     n_ptr, nullptr, loss_out, s);
-    return cuda_status(e);
+    gbce::PolicyRows q{};
+    q.logp = logp;
+    q.rows = rows;
+    q.mask = row_mask;
+    q.terms = policy_terms(options, advantages, old_logp, ref_logp);
+    q.reduction = static_cast<int>(reduction);
+    q.grad_out = grad_out;
+    q.loss_rows = reduction == GBCE_NONE ? loss_out : nullptr;
+    q.loss_out = loss_out;
+    q.dlogp = dlogp_out;
+    q.n_items = n_items_out != nullptr ? n_items_out : ws_at<int64_t>(workspace, 0);
+    return cuda_status(gbce::launch_policy_rows(q, ws_at<void>(workspace, 256), s));
 }
 
 gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
                                       int64_t vocab, int64_t row_stride, const int64_t *labels,
-                                      int64_t ignore_index, float temperature,
+                                      int64_t ignore_index, double temperature,
                                       const float *advantages, const float *old_logp,
                                       const float *ref_logp, const gbce_policy_options *options,
                                       gbce_reduction reduction, const float *grad_out,
@@ -634,14 +842,11 @@ gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int6
     p.logp_out = logp_out;
     p.grad_out = grad_out;
     p.reduction = static_cast<int>(reduction);
-    p.n_items = n_ptr;
-    set_dlogits(p, dtype, dlogits, dlogits_row_stride);
-    cudaError_t e = cudaSuccess;
-    if (reduction == GBCE_MEAN || n_items_out != nullptr)
-        e = gbce::launch_count_items(labels, rows, ignore_index, n_ptr, nullptr, nullptr, nullptr,
-                                     s);
-    if (e == cudaSuccess)
-        e = launch_post(p, dtype, gbce::kOpPolicy, gbce::kPassFused, s);
+    p.dlogits = dlogits;
+    p.d_stride = dlogits_row_stride;
+    p.ticket = ws_at<int32_t>(workspace, 8);
+    p.n_items_out = n_ptr;
+    cudaError_t e = launch_post(p, dtype, gbce::kOpPolicy, gbce::kPassFused, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
         e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
                                      n_ptr, nullptr, loss_out, s);
@@ -676,6 +881,7 @@ gbce_status preference_loss(const float *logp, int64_t rows, const uint8_t *row_
     if ((st = check_workspace(workspace, workspace_bytes,
                               preference_layout(rows, pairs).total)) != GBCE_OK)
         return st;
+    const PreferenceLayout w = preference_layout(rows, pairs);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PreferenceTerms t{};
     t.logp = logp;
@@ -687,32 +893,29 @@ gbce_status preference_loss(const float *logp, int64_t rows, const uint8_t *row_
     set_preference_options(t, options);
     t.reduction = static_cast<int>(reduction);
     t.grad_out = grad_out;
-    t.sign = 1.0f;
-    t.loss_pairs = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, 0);
+    t.loss_pairs = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, w.loss);
+    t.loss_out = reduction == GBCE_NONE ? nullptr : loss_out;
+    t.done = ws_at<int32_t>(workspace, 64);
     t.seq_score = seq_score_out;
     t.drow = dlogp_out;
     t.dev_status = dev_status;
-    cudaError_t e = cudaSuccess;
-    if (dlogp_out != nullptr && rows > 0) {
-        gbce::preference_outside_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(
-            rows, seq_offsets, 2 * pairs, dlogp_out);
-        gbce::note_launches(1);
-        e = cudaGetLastError();
-    }
+    const int64_t outside = dlogp_out != nullptr && rows > 0 ? (rows + 255) / 256 : 1;
+    gbce::preference_outside_kernel<<<static_cast<unsigned>(outside), 256, 0, s>>>(
+        rows, seq_offsets, 2 * pairs, dlogp_out, t.done);
+    gbce::note_launches(1);
+    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
         gbce::preference_pair_kernel<<<static_cast<unsigned>(pairs), gbce::kPairThreads, 0, s>>>(
             t);
         gbce::note_launches(1);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = reduce_pairs(t.loss_pairs, pairs, reduction, loss_out, s);
     return cuda_status(e);
 }
 
 gbce_status preference_loss_fwd_bwd_fused(
     const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t row_stride,
-    const int64_t *labels, int64_t ignore_index, float temperature, const int64_t *seq_offsets,
+    const int64_t *labels, int64_t ignore_index, double temperature, const int64_t *seq_offsets,
     int64_t pairs, const float *ref_logp, const gbce_preference_options *options,
     gbce_reduction reduction, const float *grad_out, float *loss_out, float *logp_out,
     float *seq_score_out, void *dlogits, int64_t dlogits_row_stride, void *workspace,
@@ -735,22 +938,25 @@ gbce_status preference_loss_fwd_bwd_fused(
     if ((st = check_workspace(workspace, workspace_bytes, w.total)) != GBCE_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int64_t *kept = ws_at<int64_t>(workspace, w.labels);
     float *logp = logp_out != nullptr ? logp_out : ws_at<float>(workspace, w.logp);
     float *grad = ws_at<float>(workspace, w.grad);
+    float *state = ws_at<float>(workspace, w.state);
     cudaError_t e = cudaSuccess;
+    PostParams p = post_params(logits, rows, vocab, row_stride, temperature, dev_status);
+    p.labels = labels;
+    p.ignore_index = ignore_index;
+    p.row_range = seq_offsets;
+    p.row_range_end = 2 * pairs;
     if (rows > 0) {
-        gbce::preference_labels_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(
-            labels, rows, ignore_index, seq_offsets, 2 * pairs, kept);
-        gbce::note_launches(1);
-        if ((e = cudaGetLastError()) != cudaSuccess)
-            return GBCE_ECUDA;
-        // log p of every kept row (its token CE loss goes to the gradient's place)
-        st = ce_fwd(logits, dtype, rows, vocab, row_stride, kept, ignore_index, temperature,
-                    GBCE_NONE, nullptr, grad, logp, nullptr, nullptr, workspace, workspace_bytes,
-                    dev_status, stream);
-        if (st != GBCE_OK)
-            return st;
+        // log p and the rest's state of every row of a sequence
+        p.logp_out = logp;
+        p.rest_state_out = state;
+        p.ticket = ws_at<int32_t>(workspace, 0);
+        p.zero_out = ws_at<int32_t>(workspace, 64);
+        p.keep_rows = 1;
+        e = launch_post(p, dtype, gbce::kOpToken, gbce::kPassFwd, s);
+    } else {
+        e = cudaMemsetAsync(workspace, 0, 256, s);
     }
     PreferenceTerms t{};
     t.logp = logp;
@@ -758,13 +964,14 @@ gbce_status preference_loss_fwd_bwd_fused(
     t.rows = rows;
     t.pairs = pairs;
     t.offsets = seq_offsets;
-    t.labels = kept;
+    t.labels = labels;
     t.ignore_index = ignore_index;
     set_preference_options(t, options);
     t.reduction = static_cast<int>(reduction);
     t.grad_out = grad_out;
-    t.sign = -1.0f;
     t.loss_pairs = reduction == GBCE_NONE ? loss_out : ws_at<float>(workspace, w.loss);
+    t.loss_out = reduction == GBCE_NONE ? nullptr : loss_out;
+    t.done = ws_at<int32_t>(workspace, 64);
     t.seq_score = seq_score_out;
     t.drow = grad;
     t.dev_status = dev_status;
@@ -774,12 +981,21 @@ gbce_status preference_loss_fwd_bwd_fused(
         gbce::note_launches(1);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = reduce_pairs(t.loss_pairs, pairs, reduction, loss_out, s);
-    if (e == cudaSuccess && rows > 0)
-        return ce_bwd(logits, dtype, rows, vocab, row_stride, kept, ignore_index, temperature,
-                      GBCE_NONE, nullptr, grad, logp, nullptr, dlogits, dlogits_row_stride,
-                      dev_status, stream);
+    if (e == cudaSuccess && rows > 0) {
+        // the rows that were read last are in L2 still: they come first
+        p.logp_out = nullptr;
+        p.rest_state_out = nullptr;
+        p.rest_state = state;
+        p.grad_out = grad;
+        p.reduction = GBCE_NONE;
+        p.ticket = ws_at<int32_t>(workspace, 128);
+        p.zero_out = nullptr;
+        p.keep_rows = 0;
+        p.reverse = 1;
+        p.dlogits = dlogits;
+        p.d_stride = dlogits_row_stride;
+        e = launch_post(p, dtype, gbce::kOpToken, gbce::kPassBwd, s);
+    }
     return cuda_status(e);
 }
 

@@ -183,9 +183,9 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     with _on(dev, stream):
         idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, logits.shape[:-1], rows, dev)
         mask = _mask(row_mask, rows, dev)
-        loss = torch.empty(rows if red == 0 else 1, dtype=torch.float32, device=dev)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         state = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        n_items = torch.empty(1, dtype=torch.int64, device=dev)
+        n_items = torch.empty((), dtype=torch.int64, device=dev)
         _check_status(dev_status, dev)
         ws, wp, wb = _row_scratch(workspace, rows, dev)
         st = lib.distill_fwd(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x), idx.data_ptr(), k,
@@ -193,7 +193,7 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
                              loss.data_ptr(), state.data_ptr(), n_items.data_ptr(), wp, wb,
                              _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "distill_fwd")
-    return DistillForward(loss if red == 0 else loss[0], state, n_items[0])
+    return DistillForward(loss, state, n_items)
 
 
 def distill_bwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
@@ -240,8 +240,8 @@ def distill_fwd_bwd_fused(logits: torch.Tensor, index, teacher_logits: torch.Ten
         idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, logits.shape[:-1], rows, dev)
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
-        loss = torch.empty(rows if red == 0 else 1, dtype=torch.float32, device=dev)
-        n_items = torch.empty(1, dtype=torch.int64, device=dev)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
+        n_items = torch.empty((), dtype=torch.int64, device=dev)
         dlogits, d = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _row_scratch(workspace, rows, dev)
@@ -251,7 +251,7 @@ def distill_fwd_bwd_fused(logits: torch.Tensor, index, teacher_logits: torch.Ten
                                        loss.data_ptr(), n_items.data_ptr(), d.data_ptr(), _stride(d),
                                        wp, wb, _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "distill_fwd_bwd_fused")
-    return DistillFused(loss if red == 0 else loss[0], dlogits, n_items[0])
+    return DistillFused(loss, dlogits, n_items)
 
 
 def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, grad_out=None,
@@ -278,8 +278,8 @@ def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, gr
         ref = _per_row(ref_logp, logp.shape, "ref_logp", dev)
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev) if want_grad else None
-        loss = torch.empty(rows if red == 0 else 1, dtype=torch.float32, device=dev)
-        n_items = torch.empty(1, dtype=torch.int64, device=dev)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
+        n_items = torch.empty((), dtype=torch.int64, device=dev)
         if want_grad and dlogp is None:
             dlogp = torch.empty(logp.shape, dtype=torch.float32, device=dev)
         _check_buffer(dlogp, "dlogp", torch.float32, rows, dev)
@@ -289,7 +289,7 @@ def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, gr
                              _ptr(dlogp) if want_grad else None, n_items.data_ptr(), wp, wb,
                              _stream_ptr(stream, dev))
     _check(st, "policy_loss")
-    return PolicyLoss(loss if red == 0 else loss[0], dlogp if want_grad else None, n_items[0])
+    return PolicyLoss(loss, dlogp if want_grad else None, n_items)
 
 
 def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp=None,
@@ -314,9 +314,9 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
         old = _per_row(old_logp, lead, "old_logp", dev)
         ref = _per_row(ref_logp, lead, "ref_logp", dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
-        loss = torch.empty(rows if red == 0 else 1, dtype=torch.float32, device=dev)
+        loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
-        n_items = torch.empty(1, dtype=torch.int64, device=dev)
+        n_items = torch.empty((), dtype=torch.int64, device=dev)
         dlogits, d = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _row_scratch(workspace, rows, dev)
@@ -327,7 +327,7 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
                                            _ptr(logp), n_items.data_ptr(), d.data_ptr(), _stride(d),
                                            wp, wb, _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "policy_loss_fwd_bwd_fused")
-    return PolicyFused(loss if red == 0 else loss[0], dlogits, logp, n_items[0])
+    return PolicyFused(loss, dlogits, logp, n_items)
 
 
 def _sequences(seq_offsets, lead, device):
@@ -375,7 +375,7 @@ def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_ou
         ref = _per_row(ref_logp, logp.shape, "ref_logp", dev)
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, pairs if red == 0 else 1, "pair", dev) if want_grad else None
-        loss = torch.empty(pairs if red == 0 else 1, dtype=torch.float32, device=dev)
+        loss = torch.empty((pairs,) if red == 0 else (), dtype=torch.float32, device=dev)
         score = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
         if want_grad and dlogp is None:
             dlogp = torch.empty(logp.shape, dtype=torch.float32, device=dev)
@@ -387,7 +387,7 @@ def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_ou
                                  _ptr(dlogp) if want_grad else None, score.data_ptr(), wp, wb,
                                  _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "preference_loss")
-    return PreferenceLoss(loss if red == 0 else loss[0], dlogp if want_grad else None, score)
+    return PreferenceLoss(loss, dlogp if want_grad else None, score)
 
 
 def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None, ref_logp=None,
@@ -412,7 +412,7 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
         lab = _flat(_int64(labels, dev), rows)
         ref = _per_row(ref_logp, lead, "ref_logp", dev)
         g = _upstream(grad_out, pairs if red == 0 else 1, "pair", dev)
-        loss = torch.empty(pairs if red == 0 else 1, dtype=torch.float32, device=dev)
+        loss = torch.empty((pairs,) if red == 0 else (), dtype=torch.float32, device=dev)
         logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
         score = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
         dlogits, d = _dlogits(dlogits, logits, x)
@@ -426,4 +426,4 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
                                                d.data_ptr(), _stride(d), wp, wb, _ptr(dev_status),
                                                _stream_ptr(stream, dev))
     _check(st, "preference_loss_fwd_bwd_fused")
-    return PreferenceFused(loss if red == 0 else loss[0], dlogits, logp, score)
+    return PreferenceFused(loss, dlogits, logp, score)

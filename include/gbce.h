@@ -551,7 +551,9 @@ gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, 
  * in fp64 in a fixed order; row losses and gradients are fp32 throughout,
  * dlogits rounded once.  workspace: gbce_workspace_size(rows, vocab, 1) bytes
  * unless stated, 16-byte aligned, of one call at a time (a captured graph
- * keeps its own); nothing in it needs zeroing.
+ * keeps its own); nothing in it needs zeroing.  The temperature is a double,
+ * in [1e-30, 1e30]: rounded to fp32 it would move every log p of a sequence in
+ * one direction.
  *
  * Source: the calls that the pages' log-probs and cross-entropies serve are
  * the RL and preference trainers of "perf(rlhf): chunk selective_log_softmax
@@ -599,7 +601,7 @@ gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, 
  */
 gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const int64_t *index, int64_t k,
-                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const float *teacher_logits, const float *teacher_rest, double temperature,
                         const uint8_t *row_mask, gbce_reduction reduction, float *loss_out,
                         float *rest_state_out, int64_t *n_items_out, void *workspace,
                         size_t workspace_bytes, int32_t *dev_status, void *stream);
@@ -607,7 +609,7 @@ gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
 /* The gradient from distill_fwd's rest state (same logits, teacher and T). */
 gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const int64_t *index, int64_t k,
-                        const float *teacher_logits, const float *teacher_rest, float temperature,
+                        const float *teacher_logits, const float *teacher_rest, double temperature,
                         const uint8_t *row_mask, gbce_reduction reduction, const float *grad_out,
                         const float *rest_state, const int64_t *n_items, void *dlogits,
                         int64_t dlogits_row_stride, int32_t *dev_status, void *stream);
@@ -616,7 +618,7 @@ gbce_status distill_bwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
 gbce_status distill_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
                                   int64_t vocab, int64_t row_stride, const int64_t *index,
                                   int64_t k, const float *teacher_logits,
-                                  const float *teacher_rest, float temperature,
+                                  const float *teacher_rest, double temperature,
                                   const uint8_t *row_mask, gbce_reduction reduction,
                                   const float *grad_out, float *loss_out, int64_t *n_items_out,
                                   void *dlogits, int64_t dlogits_row_stride, void *workspace,
@@ -662,7 +664,7 @@ gbce_status policy_loss(const float *logp, int64_t rows, const uint8_t *row_mask
  */
 gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t rows,
                                       int64_t vocab, int64_t row_stride, const int64_t *labels,
-                                      int64_t ignore_index, float temperature,
+                                      int64_t ignore_index, double temperature,
                                       const float *advantages, const float *old_logp,
                                       const float *ref_logp, const gbce_policy_options *options,
                                       gbce_reduction reduction, const float *grad_out,
@@ -726,7 +728,7 @@ gbce_status preference_loss(const float *logp, int64_t rows, const uint8_t *row_
  */
 gbce_status preference_loss_fwd_bwd_fused(
     const void *logits, gbce_dtype dtype, int64_t rows, int64_t vocab, int64_t row_stride,
-    const int64_t *labels, int64_t ignore_index, float temperature, const int64_t *seq_offsets,
+    const int64_t *labels, int64_t ignore_index, double temperature, const int64_t *seq_offsets,
     int64_t pairs, const float *ref_logp, const gbce_preference_options *options,
     gbce_reduction reduction, const float *grad_out, float *loss_out, float *logp_out,
     float *seq_score_out, void *dlogits, int64_t dlogits_row_stride, void *workspace,
