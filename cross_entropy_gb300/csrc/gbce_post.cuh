@@ -37,6 +37,46 @@ struct TwoFloat {
 
 __device__ __forceinline__ float scaled(float x, TwoFloat k) { return fmaf(x, k.hi, x * k.lo); }
 
+// A sum in two floats: 48 bits without the FP64 units, whose few lanes would set
+// the time of a short kernel.
+struct Sum2 {
+    float hi = 0.0f, lo = 0.0f;
+
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        hi = t;
+    }
+    __device__ __forceinline__ void add(Sum2 o)
+    {
+        add(o.hi);
+        lo = __fadd_rn(lo, o.lo);
+    }
+    // a - b, whose rounding error is kept
+    __device__ __forceinline__ void add_difference(float a, float b)
+    {
+        const float d = __fsub_rn(a, b), t = __fsub_rn(d, a);
+        add(d);
+        lo = __fadd_rn(lo, __fsub_rn(__fsub_rn(a, __fsub_rn(d, t)), __fadd_rn(b, t)));
+    }
+    // (what a NaN or an infinity leaves in lo says nothing)
+    __device__ __forceinline__ double value() const
+    {
+        return isfinite(hi) ? static_cast<double>(hi) + lo : static_cast<double>(hi);
+    }
+    __device__ __forceinline__ void warp_merge()
+    {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            Sum2 o;
+            o.hi = __shfl_down_sync(0xffffffffu, hi, off);
+            o.lo = __shfl_down_sync(0xffffffffu, lo, off);
+            add(o);
+        }
+    }
+};
+
 // -------------------------------------------------------------- the rest's sum
 
 // Online (max, sum) of the unlisted logits in the exp2 domain, as OnlineStats
@@ -124,8 +164,9 @@ enum RowState : int {
 // One row on its way through a CTA: what the list warp found out about it.
 struct RowSlot {
     int64_t r;
-    int state;     // RowState
-    int streamed;  // the producer copies the row (its state may turn out otherwise)
+    int early;     // RowState as far as the label, the mask and the columns tell
+    int state;     // ... and the teacher
+    int streamed;  // the producer copies the row
     float m, s;    // the rest's state: from the consumers (or, backward, for them)
     float gt;      // upstream gradient / T
     // distill: listed logits' max, and sum of 2^{(x - ml) c} without one holder of the
@@ -134,19 +175,20 @@ struct RowSlot {
     // token: column, logit; advantage, old and reference log p
     int y;
     float xy, adv, old_lp, ref_lp;
+    float dy;  // token: the gradient at its column
 };
 
 // The listed columns of a row, in shared memory.  Column col of a row is owned
 // by one consumer thread (the one whose sweep reads it); the entries of an owner
 // form a chain head[owner] -> next -> ... of which a thread walks only its own,
-// so that neither the sweep nor the patches need a barrier between threads.
+// so that leaving them out of the sweep needs no barrier between threads.
 struct ListRef {
     int32_t *head;  // [NC]
-    int32_t *col;   // [k] column; -1: no entry (or a repeat of an earlier one)
+    int32_t *col;   // [k] column; -1: no entry; -2 - column: a repeat of an earlier one
     int32_t *next;  // [k]
     float *x;       // [k] student logit
     float *lp;      // [k] teacher's log p
-    float *sum;     // [k] for repeats: log of the summed teacher terms
+    float *val;     // [k] gradient at the column
 };
 
 __host__ __device__ __forceinline__ int list_words(int nc, int k) { return nc + 5 * k; }
@@ -159,7 +201,7 @@ __device__ __forceinline__ ListRef list_at(int32_t *words, int nc, int k)
     L.next = L.col + k;
     L.x = reinterpret_cast<float *>(L.next + k);
     L.lp = L.x + k;
-    L.sum = L.lp + k;
+    L.val = L.lp + k;
     return L;
 }
 
@@ -199,46 +241,36 @@ __device__ __forceinline__ void warp_argmax(float &v, int32_t &k)
     }
 }
 
-// Read the teacher's entries of row r into L (one warp).  An index listed twice
-// is one column with the sum of both probabilities.  The teacher's distribution
-// is the softmax over its logits / T and teacher_rest.
+// The columns of row r's entries and their chains (one warp): what the sweep
+// needs.  An index listed twice is one column: the first entry keeps it and has
+// its bit set in `repeated` (this lane's entry lane + 32 i: bit i).  Returns
+// whether an index is out of range.
 template <typename T, int NC>
-__device__ void build_list(const PostParams &p, int64_t r, const T *row, const Slice &sl,
-                           const ListRef &L, RowSlot &slot, int lane)
+__device__ bool list_columns(const PostParams &p, int64_t r, const Slice &sl, const ListRef &L,
+                             int lane, uint32_t &repeated)
 {
     constexpr int VEC = Elem<T>::kVec;
     const int K = static_cast<int>(p.k);
-    const TwoFloat c = {p.c_hi, p.c_lo}, inv_t = {p.it_hi, p.it_lo};
-    const float inf = __builtin_huge_valf();
-    const float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
-    bool bad = false, nan_t = !(rest < inf);
+    const int64_t *index = p.index + r * K;
+    bool bad = false;
     for (int i = lane; i < NC; i += 32)
         L.head[i] = -1;
-#pragma unroll 2
+#pragma unroll 4
     for (int k = lane; k < K; k += 32) {
-        const int64_t t = p.index[r * K + k];
-        const float raw = p.teacher[r * K + k];
+        const int64_t t = index[k];
         const bool here = t >= 0 && t < p.vocab;
         bad |= !here && t != -1;
-        float tau = kNegInf, x = kNegInf;
-        if (here) {
-            x = Elem<T>::load(row + t);
-            tau = raw == kNegInf ? kNegInf : scaled(raw, inv_t);
-            nan_t |= !(raw < inf);
-        }
         L.col[k] = here ? static_cast<int32_t>(t) : -1;
-        L.x[k] = x;
-        L.lp[k] = tau;
     }
     bad = __any_sync(0xffffffffu, bad);
-    nan_t = __any_sync(0xffffffffu, nan_t);
     __syncwarp();
     for (int k = lane; k < K; k += 32)
         if (L.col[k] >= 0)
             L.next[k] = atomicExch(&L.head[column_owner<VEC, NC>(sl, L.col[k])], k);
     __syncwarp();
     // repeats: equal columns share an owner, so its chain shows them all
-    uint32_t repeat = 0, repeated = 0;
+    uint32_t repeat = 0;
+    repeated = 0;
     for (int k = lane, i = 0; k < K; k += 32, ++i) {
         const int32_t col = L.col[k];
         if (col < 0)
@@ -247,28 +279,58 @@ __device__ void build_list(const PostParams &p, int64_t r, const T *row, const S
             if (j != k && L.col[j] == col)
                 (j < k ? repeat : repeated) |= 1u << i;
     }
-    if (__any_sync(0xffffffffu, repeat != 0)) {
+    repeated &= ~repeat;
+    __syncwarp();
+    for (int k = lane, i = 0; k < K; k += 32, ++i)
+        if (repeat >> i & 1u)
+            L.col[k] = -2 - L.col[k];
+    return bad;
+}
+
+// The teacher's distribution, the softmax over its logits / T and teacher_rest,
+// and the student's logits at its columns (one warp, after list_columns).
+// A NaN or +inf among the teacher's logits makes the row invalid.
+template <typename T>
+__device__ void list_teacher(const PostParams &p, int64_t r, const T *row, const ListRef &L,
+                             RowSlot &slot, int lane, uint32_t repeated)
+{
+    const int K = static_cast<int>(p.k);
+    const TwoFloat c = {p.c_hi, p.c_lo}, inv_t = {p.it_hi, p.it_lo};
+    const float inf = __builtin_huge_valf();
+    const float *teacher = p.teacher + r * K;
+    const float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
+    bool nan_t = !(rest < inf);
+#pragma unroll 4
+    for (int k = lane; k < K; k += 32) {
+        const int32_t col = L.col[k];
+        const float raw = teacher[k], x = col >= 0 ? Elem<T>::load(row + col) : kNegInf;
+        nan_t |= col >= 0 && !(raw < inf);
+        L.x[k] = x;
+        L.lp[k] = col >= 0 && raw != kNegInf ? scaled(raw, inv_t) : kNegInf;
+    }
+    if (__any_sync(0xffffffffu, repeated != 0)) {
         // the first of several takes their sum, in entry order
         for (int k = lane, i = 0; k < K; k += 32, ++i) {
-            if (!(repeated >> i & 1u) || (repeat >> i & 1u))
+            if (!(repeated >> i & 1u))
                 continue;
+            const int32_t col = L.col[k];
+            const auto tau = [&](int j) {
+                if (L.col[j] != col && L.col[j] != -2 - col)
+                    return kNegInf;
+                const float raw = teacher[j];
+                nan_t |= !(raw < inf);
+                return raw == kNegInf ? kNegInf : scaled(raw, inv_t);
+            };
             float m = kNegInf, s = 0.0f;
             for (int j = k; j < K; ++j)
-                if (L.col[j] == L.col[k])
-                    m = fmaxf(m, L.lp[j]);
+                m = fmaxf(m, tau(j));
             for (int j = k; j < K; ++j)
-                if (L.col[j] == L.col[k] && L.lp[j] != kNegInf)
-                    s += expf(L.lp[j] - m);
-            L.sum[k] = s > 0.0f ? m + logf(s) : kNegInf;
-        }
-        __syncwarp();
-        for (int k = lane, i = 0; k < K; k += 32, ++i) {
-            if (repeat >> i & 1u)
-                L.col[k] = -1;
-            else if (repeated >> i & 1u)
-                L.lp[k] = L.sum[k];
+                if (tau(j) != kNegInf)
+                    s += expf(tau(j) - m);
+            L.lp[k] = s > 0.0f ? m + logf(s) : kNegInf;
         }
     }
+    nan_t = __any_sync(0xffffffffu, nan_t);
     // maxima: the teacher's over the entries and the rest, the student's
     float mt = kNegInf, ml = kNegInf;
     int32_t at = INT32_MAX, al = INT32_MAX;
@@ -308,16 +370,13 @@ __device__ void build_list(const PostParams &p, int64_t r, const T *row, const S
     sx = warp_sum(sx);
     const float lt = log1pf(st);
     for (int k = lane; k < K; k += 32)
-        if (L.col[k] >= 0)
-            L.lp[k] = (L.lp[k] - mt) - lt;
+        L.lp[k] = (L.lp[k] - mt) - lt;
     if (lane == 0) {
         // a row with a NaN (or +inf) listed logit has no softmax
         slot.ml = nan_x ? 0.0f : ml;
         slot.sl = nan_x ? kQuietNan : sx;
         slot.lp_rest = rest == kNegInf ? kNegInf : (rest - mt) - lt;
-        slot.state = (bad || nan_t) ? kRowInvalid : (mt == kNegInf ? kRowSkip : kRowLive);
-        if (bad && sl.first)
-            report(p.dev_status, GBCE_DEV_BAD_INDEX);
+        slot.state = nan_t ? kRowInvalid : (mt == kNegInf ? kRowSkip : kRowLive);
     }
 }
 
@@ -471,13 +530,13 @@ __device__ __forceinline__ float post_upstream(const PostParams &p, int64_t r, i
 // consumers, of the three CTA shapes (see launch_post).
 template <int SHAPE> struct PostShape;
 template <> struct PostShape<kShapeLong> {
-    static constexpr int kWarps = 24, kChunk = 49152, kStages = 4, kSlots = 2, kCtasPerSm = 1;
+    static constexpr int kWarps = 24, kChunk = 49152, kStages = 4, kSlots = 3, kCtasPerSm = 1;
 };
 template <> struct PostShape<kShapeMid> {
-    static constexpr int kWarps = 8, kChunk = 16384, kStages = 4, kSlots = 2, kCtasPerSm = 3;
+    static constexpr int kWarps = 8, kChunk = 16384, kStages = 4, kSlots = 3, kCtasPerSm = 3;
 };
 template <> struct PostShape<kShapeShort> {
-    static constexpr int kWarps = 4, kChunk = 8192, kStages = 2, kSlots = 2, kCtasPerSm = 5;
+    static constexpr int kWarps = 4, kChunk = 8192, kStages = 2, kSlots = 4, kCtasPerSm = 5;
 };
 
 template <int SHAPE> constexpr int post_threads() { return (PostShape<SHAPE>::kWarps + 2) * 32; }
@@ -566,6 +625,24 @@ __device__ __forceinline__ StoreGeom store_geom(const T *drow, const RowGeom &g,
     return d;
 }
 
+// The columns of a gradient row that a slice's CTA stores.
+struct StoredRange {
+    int32_t vecs;    // vectors
+    int64_t lo, hi;  // columns
+};
+
+template <int VEC>
+__device__ __forceinline__ StoredRange stored_range(const Slice &sl, const StoreGeom &d, int64_t V)
+{
+    const int64_t here = d.vecs - sl.v0, most = sl.v1 - sl.v0;
+    const int64_t first = sl.g.head + d.sh + sl.v0 * VEC;
+    StoredRange t;
+    t.vecs = static_cast<int32_t>(here < most ? (here > 0 ? here : 0) : most);
+    t.lo = sl.first ? 0 : first;
+    t.hi = sl.last ? V : first + static_cast<int64_t>(t.vecs) * VEC;
+    return t;
+}
+
 template <typename T, int OP, int PASS, int SHAPE>
 __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtasPerSm)
     post_kernel(const PostParams p)
@@ -587,9 +664,9 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
         (reinterpret_cast<uintptr_t>(dyn_smem) + (kRingAlign - 1)) & ~uintptr_t(kRingAlign - 1));
     int32_t *lists = reinterpret_cast<int32_t *>(ring + S * PITCH);
     __shared__ uint64_t full_bar[S], empty_bar[S];
-    // rows: known (to the producer), list built (to the consumers), statistics
-    // done (to the list warp), slot free again
-    __shared__ uint64_t row_bar[Q], list_bar[Q], stat_bar[Q], free_bar[Q];
+    // rows: known (to the producer), columns known and all else known (to the
+    // consumers), statistics done (to the list warp), slot free again
+    __shared__ uint64_t row_bar[Q], cols_bar[Q], list_bar[Q], stat_bar[Q], free_bar[Q];
     __shared__ RowSlot slots[Q];
     // per-warp partials, double-buffered by row (a warp may be a row ahead)
     __shared__ float red_m[2][NCW], red_s[2][NCW];
@@ -611,6 +688,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
         }
         for (int i = 0; i < Q; ++i) {
             mbar_init(&row_bar[i], 1);
+            mbar_init(&cols_bar[i], 1);
             mbar_init(&list_bar[i], 1);
             mbar_init(&stat_bar[i], 1);
             mbar_init(&free_bar[i], NCW + 1);
@@ -636,14 +714,17 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
     // ------------------------------------------------------------ list warp
     if (warp == NCW + 1) {
         bool ok = true;
-        // a swept row's loss and statistics (by the first slice's CTA)
+        const auto list_of = [&](int q) {
+            return list_at(lists + q * list_words(NC, static_cast<int>(p.k)), NC,
+                           static_cast<int>(p.k));
+        };
+        // what follows from row i's statistics: its loss (by the first slice's
+        // CTA), and the gradients at its listed columns
         const auto finish = [&](uint32_t i) {
             const int q = i % Q;
-            const RowSlot &w = slots[q];
-            if (!kStats || w.state == kRowEnd)
-                return;
+            RowSlot &w = slots[q];
             if (w.state != kRowLive) {
-                if (lane == 0 && split == 0) {
+                if (kStats && lane == 0 && split == 0) {
                     const float fill = w.state == kRowSkip ? 0.0f : kQuietNan;
                     if (p.loss_rows != nullptr)
                         p.loss_rows[w.r] = fill;
@@ -656,37 +737,79 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 }
                 return;
             }
-            if (!mbar_wait(&stat_bar[q], (i / Q) & 1)) {
+            if (kStats && !mbar_wait(&stat_bar[q], (i / Q) & 1)) {
                 ok = false;
                 return;
             }
-            if (split != 0)
-                return;
             const float m = w.m, s = w.s;
-            if (p.rest_state_out != nullptr && lane == 0) {
+            if (kStats && p.rest_state_out != nullptr && lane == 0 && split == 0) {
                 p.rest_state_out[2 * w.r] = m;
                 p.rest_state_out[2 * w.r + 1] = s;
             }
             if (kList) {
-                const ListRef L = list_at(lists + q * list_words(NC, p.k), NC, p.k);
+                const ListRef L = list_of(q);
                 const StudentRow st = student_row(m, s, w.ml, w.sl, c, inv_t);
                 float kl = lane == 0 ? kl_term(w.lp_rest, st.log_rest) : 0.0f;
-                for (int k = lane; k < p.k; k += 32)
-                    if (L.col[k] >= 0)
-                        kl += kl_term(L.lp[k], student_logp(st, L.x[k], inv_t));
+                for (int k = lane; k < p.k; k += 32) {
+                    if (L.col[k] < 0)
+                        continue;
+                    const float lp = L.lp[k], lq = student_logp(st, L.x[k], inv_t);
+                    if (kStats)
+                        kl += kl_term(lp, lq);
+                    if (kGrad)
+                        L.val[k] = w.gt * share_gap(lp, lq);
+                }
                 kl = warp_sum(kl);
-                if (lane == 0)
+                if (kStats && lane == 0 && split == 0)
                     p.loss_rows[w.r] = kl;
             } else if (lane == 0) {
                 const float lp = token_logp(m, s, w.xy, inv_t);
-                if (p.logp_out != nullptr)
+                float slope = w.gt;
+                if (kStats && p.logp_out != nullptr && split == 0)
                     p.logp_out[w.r] = lp;
                 if (OP == kOpPolicy) {
                     float loss, dlp;
                     policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
-                    p.loss_rows[w.r] = loss;
+                    if (split == 0)
+                        p.loss_rows[w.r] = loss;
+                    slope *= dlp;
                 }
+                if (kGrad)
+                    w.dy = -slope * expm1f(lp);
             }
+        };
+        // row i's listed columns, over what the sweep stored there (every thread
+        // of this CTA has stored its part: the slot is free)
+        const auto patch = [&](uint32_t i) {
+            const int q = i % Q;
+            const RowSlot &w = slots[q];
+            if (!kGrad || w.state != kRowLive)
+                return;
+            const T *row = static_cast<const T *>(p.logits) + w.r * p.row_stride;
+            T *drow = static_cast<T *>(p.dlogits) + w.r * p.d_stride;
+            const Slice sl = slice_of(row);
+            const StoreGeom dg = store_geom<T>(drow, sl.g, V);
+            const StoredRange range = stored_range<VEC>(sl, dg, V);
+            if (kList) {
+                const ListRef L = list_of(q);
+                for (int k = lane; k < p.k; k += 32)
+                    if (L.col[k] >= range.lo && L.col[k] < range.hi)
+                        E::store(drow + L.col[k], L.val[k]);
+            } else if (lane == 0 && w.y >= range.lo && w.y < range.hi) {
+                E::store(drow + w.y, w.dy);
+            }
+        };
+        // row i is done when its slot is free: then its patches, and the slot is
+        // this warp's again
+        const auto retire = [&](uint32_t i) {
+            finish(i);
+            __syncwarp();
+            if (ok && !mbar_wait(&free_bar[i % Q], (i / Q) & 1))
+                ok = false;
+            if (ok)
+                patch(i);
+            __syncwarp();
+            return ok;
         };
         const int64_t lo = p.row_range != nullptr ? p.row_range[0] : 0;
         const int64_t hi = p.row_range != nullptr ? p.row_range[p.row_range_end] : p.rows;
@@ -695,13 +818,8 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
         uint32_t i = 0;
         for (;; ++i) {
             const int q = i % Q;
-            if (i >= Q) {
-                finish(i - Q);
-                if (!ok || !mbar_wait(&free_bar[q], (i / Q - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-            }
+            if (i >= Q && !retire(i - Q))
+                break;
             RowSlot &w = slots[q];
             __syncwarp();
             const bool end = t >= p.rows;
@@ -720,12 +838,26 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                         state = kRowInvalid;
                 }
             }
+            const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
+            uint32_t repeated = 0;
             if (lane == 0) {
                 w.r = r;
-                w.state = state;
+                w.state = w.early = state;
                 w.streamed = state == kRowLive;
+                w.y = static_cast<int>(lab);
                 mbar_arrive(&row_bar[q]);
             }
+            if (kList && state == kRowLive &&
+                list_columns<T, NC>(p, r, slice_of(row), list_of(q), lane, repeated)) {
+                state = kRowInvalid;
+                if (lane == 0)
+                    w.state = w.early = state;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&cols_bar[q]);
+            if (state == kRowInvalid && lane == 0 && split == 0)
+                report(p.dev_status, kList ? GBCE_DEV_BAD_INDEX : GBCE_DEV_BAD_LABEL);
             if (i == 0 && kGrad && p.n_items != nullptr && p.reduction == GBCE_MEAN)
                 n_items = *p.n_items;
             if (i == 0 && p.n_items_out != nullptr &&
@@ -751,7 +883,6 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 next = clusters + __shfl_sync(0xffffffffu, n, 0);
             }
             if (state == kRowLive) {
-                const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
                 if (lane == 0) {
                     if (kGrad)
                         w.gt = scaled(post_upstream(p, r, n_items), inv_t);
@@ -759,22 +890,16 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                         w.m = p.rest_state[2 * r];
                         w.s = p.rest_state[2 * r + 1];
                     }
-                    if (!kList) {
-                        w.y = static_cast<int>(lab);
+                    if (!kList)
                         w.xy = E::load(row + lab);
-                    }
                     if (OP == kOpPolicy) {
                         w.adv = p.policy.advantages[r];
                         w.old_lp = p.policy.old_logp != nullptr ? p.policy.old_logp[r] : 0.0f;
                         w.ref_lp = p.policy.ref_logp != nullptr ? p.policy.ref_logp[r] : 0.0f;
                     }
                 }
-                if (kList) {
-                    const ListRef L = list_at(lists + q * list_words(NC, p.k), NC, p.k);
-                    build_list<T, NC>(p, r, row, slice_of(row), L, w, lane);
-                }
-            } else if (state == kRowInvalid && lane == 0 && split == 0) {
-                report(p.dev_status, GBCE_DEV_BAD_LABEL);
+                if (kList)
+                    list_teacher<T>(p, r, row, list_of(q), w, lane, repeated);
             }
             __syncwarp();
             if (lane == 0)
@@ -783,9 +908,8 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 break;
             t = next;
         }
-        if (ok)
-            for (uint32_t j = i > Q - 1 ? i - (Q - 1) : 0; j < i && ok; ++j)
-                finish(j);
+        for (uint32_t j = i > Q - 1 ? i - (Q - 1) : 0; j < i && ok; ++j)
+            retire(j);
         if (!ok && lane == 0)
             report(p.dev_status, GBCE_DEV_TIMEOUT);
         return;
@@ -855,13 +979,13 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
     bool alive = true;
     for (uint32_t i = 0;; ++i) {
         const int q = i % Q;
-        if (!mbar_wait(&list_bar[q], (i / Q) & 1)) {
+        if (!mbar_wait(&cols_bar[q], (i / Q) & 1)) {
             report(p.dev_status, GBCE_DEV_TIMEOUT);
             break;
         }
         RowSlot &w = slots[q];
-        const int state = w.state;
-        if (state == kRowEnd)
+        const int early = w.early;
+        if (early == kRowEnd)
             break;
         const int64_t r = w.r;
         const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
@@ -886,17 +1010,15 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 ++lap;
             }
         };
-        if (state != kRowLive) {
-            if (w.streamed)  // (found out after its copies began)
-                for (int32_t j = 0; j < nchunks * kPasses; ++j) {
-                    wait_chunk();
-                    done_chunk();
-                }
-            if (kStats && tid == 0)
-                mbar_arrive(&stat_bar[q]);
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&free_bar[q]);
+        // the rest of a row that turns out to be left out or invalid: its copies
+        // (of `passes` more passes) are let go by, and its gradient is filled
+        const auto drop = [&](int state, int passes, bool swept) {
+            for (int32_t j = 0; j < nchunks * passes; ++j) {
+                wait_chunk();
+                done_chunk();
+            }
+            if (kStats && !swept && tid == 0)
+                mbar_arrive(&stat_bar[q]);  // (every row completes a phase of it)
             if (kGrad) {
                 const float fill = state == kRowSkip ? 0.0f : kQuietNan;
                 const RowGeom gd = row_geom<T>(drow, V);
@@ -914,34 +1036,47 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 if (sl.last && gd.tail0 + tid < V)
                     E::store(drow + gd.tail0 + tid, fill);
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&free_bar[q]);
+        };
+        if (early != kRowLive) {
+            drop(early, w.streamed ? kPasses : 0, false);
             continue;
         }
 
-        const ListRef L = kList ? list_at(lists + q * list_words(NC, p.k), NC, p.k) : ListRef{};
-        const int32_t y = kList ? -1 : w.y;
-        const int first_own = kList ? L.head[tid] : -1;
         const int32_t col0 = head + static_cast<int32_t>(sl.v0) * VEC;  // of the slice's vector 0
-        // calls f(column, entry) for the listed columns this thread owns
-        const auto each_own = [&](auto &&f) {
-            if constexpr (kList) {
-                for (int j = first_own; j >= 0; j = L.next[j])
-                    if (L.col[j] >= 0)
-                        f(L.col[j], j);
-            } else {
-                if (column_owner<VEC, NC>(sl, y) == tid)
-                    f(y, 0);
-            }
-        };
-        bool own_any = false;  // in this slice's vectors
-        each_own([&](int32_t col, int) { own_any |= col >= col0 && col < col0 + nvec * VEC; });
-        const auto is_listed = [&](int32_t at) {
-            bool hit = false;
-            each_own([&](int32_t col, int) { hit |= col == at; });
-            return hit;
-        };
-
         float m, s;
         if (kStats) {
+            // the listed columns this thread owns
+            const ListRef L = kList ? list_at(lists + q * list_words(NC, static_cast<int>(p.k)), NC,
+                                              static_cast<int>(p.k))
+                                    : ListRef{};
+            const int own = kList ? L.head[tid] : -1;
+            int32_t own_col = -1;
+            bool own_any = own >= 0, own_more = false;  // one of them, more than one
+            if constexpr (kList) {
+                if (own_any) {
+                    own_col = L.col[own];
+                    own_more = L.next[own] >= 0;
+                }
+            } else if (column_owner<VEC, NC>(sl, w.y) == tid) {
+                own_col = w.y;
+                own_any = true;
+            }
+            const auto each_own = [&](auto &&f) {
+                f(own_col);
+                if constexpr (kList) {
+                    if (own_more)
+                        for (int j = L.next[own]; j >= 0; j = L.next[j])
+                            f(L.col[j]);
+                }
+            };
+            const auto is_listed = [&](int32_t at) {
+                bool hit = false;
+                each_own([&](int32_t col) { hit |= col == at; });
+                return hit;
+            };
             RestStats st;
             if (sl.first && tid < sl.g.head)
                 st.add1(is_listed(tid) ? kNegInf : E::load(row + tid), c);
@@ -958,9 +1093,9 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                     // listed columns leave the sum: -inf in the copied row, written
                     // by the thread that alone reads their vector
                     bool wrote = false;
-                    each_own([&](int32_t col, int) {
+                    each_own([&](int32_t col) {
                         const int32_t e = col - col0 - vb0 * VEC;
-                        if (col >= col0 && e >= 0 && e < nv * VEC) {
+                        if (e >= 0 && e < nv * VEC) {
                             reinterpret_cast<T *>(chunk)[e] = neg_inf_as(T());
                             wrote = true;
                         }
@@ -1036,14 +1171,23 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 w.s = s;
                 mbar_arrive(&stat_bar[q]);
             }
-        } else {
-            m = w.m;
-            s = w.s;
         }
 
         if (kGrad) {
+            if (!mbar_wait(&list_bar[q], (i / Q) & 1)) {
+                report(p.dev_status, GBCE_DEV_TIMEOUT);
+                break;
+            }
+            if (kList && w.state != kRowLive) {
+                drop(w.state, 1, true);
+                continue;
+            }
+            if (!kStats) {
+                m = w.m;
+                s = w.s;
+            }
             const float gt = w.gt;
-            float gs, dy = 0.0f;
+            float gs;
             if (kList) {
                 gs = gt * share_gap(w.lp_rest,
                                     student_row(m, s, w.ml, w.sl, c, inv_t).log_rest);
@@ -1055,8 +1199,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                     policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
                     slope *= dlp;
                 }
-                dy = -slope * expm1f(lp);
-                gs = -dy;
+                gs = slope * expm1f(lp);
             }
             const GradConsts gk = rest_consts(m, s, c.hi + c.lo, gs);
             constexpr int32_t kNoLabel = 0x7fffffff;
@@ -1066,9 +1209,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 E::store(drow + tid, grad_scalar(E::load(row + tid), gk));
             if (sl.last && dg.end + tid < V)
                 E::store(drow + dg.end + tid, grad_scalar(E::load(row + dg.end + tid), gk));
-            // this slice's stored vectors: [0, stored) from drow + dbase on
-            const int64_t here = dg.vecs - sl.v0;
-            const int32_t stored = static_cast<int32_t>(here < nvec ? (here > 0 ? here : 0) : nvec);
+            const int32_t stored = stored_range<VEC>(sl, dg, V).vecs;
             T *dbase = drow + col0 + sh;
             for (int32_t j = 0; j < nchunks; ++j) {
                 const uint4 *chunk = wait_chunk();
@@ -1099,23 +1240,6 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 }
                 done_chunk();
             }
-            // the listed columns, over what the sweep stored there: by the same
-            // thread, or (rows of another phase: other threads' vectors) once
-            // every thread of this CTA has stored
-            if (sh != 0)
-                named_sync(2, NC);
-            const int32_t s0 = sl.first ? 0 : col0 + sh;
-            const int64_t s1 = sl.last ? V : static_cast<int64_t>(col0) + sh + stored * VEC;
-            each_own([&](int32_t col, int j) {
-                if (col < s0 || col >= s1)
-                    return;  // (stored by another slice's CTA)
-                float v = dy;
-                if constexpr (kList)
-                    v = w.gt * share_gap(L.lp[j],
-                                         student_logp(student_row(m, s, w.ml, w.sl, c, inv_t),
-                                                      L.x[j], inv_t));
-                E::store(drow + col, v);
-            });
         }
         __syncwarp();
         if (lane == 0)

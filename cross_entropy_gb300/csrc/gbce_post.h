@@ -75,4 +75,9 @@ cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stre
 cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
                               int32_t *zero_out, cudaStream_t stream);
 
+// loss_out[0] = sum of the rows' losses, or (mean) that over *n_items, 0 for no
+// items; in a fixed order.
+cudaError_t launch_sum_rows(const float *loss_rows, int64_t rows, int mean, const int64_t *n_items,
+                            float *loss_out, cudaStream_t stream);
+
 }  // namespace gbce

@@ -54,6 +54,77 @@ cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- losses summed
+
+constexpr int kSumThreads = 1024, kSumWarps = kSumThreads / 32;
+
+// Sum and count over the CTA in a fixed order, in thread 0.
+__device__ __forceinline__ void cta_sum(Sum2 &s, int64_t &n, Sum2 *scratch, int64_t *counts)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = blockDim.x >> 5;
+    s.warp_merge();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        n += __shfl_down_sync(0xffffffffu, n, off);
+    if (lane == 0) {
+        scratch[warp] = s;
+        counts[warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        s = lane < warps ? scratch[lane] : Sum2{};
+        n = lane < warps ? counts[lane] : 0;
+        s.warp_merge();
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            n += __shfl_down_sync(0xffffffffu, n, off);
+    }
+}
+
+__device__ __forceinline__ float reduced(Sum2 s, bool mean, int64_t n)
+{
+    const double v = s.value();
+    return static_cast<float>(mean ? (n > 0 ? v / static_cast<double>(n) : 0.0) : v);
+}
+
+__global__ void __launch_bounds__(kSumThreads)
+    sum_rows_kernel(const float *loss_rows, int64_t rows, int mean, const int64_t *n_items,
+                    float *loss_out)
+{
+    __shared__ Sum2 scratch[kSumWarps];
+    __shared__ int64_t counts[kSumWarps];
+    // launched as a dependent of the kernel that wrote the row losses
+    grid_dependency_wait();
+    const int64_t kept = mean ? *n_items : 0;
+    Sum2 s;
+    int64_t n = 0;
+#pragma unroll 8
+    for (int64_t r = threadIdx.x; r < rows; r += kSumThreads)
+        s.add(loss_rows[r]);
+    cta_sum(s, n, scratch, counts);
+    if (threadIdx.x == 0)
+        *loss_out = reduced(s, mean != 0, kept);
+}
+
+cudaError_t launch_sum_rows(const float *loss_rows, int64_t rows, int mean, const int64_t *n_items,
+                            float *loss_out, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kSumThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err =
+        cudaLaunchKernelEx(&cfg, sum_rows_kernel, loss_rows, rows, mean, n_items, loss_out);
+    note_launches(1);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 // ------------------------------------------- policy loss of given log-probs
 
 struct PolicyRows {
@@ -69,15 +140,76 @@ struct PolicyRows {
     int64_t *n_items;
 };
 
-// A row's loss (0 where it is left out) and, from the upstream gradient, its
-// derivative.
-__device__ __forceinline__ float policy_one_row(const PolicyRows &q, int64_t r, bool live, float g)
+constexpr int kPolicyCtas = 8;  // of the cluster
+
+struct ClusterSum {
+    Sum2 scratch[kSumWarps];
+    int64_t counts[kSumWarps];
+    Sum2 cta;
+    int64_t cta_count;
+};
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// Sum and count over the cluster in a fixed order, to every thread: over each
+// CTA, then the CTAs' parts in rank order.
+__device__ void cluster_sum(ClusterSum &own, Sum2 &s, int64_t &n)
+{
+    cta_sum(s, n, own.scratch, own.counts);
+    if (threadIdx.x == 0) {
+        own.cta = s;
+        own.cta_count = n;
+    }
+    cluster_barrier();
+    const uint32_t a = smem_addr(&own.cta), b = smem_addr(&own.cta_count);
+    s = Sum2{};
+    n = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kPolicyCtas; ++i) {
+        Sum2 v;
+        int64_t k;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(v.hi), "=f"(v.lo)
+                     : "r"(map_to_rank(a, i)));
+        asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(k) : "r"(map_to_rank(b, i)));
+        s.add(v);
+        n += k;
+    }
+    cluster_barrier();  // (no CTA leaves, or writes its sums anew, before all have read them)
+}
+
+// Inputs of a row, read before the count is known.
+struct PolicyInputs {
+    float lp, adv, old_lp, ref_lp;
+    bool live;
+};
+
+__device__ __forceinline__ PolicyInputs policy_inputs(const PolicyRows &q, int64_t r)
+{
+    PolicyInputs x = {0.0f, 0.0f, 0.0f, 0.0f, false};
+    if (r < q.rows) {
+        x.live = q.mask == nullptr || q.mask[r] != 0;
+        x.lp = q.logp[r];
+        x.adv = q.terms.advantages[r];
+        x.old_lp = q.terms.old_logp != nullptr ? q.terms.old_logp[r] : 0.0f;
+        x.ref_lp = q.terms.ref_logp != nullptr ? q.terms.ref_logp[r] : 0.0f;
+    }
+    return x;
+}
+
+// A row's loss (0 where it is left out), and its derivative stored.
+__device__ __forceinline__ float policy_one_row(const PolicyRows &q, int64_t r,
+                                                const PolicyInputs &x, float g)
 {
     float loss = 0.0f, d = 0.0f;
-    if (live) {
-        const PolicyTerms &t = q.terms;
-        policy_row(t, t.advantages[r], t.old_logp != nullptr ? t.old_logp[r] : 0.0f,
-                   t.ref_logp != nullptr ? t.ref_logp[r] : 0.0f, q.logp[r], loss, d);
+    if (r >= q.rows)
+        return 0.0f;
+    if (x.live) {
+        policy_row(q.terms, x.adv, x.old_lp, x.ref_lp, x.lp, loss, d);
         if (q.reduction == GBCE_NONE && q.dlogp != nullptr)
             g = q.grad_out[r];
         d *= g;
@@ -89,182 +221,110 @@ __device__ __forceinline__ float policy_one_row(const PolicyRows &q, int64_t r, 
     return loss;
 }
 
-constexpr int kPolicyThreads = 1024, kPolicyWarps = kPolicyThreads / 32;
-constexpr int kPolicyCtas = 8;  // of the cluster
-
-// Sums of a count and a loss over the cluster in a fixed order, to every thread:
-// over the CTA's warps, then over the CTAs' parts in rank order.
-struct ClusterSum {
-    double loss[kPolicyWarps];
-    int64_t count[kPolicyWarps];
-    double cta_loss;
-    int64_t cta_count;
-};
-
-__device__ __forceinline__ void warp_sums(double &s, int64_t &n)
+__device__ __forceinline__ float policy_upstream(const PolicyRows &q, int64_t n)
 {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, off);
-        n += __shfl_xor_sync(0xffffffffu, n, off);
-    }
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-
-__device__ void cluster_sums(ClusterSum &own, double &s, int64_t &n)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    warp_sums(s, n);
-    if (lane == 0) {
-        own.loss[warp] = s;
-        own.count[warp] = n;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        s = own.loss[lane];
-        n = own.count[lane];
-        warp_sums(s, n);
-        if (lane == 0) {
-            own.cta_loss = s;
-            own.cta_count = n;
-        }
-    }
-    cluster_barrier();
-    const uint32_t a = smem_addr(&own.cta_loss), b = smem_addr(&own.cta_count);
-    s = 0.0;
-    n = 0;
-    for (uint32_t i = 0; i < kPolicyCtas; ++i) {
-        double v;
-        int64_t k;
-        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(a, i)));
-        asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(k) : "r"(map_to_rank(b, i)));
-        s += v;
-        n += k;
-    }
-    cluster_barrier();  // (no CTA leaves, or writes its sums anew, before all have read them)
+    if (q.dlogp == nullptr || q.reduction == GBCE_NONE)
+        return 1.0f;
+    return q.reduction == GBCE_MEAN && n > 0 ? q.grad_out[0] / static_cast<float>(n)
+                                             : q.grad_out[0];
 }
 
 // One cluster for all rows: the count, the rows, the reduced loss, in one
 // launch.  Latency is what such a call costs (17 to 21 bytes and some twenty
-// operations a row): three launches of one CTA, one CTA and a grid took 48 us at
-// 65536 rows.
-__global__ void __cluster_dims__(kPolicyCtas, 1, 1) __launch_bounds__(kPolicyThreads)
+// operations a row), so the first rows' inputs are read along with the mask:
+// 65536 rows took 48 us as three launches with one CTA for each of the sums.
+__global__ void __cluster_dims__(kPolicyCtas, 1, 1) __launch_bounds__(kSumThreads)
     policy_cluster_kernel(const PolicyRows q)
 {
     __shared__ ClusterSum sums;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPolicyThreads + threadIdx.x;
-    constexpr int64_t kStep = static_cast<int64_t>(kPolicyCtas) * kPolicyThreads;
-    double s = 0.0;
+    constexpr int kAhead = 4;
+    constexpr int64_t kStep = static_cast<int64_t>(kPolicyCtas) * kSumThreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
+    PolicyInputs x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        x[i] = policy_inputs(q, first + i * kStep);
+    Sum2 s;
     int64_t n = 0;
-    if (q.mask == nullptr)
-        n = first == 0 ? q.rows : 0;
-    else
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        n += x[i].live;
 #pragma unroll 4
-        for (int64_t r = first; r < q.rows; r += kStep)
-            n += q.mask[r] != 0;
-    cluster_sums(sums, s, n);
-    float g = 1.0f;
-    if (q.dlogp != nullptr && q.reduction != GBCE_NONE)
-        g = q.reduction == GBCE_MEAN && n > 0 ? q.grad_out[0] / static_cast<float>(n)
-                                              : q.grad_out[0];
-    s = 0.0;
+    for (int64_t r = first + kAhead * kStep; r < q.rows; r += kStep)
+        n += q.mask == nullptr || q.mask[r] != 0;
+    cluster_sum(sums, s, n);
+    const float g = policy_upstream(q, n);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        s.add(policy_one_row(q, first + i * kStep, x[i], g));
 #pragma unroll 2
-    for (int64_t r = first; r < q.rows; r += kStep)
-        s += policy_one_row(q, r, q.mask == nullptr || q.mask[r] != 0, g);
+    for (int64_t r = first + kAhead * kStep; r < q.rows; r += kStep)
+        s.add(policy_one_row(q, r, policy_inputs(q, r), g));
     if (first == 0)
         *q.n_items = n;
     if (q.reduction == GBCE_NONE)
         return;
     const int64_t kept = n;
-    cluster_sums(sums, s, n);
+    cluster_sum(sums, s, n);
     if (first == 0)
-        *q.loss_out = static_cast<float>(
-            q.reduction == GBCE_MEAN ? (kept > 0 ? s / static_cast<double>(kept) : 0.0) : s);
+        *q.loss_out = reduced(s, q.reduction == GBCE_MEAN, kept);
 }
 
 // Many rows: a grid counts the rows of each CTA's part, a grid takes them (every
 // CTA summing the parts' counts itself), one CTA sums the parts' losses.
 constexpr int kPolicyPartRows = 4096, kPolicyMaxParts = 65536;
 
-__global__ void __launch_bounds__(kPolicyThreads)
+__global__ void __launch_bounds__(kSumThreads)
     policy_count_kernel(const uint8_t *mask, int64_t rows, int64_t part, int64_t *counts)
 {
     __shared__ ClusterSum sums;
     const int64_t lo = blockIdx.x * part, hi = lo + part < rows ? lo + part : rows;
-    double s = 0.0;
+    Sum2 s;
     int64_t n = 0;
-    for (int64_t r = lo + threadIdx.x; r < hi; r += kPolicyThreads)
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kSumThreads)
         n += mask == nullptr || mask[r] != 0;
-    warp_sums(s, n);
-    if ((threadIdx.x & 31) == 0)
-        sums.count[threadIdx.x >> 5] = n;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        n = sums.count[threadIdx.x];
-        warp_sums(s, n);
-        if (threadIdx.x == 0)
-            counts[blockIdx.x] = n;
-    }
+    cta_sum(s, n, sums.scratch, sums.counts);
+    if (threadIdx.x == 0)
+        counts[blockIdx.x] = n;
 }
 
-// The CTA's sums of (a thread's) loss and count, to every thread.
-__device__ void cta_sums(ClusterSum &own, double &s, int64_t &n)
-{
-    warp_sums(s, n);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        own.loss[threadIdx.x >> 5] = s;
-        own.count[threadIdx.x >> 5] = n;
-    }
-    __syncthreads();
-    s = own.loss[threadIdx.x & 31];
-    n = own.count[threadIdx.x & 31];
-    warp_sums(s, n);
-}
-
-__global__ void __launch_bounds__(kPolicyThreads)
-    policy_part_kernel(const PolicyRows q, int64_t part, const int64_t *counts, double *losses)
+__global__ void __launch_bounds__(kSumThreads)
+    policy_part_kernel(const PolicyRows q, int64_t part, const int64_t *counts, Sum2 *losses)
 {
     __shared__ ClusterSum sums;
-    double s = 0.0;
+    Sum2 s;
     int64_t n = 0;
-    for (int64_t i = threadIdx.x; i < gridDim.x; i += kPolicyThreads)
+    for (int64_t i = threadIdx.x; i < gridDim.x; i += kSumThreads)
         n += counts[i];
-    cta_sums(sums, s, n);
-    float g = 1.0f;
-    if (q.dlogp != nullptr && q.reduction != GBCE_NONE)
-        g = q.reduction == GBCE_MEAN && n > 0 ? q.grad_out[0] / static_cast<float>(n)
-                                              : q.grad_out[0];
+    cta_sum(s, n, sums.scratch, sums.counts);
+    if (threadIdx.x == 0)
+        sums.cta_count = n;
+    __syncthreads();
+    n = sums.cta_count;
+    const float g = policy_upstream(q, n);
     const int64_t lo = blockIdx.x * part, hi = lo + part < q.rows ? lo + part : q.rows;
-    s = 0.0;
-    for (int64_t r = lo + threadIdx.x; r < hi; r += kPolicyThreads)
-        s += policy_one_row(q, r, q.mask == nullptr || q.mask[r] != 0, g);
+    s = Sum2{};
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kSumThreads)
+        s.add(policy_one_row(q, r, policy_inputs(q, r), g));
     if (blockIdx.x == 0 && threadIdx.x == 0)
         *q.n_items = n;
-    n = 0;
-    cta_sums(sums, s, n);
+    cta_sum(s, n, sums.scratch, sums.counts);
     if (threadIdx.x == 0)
         losses[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(kPolicyThreads)
-    policy_sum_kernel(const double *losses, int64_t parts, int mean, const int64_t *n_items,
+__global__ void __launch_bounds__(kSumThreads)
+    policy_sum_kernel(const Sum2 *losses, int64_t parts, int mean, const int64_t *n_items,
                       float *loss_out)
 {
     __shared__ ClusterSum sums;
-    double s = 0.0;
+    Sum2 s;
     int64_t n = 0;
-    for (int64_t i = threadIdx.x; i < parts; i += kPolicyThreads)
-        s += losses[i];
-    cta_sums(sums, s, n);
-    const int64_t kept = *n_items;
+    for (int64_t i = threadIdx.x; i < parts; i += kSumThreads)
+        s.add(losses[i]);
+    cta_sum(s, n, sums.scratch, sums.counts);
     if (threadIdx.x == 0)
-        *loss_out = static_cast<float>(mean ? (kept > 0 ? s / static_cast<double>(kept) : 0.0) : s);
+        *loss_out = reduced(s, mean != 0, *n_items);
 }
 
 // Up to this many rows go to the one cluster.
@@ -273,7 +333,7 @@ constexpr int64_t kPolicyClusterRows = 131072;
 cudaError_t launch_policy_rows(const PolicyRows &q, void *parts, cudaStream_t stream)
 {
     if (q.rows <= kPolicyClusterRows) {
-        policy_cluster_kernel<<<kPolicyCtas, kPolicyThreads, 0, stream>>>(q);
+        policy_cluster_kernel<<<kPolicyCtas, kSumThreads, 0, stream>>>(q);
         note_launches(1);
         return cudaGetLastError();
     }
@@ -281,15 +341,15 @@ cudaError_t launch_policy_rows(const PolicyRows &q, void *parts, cudaStream_t st
     if ((q.rows + part - 1) / part > kPolicyMaxParts)
         part = (q.rows + kPolicyMaxParts - 1) / kPolicyMaxParts;
     const int64_t n = (q.rows + part - 1) / part;
-    double *losses = static_cast<double *>(parts);
+    Sum2 *losses = static_cast<Sum2 *>(parts);
     int64_t *counts = reinterpret_cast<int64_t *>(losses + n);
-    policy_count_kernel<<<static_cast<unsigned>(n), kPolicyThreads, 0, stream>>>(q.mask, q.rows,
+    policy_count_kernel<<<static_cast<unsigned>(n), kSumThreads, 0, stream>>>(q.mask, q.rows,
                                                                                  part, counts);
-    policy_part_kernel<<<static_cast<unsigned>(n), kPolicyThreads, 0, stream>>>(q, part, counts,
+    policy_part_kernel<<<static_cast<unsigned>(n), kSumThreads, 0, stream>>>(q, part, counts,
                                                                                 losses);
     note_launches(2);
     if (q.reduction != GBCE_NONE) {
-        policy_sum_kernel<<<1, kPolicyThreads, 0, stream>>>(losses, n, q.reduction == GBCE_MEAN,
+        policy_sum_kernel<<<1, kSumThreads, 0, stream>>>(losses, n, q.reduction == GBCE_MEAN,
                                                             q.n_items, q.loss_out);
         note_launches(1);
     }
@@ -322,7 +382,8 @@ struct PreferenceTerms {
     const int64_t *labels;
     int64_t ignore_index;
     const uint8_t *mask;
-    double beta, margin, eps;
+    double beta, margin;
+    float eps;
     int squared, average;
     int reduction;
     const float *grad_out;  // [pairs] or [1]
@@ -343,75 +404,74 @@ __device__ __forceinline__ bool preference_live(const PreferenceTerms &t, int64_
     return t.mask == nullptr || t.mask[r] != 0;
 }
 
-// Sum over the CTA in a fixed tree, to every thread.
-__device__ double cta_sum(double v, double *scratch)
-{
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, off);
-    if ((threadIdx.x & 31) == 0)
-        scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < kPairThreads / 32; ++w)
-        v += scratch[w];
-    __syncthreads();
-    return v;
-}
-
-// One CTA per pair: the scores of its two sequences, summed in fp64 in a fixed
-// order (a sum of thousands of log-probs meets another of the same size), the
-// pair's loss, and the derivative by each of its rows' log-probs.
+// One CTA per pair: the scores of its two sequences, summed in two floats in a
+// fixed order (a sum of thousands of log-probs meets another of the same size),
+// the pair's loss, and the derivative by each of its rows' log-probs; the last
+// CTA to finish sums the losses.  (With FP64 sums and functions in every thread:
+// 18 us at two pairs of 16 rows.)
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PreferenceTerms t)
 {
-    __shared__ double scratch[kPairThreads / 32];
+    __shared__ Sum2 scratch[kPairThreads / 32];
+    __shared__ int64_t counts[kPairThreads / 32];
+    __shared__ float s_d[2];
+    __shared__ int s_last;
     const int tid = threadIdx.x;
     const int64_t i = blockIdx.x;
-    double score[2], weight[2];
+    double score[2] = {0.0, 0.0}, weight[2] = {1.0, 1.0};
     bool bad = t.offsets[0] < 0 || t.offsets[2 * t.pairs] > t.rows;
     SeqRows q[2];
     for (int side = 0; side < 2; ++side) {
-        const int64_t s = i + side * t.pairs;
-        q[side] = seq_rows(t.offsets, s, t.rows);
-        bad |= t.offsets[s] > t.offsets[s + 1] || t.offsets[s] < 0 || t.offsets[s + 1] > t.rows;
-        double sum = 0.0, count = 0.0;
+        const int64_t at = i + side * t.pairs;
+        q[side] = seq_rows(t.offsets, at, t.rows);
+        bad |= t.offsets[at] > t.offsets[at + 1] || t.offsets[at] < 0 ||
+               t.offsets[at + 1] > t.rows;
+        Sum2 s;
+        int64_t n = 0;
+#pragma unroll 4
         for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
             if (preference_live(t, r)) {
-                const double ref = t.ref_logp != nullptr ? t.ref_logp[r] : 0.0;
-                sum += static_cast<double>(t.logp[r]) - ref;
-                count += 1.0;
+                s.add_difference(t.logp[r], t.ref_logp != nullptr ? t.ref_logp[r] : 0.0f);
+                ++n;
             }
-        sum = cta_sum(sum, scratch);
-        count = cta_sum(count, scratch);
-        weight[side] = t.average ? 1.0 / (count > 1.0 ? count : 1.0) : 1.0;
-        score[side] = sum * weight[side];
+        cta_sum(s, n, scratch, counts);
+        if (tid == 0) {
+            weight[side] = t.average && n > 1 ? 1.0 / static_cast<double>(n) : 1.0;
+            score[side] = s.value() * weight[side];
+        }
+        __syncthreads();  // (the scratch is free again)
     }
-    // loss and dloss/dh, h the difference of the scores
-    const double h = score[0] - score[1];
-    double loss, dh;
-    if (t.squared) {
-        const double e = h - 0.5 / t.beta;
-        loss = e * e;
-        dh = 2.0 * e;
-    } else {
-        // -(1 - eps) log sig(z) - eps log sig(-z) = softplus(-z) + eps z
-        const double z = t.beta * (h - t.margin), e = exp(-fabs(z));
-        const double small = e / (1.0 + e);           // sig(-|z|)
-        const double other = z > 0.0 ? small : 1.0 - small;  // sig(-z)
-        loss = (z > 0.0 ? 0.0 : -z) + log1p(e) + (t.eps != 0.0 ? t.eps * z : 0.0);
-        dh = t.beta * (t.eps - other);
-    }
-    if (bad) {
-        loss = dh = __longlong_as_double(0x7ff8000000000000ll);
-        if (tid == 0)
-            report(t.dev_status, GBCE_DEV_BAD_INDEX);
-    }
-    __shared__ int s_last;
     if (tid == 0) {
-        t.loss_pairs[i] = static_cast<float>(loss);
+        // loss and dloss/dh, h the difference of the scores
+        const double h = score[0] - score[1];
+        float loss, dh;
+        if (t.squared) {
+            const float e = static_cast<float>(h - 0.5 / t.beta);
+            loss = e * e;
+            dh = 2.0f * e;
+        } else {
+            // -(1 - eps) log sig(z) - eps log sig(-z) = softplus(-z) + eps z
+            const float z = static_cast<float>(t.beta * (h - t.margin));
+            const float e = expf(-fabsf(z)), small = e / (1.0f + e);  // sig(-|z|)
+            loss = (z > 0.0f ? 0.0f : -z) + log1pf(e) + (t.eps != 0.0f ? t.eps * z : 0.0f);
+            // sig(-z) - eps, which for z < 0 is 1 - eps - sig(z)
+            dh = static_cast<float>(-t.beta) *
+                 (z > 0.0f ? small - t.eps : (1.0f - t.eps) - small);
+        }
+        if (bad) {
+            loss = dh = kQuietNan;
+            report(t.dev_status, GBCE_DEV_BAD_INDEX);
+        }
+        t.loss_pairs[i] = loss;
         if (t.seq_score != nullptr) {
             t.seq_score[i] = static_cast<float>(score[0]);
             t.seq_score[i + t.pairs] = static_cast<float>(score[1]);
+        }
+        if (t.drow != nullptr) {
+            double g = t.reduction == GBCE_NONE ? t.grad_out[i] : t.grad_out[0];
+            if (t.reduction == GBCE_MEAN)
+                g /= static_cast<double>(t.pairs);
+            s_d[0] = static_cast<float>(dh * weight[0] * g);
+            s_d[1] = static_cast<float>(-dh * weight[1] * g);
         }
         s_last = 0;
         if (t.loss_out != nullptr) {
@@ -419,29 +479,20 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
             s_last = atomicAdd(t.done, 1) == static_cast<int32_t>(t.pairs) - 1;
         }
     }
-    if (t.loss_out != nullptr) {
-        __syncthreads();
-        if (s_last) {
-            // the last pair to finish sums them all, in pair order
-            __threadfence();
-            double sum = 0.0;
-            for (int64_t j = tid; j < t.pairs; j += kPairThreads)
-                sum += static_cast<double>(__ldcg(t.loss_pairs + j));
-            sum = cta_sum(sum, scratch);
-            if (tid == 0)
-                *t.loss_out = static_cast<float>(
-                    t.reduction == GBCE_MEAN ? sum / static_cast<double>(t.pairs) : sum);
-        }
-    }
-    if (t.drow == nullptr)
-        return;
-    double g = t.reduction == 0 ? t.grad_out[i] : t.grad_out[0];
-    if (t.reduction == 2)
-        g /= static_cast<double>(t.pairs);
-    for (int side = 0; side < 2; ++side) {
-        const double d = (side == 0 ? dh : -dh) * weight[side] * g;
-        for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
-            t.drow[r] = preference_live(t, r) ? static_cast<float>(d) : 0.0f;
+    __syncthreads();
+    if (t.drow != nullptr)
+        for (int side = 0; side < 2; ++side)
+            for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
+                t.drow[r] = preference_live(t, r) ? s_d[side] : 0.0f;
+    if (s_last) {
+        __threadfence();
+        Sum2 s;
+        int64_t n = 0;
+        for (int64_t j = tid; j < t.pairs; j += kPairThreads)
+            s.add(__ldcg(t.loss_pairs + j));
+        cta_sum(s, n, scratch, counts);
+        if (tid == 0)
+            *t.loss_out = reduced(s, t.reduction == GBCE_MEAN, t.pairs);
     }
 }
 
@@ -672,8 +723,7 @@ gbce_status distill_fwd(const void *logits, gbce_dtype dtype, int64_t rows, int6
     p.n_items_out = n_ptr;
     cudaError_t e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFwd, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
-                                     n_ptr, nullptr, loss_out, s);
+        e = gbce::launch_sum_rows(p.loss_rows, rows, reduction == GBCE_MEAN, n_ptr, loss_out, s);
     return cuda_status(e);
 }
 
@@ -757,8 +807,7 @@ gbce_status distill_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int64_t 
     p.n_items_out = n_ptr;
     cudaError_t e = launch_post(p, dtype, gbce::kOpDistill, gbce::kPassFused, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
-                                     n_ptr, nullptr, loss_out, s);
+        e = gbce::launch_sum_rows(p.loss_rows, rows, reduction == GBCE_MEAN, n_ptr, loss_out, s);
     return cuda_status(e);
 }
 
@@ -848,8 +897,7 @@ gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int6
     p.n_items_out = n_ptr;
     cudaError_t e = launch_post(p, dtype, gbce::kOpPolicy, gbce::kPassFused, s);
     if (e == cudaSuccess && reduction != GBCE_NONE)
-        e = gbce::launch_reduce_loss(p.loss_rows, nullptr, rows, 0, static_cast<int>(reduction),
-                                     n_ptr, nullptr, loss_out, s);
+        e = gbce::launch_sum_rows(p.loss_rows, rows, reduction == GBCE_MEAN, n_ptr, loss_out, s);
     return cuda_status(e);
 }
 

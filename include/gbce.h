@@ -548,7 +548,7 @@ gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, 
  * q = softmax(z) over the row's vocab columns.  A row that is left out
  * (row_mask[r] == 0, or label == ignore_index) has loss 0 and a zero gradient
  * row whatever it holds; its logits are not read.  Sums over rows are taken
- * in fp64 in a fixed order; row losses and gradients are fp32 throughout,
+ * with 48 bits in a fixed order; row losses and gradients are fp32 throughout,
  * dlogits rounded once.  workspace: gbce_workspace_size(rows, vocab, 1) bytes
  * unless stated, 16-byte aligned, of one call at a time (a captured graph
  * keeps its own); nothing in it needs zeroing.  The temperature is a double,
@@ -685,7 +685,7 @@ gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int6
  *   GBCE_PREFERENCE_SQUARED: loss_i = (h_i - 1 / (2 beta))^2.
  * A sequence may be empty, or all of its rows left out (score 0).  Rows before
  * the first sequence or behind the last have no part in anything (log p 0, a
- * zero gradient).  Scores, losses and their derivatives are taken in fp64.
+ * zero gradient).  Scores are summed with 48 bits.
  * Reductions are over pairs (MEAN: / pairs).  Offsets are device memory:
  * ones that decrease or leave [0, rows] set GBCE_DEV_BAD_INDEX and make the
  * losses of the pairs they belong to NaN (an end of the whole range: of all
