@@ -287,6 +287,22 @@ __device__ bool list_columns(const PostParams &p, int64_t r, const Slice &sl, co
     return bad;
 }
 
+// Bring a row's entries into L2.
+__device__ __forceinline__ void prefetch_entries(const PostParams &p, int64_t r, int lane)
+{
+    const auto line = [&](const void *base, int64_t bytes, int i) {
+        const int64_t at = 128 * static_cast<int64_t>(i) < bytes ? 128 * i : bytes - 1;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(base) + at));
+    };
+    // (256 entries: 17 lines of columns at most, 9 of logits)
+    if (lane < 18)
+        line(p.index + r * p.k, p.k * 8, lane);
+    else if (lane < 28)
+        line(p.teacher + r * p.k, p.k * 4, lane - 18);
+    else if (lane == 28 && p.teacher_rest != nullptr)
+        line(p.teacher_rest + r, 4, 0);
+}
+
 // The teacher's distribution, the softmax over its logits / T and teacher_rest,
 // and the student's logits at its columns (one warp, after list_columns).
 // A NaN or +inf among the teacher's logits makes the row invalid.
@@ -813,7 +829,22 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
         };
         const int64_t lo = p.row_range != nullptr ? p.row_range[0] : 0;
         const int64_t hi = p.row_range != nullptr ? p.row_range[p.row_range_end] : p.rows;
+        // Rows ahead: the row after the one at hand is known while that one's list
+        // is made (its ticket was asked for a row earlier), so that its label or
+        // mask is here, and its entries are in L2, when its turn comes.
+        const auto row_at = [&](int64_t t) { return p.reverse ? p.rows - 1 - t : t; };
+        const auto key_of = [&](int64_t t) -> int64_t {  // label, or mask
+            if (t >= p.rows)
+                return 0;
+            if (kList)
+                return p.row_mask != nullptr ? p.row_mask[row_at(t)] : 1;
+            return p.labels[row_at(t)];
+        };
         int64_t t = cluster;
+        int64_t key = key_of(t);
+        int32_t drawn = 0;
+        if (p.ticket != nullptr && lane == 0)
+            drawn = atomicAdd(p.ticket, 1);
         int64_t n_items = 0;
         uint32_t i = 0;
         for (;; ++i) {
@@ -823,20 +854,13 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             RowSlot &w = slots[q];
             __syncwarp();
             const bool end = t >= p.rows;
-            const int64_t r = p.reverse ? p.rows - 1 - t : t;
+            const int64_t r = row_at(t);
             int state = end ? kRowEnd : kRowLive;
-            int64_t lab = 0;
             if (!end) {
-                if (kList) {
-                    if (p.row_mask != nullptr && p.row_mask[r] == 0)
-                        state = kRowSkip;
-                } else {
-                    lab = p.labels[r];
-                    if (lab == p.ignore_index || r < lo || r >= hi)
-                        state = kRowSkip;
-                    else if (lab < 0 || lab >= V)
-                        state = kRowInvalid;
-                }
+                if (kList ? key == 0 : key == p.ignore_index || r < lo || r >= hi)
+                    state = kRowSkip;
+                else if (!kList && (key < 0 || key >= V))
+                    state = kRowInvalid;
             }
             const T *row = static_cast<const T *>(p.logits) + r * p.row_stride;
             uint32_t repeated = 0;
@@ -844,7 +868,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 w.r = r;
                 w.state = w.early = state;
                 w.streamed = state == kRowLive;
-                w.y = static_cast<int>(lab);
+                w.y = static_cast<int>(key);
                 mbar_arrive(&row_bar[q]);
             }
             if (kList && state == kRowLive &&
@@ -874,30 +898,41 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             }
             if (i == 0 && p.zero_out != nullptr && blockIdx.x == 0 && lane == 0)
                 *p.zero_out = 0;
-            // the next row: a ticket where CTAs take more than one row each
             int64_t next = t + clusters;
-            if (!end && p.ticket != nullptr) {
-                int32_t n = 0;
-                if (lane == 0)
-                    n = atomicAdd(p.ticket, 1);
-                next = clusters + __shfl_sync(0xffffffffu, n, 0);
-            }
+            if (p.ticket != nullptr)
+                next = clusters + __shfl_sync(0xffffffffu, drawn, 0);
+            if (p.ticket != nullptr && lane == 0 && next < p.rows)
+                drawn = atomicAdd(p.ticket, 1);
+            const int64_t next_key = key_of(next);
+            if (kList && next < p.rows)
+                prefetch_entries(p, row_at(next), lane);
             if (state == kRowLive) {
-                if (lane == 0) {
-                    if (kGrad)
-                        w.gt = scaled(post_upstream(p, r, n_items), inv_t);
-                    if (!kStats) {
-                        w.m = p.rest_state[2 * r];
-                        w.s = p.rest_state[2 * r + 1];
-                    }
-                    if (!kList)
-                        w.xy = E::load(row + lab);
-                    if (OP == kOpPolicy) {
-                        w.adv = p.policy.advantages[r];
-                        w.old_lp = p.policy.old_logp != nullptr ? p.policy.old_logp[r] : 0.0f;
-                        w.ref_lp = p.policy.ref_logp != nullptr ? p.policy.ref_logp[r] : 0.0f;
-                    }
+                // the row's own values, one lane each
+                const float *from = nullptr;
+                float *to = nullptr;
+                if (!kStats && lane < 2) {
+                    from = p.rest_state + 2 * r + lane;
+                    to = lane == 0 ? &w.m : &w.s;
                 }
+                if (OP == kOpPolicy && lane >= 2 && lane < 5) {
+                    from = lane == 2   ? p.policy.advantages
+                           : lane == 3 ? p.policy.old_logp
+                                       : p.policy.ref_logp;
+                    from = from != nullptr ? from + r : nullptr;
+                    to = lane == 2 ? &w.adv : lane == 3 ? &w.old_lp : &w.ref_lp;
+                }
+                const float value = from != nullptr ? *from : 0.0f;
+                float xy = 0.0f, gt = 0.0f;
+                if (!kList && lane == 5)
+                    xy = E::load(row + key);
+                if (kGrad && lane == 6)
+                    gt = scaled(post_upstream(p, r, n_items), inv_t);
+                if (to != nullptr)
+                    *to = value;
+                if (!kList && lane == 5)
+                    w.xy = xy;
+                if (kGrad && lane == 6)
+                    w.gt = gt;
                 if (kList)
                     list_teacher<T>(p, r, row, list_of(q), w, lane, repeated);
             }
@@ -907,6 +942,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             if (end)
                 break;
             t = next;
+            key = next_key;
         }
         for (uint32_t j = i > Q - 1 ? i - (Q - 1) : 0; j < i && ok; ++j)
             retire(j);
@@ -1358,13 +1394,48 @@ cudaError_t launch_post_shape(const PostParams &params, int sms, cudaStream_t st
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
+// The CTA shape for rows that are not split.
+//
+// Fused calls re-read each row from L2, so the rows in flight (one per CTA)
+// must fit there: of the shapes for which they do, the one with the most CTAs,
+// as many small CTAs hide a row's serial steps (its list, its merge) best.
+// Measured in us, short / mid / long: distillation, 32 entries, 613 rows x 16384
+// bf16 21 / 27 / 39, 700 x 50256 bf16 42 / 50 / 52, 512 x 32768 fp32 39 / 48 / 46,
+// 4096 x 32768 fp32 222 / 197 / 236, 8192 x 65536 bf16 422 / 367 / 445, 2000 x
+// 100000 bf16 193 / 175 / 166, 4096 x 152064 bf16 578 / 541 / 429.  Rows of 48 KB
+// and more that come in several waves do better with the larger ring of the mid
+// shape (policy loss, 8192 x 32768 bf16 189 / 177 / 283).
+// One pass only (nothing re-read): 4000 rows x 8192 and up the same order, the
+// long shape for the longest rows (log-probs and gradient of the preference
+// loss, 1000 x 152064: 195 / 187 / 171; 8192 x 32768: 285 / 277 / 346).
+template <typename T>
+int post_shape(const PostParams &p, int op, int pass, int sms)
+{
+    const int64_t row = p.vocab * static_cast<int64_t>(sizeof(T));
+    const int64_t many = static_cast<int64_t>(sms) * PostShape<kShapeShort>::kCtasPerSm;
+    const int64_t some = static_cast<int64_t>(sms) * PostShape<kShapeMid>::kCtasPerSm;
+    const auto fits = [&](int64_t ctas) {
+        return (p.rows < ctas ? p.rows : ctas) * row <= kPostL2Budget;
+    };
+    const bool waves = p.rows > many;
+    if (pass == kPassFused) {
+        if (fits(many) && !(waves && row >= 48 * 1024))
+            return kShapeShort;
+        return fits(some) ? kShapeMid : kShapeLong;
+    }
+    if (row < 48 * 1024 || (!waves && row < 128 * 1024) || (op == kOpDistill && row < 96 * 1024))
+        return kShapeShort;
+    if (op == kOpDistill)
+        return pass == kPassFwd && row >= 256 * 1024 && p.rows < 4 * some ? kShapeLong : kShapeMid;
+    return row < 128 * 1024 ? kShapeMid : kShapeLong;
+}
+
 template <typename T, int OP, int PASS>
 cudaError_t launch_post_as(PostParams p, cudaStream_t stream)
 {
     const int sms = device_sm_count();
     if (sms <= 0)
         return cudaErrorInvalidDevice;
-    const int64_t row_bytes = p.vocab * static_cast<int64_t>(sizeof(T));
     p.splits = 1;
     // few rows: each one's slices on the CTAs of a cluster
     const int64_t slots = static_cast<int64_t>(sms) * PostShape<kShapeMid>::kCtasPerSm;
@@ -1375,11 +1446,14 @@ cudaError_t launch_post_as(PostParams p, cudaStream_t stream)
         p.splits = static_cast<int>(n < kMaxClusterCtas ? n : kMaxClusterCtas);
         return launch_post_shape<T, OP, PASS, kShapeMid>(p, sms, stream);
     }
-    if (row_bytes >= 96 * 1024)
+    switch (post_shape<T>(p, OP, PASS, sms)) {
+    case kShapeLong:
         return launch_post_shape<T, OP, PASS, kShapeLong>(p, sms, stream);
-    if (row_bytes >= 24 * 1024)
+    case kShapeMid:
         return launch_post_shape<T, OP, PASS, kShapeMid>(p, sms, stream);
-    return launch_post_shape<T, OP, PASS, kShapeShort>(p, sms, stream);
+    default:
+        return launch_post_shape<T, OP, PASS, kShapeShort>(p, sms, stream);
+    }
 }
 
 template <typename T>

@@ -141,23 +141,26 @@ def _row_scratch(ws, rows, device):
 
 
 def _dlogits(buf, logits, x):
+    """The gradient's buffer, its address and its row stride."""
     if buf is None:
         buf = torch.empty(logits.shape, dtype=x.dtype, device=x.device)
+        return buf, buf.data_ptr(), x.shape[1]
     d = _matrix(buf, "dlogits")
     _check_dlogits(d, x)
-    return buf, d
+    return buf, d.data_ptr(), _stride(d)
 
 
-def _teacher(index, teacher_logits, teacher_rest, lead, rows, device):
+def _teacher(index, teacher_logits, teacher_rest, rows, device):
     idx = _int64(index, device)
-    k = idx.shape[-1] if idx.dim() else 0
-    if idx.dim() < 1 or idx.numel() != rows * k:
-        raise ValueError(f"index must have shape {tuple(lead)} + (k,), got {tuple(idx.shape)}")
-    idx = _flat(idx, rows, k)
-    if tuple(teacher_logits.shape) != tuple(index.shape):
-        raise ValueError(f"teacher_logits must have index's shape {tuple(index.shape)}, got "
-                         f"{tuple(teacher_logits.shape)}")
-    t = _floats(teacher_logits, (rows, k), device)
+    t = teacher_logits
+    if t.dtype != torch.float32 or t.device != device:
+        t = t.to(device=device, dtype=torch.float32)
+    t = t.contiguous()
+    shape = idx.shape
+    k = shape[-1] if shape else 0
+    if t.shape != shape or idx.numel() != rows * k:
+        raise ValueError(f"index and teacher_logits must have one shape [..., k] with k entries for "
+                         f"each of the {rows} rows, got {tuple(shape)} and {tuple(t.shape)}")
     rest = None if teacher_rest is None else _floats(teacher_rest, (rows,), device)
     return idx, k, t, rest
 
@@ -181,7 +184,7 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     dev = x.device
     red = REDUCTIONS[reduction]
     with _on(dev, stream):
-        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, logits.shape[:-1], rows, dev)
+        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, rows, dev)
         mask = _mask(row_mask, rows, dev)
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         state = torch.empty((rows, 2), dtype=torch.float32, device=dev)
@@ -209,16 +212,16 @@ def distill_bwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     dev = x.device
     red = REDUCTIONS[reduction]
     with _on(dev, stream):
-        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, logits.shape[:-1], rows, dev)
+        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, rows, dev)
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
         state = _floats(rest_state, (rows, 2), dev)
         n = None if n_items is None else _int64(n_items, dev).reshape(1)
-        dlogits, d = _dlogits(dlogits, logits, x)
+        dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         st = lib.distill_bwd(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x), idx.data_ptr(), k,
                              t.data_ptr(), _ptr(rest), float(temperature), _ptr(mask), red,
-                             g.data_ptr(), state.data_ptr(), _ptr(n), d.data_ptr(), _stride(d),
+                             g.data_ptr(), state.data_ptr(), _ptr(n), dp, ds,
                              _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "distill_bwd")
     return dlogits
@@ -237,18 +240,18 @@ def distill_fwd_bwd_fused(logits: torch.Tensor, index, teacher_logits: torch.Ten
     dev = x.device
     red = REDUCTIONS[reduction]
     with _on(dev, stream):
-        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, logits.shape[:-1], rows, dev)
+        idx, k, t, rest = _teacher(index, teacher_logits, teacher_rest, rows, dev)
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         n_items = torch.empty((), dtype=torch.int64, device=dev)
-        dlogits, d = _dlogits(dlogits, logits, x)
+        dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _row_scratch(workspace, rows, dev)
         st = lib.distill_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
                                        idx.data_ptr(), k, t.data_ptr(), _ptr(rest),
                                        float(temperature), _ptr(mask), red, g.data_ptr(),
-                                       loss.data_ptr(), n_items.data_ptr(), d.data_ptr(), _stride(d),
+                                       loss.data_ptr(), n_items.data_ptr(), dp, ds,
                                        wp, wb, _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "distill_fwd_bwd_fused")
     return DistillFused(loss, dlogits, n_items)
@@ -317,14 +320,14 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
         n_items = torch.empty((), dtype=torch.int64, device=dev)
-        dlogits, d = _dlogits(dlogits, logits, x)
+        dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _row_scratch(workspace, rows, dev)
         st = lib.policy_loss_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
                                            lab.data_ptr(), int(ignore_index), float(temperature),
                                            adv.data_ptr(), _ptr(old), _ptr(ref),
                                            ctypes.addressof(opt), red, g.data_ptr(), loss.data_ptr(),
-                                           _ptr(logp), n_items.data_ptr(), d.data_ptr(), _stride(d),
+                                           _ptr(logp), n_items.data_ptr(), dp, ds,
                                            wp, wb, _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "policy_loss_fwd_bwd_fused")
     return PolicyFused(loss, dlogits, logp, n_items)
@@ -415,7 +418,7 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
         loss = torch.empty((pairs,) if red == 0 else (), dtype=torch.float32, device=dev)
         logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
         score = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
-        dlogits, d = _dlogits(dlogits, logits, x)
+        dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _scratch(workspace, preference_workspace_size(rows, pairs), dev)
         st = lib.preference_loss_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
@@ -423,7 +426,7 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
                                                float(temperature), off.data_ptr(), pairs, _ptr(ref),
                                                ctypes.addressof(opt), red, g.data_ptr(),
                                                loss.data_ptr(), _ptr(logp), score.data_ptr(),
-                                               d.data_ptr(), _stride(d), wp, wb, _ptr(dev_status),
+                                               dp, ds, wp, wb, _ptr(dev_status),
                                                _stream_ptr(stream, dev))
     _check(st, "preference_loss_fwd_bwd_fused")
     return PreferenceFused(loss, dlogits, logp, score)
