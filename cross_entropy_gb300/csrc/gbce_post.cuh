@@ -422,11 +422,6 @@ __device__ __forceinline__ StudentRow student_row(float m, float s, float ml, fl
     return q;
 }
 
-__device__ __forceinline__ float student_logp(const StudentRow &q, float x, TwoFloat inv_t)
-{
-    return scaled(x - q.M, inv_t) - q.log_s;
-}
-
 // (e^u - 1 - u) / u^2 for |u| < 1/4, by its series: the next term is below
 // 2^-24 of the sum.
 __device__ __forceinline__ float phi_series(float u)
@@ -463,6 +458,24 @@ __device__ __forceinline__ float share_gap(float lp, float lq)
         return expf(lq);
     const float u = lq - lp;
     return fabsf(u) < 1.0f ? expf(lp) * expm1f(u) : expf(lq) - expf(lp);
+}
+
+// q_rest - p_rest.  Every consumer thread waits for it between its two sweeps, so
+// the usual teacher, one without a rest, takes q_rest as the plain quotient.
+__device__ __forceinline__ float rest_gap(float m, float s, float ml, float sl, float lp_rest,
+                                          TwoFloat c, TwoFloat inv_t)
+{
+    if (lp_rest != kNegInf)
+        return share_gap(lp_rest, student_row(m, s, ml, sl, c, inv_t).log_rest);
+    const float M = fmaxf(m, ml);
+    const float rest = m == kNegInf ? s : s * ex2(scaled(m - M, c));
+    const float listed = ml == kNegInf ? 0.0f : (1.0f + sl) * ex2(scaled(ml - M, c));
+    return __fdividef(rest, rest + listed);
+}
+
+__device__ __forceinline__ float student_logp(const StudentRow &q, float x, TwoFloat inv_t)
+{
+    return scaled(x - q.M, inv_t) - q.log_s;
 }
 
 // ----------------------------------------------------- one token's log p
@@ -580,8 +593,8 @@ __device__ __forceinline__ void rest_add(RestStats &st, const uint4 &a, TwoFloat
            make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), c);
 }
 
-// Orders this thread's writes to shared memory before the bulk copies that
-// refill it (issued by another thread once this one has released the stage).
+// Orders the consumers' writes to a stage (which the release of the stage has
+// made this thread see) before the bulk copy that refills it.
 __device__ __forceinline__ void fence_before_refill()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -989,6 +1002,8 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                         ok = false;
                         break;
                     }
+                    if (kStats)
+                        fence_before_refill();
                     const bool grad = kGrad && pass == kPasses - 1;
                     const int64_t left = (grad ? total_grad : total) - off;
                     const int64_t most = CHUNK + (grad ? more : 0);
@@ -1128,16 +1143,11 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 if (own_any && alive) {
                     // listed columns leave the sum: -inf in the copied row, written
                     // by the thread that alone reads their vector
-                    bool wrote = false;
                     each_own([&](int32_t col) {
                         const int32_t e = col - col0 - vb0 * VEC;
-                        if (e >= 0 && e < nv * VEC) {
+                        if (e >= 0 && e < nv * VEC)
                             reinterpret_cast<T *>(chunk)[e] = neg_inf_as(T());
-                            wrote = true;
-                        }
                     });
-                    if (wrote)
-                        fence_before_refill();
                 }
                 if (alive && nv == CV) {
                     uint4 raw[PER_THREAD];
@@ -1225,8 +1235,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             const float gt = w.gt;
             float gs;
             if (kList) {
-                gs = gt * share_gap(w.lp_rest,
-                                    student_row(m, s, w.ml, w.sl, c, inv_t).log_rest);
+                gs = gt * rest_gap(m, s, w.ml, w.sl, w.lp_rest, c, inv_t);
             } else {
                 const float lp = token_logp(m, s, w.xy, inv_t);
                 float slope = gt;  // (g / T) dloss / dlog p
