@@ -728,7 +728,12 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
     __syncthreads();
     if (C > 1)
         cluster_arrive_relaxed();
-    grid_dependency_wait();
+    // With a ticket, the kernel before this one is the library's own count (or
+    // clearing), which starts only once everything before it is complete: the
+    // first row does not wait for it, only what it wrote does (list warp).
+    // Otherwise it is the caller's, and may still be writing what is read here.
+    if (p.ticket == nullptr)
+        grid_dependency_wait();
 
     const auto slice_of = [&](const T *row) {
         Slice sl;
@@ -856,8 +861,6 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
         int64_t t = cluster;
         int64_t key = key_of(t);
         int32_t drawn = 0;
-        if (p.ticket != nullptr && lane == 0)
-            drawn = atomicAdd(p.ticket, 1);
         int64_t n_items = 0;
         uint32_t i = 0;
         for (;; ++i) {
@@ -895,6 +898,11 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 mbar_arrive(&cols_bar[q]);
             if (state == kRowInvalid && lane == 0 && split == 0)
                 report(p.dev_status, kList ? GBCE_DEV_BAD_INDEX : GBCE_DEV_BAD_LABEL);
+            if (i == 0 && p.ticket != nullptr) {
+                grid_dependency_wait();
+                if (lane == 0)
+                    drawn = atomicAdd(p.ticket, 1);
+            }
             if (i == 0 && kGrad && p.n_items != nullptr && p.reduction == GBCE_MEAN)
                 n_items = *p.n_items;
             if (i == 0 && p.n_items_out != nullptr &&
@@ -1414,9 +1422,12 @@ cudaError_t launch_post_shape(const PostParams &params, int sms, cudaStream_t st
 // 100000 bf16 193 / 175 / 166, 4096 x 152064 bf16 578 / 541 / 429.  Rows of 48 KB
 // and more that come in several waves do better with the larger ring of the mid
 // shape (policy loss, 8192 x 32768 bf16 189 / 177 / 283).
-// One pass only (nothing re-read): 4000 rows x 8192 and up the same order, the
-// long shape for the longest rows (log-probs and gradient of the preference
-// loss, 1000 x 152064: 195 / 187 / 171; 8192 x 32768: 285 / 277 / 346).
+// One pass only (nothing re-read): short up to one wave of its CTAs, but mid where
+// one wave of those holds the rows and they are long (distillation's loss, 700 x
+// 100000 bf16 40 / 56 / 50, 400 x 152064 41 / 33 / 39); several waves of long rows
+// want fewer and larger CTAs (both sweeps of the preference loss, 1000 x 152064
+// bf16 195 / 187 / 171; 8192 x 32768 285 / 277 / 346), lists more of them
+// (distillation's loss, 8192 x 65536 bf16 199 / 185 / 308).
 template <typename T>
 int post_shape(const PostParams &p, int op, int pass, int sms)
 {
@@ -1432,11 +1443,14 @@ int post_shape(const PostParams &p, int op, int pass, int sms)
             return kShapeShort;
         return fits(some) ? kShapeMid : kShapeLong;
     }
-    if (row < 48 * 1024 || (!waves && row < 128 * 1024) || (op == kOpDistill && row < 96 * 1024))
-        return kShapeShort;
-    if (op == kOpDistill)
+    if (!waves)
+        return p.rows <= some && row >= 160 * 1024 ? kShapeMid : kShapeShort;
+    if (op == kOpDistill) {
+        if (row < 96 * 1024)
+            return kShapeShort;
         return pass == kPassFwd && row >= 256 * 1024 && p.rows < 4 * some ? kShapeLong : kShapeMid;
-    return row < 128 * 1024 ? kShapeMid : kShapeLong;
+    }
+    return row < 48 * 1024 ? kShapeShort : row < 128 * 1024 ? kShapeMid : kShapeLong;
 }
 
 template <typename T, int OP, int PASS>

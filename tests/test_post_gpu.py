@@ -642,3 +642,128 @@ def test_rows_past_32_bits(gbce):
     close(out.loss, per.mean(), LOSS_TOL, ref.kl_bound(per, move).mean())
     rows_close(out.dlogits[-3:], dz / 3.0, BF16)
     assert not bool(out.dlogits[:-3].any())
+
+
+@pytest.mark.parametrize("rows,V,dtype,pad", [(3, 40001, BF16, 7), (30, 70001, BF16, 3), (5, 33001, F32, 1)])
+def test_split_rows_of_another_phase(gbce, rows, V, dtype, pad):
+    """Few long rows (each one's slices on several CTAs) whose gradient lies at another offset modulo
+    16 bytes, the listed columns on both sides of every slice's ends."""
+    g = gen(V)
+    x = logits_of(rows, V, dtype, g)
+    K = 256
+    ends = torch.cat([torch.arange(16), torch.arange(V - 16, V),
+                      *[V * i // 8 + torch.arange(-12, 12) for i in range(1, 8)]])
+    more = torch.randperm(V - 100, generator=g) + 50
+    cols = torch.unique(torch.cat([ends, more[:400]]))
+    idx = torch.stack([cols[torch.randperm(cols.numel(), generator=g)[:K]] for _ in range(rows)])
+    t = x.float().gather(1, idx) + torch.randn((rows, K), generator=g)
+    r = torch.logsumexp(t, 1) - 1.0
+    distill_check(gbce, x, idx, t, r, 1.0, None, "none", pad=pad)
+    lab = cols[torch.randint(0, cols.numel(), (rows,), generator=g)]
+    xg = on_gpu(x, pad)
+    lp, comp, z = ref.logp_rows(x, lab, 1.0)
+    out = gbce.policy_loss_fwd_bwd_fused(xg, gpu(lab), gpu(torch.ones(rows)), None, None, torch.ones(rows),
+                                         reduction="none")
+    rows_close(out.dlogits, ref.softmax_grad(z, lab, comp, torch.ones(rows).double(), 1.0), dtype)
+    pref = gbce.preference_loss_fwd_bwd_fused(xg, gpu(lab), [0, 1, rows], beta=1.0, average=True)
+    _, _, d, _ = ref.preference(lp, [0, 1, rows], None, lab >= 0, 1.0, 0.0, 0.0, "sigmoid", True)
+    e = 2 * LOGP_TOL[dtype] * float(lp.abs().max())     # of each score's mean, times the slope's slope <= 1
+    unit = ref.softmax_grad(z, lab, comp, torch.ones(rows).double(), 1.0).norm(dim=1)
+    rows_close(pref.dlogits, ref.softmax_grad(z, lab, comp, -d, 1.0), dtype, floor=e * unit)
+
+
+@pytest.mark.parametrize("rows", [131072, 131073, 300001])
+@pytest.mark.parametrize("masked", [False, True])
+def test_long_vectors_of_log_probs(gbce, rows, masked):
+    """On both sides of where the policy loss of log-probs takes a grid instead of one cluster."""
+    g = gen(rows)
+    lp = -3.0 * torch.rand(rows, generator=g)
+    adv = torch.randn(rows, generator=g)
+    old = lp - 0.05 * torch.randn(rows, generator=g)
+    mask = (torch.rand(rows, generator=g) < 0.3).to(torch.uint8) if masked else None
+    live = torch.ones(rows, dtype=torch.bool) if mask is None else mask != 0
+    loss, d = ref.policy(lp.double(), adv.double(), old.double(), None, 0.9, 5.0, 0.0)
+    n = int(live.sum())
+    for reduction, div in (("mean", n), ("sum", 1)):
+        out = gbce.policy_loss(gpu(lp), gpu(adv), gpu(old), None, torch.full((1,), 2.0), gpu(mask), clip_low=0.9,
+                               clip_high=5.0, reduction=reduction)
+        assert int(out.n_items) == n
+        kept = loss * live
+        # an exp and two products a row (four roundings), 48-bit sums, one rounding of the result
+        close(out.loss, kept.sum() / div, 2 * ref.EPS32, 6 * ref.EPS32 * kept.abs().sum() / div)
+        close(out.dlogp, 2.0 * d * live / div, 8 * ref.EPS32)
+    per = gbce.policy_loss(gpu(lp), gpu(adv), gpu(old), None, None, gpu(mask), clip_low=0.9, clip_high=5.0,
+                           reduction="none", want_grad=False)
+    assert per.dlogp is None
+    close(per.loss, loss * live, 6 * ref.EPS32)
+
+
+def test_same_bits_again_and_beside_another_call(gbce):
+    """The same call gives the same bits, also while another runs on another stream, and rows that
+    come in several waves of CTAs give what they give alone."""
+    g = gen(51)
+    rows, V, K = 2000, 2048, 20
+    x = gpu(logits_of(rows, V, BF16, g))
+    idx, t, r = (gpu(v) for v in teacher_of(x.cpu(), K, g, False, True))
+    lab = gpu(torch.randint(0, V, (rows,), generator=g))
+    adv = gpu(torch.randn(rows, generator=g))
+    off = torch.tensor([0, 300, 900, 1500, 2000], device=DEV)
+
+    def calls():
+        a = gbce.distill_fwd_bwd_fused(x, idx, t, r)
+        b = gbce.policy_loss_fwd_bwd_fused(x, lab, adv)
+        c = gbce.preference_loss_fwd_bwd_fused(x, lab, off)
+        return [a.loss, a.dlogits, b.loss, b.dlogits, c.loss, c.dlogits, c.seq_score]
+
+    first = calls()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s in (s1, s2):
+            with torch.cuda.stream(s):
+                outs.append(calls())
+    torch.cuda.synchronize()
+    for out in outs:
+        for a, b in zip(first, out):
+            assert torch.equal(a, b)
+    one = gbce.distill_fwd_bwd_fused(x[7:9], idx[7:9], t[7:9], r[7:9], torch.full((1,), 2.0 / rows))
+    # (rows of another wave, shape or split: the same formula, other orders of the same sums)
+    rows_close(one.dlogits, first[1][7:9].double().cpu(), BF16)
+
+
+@pytest.mark.parametrize("rows,V", [(300, 152064), (800, 40000), (470, 100003)])
+def test_long_rows_in_every_shape(gbce, rows, V):
+    """Several rows per CTA of the larger shapes, one row in three left out."""
+    g = gen(V)
+    x = torch.randn((rows, V), device=DEV).mul_(2.0).to(BF16)
+    idx = torch.randint(0, V // 8, (rows, 8), generator=g) + torch.arange(8) * (V // 8)
+    lab = torch.randint(0, V, (rows,), generator=g)
+    t = torch.randn((rows, 8), generator=g) + 8.0
+    mask = (torch.arange(rows) % 3 != 1).to(torch.uint8)
+    kept = lab.masked_fill(mask == 0, IGNORE)
+    some = [0, 1, 2, rows // 2, rows - 2, rows - 1]
+    out = gbce.distill_fwd_bwd_fused(x, gpu(idx), gpu(t), None, torch.ones(rows), 1.0, gpu(mask), "none")
+    f = gbce.distill_fwd(x, gpu(idx), gpu(t), None, 1.0, gpu(mask), "none")
+    b = gbce.distill_bwd(x, gpu(idx), gpu(t), None, torch.ones(rows), f.rest_state, None, 1.0, gpu(mask), "none")
+    per, dz, move = ref.distill(x[some].cpu().float(), idx[some], t[some], None, 1.0, mask[some])
+    for loss, d in ((out.loss, out.dlogits), (f.loss, b)):
+        close(loss[some], per, LOSS_TOL, ref.kl_bound(per, move))
+        rows_close(d[some], dz, BF16, floor=ref.gap_bound(move))
+        assert not bool(d[1::3].any()) and not bool(loss[1::3].any())
+    assert bool((out.dlogits.sum(1).abs() < 0.05).all())
+    p = gbce.policy_loss_fwd_bwd_fused(x, gpu(kept), gpu(torch.ones(rows)), None, None, torch.ones(rows),
+                                       reduction="none")
+    lp, comp, z = ref.logp_rows(x[some].cpu(), lab[some], 1.0)
+    live = mask[some].bool()
+    close(p.logp[some], torch.where(live, lp, 0 * lp), LOGP_TOL[BF16])
+    rows_close(p.dlogits[some], ref.softmax_grad(z, lab[some], comp, live.double(), 1.0), BF16)
+    q = gbce.preference_loss_fwd_bwd_fused(x, gpu(kept), [0, rows // 2, rows], average=True, beta=1.0)
+    close(q.logp[some], torch.where(live, lp, 0 * lp), LOGP_TOL[BF16])
+    slope = float(q.dlogits[0].float().norm()) / float(p.dlogits[0].float().norm())
+    half = int((mask[:rows // 2] != 0).sum())
+    h = q.seq_score.double().cpu()
+    want = float(torch.sigmoid(h[1] - h[0])) / half
+    assert abs(slope - want) <= 8e-3 * want      # two bf16 gradients' norms
