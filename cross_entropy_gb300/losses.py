@@ -23,12 +23,13 @@ stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (REDUCTIONS, _check, _check_buffer, _check_dlogits, _check_status, _dtype_code, _ptr,
-               load_library)
+from . import (GBCE_BF16, GBCE_F32, REDUCTIONS, _check, _check_buffer, _check_dlogits, _check_status,
+               _dtype_code, _ptr, load_library)
 from .linear import _flat, _floats, _int64, _mask, _matrix, _on, _stream_ptr, _stride
 
 KINDS = {"sigmoid": 0, "squared": 1}
@@ -87,14 +88,27 @@ class PreferenceOptions(ctypes.Structure):
                 ("average", ctypes.c_int32)]
 
 
+@functools.lru_cache(maxsize=64)
+def _policy_options(clip_low, clip_high, kl_beta):
+    """The options and their (host) address."""
+    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_beta))
+    return opt, ctypes.addressof(opt)
+
+
 def preference_workspace_size(rows: int, pairs: int) -> int:
     return int(load_library().gbce_preference_workspace_size(int(rows), int(pairs)))
 
 
-def _logits(logits: torch.Tensor) -> torch.Tensor:
+_CODES = {torch.float32: GBCE_F32, torch.bfloat16: GBCE_BF16}
+
+
+def _logits(logits: torch.Tensor):
+    """The [rows, vocab] view (no copy), its type's code, and its row stride."""
     x = _matrix(logits, "logits")
-    _dtype_code(x)
-    return x
+    code = _CODES.get(x.dtype)
+    if code is None:
+        _dtype_code(x)  # (raises)
+    return x, code, _stride(x)
 
 
 def _per_row(x, lead, what, device):
@@ -137,7 +151,14 @@ def _scratch(ws, need, device):
 
 
 def _row_scratch(ws, rows, device):
-    return _scratch(ws, load_library().gbce_workspace_size(rows, 1, 1), device)
+    """The workspace, its address and size, and the item count: the workspace's own first element
+    where the workspace is this call's (an allocation less), else one of its own."""
+    if ws is None and rows > 0:
+        need = load_library().gbce_workspace_size(rows, 1, 1)
+        ws = torch.empty((need + 7) // 8, dtype=torch.int64, device=device)
+        return ws, ws.data_ptr(), need, ws[0]
+    ws, wp, wb = _scratch(ws, 0, device)
+    return ws, wp, wb, torch.empty((), dtype=torch.int64, device=device)
 
 
 def _dlogits(buf, logits, x):
@@ -179,7 +200,7 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     listed entries are renormalised.
     """
     lib = load_library()
-    x = _logits(logits)
+    x, code, xs = _logits(logits)
     rows, vocab = x.shape
     dev = x.device
     red = REDUCTIONS[reduction]
@@ -188,10 +209,9 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
         mask = _mask(row_mask, rows, dev)
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         state = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        n_items = torch.empty((), dtype=torch.int64, device=dev)
         _check_status(dev_status, dev)
-        ws, wp, wb = _row_scratch(workspace, rows, dev)
-        st = lib.distill_fwd(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x), idx.data_ptr(), k,
+        ws, wp, wb, n_items = _row_scratch(workspace, rows, dev)
+        st = lib.distill_fwd(x.data_ptr(), code, rows, vocab, xs, idx.data_ptr(), k,
                              t.data_ptr(), _ptr(rest), float(temperature), _ptr(mask), red,
                              loss.data_ptr(), state.data_ptr(), n_items.data_ptr(), wp, wb,
                              _ptr(dev_status), _stream_ptr(stream, dev))
@@ -207,7 +227,7 @@ def distill_bwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     """dL/dlogits of :func:`distill_fwd`, given the same arguments, its ``rest_state`` and (for
     'mean') its ``n_items``."""
     lib = load_library()
-    x = _logits(logits)
+    x, code, xs = _logits(logits)
     rows, vocab = x.shape
     dev = x.device
     red = REDUCTIONS[reduction]
@@ -219,7 +239,7 @@ def distill_bwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
         n = None if n_items is None else _int64(n_items, dev).reshape(1)
         dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
-        st = lib.distill_bwd(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x), idx.data_ptr(), k,
+        st = lib.distill_bwd(x.data_ptr(), code, rows, vocab, xs, idx.data_ptr(), k,
                              t.data_ptr(), _ptr(rest), float(temperature), _ptr(mask), red,
                              g.data_ptr(), state.data_ptr(), _ptr(n), dp, ds,
                              _ptr(dev_status), _stream_ptr(stream, dev))
@@ -235,7 +255,7 @@ def distill_fwd_bwd_fused(logits: torch.Tensor, index, teacher_logits: torch.Ten
                           dev_status: Optional[torch.Tensor] = None, stream=None) -> DistillFused:
     """:func:`distill_fwd` and its gradient in one call (upstream gradient known up front)."""
     lib = load_library()
-    x = _logits(logits)
+    x, code, xs = _logits(logits)
     rows, vocab = x.shape
     dev = x.device
     red = REDUCTIONS[reduction]
@@ -244,11 +264,10 @@ def distill_fwd_bwd_fused(logits: torch.Tensor, index, teacher_logits: torch.Ten
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
-        n_items = torch.empty((), dtype=torch.int64, device=dev)
         dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
-        ws, wp, wb = _row_scratch(workspace, rows, dev)
-        st = lib.distill_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
+        ws, wp, wb, n_items = _row_scratch(workspace, rows, dev)
+        st = lib.distill_fwd_bwd_fused(x.data_ptr(), code, rows, vocab, xs,
                                        idx.data_ptr(), k, t.data_ptr(), _ptr(rest),
                                        float(temperature), _ptr(mask), red, g.data_ptr(),
                                        loss.data_ptr(), n_items.data_ptr(), dp, ds,
@@ -273,7 +292,7 @@ def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, gr
         raise ValueError("logp must be a CUDA tensor (no CPU path exists)")
     dev, rows = logp.device, logp.numel()
     red = REDUCTIONS[reduction]
-    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_beta))
+    opt = _policy_options(clip_low, clip_high, kl_beta)
     with _on(dev, stream):
         lp = _floats(logp, (rows,), dev)
         adv = _per_row(advantages, logp.shape, "advantages", dev)
@@ -282,13 +301,12 @@ def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, gr
         mask = _mask(row_mask, rows, dev)
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev) if want_grad else None
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
-        n_items = torch.empty((), dtype=torch.int64, device=dev)
         if want_grad and dlogp is None:
             dlogp = torch.empty(logp.shape, dtype=torch.float32, device=dev)
         _check_buffer(dlogp, "dlogp", torch.float32, rows, dev)
-        ws, wp, wb = _row_scratch(workspace, rows, dev)
+        ws, wp, wb, n_items = _row_scratch(workspace, rows, dev)
         st = lib.policy_loss(lp.data_ptr(), rows, _ptr(mask), adv.data_ptr(), _ptr(old), _ptr(ref),
-                             ctypes.addressof(opt), red, _ptr(g), loss.data_ptr(),
+                             opt[1], red, _ptr(g), loss.data_ptr(),
                              _ptr(dlogp) if want_grad else None, n_items.data_ptr(), wp, wb,
                              _stream_ptr(stream, dev))
     _check(st, "policy_loss")
@@ -306,11 +324,11 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
     """:func:`policy_loss` of log p of the labels, and its gradient with respect to the logits,
     in one sweep; rows with label ``ignore_index`` (prompt, padding) are left out."""
     lib = load_library()
-    x = _logits(logits)
+    x, code, xs = _logits(logits)
     rows, vocab = x.shape
     lead, dev = logits.shape[:-1], x.device
     red = REDUCTIONS[reduction]
-    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_beta))
+    opt = _policy_options(clip_low, clip_high, kl_beta)
     with _on(dev, stream):
         lab = _flat(_int64(labels, dev), rows)
         adv = _per_row(advantages, lead, "advantages", dev)
@@ -319,14 +337,13 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
         g = _upstream(grad_out, rows if red == 0 else 1, "row", dev)
         loss = torch.empty((rows,) if red == 0 else (), dtype=torch.float32, device=dev)
         logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
-        n_items = torch.empty((), dtype=torch.int64, device=dev)
         dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
-        ws, wp, wb = _row_scratch(workspace, rows, dev)
-        st = lib.policy_loss_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
+        ws, wp, wb, n_items = _row_scratch(workspace, rows, dev)
+        st = lib.policy_loss_fwd_bwd_fused(x.data_ptr(), code, rows, vocab, xs,
                                            lab.data_ptr(), int(ignore_index), float(temperature),
                                            adv.data_ptr(), _ptr(old), _ptr(ref),
-                                           ctypes.addressof(opt), red, g.data_ptr(), loss.data_ptr(),
+                                           opt[1], red, g.data_ptr(), loss.data_ptr(),
                                            _ptr(logp), n_items.data_ptr(), dp, ds,
                                            wp, wb, _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "policy_loss_fwd_bwd_fused")
@@ -347,9 +364,12 @@ def _sequences(seq_offsets, lead, device):
     return off, (off.numel() - 1) // 2
 
 
+@functools.lru_cache(maxsize=64)
 def _preference_options(beta, margin, label_smoothing, kind, average):
-    return PreferenceOptions(float(beta), float(margin), float(label_smoothing), KINDS[kind],
-                             1 if average else 0)
+    """The options and their (host) address."""
+    opt = PreferenceOptions(float(beta), float(margin), float(label_smoothing), KINDS[kind],
+                            1 if average else 0)
+    return opt, ctypes.addressof(opt)
 
 
 def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_out=None,
@@ -386,7 +406,7 @@ def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_ou
         _check_status(dev_status, dev)
         ws, wp, wb = _scratch(workspace, preference_workspace_size(rows, pairs), dev)
         st = lib.preference_loss(lp.data_ptr(), rows, _ptr(mask), off.data_ptr(), pairs, _ptr(ref),
-                                 ctypes.addressof(opt), red, _ptr(g), loss.data_ptr(),
+                                 opt[1], red, _ptr(g), loss.data_ptr(),
                                  _ptr(dlogp) if want_grad else None, score.data_ptr(), wp, wb,
                                  _ptr(dev_status), _stream_ptr(stream, dev))
     _check(st, "preference_loss")
@@ -405,7 +425,7 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
     """:func:`preference_loss` of log p of the labels, and its gradient with respect to the
     logits; rows with label ``ignore_index`` are left out of their sequence."""
     lib = load_library()
-    x = _logits(logits)
+    x, code, xs = _logits(logits)
     rows, vocab = x.shape
     lead, dev = logits.shape[:-1], x.device
     red = REDUCTIONS[reduction]
@@ -421,10 +441,10 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
         dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _scratch(workspace, preference_workspace_size(rows, pairs), dev)
-        st = lib.preference_loss_fwd_bwd_fused(x.data_ptr(), _dtype_code(x), rows, vocab, _stride(x),
+        st = lib.preference_loss_fwd_bwd_fused(x.data_ptr(), code, rows, vocab, xs,
                                                lab.data_ptr(), int(ignore_index),
                                                float(temperature), off.data_ptr(), pairs, _ptr(ref),
-                                               ctypes.addressof(opt), red, g.data_ptr(),
+                                               opt[1], red, g.data_ptr(),
                                                loss.data_ptr(), _ptr(logp), score.data_ptr(),
                                                dp, ds, wp, wb, _ptr(dev_status),
                                                _stream_ptr(stream, dev))
