@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                     const uint32_t bytes = static_cast<uint32_t>(left < most ? left : most);
                     mbar_arrive_expect_tx(&full_bar[pos], bytes);
                     bulk_load(ring + pos * PITCH, body + off, bytes, &full_bar[pos],
-                              pass + 1 < kPasses || p.keep_rows ? keep : stream);
+                              pass + 1 < kPasses || r >= p.keep_from ? keep : stream);
                     if (++pos == S) {
                         pos = 0;
                         ++lap;

@@ -63,7 +63,7 @@ struct PostParams {
     int32_t *ticket;    // hands out the rows beyond the first wave
     int32_t *zero_out;  // zeroed on the way, nullable
     int splits;       // CTAs (a cluster) per row
-    int keep_rows;    // forward: leave the rows in L2 for a backward pass that follows
+    int64_t keep_from;  // forward: rows from here on stay in L2 for a backward pass that follows
     int reverse;      // walk the rows from the last to the first
 };
 

@@ -592,6 +592,7 @@ PostParams post_params(const void *logits, int64_t rows, int64_t vocab, int64_t 
     two_floats(it, p.it_hi, p.it_lo);
     p.k = 1;
     p.splits = 1;
+    p.keep_from = INT64_MAX;
     p.dev_status = dev_status;
     return p;
 }
@@ -1001,7 +1002,11 @@ gbce_status preference_loss_fwd_bwd_fused(
         p.rest_state_out = state;
         p.ticket = ws_at<int32_t>(workspace, 0);
         p.zero_out = ws_at<int32_t>(workspace, 64);
-        p.keep_rows = 1;
+        // the last rows stay in L2 (with all of them marked to stay, a batch that
+        // exceeds L2 loses 2% to its own rows' evictions)
+        const int64_t row = vocab * static_cast<int64_t>(elem_size(dtype));
+        const int64_t fit = (int64_t(96) << 20) / row;
+        p.keep_from = rows > fit ? rows - fit : 0;
         e = launch_post(p, dtype, gbce::kOpToken, gbce::kPassFwd, s);
     } else {
         e = cudaMemsetAsync(workspace, 0, 256, s);
@@ -1038,7 +1043,7 @@ gbce_status preference_loss_fwd_bwd_fused(
         p.reduction = GBCE_NONE;
         p.ticket = ws_at<int32_t>(workspace, 128);
         p.zero_out = nullptr;
-        p.keep_rows = 0;
+        p.keep_from = INT64_MAX;
         p.reverse = 1;
         p.dlogits = dlogits;
         p.d_stride = dlogits_row_stride;
