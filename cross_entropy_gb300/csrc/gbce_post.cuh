@@ -241,6 +241,8 @@ __device__ __forceinline__ void warp_argmax(float &v, int32_t &k)
     }
 }
 
+constexpr int kBatch = 4;  // entries that a lane loads at a time
+
 // The columns of row r's entries and their chains (one warp): what the sweep
 // needs.  An index listed twice is one column: the first entry keeps it and has
 // its bit set in `repeated` (this lane's entry lane + 32 i: bit i).  Returns
@@ -255,12 +257,19 @@ __device__ bool list_columns(const PostParams &p, int64_t r, const Slice &sl, co
     bool bad = false;
     for (int i = lane; i < NC; i += 32)
         L.head[i] = -1;
-#pragma unroll 4
-    for (int k = lane; k < K; k += 32) {
-        const int64_t t = index[k];
-        const bool here = t >= 0 && t < p.vocab;
-        bad |= !here && t != -1;
-        L.col[k] = here ? static_cast<int32_t>(t) : -1;
+    // (kBatch loads of a lane in flight together: one memory latency, not K / 32)
+    for (int k0 = lane; k0 < K; k0 += 32 * kBatch) {
+        int64_t t[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            t[b] = k0 + 32 * b < K ? __ldg(index + k0 + 32 * b) : -1;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const bool here = t[b] >= 0 && t[b] < p.vocab;
+            bad |= !here && t[b] != -1;
+            if (k0 + 32 * b < K)
+                L.col[k0 + 32 * b] = here ? static_cast<int32_t>(t[b]) : -1;
+        }
     }
     bad = __any_sync(0xffffffffu, bad);
     __syncwarp();
@@ -316,13 +325,26 @@ __device__ void list_teacher(const PostParams &p, int64_t r, const T *row, const
     const float *teacher = p.teacher + r * K;
     const float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
     bool nan_t = !(rest < inf);
-#pragma unroll 4
-    for (int k = lane; k < K; k += 32) {
-        const int32_t col = L.col[k];
-        const float raw = teacher[k], x = col >= 0 ? Elem<T>::load(row + col) : kNegInf;
-        nan_t |= col >= 0 && !(raw < inf);
-        L.x[k] = x;
-        L.lp[k] = col >= 0 && raw != kNegInf ? scaled(raw, inv_t) : kNegInf;
+    for (int k0 = lane; k0 < K; k0 += 32 * kBatch) {
+        float raw[kBatch], x[kBatch];
+        bool in[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + 32 * b;
+            const int32_t col = k < K ? L.col[k] : -1;
+            in[b] = col >= 0;
+            raw[b] = in[b] ? __ldg(teacher + k) : kNegInf;
+            x[b] = in[b] ? Elem<T>::load(row + col) : kNegInf;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + 32 * b;
+            nan_t |= in[b] && !(raw[b] < inf);
+            if (k < K) {
+                L.x[k] = x[b];
+                L.lp[k] = raw[b] != kNegInf ? scaled(raw[b], inv_t) : kNegInf;
+            }
+        }
     }
     if (__any_sync(0xffffffffu, repeated != 0)) {
         // the first of several takes their sum, in entry order
@@ -422,11 +444,13 @@ __device__ __forceinline__ StudentRow student_row(float m, float s, float ml, fl
     return q;
 }
 
-// (e^u - 1 - u) / u^2 for |u| < 1/4, by its series: the next term is below
-// 2^-24 of the sum.
+// (e^u - 1 - u) / u^2 for |u| < 1/2, by its series: the next term is below
+// 2^-28 of the sum.
 __device__ __forceinline__ float phi_series(float u)
 {
-    float h = 1.0f / 5040.0f;
+    float h = 1.0f / 362880.0f;
+    h = fmaf(h, u, 1.0f / 40320.0f);
+    h = fmaf(h, u, 1.0f / 5040.0f);
     h = fmaf(h, u, 1.0f / 720.0f);
     h = fmaf(h, u, 1.0f / 120.0f);
     h = fmaf(h, u, 1.0f / 24.0f);
@@ -434,30 +458,31 @@ __device__ __forceinline__ float phi_series(float u)
     return fmaf(h, u, 0.5f);
 }
 
-// p phi(u), u = log q - log p, phi(u) = e^u - 1 - u >= 0: one term of
-// KL = sum p (log p - log q) written as a sum of non-negative terms (both
-// distributions sum to 1, so the extra q - p sum to 0).  A near-converged
-// student keeps its loss, where the plain terms cancel to fp32's rounding.
-__device__ __forceinline__ float kl_term(float lp, float lq)
-{
-    const float q = expf(lq);
-    if (lp == kNegInf)
-        return q;
-    const float p = expf(lp), u = lq - lp;
-    if (fabsf(u) < 0.25f)
-        return p * u * u * phi_series(u);
-    if (u > 1.0f)
-        return (q - p) - p * u;
-    return p > 0.0f ? p * (expm1f(u) - u) : 0.0f;
-}
+// One entry of the two distributions (p teacher, q student), u = log q - log p:
+//  kl   p phi(u), phi(u) = e^u - 1 - u >= 0: one term of KL = sum p (log p -
+//       log q) written as a sum of non-negative terms (both distributions sum to
+//       1, so the extra q - p sum to 0);
+//  gap  q - p.
+// Near u = 0 both come from phi's series: a near-converged student keeps its
+// loss and gradient, where the plain terms cancel to fp32's rounding (beyond, the
+// differences cancel a factor of 17 and 4 at most).
+struct EntryTerms {
+    float kl, gap;
+};
 
-// q - p without the cancellation of two nearly equal values.
-__device__ __forceinline__ float share_gap(float lp, float lq)
+__device__ __forceinline__ EntryTerms entry_terms(float lp, float lq)
 {
-    if (lp == kNegInf)
-        return expf(lq);
-    const float u = lq - lp;
-    return fabsf(u) < 1.0f ? expf(lp) * expm1f(u) : expf(lq) - expf(lp);
+    const float p = expf(lp), q = expf(lq), u = lq - lp;
+    const float near = u * phi_series(u);
+    const bool close = fabsf(u) < 0.5f;
+    EntryTerms t;
+    t.gap = close ? p * fmaf(u, near, u) : q - p;
+    t.kl = close ? p * (u * near) : (q - p) - p * u;
+    if (!(p > 0.0f) && p == p) {  // (0 log 0 = 0)
+        t.kl = q;
+        t.gap = q;
+    }
+    return t;
 }
 
 // q_rest - p_rest.  Every consumer thread waits for it between its two sweeps, so
@@ -466,7 +491,7 @@ __device__ __forceinline__ float rest_gap(float m, float s, float ml, float sl, 
                                           TwoFloat c, TwoFloat inv_t)
 {
     if (lp_rest != kNegInf)
-        return share_gap(lp_rest, student_row(m, s, ml, sl, c, inv_t).log_rest);
+        return entry_terms(lp_rest, student_row(m, s, ml, sl, c, inv_t).log_rest).gap;
     const float M = fmaxf(m, ml);
     const float rest = m == kNegInf ? s : s * ex2(scaled(m - M, c));
     const float listed = ml == kNegInf ? 0.0f : (1.0f + sl) * ex2(scaled(ml - M, c));
@@ -517,7 +542,7 @@ __device__ __forceinline__ void policy_row(const PolicyTerms &t, float A, float 
     }
     if (t.ref_logp != nullptr && t.kl_beta != 0.0f) {
         const float d = ref_lp - lp, e = expm1f(d);
-        const float k3 = fabsf(d) < 0.25f ? d * d * phi_series(d) : e - d;
+        const float k3 = fabsf(d) < 0.5f ? d * d * phi_series(d) : e - d;
         loss = fmaf(t.kl_beta, k3, loss);
         dlp = fmaf(-t.kl_beta, e, dlp);
     }
@@ -783,15 +808,16 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             if (kList) {
                 const ListRef L = list_of(q);
                 const StudentRow st = student_row(m, s, w.ml, w.sl, c, inv_t);
-                float kl = lane == 0 ? kl_term(w.lp_rest, st.log_rest) : 0.0f;
+                float kl = lane == 0 ? entry_terms(w.lp_rest, st.log_rest).kl : 0.0f;
+#pragma unroll 2
                 for (int k = lane; k < p.k; k += 32) {
                     if (L.col[k] < 0)
                         continue;
-                    const float lp = L.lp[k], lq = student_logp(st, L.x[k], inv_t);
-                    if (kStats)
-                        kl += kl_term(lp, lq);
+                    const EntryTerms t =
+                        entry_terms(L.lp[k], student_logp(st, L.x[k], inv_t));
+                    kl += t.kl;
                     if (kGrad)
-                        L.val[k] = w.gt * share_gap(lp, lq);
+                        L.val[k] = w.gt * t.gap;
                 }
                 kl = warp_sum(kl);
                 if (kStats && lane == 0 && split == 0)
