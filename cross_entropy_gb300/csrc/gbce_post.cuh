@@ -273,13 +273,25 @@ __device__ bool list_columns(const PostParams &p, int64_t r, const Slice &sl, co
     }
     bad = __any_sync(0xffffffffu, bad);
     __syncwarp();
+#pragma unroll 4
     for (int k = lane; k < K; k += 32)
         if (L.col[k] >= 0)
             L.next[k] = atomicExch(&L.head[column_owner<VEC, NC>(sl, L.col[k])], k);
     __syncwarp();
-    // repeats: equal columns share an owner, so its chain shows them all
-    uint32_t repeat = 0;
+    // Repeats: equal columns share an owner, so its chain shows them all, each
+    // pair to the one of the two that was put in later.  There are none as a rule.
+    bool same = false;
+#pragma unroll 4
+    for (int k = lane; k < K; k += 32) {
+        const int32_t col = L.col[k];
+        if (col >= 0)
+            for (int j = L.next[k]; j >= 0; j = L.next[j])
+                same |= L.col[j] == col;
+    }
     repeated = 0;
+    if (!__any_sync(0xffffffffu, same))
+        return bad;
+    uint32_t repeat = 0;
     for (int k = lane, i = 0; k < K; k += 32, ++i) {
         const int32_t col = L.col[k];
         if (col < 0)
@@ -1445,9 +1457,9 @@ cudaError_t launch_post_shape(const PostParams &params, int sms, cudaStream_t st
 // Measured in us, short / mid / long: distillation, 32 entries, 613 rows x 16384
 // bf16 21 / 27 / 39, 700 x 50256 bf16 42 / 50 / 52, 512 x 32768 fp32 39 / 48 / 46,
 // 4096 x 32768 fp32 222 / 197 / 236, 8192 x 65536 bf16 422 / 367 / 445, 2000 x
-// 100000 bf16 193 / 175 / 166, 4096 x 152064 bf16 578 / 541 / 429.  Rows of 48 KB
-// and more that come in several waves do better with the larger ring of the mid
-// shape (policy loss, 8192 x 32768 bf16 189 / 177 / 283).
+// 100000 bf16 193 / 175 / 166, 4096 x 152064 bf16 578 / 541 / 429.  Without lists,
+// rows of 48 KB and more that come in several waves do better with the larger ring
+// of the mid shape (policy loss, 8192 x 32768 bf16 189 / 177 / 283).
 // One pass only (nothing re-read): short up to one wave of its CTAs, but mid where
 // one wave of those holds the rows and they are long (distillation's loss, 700 x
 // 100000 bf16 40 / 56 / 50, 400 x 152064 41 / 33 / 39); several waves of long rows
@@ -1465,7 +1477,7 @@ int post_shape(const PostParams &p, int op, int pass, int sms)
     };
     const bool waves = p.rows > many;
     if (pass == kPassFused) {
-        if (fits(many) && !(waves && row >= 48 * 1024))
+        if (fits(many) && !(op == kOpPolicy && waves && row >= 48 * 1024))
             return kShapeShort;
         return fits(some) ? kShapeMid : kShapeLong;
     }
