@@ -734,7 +734,9 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
     // consumers), statistics done (to the list warp), slot free again
     __shared__ uint64_t row_bar[Q], cols_bar[Q], list_bar[Q], stat_bar[Q], free_bar[Q];
     __shared__ RowSlot slots[Q];
-    // per-warp partials, double-buffered by row (a warp may be a row ahead)
+    // per-warp partials, double-buffered by swept row: a warp that has merged one
+    // row can write the next one's while a slower warp still reads (rows that are
+    // not swept have no barrier, so they do not count)
     __shared__ float red_m[2][NCW], red_s[2][NCW];
     __shared__ uint64_t xbar;  // cluster of CTAs per row: every slice's partial
     __shared__ __align__(16) float4 xchg[kMaxClusterCtas];
@@ -1074,6 +1076,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
     // ------------------------------------------------------------ consumers
     uint32_t pos = 0, lap = 0;
     bool alive = true;
+    uint32_t swept_rows = 0;
     for (uint32_t i = 0;; ++i) {
         const int q = i % Q;
         if (!mbar_wait(&cols_bar[q], (i / Q) & 1)) {
@@ -1191,7 +1194,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                     // by the thread that alone reads their vector
                     each_own([&](int32_t col) {
                         const int32_t e = col - col0 - vb0 * VEC;
-                        if (e >= 0 && e < nv * VEC)
+                        if (col >= col0 && e >= 0 && e < nv * VEC)
                             reinterpret_cast<T *>(chunk)[e] = neg_inf_as(T());
                     });
                 }
@@ -1222,7 +1225,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 done_chunk();
             }
             // each warp's state, one barrier, then every warp merges them all
-            const int rb = i & 1;
+            const int rb = static_cast<int>(swept_rows++ & 1u);
             m = st.m;
             s = st.sum();
             if (s != s)  // (a thread that met only NaN has no max: its NaN must still count)

@@ -767,3 +767,30 @@ def test_long_rows_in_every_shape(gbce, rows, V):
     h = q.seq_score.double().cpu()
     want = float(torch.sigmoid(h[1] - h[0])) / half
     assert abs(slope - want) <= 8e-3 * want      # two bf16 gradients' norms
+
+
+@pytest.mark.parametrize("V,dtype", [(64, BF16), (600, F32), (5000, BF16)])
+def test_rows_left_out_between_others_change_nothing(gbce, V, dtype):
+    """A kept row has the same bits whatever rows lie between: short rows, of which a CTA takes
+    several, with every pattern of rows left out."""
+    g = gen(V + 1)
+    rows, K = 6000, 6
+    x = gpu(logits_of(rows, V, dtype, g))
+    idx, t, r = (gpu(v) for v in teacher_of(x.cpu(), K, g, False, True))
+    lab = gpu(torch.randint(0, V, (rows,), generator=g))
+    adv = gpu(torch.randn(rows, generator=g))
+    one = torch.ones(rows, device=DEV)
+    a = gbce.distill_fwd_bwd_fused(x, idx, t, r, one, 1.0, None, "none")
+    f = gbce.distill_fwd(x, idx, t, r, 1.0, None, "none")
+    b = gbce.policy_loss_fwd_bwd_fused(x, lab, adv, None, None, one, reduction="none")
+    n = torch.arange(rows, device=DEV)
+    for keep in (n % 2 == 0, n % 3 == 1, (n // 3) % 2 == 0, torch.rand(rows, generator=g).to(DEV) < 0.5):
+        for _ in range(3):
+            c = gbce.distill_fwd_bwd_fused(x, idx, t, r, one, 1.0, keep, "none")
+            h = gbce.distill_fwd(x, idx, t, r, 1.0, keep, "none")
+            d = gbce.policy_loss_fwd_bwd_fused(x, lab.masked_fill(~keep, IGNORE), adv, None, None, one,
+                                               reduction="none")
+            for got, want in ((c.loss, a.loss), (c.dlogits, a.dlogits), (h.loss, f.loss),
+                              (h.rest_state, f.rest_state), (d.loss, b.loss), (d.dlogits, b.dlogits)):
+                assert torch.equal(got[keep], want[keep])
+            assert not bool(c.dlogits[~keep].any()) and not bool(d.dlogits[~keep].any())
