@@ -1529,6 +1529,8 @@ cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stre
 {
     if (p.rows == 0)
         return cudaSuccess;
+    if (p.vocab * static_cast<int64_t>(sizeof(T)) <= kShortRowBytes)
+        return launch_post_short<T>(p, op, pass, stream);
     if (op == kOpPolicy)
         return launch_post_as<T, kOpPolicy, kPassFused>(p, stream);
     if (op == kOpToken)

@@ -70,6 +70,15 @@ struct PostParams {
 template <typename T>
 cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stream);
 
+// The same for short rows (gbce_post_short.cuh).
+template <typename T>
+cudaError_t launch_post_short(const PostParams &p, int op, int pass, cudaStream_t stream);
+
+// Bytes of a row up to which it goes there; to one warp; to four.
+constexpr int64_t kShortRowBytes = 65536, kShortWarpBytes = 4096, kShortMidBytes = 16384;
+// The most shared memory a CTA of theirs takes.
+constexpr int kShortSmemMax = 65536 + 64 + 8 * kMaxListed;
+
 // n_items = number of rows with mask != 0 (rows when mask is null) into *n_out;
 // *zero_out (nullable) is zeroed.
 cudaError_t launch_count_mask(const uint8_t *mask, int64_t rows, int64_t *n_out,
