@@ -604,7 +604,7 @@ template <> struct PostShape<kShapeMid> {
     static constexpr int kWarps = 8, kChunk = 16384, kStages = 4, kCtasPerSm = 3;
 };
 template <> struct PostShape<kShapeShort> {
-    static constexpr int kWarps = 4, kChunk = 8192, kStages = 2, kCtasPerSm = 5;
+    static constexpr int kWarps = 4, kChunk = 16384, kStages = 2, kCtasPerSm = 5;
 };
 
 template <int SHAPE> constexpr int post_threads() { return (PostShape<SHAPE>::kWarps + 2) * 32; }

@@ -75,9 +75,10 @@ template <typename T>
 cudaError_t launch_post_short(const PostParams &p, int op, int pass, cudaStream_t stream);
 
 // Bytes of a row up to which it goes there; to one warp; to four.
-constexpr int64_t kShortRowBytes = 65536, kShortWarpBytes = 4096, kShortMidBytes = 16384;
+constexpr int64_t kShortRowBytes = 104 * 1024, kShortWarpBytes = 8192, kShortMidBytes = 49152;
+constexpr int64_t kShortFewRows = 400;
 // The most shared memory a CTA of theirs takes.
-constexpr int kShortSmemMax = 65536 + 64 + 8 * kMaxListed;
+constexpr int kShortSmemMax = kShortRowBytes + 64 + 8 * kMaxListed;
 
 // n_items = number of rows with mask != 0 (rows when mask is null) into *n_out;
 // *zero_out (nullable) is zeroed.

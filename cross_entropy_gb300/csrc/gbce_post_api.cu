@@ -382,7 +382,7 @@ struct PreferenceTerms {
     const int64_t *labels;
     int64_t ignore_index;
     const uint8_t *mask;
-    double beta, margin;
+    double beta, margin, half_over_beta;  // the last: 1 / (2 beta)
     float eps;
     int squared, average;
     int reduction;
@@ -404,48 +404,67 @@ __device__ __forceinline__ bool preference_live(const PreferenceTerms &t, int64_
     return t.mask == nullptr || t.mask[r] != 0;
 }
 
-// One CTA per pair: the scores of its two sequences, summed in two floats in a
-// fixed order (a sum of thousands of log-probs meets another of the same size),
-// the pair's loss, and the derivative by each of its rows' log-probs; the last
-// CTA to finish sums the losses.  (With FP64 sums and functions in every thread:
-// 18 us at two pairs of 16 rows.)
+// One CTA per pair, half of it per sequence: the scores, summed in two floats in
+// a fixed order (a sum of thousands of log-probs meets another of the same
+// size), the pair's loss, and the derivative by each of its rows' log-probs; the
+// last CTA to finish sums the losses.  All of it is latency, so the halves work
+// side by side and no thread divides in FP64 unless `average` asks for it (with
+// FP64 sums and functions in every thread: 18 us at two pairs of 16 rows).
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PreferenceTerms t)
 {
-    __shared__ Sum2 scratch[kPairThreads / 32];
-    __shared__ int64_t counts[kPairThreads / 32];
+    constexpr int kWarps = kPairThreads / 32, kHalf = kPairThreads / 2;
+    __shared__ Sum2 scratch[kWarps];
+    __shared__ int64_t counts[kWarps];
     __shared__ float s_d[2];
     __shared__ int s_last;
-    const int tid = threadIdx.x;
-    const int64_t i = blockIdx.x;
-    double score[2] = {0.0, 0.0}, weight[2] = {1.0, 1.0};
+    // a dependent of the kernel that wrote the log-probs
+    grid_dependency_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int side = tid / kHalf, first = tid - side * kHalf;
+    const int64_t i = blockIdx.x, at = i + side * t.pairs;
+    const SeqRows q = seq_rows(t.offsets, at, t.rows);
     bool bad = t.offsets[0] < 0 || t.offsets[2 * t.pairs] > t.rows;
-    SeqRows q[2];
-    for (int side = 0; side < 2; ++side) {
-        const int64_t at = i + side * t.pairs;
-        q[side] = seq_rows(t.offsets, at, t.rows);
-        bad |= t.offsets[at] > t.offsets[at + 1] || t.offsets[at] < 0 ||
-               t.offsets[at + 1] > t.rows;
-        Sum2 s;
-        int64_t n = 0;
+    bad |= t.offsets[at] > t.offsets[at + 1] || t.offsets[at] < 0 || t.offsets[at + 1] > t.rows;
+    Sum2 s;
+    int64_t n = 0;
 #pragma unroll 4
-        for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
-            if (preference_live(t, r)) {
-                s.add_difference(t.logp[r], t.ref_logp != nullptr ? t.ref_logp[r] : 0.0f);
-                ++n;
-            }
-        cta_sum(s, n, scratch, counts);
-        if (tid == 0) {
-            weight[side] = t.average && n > 1 ? 1.0 / static_cast<double>(n) : 1.0;
-            score[side] = s.value() * weight[side];
+    for (int64_t r = q.lo + first; r < q.hi; r += kHalf)
+        if (preference_live(t, r)) {
+            s.add_difference(t.logp[r], t.ref_logp != nullptr ? t.ref_logp[r] : 0.0f);
+            ++n;
         }
-        __syncthreads();  // (the scratch is free again)
+    s.warp_merge();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        n += __shfl_down_sync(0xffffffffu, n, off);
+    if (lane == 0) {
+        scratch[warp] = s;
+        counts[warp] = n;
     }
+    bad = __syncthreads_or(bad);
     if (tid == 0) {
+        double score[2];
+        float weight[2];
+        for (int k = 0; k < 2; ++k) {
+            s = scratch[k * kWarps / 2];
+            n = counts[k * kWarps / 2];
+            for (int w = 1; w < kWarps / 2; ++w) {
+                s.add(scratch[k * kWarps / 2 + w]);
+                n += counts[k * kWarps / 2 + w];
+            }
+            score[k] = s.value();
+            weight[k] = 1.0f;
+            if (t.average && n > 1) {
+                const double inv = 1.0 / static_cast<double>(n);
+                score[k] *= inv;
+                weight[k] = static_cast<float>(inv);
+            }
+        }
         // loss and dloss/dh, h the difference of the scores
         const double h = score[0] - score[1];
         float loss, dh;
         if (t.squared) {
-            const float e = static_cast<float>(h - 0.5 / t.beta);
+            const float e = static_cast<float>(h - t.half_over_beta);
             loss = e * e;
             dh = 2.0f * e;
         } else {
@@ -467,33 +486,44 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
             t.seq_score[i + t.pairs] = static_cast<float>(score[1]);
         }
         if (t.drow != nullptr) {
-            double g = t.reduction == GBCE_NONE ? t.grad_out[i] : t.grad_out[0];
+            float g = t.reduction == GBCE_NONE ? t.grad_out[i] : t.grad_out[0];
             if (t.reduction == GBCE_MEAN)
-                g /= static_cast<double>(t.pairs);
-            s_d[0] = static_cast<float>(dh * weight[0] * g);
-            s_d[1] = static_cast<float>(-dh * weight[1] * g);
-        }
-        s_last = 0;
-        if (t.loss_out != nullptr) {
-            __threadfence();  // the loss before the count
-            s_last = atomicAdd(t.done, 1) == static_cast<int32_t>(t.pairs) - 1;
+                g /= static_cast<float>(t.pairs);
+            s_d[0] = dh * weight[0] * g;
+            s_d[1] = -dh * weight[1] * g;
         }
     }
     __syncthreads();
-    if (t.drow != nullptr)
-        for (int side = 0; side < 2; ++side)
-            for (int64_t r = q[side].lo + tid; r < q[side].hi; r += kPairThreads)
-                t.drow[r] = preference_live(t, r) ? s_d[side] : 0.0f;
+    if (t.drow != nullptr) {
+        const float d = s_d[side];
+        for (int64_t r = q.lo + first; r < q.hi; r += kHalf)
+            t.drow[r] = preference_live(t, r) ? d : 0.0f;
+    }
+    if (t.loss_out == nullptr)
+        return;
+    if (tid == 0) {
+        __threadfence();  // the loss before the count
+        s_last = atomicAdd(t.done, 1) == static_cast<int32_t>(t.pairs) - 1;
+    }
+    __syncthreads();
     if (s_last) {
         __threadfence();
-        Sum2 s;
-        int64_t n = 0;
+        s = Sum2{};
+        n = 0;
         for (int64_t j = tid; j < t.pairs; j += kPairThreads)
             s.add(__ldcg(t.loss_pairs + j));
         cta_sum(s, n, scratch, counts);
         if (tid == 0)
             *t.loss_out = reduced(s, t.reduction == GBCE_MEAN, t.pairs);
     }
+}
+
+cudaError_t launch_pairs(const PreferenceTerms &t, cudaStream_t stream)
+{
+    const PostLaunch l(t.pairs, kPairThreads, 0, 1, stream);
+    const cudaError_t err = cudaLaunchKernelEx(&l.cfg, preference_pair_kernel, t);
+    note_launches(1);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 // Zeros for the rows of no sequence (a preference call from log-probs), and
@@ -660,6 +690,7 @@ void set_preference_options(PreferenceTerms &t, const gbce_preference_options *o
 {
     t.beta = o->beta;
     t.margin = o->margin;
+    t.half_over_beta = 0.5 / static_cast<double>(o->beta);
     t.eps = o->label_smoothing;
     t.squared = o->kind == GBCE_PREFERENCE_SQUARED;
     t.average = o->average != 0;
@@ -953,12 +984,8 @@ gbce_status preference_loss(const float *logp, int64_t rows, const uint8_t *row_
         rows, seq_offsets, 2 * pairs, dlogp_out, t.done);
     gbce::note_launches(1);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) {
-        gbce::preference_pair_kernel<<<static_cast<unsigned>(pairs), gbce::kPairThreads, 0, s>>>(
-            t);
-        gbce::note_launches(1);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess)
+        e = gbce::launch_pairs(t, s);
     return cuda_status(e);
 }
 
@@ -1028,12 +1055,8 @@ gbce_status preference_loss_fwd_bwd_fused(
     t.seq_score = seq_score_out;
     t.drow = grad;
     t.dev_status = dev_status;
-    if (e == cudaSuccess) {
-        gbce::preference_pair_kernel<<<static_cast<unsigned>(pairs), gbce::kPairThreads, 0, s>>>(
-            t);
-        gbce::note_launches(1);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess)
+        e = gbce::launch_pairs(t, s);
     if (e == cudaSuccess && rows > 0) {
         // the rows that were read last are in L2 still: they come first
         p.logp_out = nullptr;

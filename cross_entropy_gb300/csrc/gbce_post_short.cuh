@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             const bool here = inside && k < K;
             idx[b] = here ? __ldg(p.index + r * K + k) : -1;
             tau[b] = here ? __ldg(p.teacher + r * K + k) : kNegInf;
+            x[b] = kNegInf;
         }
         if (inside && p.teacher_rest != nullptr)
             rest = p.teacher_rest[r];
@@ -309,24 +310,24 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     float xy = 0.0f;
     if constexpr (kList) {
 #pragma unroll
-        for (int b = 0; b < KE; ++b)
+        for (int b = 0; b < KE && b * NT < K; ++b)
             x[b] = col[b] >= 0 ? as_float(buf[phase + col[b]]) : kNegInf;
         G::sync();
         // an index listed twice: of the entries that leave their numbers at a
         // column only one finds its own there
 #pragma unroll
-        for (int b = 0; b < KE; ++b)
+        for (int b = 0; b < KE && b * NT < K; ++b)
             if (col[b] >= 0)
                 buf[phase + col[b]] = tag_as(T(), tid + b * NT);
         G::sync();
         bool twice = false;
 #pragma unroll
-        for (int b = 0; b < KE; ++b)
+        for (int b = 0; b < KE && b * NT < K; ++b)
             if (col[b] >= 0)
                 twice |= tag_of(buf[phase + col[b]]) != tid + b * NT;
         twice = G::any(twice);
 #pragma unroll
-        for (int b = 0; b < KE; ++b) {
+        for (int b = 0; b < KE && b * NT < K; ++b) {
             if (col[b] >= 0)
                 buf[phase + col[b]] = neg_inf_as(T());
             nan_t |= col[b] >= 0 && !(tau[b] < inf);
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
                 }
             G::sync();
 #pragma unroll 1
-            for (int b = 0; b < KE; ++b) {
+            for (int b = 0; b < KE && b * NT < K; ++b) {
                 const int k = tid + b * NT;
                 if (k >= K || list_col[k] < 0)
                     continue;
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             }
         }
 #pragma unroll
-        for (int b = 0; b < KE; ++b)
+        for (int b = 0; b < KE && b * NT < K; ++b)
             if (col[b] >= 0) {
                 nan_x |= x[b] != x[b] || x[b] == inf;
                 teacher.merge(tau[b], 0.0f, exp_t);
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         const StudentRow q = student_row(m, s, student.m, student.s, c, inv_t);
         float kl = tid == 0 ? entry_terms(lp_rest, q.log_rest).kl : 0.0f;
 #pragma unroll
-        for (int b = 0; b < KE; ++b) {
+        for (int b = 0; b < KE && b * NT < K; ++b) {
             if (col[b] < 0)
                 continue;
             const EntryTerms t =
@@ -565,12 +566,13 @@ cudaError_t launch_short_as(PostParams p, cudaStream_t stream)
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// How many warps a row gets.
+// How many warps a row gets.  One warp each keeps most rows in flight where there
+// are more of them than one wave of CTAs.
 template <typename T, int OP, int PASS>
 cudaError_t launch_short_pass(const PostParams &p, cudaStream_t stream)
 {
     const int64_t row = p.vocab * static_cast<int64_t>(sizeof(T));
-    if (row <= kShortWarpBytes)
+    if (row <= kShortWarpBytes && p.rows > kShortFewRows)
         return launch_short_as<T, OP, PASS, 1>(p, stream);
     if (row <= kShortMidBytes)
         return launch_short_as<T, OP, PASS, 4>(p, stream);
