@@ -89,14 +89,20 @@ class PreferenceOptions(ctypes.Structure):
 
 
 @functools.lru_cache(maxsize=64)
-def _policy_options(clip_low, clip_high, kl_beta):
-    """The options and their (host) address."""
-    opt = PolicyOptions(float(clip_low), float(clip_high), float(kl_beta))
+def _policy_options(clip_low: float, clip_high: float, kl_beta: float):
+    """The options and their (host) address; by value, so only of plain numbers."""
+    opt = PolicyOptions(clip_low, clip_high, kl_beta)
     return opt, ctypes.addressof(opt)
 
 
+@functools.lru_cache(maxsize=256)
 def preference_workspace_size(rows: int, pairs: int) -> int:
     return int(load_library().gbce_preference_workspace_size(int(rows), int(pairs)))
+
+
+@functools.lru_cache(maxsize=256)
+def _row_workspace_size(rows: int) -> int:
+    return int(load_library().gbce_workspace_size(rows, 1, 1))
 
 
 _CODES = {torch.float32: GBCE_F32, torch.bfloat16: GBCE_BF16}
@@ -154,7 +160,7 @@ def _row_scratch(ws, rows, device):
     """The workspace, its address and size, and the item count: the workspace's own first element
     where the workspace is this call's (an allocation less), else one of its own."""
     if ws is None and rows > 0:
-        need = load_library().gbce_workspace_size(rows, 1, 1)
+        need = _row_workspace_size(rows)
         ws = torch.empty((need + 7) // 8, dtype=torch.int64, device=device)
         return ws, ws.data_ptr(), need, ws[0]
     ws, wp, wb = _scratch(ws, 0, device)
@@ -292,7 +298,7 @@ def policy_loss(logp: torch.Tensor, advantages, old_logp=None, ref_logp=None, gr
         raise ValueError("logp must be a CUDA tensor (no CPU path exists)")
     dev, rows = logp.device, logp.numel()
     red = REDUCTIONS[reduction]
-    opt = _policy_options(clip_low, clip_high, kl_beta)
+    opt = _policy_options(float(clip_low), float(clip_high), float(kl_beta))
     with _on(dev, stream):
         lp = _floats(logp, (rows,), dev)
         adv = _per_row(advantages, logp.shape, "advantages", dev)
@@ -328,7 +334,7 @@ def policy_loss_fwd_bwd_fused(logits: torch.Tensor, labels, advantages, old_logp
     rows, vocab = x.shape
     lead, dev = logits.shape[:-1], x.device
     red = REDUCTIONS[reduction]
-    opt = _policy_options(clip_low, clip_high, kl_beta)
+    opt = _policy_options(float(clip_low), float(clip_high), float(kl_beta))
     with _on(dev, stream):
         lab = _flat(_int64(labels, dev), rows)
         adv = _per_row(advantages, lead, "advantages", dev)
@@ -365,10 +371,10 @@ def _sequences(seq_offsets, lead, device):
 
 
 @functools.lru_cache(maxsize=64)
-def _preference_options(beta, margin, label_smoothing, kind, average):
-    """The options and their (host) address."""
-    opt = PreferenceOptions(float(beta), float(margin), float(label_smoothing), KINDS[kind],
-                            1 if average else 0)
+def _preference_options(beta: float, margin: float, label_smoothing: float, kind: int,
+                        average: bool):
+    """The options and their (host) address; by value, so only of plain numbers."""
+    opt = PreferenceOptions(beta, margin, label_smoothing, kind, 1 if average else 0)
     return opt, ctypes.addressof(opt)
 
 
@@ -391,7 +397,8 @@ def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_ou
         raise ValueError("logp must be a CUDA tensor (no CPU path exists)")
     dev, rows = logp.device, logp.numel()
     red = REDUCTIONS[reduction]
-    opt = _preference_options(beta, margin, label_smoothing, kind, average)
+    opt = _preference_options(float(beta), float(margin), float(label_smoothing), KINDS[kind],
+                              bool(average))
     with _on(dev, stream):
         off, pairs = _sequences(seq_offsets, logp.shape, dev)
         lp = _floats(logp, (rows,), dev)
@@ -429,15 +436,16 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
     rows, vocab = x.shape
     lead, dev = logits.shape[:-1], x.device
     red = REDUCTIONS[reduction]
-    opt = _preference_options(beta, margin, label_smoothing, kind, average)
+    opt = _preference_options(float(beta), float(margin), float(label_smoothing), KINDS[kind],
+                              bool(average))
     with _on(dev, stream):
         off, pairs = _sequences(seq_offsets, lead, dev)
         lab = _flat(_int64(labels, dev), rows)
         ref = _per_row(ref_logp, lead, "ref_logp", dev)
         g = _upstream(grad_out, pairs if red == 0 else 1, "pair", dev)
         loss = torch.empty((pairs,) if red == 0 else (), dtype=torch.float32, device=dev)
-        logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
         score = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
+        logp = torch.empty(rows, dtype=torch.float32, device=dev) if want_logp else None
         dlogits, dp, ds = _dlogits(dlogits, logits, x)
         _check_status(dev_status, dev)
         ws, wp, wb = _scratch(workspace, preference_workspace_size(rows, pairs), dev)
