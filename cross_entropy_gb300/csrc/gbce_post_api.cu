@@ -417,7 +417,9 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
     __shared__ int64_t counts[kWarps];
     __shared__ float s_d[2];
     __shared__ int s_last;
-    // a dependent of the kernel that wrote the log-probs
+    // a dependent of the kernel that wrote the log-probs; the gradient's kernel may
+    // take its place meanwhile
+    launch_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int side = tid / kHalf, first = tid - side * kHalf;

@@ -70,20 +70,14 @@ struct LedSum {
     // of the warp's lanes, on every lane, in a fixed order
     template <typename Exp> __device__ __forceinline__ void warp_merge(Exp exp_of)
     {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            // (both lanes of a pair take the lower one's first: the same bits on both)
-            float m2 = __shfl_xor_sync(0xffffffffu, m, off);
-            float s2 = __shfl_xor_sync(0xffffffffu, s, off);
-            if (threadIdx.x & off) {
-                const float a = m, b = s;
-                m = m2;
-                s = s2;
-                m2 = a;
-                s2 = b;
-            }
-            merge(m2, s2, exp_of);
-        }
+        float M;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
+        const int holder = __ffs(__ballot_sync(0xffffffffu, m == M)) - 1;
+        float v = s;
+        if ((threadIdx.x & 31) != holder)
+            v = m == kNegInf ? 0.0f : (1.0f + s) * exp_of(m - M);
+        s = warp_sum(v);
+        m = M;
     }
 };
 
@@ -132,7 +126,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
 
     // With `ordered` the kernel before this one is the library's own count of the
     // rows, which starts once everything before it is complete: only what it wrote
-    // is waited for.
+    // is waited for (wait_for_count).
     if (!ordered)
         grid_dependency_wait();
     const int64_t at = static_cast<int64_t>(blockIdx.x) * G::kRows + group;
@@ -233,15 +227,17 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         if (blockIdx.x == 0 && threadIdx.x == 0)
             *p.n_items_out = n_items;
     }
-    if (ordered)
-        grid_dependency_wait();
     if (!inside)
         return;
-    if (kGrad && p.n_items != nullptr && p.reduction == GBCE_MEAN)
-        n_items = *p.n_items;
+    // (on every way out: the kernel after this one may read the count)
+    const auto wait_for_count = [&] {
+        if (ordered)
+            grid_dependency_wait();
+    };
 
     // a row that is left out or invalid: its outputs
     const auto fill = [&] {
+        wait_for_count();
         const float v = state == kRowSkip ? 0.0f : kQuietNan;
         if (kStats && tid == 0) {
             if (p.loss_rows != nullptr)
@@ -291,6 +287,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     if (G::any(!mbar_wait(&copy_bar[group], 0))) {
         report(p.dev_status, GBCE_DEV_TIMEOUT);
         mbar_wait(&copy_bar[group], 0);
+        wait_for_count();
         return;
     }
     if (kList && bad) {
@@ -396,11 +393,11 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         RestStats st;
         uint4 none;
         none.x = none.y = none.z = none.w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        for (int v0 = tid; v0 < nv; v0 += U * NT) {
+        for (int v = tid; v < nv; v += U * NT) {
             uint4 raw[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                raw[u] = v0 + u * NT < nv ? vec[v0 + u * NT] : none;
+                raw[u] = v + u * NT < nv ? vec[v + u * NT] : none;
 #pragma unroll
             for (int u = 0; u < U; u += 2) {
                 const float own = FastVec<T>::vmax(raw[u], raw[u + 1]);
@@ -418,7 +415,8 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         warp_merge_rest(m, s, c, st.residual(c));
     }
     int nans = 0;
-    if (kList) {
+    const bool listing = kList && warp * 32 < K;  // the warp has entries (the first one the rest too)
+    if (listing) {
         teacher.warp_merge(exp_t);
         student.warp_merge(exp_c);
         nans = (__any_sync(0xffffffffu, nan_t) ? 1 : 0) | (__any_sync(0xffffffffu, nan_x) ? 2 : 0);
@@ -456,6 +454,13 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         p.rest_state_out[2 * r] = m;
         p.rest_state_out[2 * r + 1] = s;
     }
+
+    // The kernel after this one (the losses' sum, the pairs) may take its place; it
+    // waits for this one's outputs.
+    launch_dependents();
+    wait_for_count();
+    if (kGrad && p.n_items != nullptr && p.reduction == GBCE_MEAN)
+        n_items = *p.n_items;
 
     // the loss of a token, and what the sweep over the unlisted columns is scaled by
     const float gt = kGrad ? scaled(post_upstream(p, r, n_items), inv_t) : 0.0f;
@@ -509,29 +514,33 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             E::store(drow + y, dy);
     }
     if constexpr (kList) {
-        const StudentRow q = student_row(m, s, student.m, student.s, c, inv_t);
-        float kl = tid == 0 ? entry_terms(lp_rest, q.log_rest).kl : 0.0f;
-#pragma unroll
-        for (int b = 0; b < KE && b * NT < K; ++b) {
-            if (col[b] < 0)
-                continue;
-            const EntryTerms t =
-                entry_terms((tau[b] - teacher.m) - lt, student_logp(q, x[b], inv_t));
-            kl += t.kl;
-            if (kGrad)
-                E::store(drow + col[b], gt * t.gap);
-        }
-        if (kStats) {
-            kl = warp_sum(kl);
-            if (W > 1) {
-                if (lane == 0)
-                    partial[warp].m = kl;
-                __syncthreads();
-                kl = warp_sum(lane < W ? partial[lane].m : 0.0f);
-            }
+        float kl = 0.0f;
+        if (listing) {
+            const StudentRow q = student_row(m, s, student.m, student.s, c, inv_t);
             if (tid == 0)
-                p.loss_rows[r] = kl;
+                kl = entry_terms(lp_rest, q.log_rest).kl;
+#pragma unroll
+            for (int b = 0; b < KE && b * NT < K; ++b) {
+                if (col[b] < 0)
+                    continue;
+                const EntryTerms t =
+                    entry_terms((tau[b] - teacher.m) - lt, student_logp(q, x[b], inv_t));
+                kl += t.kl;
+                if (kGrad)
+                    E::store(drow + col[b], gt * t.gap);
+            }
+            kl = warp_sum(kl);
         }
+        if (!kStats)
+            return;
+        if (W > 1 && K > 32) {
+            if (lane == 0)
+                partial[warp].m = kl;
+            G::sync();
+            kl = warp_sum(lane < W ? partial[lane].m : 0.0f);
+        }
+        if (tid == 0)
+            p.loss_rows[r] = kl;
     }
 }
 
