@@ -13,10 +13,14 @@
 //   listed k:    a value of its own.
 //
 // A CTA is a ring of bulk copies (one producer thread), NCW consumer warps
-// that sweep the copied vectors, and one list warp that runs ahead: it takes
+// that sweep the copied vectors, and one list warp that is a row ahead: it takes
 // the next row, gathers its listed columns while the consumers still sweep the
 // row before, and finishes the loss of each swept row.  What bounds it is HBM:
 // logits once in, gradients once out; the gradient pass reads its row from L2.
+// At 8192 x 152064 bf16, of 6.79 TB/s measured for a copy: distillation with 64
+// entries 787 us (0.91), policy loss with 15% of the rows left out 717 us (0.95),
+// preference loss of 4096 rows, whose logits are read twice, 487 us (0.94 of the
+// bytes it moves).
 #pragma once
 
 #include "gbce_kernels.cuh"
@@ -79,6 +83,19 @@ struct Sum2 {
 
 // -------------------------------------------------------------- the rest's sum
 
+// The SFU's 2^x is low on the average: by 5.0e-8 of its value for x <= -1, by 2.1e-8
+// between -1 and 0, not at all at 0 (measured over 2^20 arguments per unit).  A sum
+// over a row would carry that in one direction in every row.
+constexpr float kEx2Low = 5e-8f;
+
+// 2^x for the factors that whole sums are multiplied by, without it: one more
+// step of the last place for three results in four, which is 5.8e-8 on the average.
+__device__ __forceinline__ float ex2_level(float x)
+{
+    const float y = ex2(x);
+    return x > -1.0f ? fmaf(y, 2e-8f, y) : fmaf(y, kEx2Low, y);
+}
+
 // Online (max, sum) of the unlisted logits in the exp2 domain, as OnlineStats
 // but with exponents from both parts of c (one more packed multiply-add per
 // pair; the sweep has issue slots to spare).
@@ -92,7 +109,7 @@ struct RestStats {
     {
         if (vmax > m) {
             const float nmc_new = -scaled(vmax, c);
-            const float f = ex2(nmc_new - nmc);
+            const float f = ex2_level(nmc_new - nmc);
             const float2 ff = make_float2(f, f);
             sa = fmul2(sa, ff);
             sb = fmul2(sb, ff);
@@ -137,7 +154,7 @@ __device__ __forceinline__ void warp_merge_rest(float &m, float &s, TwoFloat c, 
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
     float v = 0.0f;
     if (M != kNegInf && m != kNegInf)
-        v = __fmul_rn(s, ex2(__fsub_rn(scaled(m - M, c), r)));
+        v = __fmul_rn(s, ex2_level(__fsub_rn(scaled(m - M, c), r)));
     m = M;
     s = warp_sum(v);
 }
@@ -147,8 +164,8 @@ __device__ __forceinline__ void merge_rest(float &m, float &s, float m2, float s
 {
     const float M = fmaxf(m, m2);
     if (M != kNegInf)
-        s = __fadd_rn(m == kNegInf ? 0.0f : __fmul_rn(s, ex2(scaled(m - M, c))),
-                      m2 == kNegInf ? 0.0f : __fmul_rn(s2, ex2(scaled(m2 - M, c))));
+        s = __fadd_rn(m == kNegInf ? 0.0f : __fmul_rn(s, ex2_level(scaled(m - M, c))),
+                      m2 == kNegInf ? 0.0f : __fmul_rn(s2, ex2_level(scaled(m2 - M, c))));
     m = M;
 }
 
@@ -517,22 +534,41 @@ __device__ __forceinline__ float student_logp(const StudentRow &q, float x, TwoF
 
 // ----------------------------------------------------- one token's log p
 
-// The SFU's 2^x is low by 8e-8 of its value on the average of a row's exponents
-// (measured: log p of 2048 rows of 152064 logits, T 0.7 to 1.3, lies 8.1e-8 to
-// 1.1e-7 above fp64's), and so is the rest's sum.
-constexpr float kEx2Low = 8e-8f;
+// What is left in a sum of what its terms' 2^x lacks: the factors, levelled two or
+// three times, overshoot by 8e-9 each.  With it log p of 1000 to 4000 rows of 100 to
+// 152064 logits, T 0.7 to 2, lies -3e-8 to 5e-8 of 1 - p from fp64's on the average, a
+// quarter of its scatter.
+constexpr float kSumLow = 2.5e-8f;
 
-// finalize_logp with 1 / T in two floats.
+// log p of one column from the rest's (m, s): -log(1 + e^a), a = log s + (m - xy) / T,
+// with a in two floats throughout: log s from its exponent and mantissa, the
+// quotient with what its products round off.  A preference loss sums hundreds of
+// these, and in one float a alone is off by 2.5e-7 (rms) before log p is rounded.
 __device__ __forceinline__ float token_logp(float m, float s, float xy, TwoFloat inv_t)
 {
     if (!(s > 0.0f))
         return (s == 0.0f && xy == xy) ? 0.0f : kQuietNan;
-    // the sum's rounding error joins kEx2Low, or a term below half its step would
-    // vanish in every row
-    const float ls = logf(s), d = scaled(m - xy, inv_t), a = __fadd_rn(ls, d);
-    const float b = __fsub_rn(a, ls);
-    const float err = __fadd_rn(__fsub_rn(ls, __fsub_rn(a, b)), __fsub_rn(d, b));
-    return -softplus(isfinite(a) ? a + (err + kEx2Low) : a);
+    // s = 2^k f, f in [1, 2): log s = k log 2 + log f, k log 2 exact in its first part
+    // (14 bits of log 2)
+    const uint32_t bits = __float_as_uint(s);
+    const bool split = bits >= 0x00800000u && bits < 0x7f800000u;  // (normal)
+    const int k = split ? static_cast<int>(bits >> 23) - 127 : 0;
+    const float f = split ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : s;
+    const float k_hi = k * 0x1.62e4p-1f, rest = fmaf(k, 0x1.7f7d1cp-20f, logf(f));
+    // d = (m - xy) / T
+    const float gap = __fsub_rn(m, xy), gap_lo = __fsub_rn(__fsub_rn(m, gap), xy);
+    const float d = scaled(gap, inv_t);
+    const float d_lo = fmaf(gap, inv_t.hi, -d) + fmaf(gap, inv_t.lo, gap_lo * inv_t.hi);
+    // a = hi + lo
+    const float t = __fadd_rn(k_hi, d), b = __fsub_rn(t, k_hi);
+    if (!isfinite(t) || !split)
+        return -softplus(t + rest);
+    const float small =
+        __fadd_rn(__fsub_rn(k_hi, __fsub_rn(t, b)), __fsub_rn(d, b)) +
+        (d_lo + (kSumLow - __fdividef(kSumLow, s)) + rest);  // (the largest term is 1 exactly)
+    const float hi = __fadd_rn(t, small), lo = __fsub_rn(small, __fsub_rn(hi, t));
+    const float e = expf(-fabsf(hi)), sig = __fdividef(e, 1.0f + e);  // sigma(-|a|)
+    return hi > 0.0f ? -(hi + (log1pf(e) + (lo - lo * sig))) : -(log1pf(e) + lo * sig);
 }
 
 // The clipped policy loss of one row from its log p, and its derivative:
@@ -1349,8 +1385,9 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
 
 // Shared memory of an SM, and what a CTA's static arrays and the system take of it.
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerCta = 2048 + 1024;
-// Bytes of rows that may wait in L2 for their gradient pass.
-constexpr int64_t kPostL2Budget = int64_t(76) << 20;
+// Bytes of rows that may wait in L2 for their gradient pass, beside the gradients
+// of others; where all of them do at once.
+constexpr int64_t kPostL2Budget = int64_t(76) << 20, kPostL2Wave = int64_t(88) << 20;
 // The least columns a slice of a split row has.
 constexpr int64_t kPostSliceElems = 8192;
 
@@ -1456,46 +1493,36 @@ cudaError_t launch_post_shape(const PostParams &params, int sms, cudaStream_t st
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// The CTA shape for rows that are not split.
+// The CTA shape for streamed rows (longer than kShortRowBytes) that are not split.
 //
 // Fused calls re-read each row from L2, so the rows in flight (one per CTA)
-// must fit there: of the shapes for which they do, the one with the most CTAs,
-// as many small CTAs hide a row's serial steps (its list, its merge) best.
-// Measured in us, short / mid / long: distillation, 32 entries, 613 rows x 16384
-// bf16 21 / 27 / 39, 700 x 50256 bf16 42 / 50 / 52, 512 x 32768 fp32 39 / 48 / 46,
-// 4096 x 32768 fp32 222 / 197 / 236, 8192 x 65536 bf16 422 / 367 / 445, 2000 x
-// 100000 bf16 193 / 175 / 166, 4096 x 152064 bf16 578 / 541 / 429.  Without lists,
-// rows of 48 KB and more that come in several waves do better with the larger ring
-// of the mid shape (policy loss, 8192 x 32768 bf16 189 / 177 / 283).
-// One pass only (nothing re-read): short up to one wave of its CTAs, but mid where
-// one wave of those holds the rows and they are long (distillation's loss, 700 x
-// 100000 bf16 40 / 56 / 50, 400 x 152064 41 / 33 / 39); several waves of long rows
-// want fewer and larger CTAs (both sweeps of the preference loss, 1000 x 152064
-// bf16 195 / 187 / 171; 8192 x 32768 285 / 277 / 346), lists more of them
-// (distillation's loss, 8192 x 65536 bf16 199 / 185 / 308).
+// must fit there: of the shapes for which they do, the one with the most CTAs
+// for rows of one wave (small CTAs hide a row's serial steps, its list and its
+// merge, best), but mid where one wave of those holds the rows and they are
+// long; the mid shape's larger ring for several waves.  Measured in us, short /
+// mid / long: distillation, 32 entries, 700 x 60000 bf16 39 / 44 / 50, 500 x 32768
+// fp32 31 / 38 / 40, 300 x 100000 bf16 33 / 28 / 33, 4096 x 32768 fp32 214 / 179 / 229,
+// 8192 x 65536 bf16 422 / 346 / 426, 2000 x 100000 181 / 158 / 150, 4096 x 152064 557 /
+// 524 / 412; policy loss, 4000 x 60000 188 / 158 / 197, 2000 x 100000 177 / 156 / 149.
+// One pass only (nothing re-read): one wave by the same rule (both sweeps of the
+// preference loss, 700 x 100000 bf16 67 / 81 / 77, 400 x 152064 62 / 59 / 69); several
+// waves of long rows want fewer and larger CTAs (1000 x 152064 162 / 142 / 137, 4096 x
+// 60000 209 / 207 / 231), lists more of them (distillation in two calls, 4096 x
+// 152064 596 / 590 / 607, 4096 x 60000 250 / 254 / 376).
 template <typename T>
 int post_shape(const PostParams &p, int op, int pass, int sms)
 {
     const int64_t row = p.vocab * static_cast<int64_t>(sizeof(T));
     const int64_t many = static_cast<int64_t>(sms) * PostShape<kShapeShort>::kCtasPerSm;
     const int64_t some = static_cast<int64_t>(sms) * PostShape<kShapeMid>::kCtasPerSm;
-    const auto fits = [&](int64_t ctas) {
-        return (p.rows < ctas ? p.rows : ctas) * row <= kPostL2Budget;
-    };
-    const bool waves = p.rows > many;
-    if (pass == kPassFused) {
-        if (fits(many) && !(op == kOpPolicy && waves && row >= 48 * 1024))
-            return kShapeShort;
-        return fits(some) ? kShapeMid : kShapeLong;
-    }
-    if (!waves)
+    const bool one_wave = p.rows <= many, fused = pass == kPassFused;
+    if (one_wave && (!fused || p.rows * row <= kPostL2Wave))
         return p.rows <= some && row >= 160 * 1024 ? kShapeMid : kShapeShort;
-    if (op == kOpDistill) {
-        if (row < 96 * 1024)
-            return kShapeShort;
+    if (fused)
+        return (p.rows < some ? p.rows : some) * row <= kPostL2Budget ? kShapeMid : kShapeLong;
+    if (op == kOpDistill)
         return pass == kPassFwd && row >= 256 * 1024 && p.rows < 4 * some ? kShapeLong : kShapeMid;
-    }
-    return row < 48 * 1024 ? kShapeShort : row < 128 * 1024 ? kShapeMid : kShapeLong;
+    return row < 128 * 1024 ? kShapeMid : kShapeLong;
 }
 
 template <typename T, int OP, int PASS>
@@ -1529,7 +1556,11 @@ cudaError_t launch_post(const PostParams &p, int op, int pass, cudaStream_t stre
 {
     if (p.rows == 0)
         return cudaSuccess;
-    if (p.vocab * static_cast<int64_t>(sizeof(T)) <= kShortRowBytes)
+    // Short rows are kept in shared memory; a few that would make a CTA long are
+    // split over a cluster below (policy loss, 8 x 50000 bf16 7.9 us, whole 8.5; 100 x
+    // 40000 11.8, whole 8.9; 24 x 16384 6.9, whole 6.3).
+    const int64_t row = p.vocab * static_cast<int64_t>(sizeof(T));
+    if (row <= kShortRowBytes && (row <= kShortAlwaysBytes || p.rows > kShortFewest))
         return launch_post_short<T>(p, op, pass, stream);
     if (op == kOpPolicy)
         return launch_post_as<T, kOpPolicy, kPassFused>(p, stream);

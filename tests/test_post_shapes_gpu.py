@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 SIZES = [(401, 4096, 33, BF16, 0, 0), (402, 4097, 7, BF16, 3, 1), (400, 2048, 32, F32, 0, 2),
          (1024, 65, 60, F32, 1, 1), (1027, 300, 256, BF16, 5, 3), (30, 24576, 200, BF16, 1, 5),
          (20, 24577, 256, BF16, 0, 0), (9, 53248, 64, BF16, 3, 3), (6, 53249, 64, BF16, 0, 1),
-         (5, 26625, 130, F32, 2, 0), (240, 53255, 50, BF16, 7, 1)]
+         (5, 26625, 130, F32, 2, 0), (240, 53255, 50, BF16, 7, 1), (17, 32769, 64, BF16, 3, 3),
+         (16, 32769, 64, BF16, 0, 0), (40, 53248, 100, BF16, 1, 0), (18, 26624, 256, F32, 0, 1)]
 
 
 @pytest.mark.parametrize("rows,V,K,dtype,pad,shift", SIZES)
@@ -35,7 +36,7 @@ def test_preference(gbce, rows, V, K, dtype, pad, shift):  # noqa: F811
     base.test_preference(gbce, rows, V, 2, dtype, pad, 1, "sigmoid", True, True, "mean", 2.0, 0.1, 0.5)
 
 
-@pytest.mark.parametrize("rows,V,dtype", [(500, 3001, BF16), (500, 700, F32), (9, 20001, BF16), (9, 40001, BF16),
+@pytest.mark.parametrize("rows,V,dtype", [(500, 3001, BF16), (500, 700, F32), (9, 20001, BF16), (9, 40001, BF16), (30, 40001, BF16),
                                           (9, 60001, BF16), (240, 60001, BF16), (240, 27001, F32)])
 def test_bad_rows_among_good_ones(gbce, rows, V, dtype):  # noqa: F811
     g = gen(V + rows)
@@ -141,3 +142,15 @@ def test_the_same_bits_in_a_graph_beside_eager_calls(gbce, rows, V):  # noqa: F8
     torch.cuda.synchronize()
     for a, b, w in zip(held, other, want):
         assert torch.equal(a, w) and torch.equal(b, w)
+
+
+@pytest.mark.parametrize("rows,V,K", [(402, 1, 3), (402, 90, 256), (7, 90, 256), (20, 30000, 256), (230, 60000, 256)])
+def test_lists_of_one_column(gbce, rows, V, K):  # noqa: F811
+    """Every entry names the same column, or one of two: their teacher's sums in entry order."""
+    g = gen(V + K)
+    x = logits_of(rows, V, F32 if V < 100 else BF16, g)
+    idx = torch.full((rows, K), V - 1)
+    idx[::2, ::3] = 0
+    t = torch.randn((rows, K), generator=g)
+    r = torch.randn(rows, generator=g) if V > 2 else None
+    base.distill_check(gbce, x, idx, t, r, 0.9, None, "mean", seed=V)
