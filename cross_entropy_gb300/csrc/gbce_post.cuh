@@ -544,10 +544,16 @@ constexpr float kSumLow = 2.5e-8f;
 // with a in two floats throughout: log s from its exponent and mantissa, the
 // quotient with what its products round off.  A preference loss sums hundreds of
 // these, and in one float a alone is off by 2.5e-7 (rms) before log p is rounded.
-__device__ __forceinline__ float token_logp(float m, float s, float xy, TwoFloat inv_t)
+struct TokenTerms {
+    float lp, other;  // log p, 1 - p
+};
+
+__device__ __forceinline__ TokenTerms token_terms(float m, float s, float xy, TwoFloat inv_t)
 {
-    if (!(s > 0.0f))
-        return (s == 0.0f && xy == xy) ? 0.0f : kQuietNan;
+    if (!(s > 0.0f)) {
+        const float v = (s == 0.0f && xy == xy) ? 0.0f : kQuietNan;
+        return {v, v};
+    }
     // s = 2^k f, f in [1, 2): log s = k log 2 + log f, k log 2 exact in its first part
     // (14 bits of log 2)
     const uint32_t bits = __float_as_uint(s);
@@ -561,14 +567,18 @@ __device__ __forceinline__ float token_logp(float m, float s, float xy, TwoFloat
     const float d_lo = fmaf(gap, inv_t.hi, -d) + fmaf(gap, inv_t.lo, gap_lo * inv_t.hi);
     // a = hi + lo
     const float t = __fadd_rn(k_hi, d), b = __fsub_rn(t, k_hi);
-    if (!isfinite(t) || !split)
-        return -softplus(t + rest);
+    if (!isfinite(t) || !split) {
+        const float lp = -softplus(t + rest);
+        return {lp, -expm1f(lp)};
+    }
     const float small =
         __fadd_rn(__fsub_rn(k_hi, __fsub_rn(t, b)), __fsub_rn(d, b)) +
         (d_lo + (kSumLow - __fdividef(kSumLow, s)) + rest);  // (the largest term is 1 exactly)
     const float hi = __fadd_rn(t, small), lo = __fsub_rn(small, __fsub_rn(hi, t));
     const float e = expf(-fabsf(hi)), sig = __fdividef(e, 1.0f + e);  // sigma(-|a|)
-    return hi > 0.0f ? -(hi + (log1pf(e) + (lo - lo * sig))) : -(log1pf(e) + lo * sig);
+    if (hi > 0.0f)
+        return {-(hi + (log1pf(e) + (lo - lo * sig))), 1.0f - sig};
+    return {-(log1pf(e) + lo * sig), sig};
 }
 
 // The clipped policy loss of one row from its log p, and its derivative:
@@ -875,19 +885,19 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 if (kStats && lane == 0 && split == 0)
                     p.loss_rows[w.r] = kl;
             } else if (lane == 0) {
-                const float lp = token_logp(m, s, w.xy, inv_t);
+                const TokenTerms y = token_terms(m, s, w.xy, inv_t);
                 float slope = w.gt;
                 if (kStats && p.logp_out != nullptr && split == 0)
-                    p.logp_out[w.r] = lp;
+                    p.logp_out[w.r] = y.lp;
                 if (OP == kOpPolicy) {
                     float loss, dlp;
-                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
+                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, y.lp, loss, dlp);
                     if (split == 0)
                         p.loss_rows[w.r] = loss;
                     slope *= dlp;
                 }
                 if (kGrad)
-                    w.dy = -slope * expm1f(lp);
+                    w.dy = slope * y.other;
             }
         };
         // row i's listed columns, over what the sweep stored there (every thread
@@ -1326,14 +1336,14 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             if (kList) {
                 gs = gt * rest_gap(m, s, w.ml, w.sl, w.lp_rest, c, inv_t);
             } else {
-                const float lp = token_logp(m, s, w.xy, inv_t);
+                const TokenTerms y = token_terms(m, s, w.xy, inv_t);
                 float slope = gt;  // (g / T) dloss / dlog p
                 if (OP == kOpPolicy) {
                     float loss, dlp;
-                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, lp, loss, dlp);
+                    policy_row(p.policy, w.adv, w.old_lp, w.ref_lp, y.lp, loss, dlp);
                     slope *= dlp;
                 }
-                gs = slope * expm1f(lp);
+                gs = -slope * y.other;
             }
             const GradConsts gk = rest_consts(m, s, c.hi + c.lo, gs);
             constexpr int32_t kNoLabel = 0x7fffffff;

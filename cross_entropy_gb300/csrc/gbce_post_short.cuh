@@ -209,8 +209,11 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         *p.zero_out = 0;
 
     int64_t n_items = 0;
-    if (p.n_items_out != nullptr && (blockIdx.x == 0 || (kGrad && p.reduction == GBCE_MEAN))) {
-        // few rows: every CTA counts the rows that are kept
+    if (p.n_items_out != nullptr &&
+        (blockIdx.x == 0 ||
+         (kGrad && p.reduction == GBCE_MEAN && (G::kRows > 1 || state == kRowLive)))) {
+        // few rows: every CTA that needs it counts the rows that are kept
+#pragma unroll 4
         for (int64_t j = threadIdx.x; j < p.rows; j += G::kCta)
             n_items += kList ? (p.row_mask == nullptr || p.row_mask[j] != 0)
                              : p.labels[j] != p.ignore_index;
@@ -471,19 +474,19 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
         if (kGrad)
             gs = gt * rest_gap(m, s, student.m, student.s, lp_rest, c, inv_t);
     } else {
-        const float lp = token_logp(m, s, xy, inv_t);
+        const TokenTerms q = token_terms(m, s, xy, inv_t);
         float slope = gt;
         if (kStats && p.logp_out != nullptr && tid == 0)
-            p.logp_out[r] = lp;
+            p.logp_out[r] = q.lp;
         if (OP == kOpPolicy) {
             float loss, dlp;
-            policy_row(p.policy, adv, old_lp, ref_lp, lp, loss, dlp);
+            policy_row(p.policy, adv, old_lp, ref_lp, q.lp, loss, dlp);
             if (tid == 0)
                 p.loss_rows[r] = loss;
             slope *= dlp;
         }
-        gs = slope * expm1f(lp);
-        dy = -gs;
+        dy = slope * q.other;
+        gs = -dy;
     }
 
     if (kGrad) {
@@ -544,8 +547,11 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     }
 }
 
-// Rows of a batch up to which every CTA counts the kept ones itself.
-constexpr int64_t kShortSelfCount = 1024;
+// Rows of a batch up to which no kernel is launched to count the kept ones: where
+// every CTA needs the number (a mean's gradient; us, counted by every CTA / before:
+// policy loss, 1000 x 2000 7.7 / 7.5 and one launch less for the host, 2000 x 14000 30 / 25),
+// and where only the call's result does, for which one CTA counts.
+constexpr int64_t kShortSelfCount = 1024, kShortOneCount = 16384;
 
 template <typename T, int OP, int PASS, int W>
 cudaError_t launch_short_as(PostParams p, cudaStream_t stream)
@@ -557,7 +563,8 @@ cudaError_t launch_short_as(PostParams p, cudaStream_t stream)
     if (err != cudaSuccess)
         return err;
     int ordered = 0;
-    if (p.n_items_out != nullptr && p.rows > kShortSelfCount) {
+    const bool each = PASS != kPassFwd && p.reduction == GBCE_MEAN;
+    if (p.n_items_out != nullptr && p.rows > (each ? kShortSelfCount : kShortOneCount)) {
         err = OP == kOpDistill
                   ? launch_count_mask(p.row_mask, p.rows, p.n_items_out, nullptr, stream)
                   : launch_count_items(p.labels, p.rows, p.ignore_index, p.n_items_out, nullptr,
