@@ -110,6 +110,9 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     extern __shared__ __align__(128) uint8_t dyn_smem[];
     __shared__ uint64_t copy_bar[G::kRows];
     __shared__ ShortPartial partial[W];
+    // each warp's part of the loss, beside `partial`: a slower warp may still be
+    // reading that (no barrier lies between the two in the forward pass)
+    __shared__ float partial_kl[W];
     __shared__ int64_t counts[G::kCta / 32];
 
     const int lane = threadIdx.x & 31;
@@ -538,9 +541,9 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             return;
         if (W > 1 && K > 32) {
             if (lane == 0)
-                partial[warp].m = kl;
+                partial_kl[warp] = kl;
             G::sync();
-            kl = warp_sum(lane < W ? partial[lane].m : 0.0f);
+            kl = warp_sum(lane < W ? partial_kl[lane] : 0.0f);
         }
         if (tid == 0)
             p.loss_rows[r] = kl;
