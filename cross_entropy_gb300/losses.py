@@ -373,7 +373,11 @@ def _sequences(seq_offsets, lead, device):
 @functools.lru_cache(maxsize=64)
 def _preference_options(beta: float, margin: float, label_smoothing: float, kind: int,
                         average: bool):
-    """The options and their (host) address; by value, so only of plain numbers."""
+    """The options and their (host) address; by value, so only of plain numbers.  Margin and
+    smoothing are the sigmoid's: the library refuses them with the squared kind, so that one set
+    of options can serve both kinds they stop here."""
+    if kind == KINDS["squared"]:
+        margin = label_smoothing = 0.0
     opt = PreferenceOptions(beta, margin, label_smoothing, kind, 1 if average else 0)
     return opt, ctypes.addressof(opt)
 
@@ -391,6 +395,8 @@ def preference_loss(logp: torch.Tensor, seq_offsets=None, ref_logp=None, grad_ou
     answers before the rejected ones, and the end; None for logp [2 pairs, length].
     ``ref_logp`` is the reference policy's log-probs of the same tokens (None: no
     reference); ``average`` divides each sequence's sum by its live tokens.
+    ``margin`` and ``label_smoothing`` are options of the sigmoid kind; the squared
+    kind has neither and takes no notice of them.
     """
     lib = load_library()
     if not logp.is_cuda:
@@ -429,8 +435,8 @@ def preference_loss_fwd_bwd_fused(logits: torch.Tensor, labels, seq_offsets=None
                                   workspace: Optional[torch.Tensor] = None,
                                   dev_status: Optional[torch.Tensor] = None,
                                   stream=None) -> PreferenceFused:
-    """:func:`preference_loss` of log p of the labels, and its gradient with respect to the
-    logits; rows with label ``ignore_index`` are left out of their sequence."""
+    """:func:`preference_loss` (and its options) of log p of the labels, and its gradient with
+    respect to the logits; rows with label ``ignore_index`` are left out of their sequence."""
     lib = load_library()
     x, code, xs = _logits(logits)
     rows, vocab = x.shape

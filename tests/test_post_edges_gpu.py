@@ -43,3 +43,19 @@ def test_forward_of_many_listed_entries(gbce, rows, V, K, dtype):  # noqa: F811
     for _ in range(100):
         again = gbce.distill_fwd(x, idx, t, None, 1.0, None, "none")
         assert torch.equal(again.loss, first.loss) and torch.equal(again.rest_state, first.rest_state)
+
+
+def test_squared_preference_takes_no_notice_of_the_sigmoids_options(gbce):  # noqa: F811
+    """One set of options serves both kinds: the squared loss has neither a margin nor smoothing."""
+    g = gen(5)
+    x, lab = gpu(logits_of(12, 90, F32, g)), gpu(torch.randint(0, 90, (12,), generator=g))
+    off = [0, 3, 6, 9, 12]
+    want = gbce.preference_loss_fwd_bwd_fused(x, lab, off, kind="squared", beta=0.5)
+    got = gbce.preference_loss_fwd_bwd_fused(x, lab, off, kind="squared", beta=0.5, margin=0.5, label_smoothing=0.1)
+    assert torch.equal(got.loss, want.loss) and torch.equal(got.dlogits, want.dlogits)
+    one = gbce.preference_loss(want.logp, off, kind="squared", beta=0.5, margin=0.5, label_smoothing=0.1)
+    two = gbce.preference_loss(want.logp, off, kind="squared", beta=0.5)
+    assert torch.equal(one.loss, two.loss) and torch.equal(one.dlogp, two.dlogp)
+    # in effect for the other kind
+    assert not torch.equal(gbce.preference_loss(want.logp, off, margin=0.5).loss,
+                           gbce.preference_loss(want.logp, off).loss)
