@@ -399,11 +399,10 @@ def run(st):
                              st["grad_out"], st["mask"], clip_low=st["clip_low"],
                              clip_high=st["clip_high"], kl_beta=st["beta"], reduction=red)
         return dict(loss=r.loss, dlogp=r.dlogp, n_items=r.n_items)
-    # the squared kind has neither a margin nor smoothing, and its call refuses them
-    only = dict(margin=st["margin"], label_smoothing=st["smoothing"]) if st["kind"] == "sigmoid" else {}
     r = gbce.preference_loss_fwd_bwd_fused(st["logits"], st["labels"], st["offsets"], st["ref_logp"],
-                                           st["grad_out"], beta=st["beta"], kind=st["kind"],
-                                           average=st["average"], temperature=T, reduction=red, **only)
+                                           st["grad_out"], beta=st["beta"], margin=st["margin"],
+                                           label_smoothing=st["smoothing"], kind=st["kind"],
+                                           average=st["average"], temperature=T, reduction=red)
     return dict(loss=r.loss, logp=r.logp, seq_score=r.seq_score, dlogits=r.dlogits)
 
 
