@@ -99,12 +99,18 @@ __device__ __forceinline__ float ex2_level(float x)
 // Online (max, sum) of the unlisted logits in the exp2 domain, as OnlineStats
 // but with exponents from both parts of c (one more packed multiply-add per
 // pair; the sweep has issue slots to spare).
+//
+// Far logits, |x| c >= 2^31 (a mask of the type's lowest value, whose x c is not
+// even finite): no shift can be taken off them, and none is needed.  Two of them
+// that differ do so by 2^7 or more in the exponent, so beside the max only its
+// equals count, each 1; the shift stays infinite, which drops what came before.
 struct RestStats {
     float m = kNegInf;
     float nmc = __builtin_huge_valf();  // -m c, the shift added to every x c
     float2 sa = make_float2(0.0f, 0.0f);
     float2 sb = make_float2(0.0f, 0.0f);
 
+    // (vmax not far)
     __device__ __forceinline__ void raise_to(float vmax, TwoFloat c)
     {
         if (vmax > m) {
@@ -117,12 +123,23 @@ struct RestStats {
             nmc = nmc_new;
         }
     }
-    // (x c_lo spans many steps of nmc, so what rounding takes from it differs
-    // from logit to logit and leaves the sum alone)
+    // (a vmax that is not far lies beside another thread's far one, which drops it)
+    __device__ __forceinline__ void raise_to_far(float vmax, float far)
+    {
+        if (vmax > m && fabsf(vmax) >= far) {
+            const float2 zero = make_float2(0.0f, 0.0f);
+            sa = fmul2(sa, zero);  // (a NaN stays)
+            sb = fmul2(sb, zero);
+            m = vmax;
+            nmc = vmax > 0.0f ? kNegInf : __builtin_huge_valf();
+        }
+    }
+    // (the large part of x c meets the shift first, where the two cancel: what is
+    // rounded is the exponent's own size, and at the max it is residual()'s very steps)
     __device__ __forceinline__ float2 terms(float2 x, TwoFloat c) const
     {
         const float2 hi = make_float2(c.hi, c.hi), lo = make_float2(c.lo, c.lo);
-        const float2 z = ffma2(x, hi, ffma2(x, lo, make_float2(nmc, nmc)));
+        const float2 z = ffma2(x, lo, ffma2(x, hi, make_float2(nmc, nmc)));
         return make_float2(ex2(z.x), ex2(z.y));
     }
     __device__ __forceinline__ void add(float2 p, float2 q, TwoFloat c)
@@ -130,11 +147,20 @@ struct RestStats {
         sa = fadd2(sa, terms(p, c));
         sb = fadd2(sb, terms(q, c));
     }
-    __device__ __forceinline__ void add1(float x, TwoFloat c)
+    __device__ __forceinline__ void add1(float x, TwoFloat c, float far)
     {
-        raise_to(x, c);
-        if (x != kNegInf)
-            sa.x += ex2(fmaf(x, c.hi, fmaf(x, c.lo, nmc)));
+        if (fabsf(x) < far) {
+            raise_to(x, c);
+            sa.x += ex2(fmaf(x, c.lo, fmaf(x, c.hi, nmc)));
+        } else if (x != kNegInf) {
+            raise_to_far(x, far);
+            sa.x += far_term(x, m);
+        }
+    }
+    // What a logit adds beside a far max `top`: +inf and NaN have no softmax.
+    __device__ static __forceinline__ float far_term(float x, float top)
+    {
+        return x != x || x == __builtin_huge_valf() ? __builtin_nanf("") : (x == top ? 1.0f : 0.0f);
     }
     __device__ __forceinline__ float sum() const
     {
@@ -143,7 +169,7 @@ struct RestStats {
     // what every exponent carries of the shift's rounding (OnlineStats::residual)
     __device__ __forceinline__ float residual(TwoFloat c) const
     {
-        return isfinite(m) ? fmaf(m, c.lo, fmaf(m, c.hi, nmc)) : 0.0f;
+        return isfinite(nmc) ? fmaf(m, c.lo, fmaf(m, c.hi, nmc)) : 0.0f;
     }
 };
 
@@ -610,17 +636,25 @@ __device__ __forceinline__ void policy_row(const PolicyTerms &t, float A, float 
 
 // Constants of the sweep over the unlisted columns: gs 2^{(x - m) c - log2 s}.
 // Every exponent is <= 0 and relative to the rest's own max, so no element
-// carries the rounding of a large offset.
+// carries the rounding of a large offset.  The bf16 sweep adds the offset to x c in
+// one step: what kbx rounds off goes into gs, and c is taken smaller where m c would
+// pass 2^30 (two bf16 logits that differ are 2^22 apart there, whatever c is).
+template <typename T>
 __device__ __forceinline__ GradConsts rest_consts(float m, float s, float c, float gs)
 {
     const bool none = !(s > 0.0f) || !isfinite(m);  // nothing unlisted has mass
     GradConsts k;
-    k.c = c;
     k.off = 0.0f;
     k.nxy = none ? 0.0f : -m;
+    k.c = sizeof(T) == 2 && !none ? fminf(c, 0x1p30f / fabsf(m)) : c;
     k.kb = none ? 0.0f : -log2f(s);
-    k.kbx = none ? 0.0f : fmaf(-m, c, k.kb);
+    k.kbx = none ? 0.0f : fmaf(-m, k.c, k.kb);
     k.gs = none && !(s != s) && m != __builtin_huge_valf() ? 0.0f : gs;
+    if (sizeof(T) == 2 && !none) {
+        const float kept = fmaf(m, k.c, k.kbx);  // kb as kbx has it
+        k.gs *= ex2(k.kb - kept);
+        k.kb = kept;
+    }
     k.dy = 0.0f;
     k.c0 = 0.0f;
     k.ea = k.eb = 0.0f;
@@ -676,6 +710,49 @@ __device__ __forceinline__ void rest_add(RestStats &st, const uint4 &a, TwoFloat
 {
     st.add(make_float2(__uint_as_float(a.x), __uint_as_float(a.y)),
            make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), c);
+}
+
+// ... and one whose largest logit is far, NaN or -inf (few are).
+template <typename T>
+__device__ __forceinline__ void rest_add_far(RestStats &st, const uint4 &a, float far)
+{
+    constexpr int VEC = Elem<T>::kVec;
+    const float top = FastVec<T>::vmax(a);
+    if (top == kNegInf)
+        return;
+    st.raise_to_far(top, far);
+    float f[VEC];
+    Elem<T>::unpack(a, f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        st.sa.x += RestStats::far_term(f[e], st.m);
+}
+
+// One vector, and two with `top` the largest of them, or of the warp's.
+template <typename T>
+__device__ __forceinline__ void rest_take(RestStats &st, const uint4 &a, TwoFloat c, float far)
+{
+    const float top = FastVec<T>::vmax(a);
+    if (fabsf(top) < far) {
+        st.raise_to(top, c);
+        rest_add(st, a, c, static_cast<const T *>(nullptr));
+    } else {
+        rest_add_far<T>(st, a, far);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void rest_take(RestStats &st, const uint4 &a, const uint4 &b, float top,
+                                          TwoFloat c, float far)
+{
+    if (fabsf(top) < far) {
+        st.raise_to(top, c);
+        rest_add(st, a, c, static_cast<const T *>(nullptr));
+        rest_add(st, b, c, static_cast<const T *>(nullptr));
+    } else {
+        rest_add_far<T>(st, a, far);
+        rest_add_far<T>(st, b, far);
+    }
 }
 
 // Orders the consumers' writes to a stage (which the release of the stage has
@@ -1229,12 +1306,12 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
             };
             RestStats st;
             if (sl.first && tid < sl.g.head)
-                st.add1(is_listed(tid) ? kNegInf : E::load(row + tid), c);
+                st.add1(is_listed(tid) ? kNegInf : E::load(row + tid), c, p.far);
             if (sl.last && sl.g.tail0 + tid < V)
                 st.add1(is_listed(static_cast<int32_t>(sl.g.tail0) + tid)
                             ? kNegInf
                             : E::load(row + sl.g.tail0 + tid),
-                        c);
+                        c, p.far);
             for (int32_t j = 0; j < nchunks; ++j) {
                 uint4 *chunk = wait_chunk();
                 const int32_t vb0 = j * CV;
@@ -1257,20 +1334,12 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                     for (int u = 0; u < PER_THREAD; u += 2) {
                         const float own = FastVec<T>::vmax(raw[u], raw[u + 1]);
                         // (many warps: the running max rises for the whole warp at once)
-                        st.raise_to(NCW > 8 ? warp_max_active(own) : own, c);
-                        if (own != kNegInf) {
-                            rest_add(st, raw[u], c, static_cast<const T *>(nullptr));
-                            rest_add(st, raw[u + 1], c, static_cast<const T *>(nullptr));
-                        }
+                        rest_take<T>(st, raw[u], raw[u + 1],
+                                     NCW > 8 ? warp_max_active(own) : own, c, p.far);
                     }
                 } else if (alive) {
-                    for (int32_t v = tid; v < nv; v += NC) {
-                        const uint4 raw = chunk[v];
-                        const float own = FastVec<T>::vmax(raw);
-                        st.raise_to(own, c);
-                        if (own != kNegInf)
-                            rest_add(st, raw, c, static_cast<const T *>(nullptr));
-                    }
+                    for (int32_t v = tid; v < nv; v += NC)
+                        rest_take<T>(st, chunk[v], c, p.far);
                 }
                 done_chunk();
             }
@@ -1345,7 +1414,7 @@ __global__ void __launch_bounds__(post_threads<SHAPE>(), PostShape<SHAPE>::kCtas
                 }
                 gs = -slope * y.other;
             }
-            const GradConsts gk = rest_consts(m, s, c.hi + c.lo, gs);
+            const GradConsts gk = rest_consts<T>(m, s, c.hi + c.lo, gs);
             constexpr int32_t kNoLabel = 0x7fffffff;
             const StoreGeom dg = store_geom<T>(drow, sl.g, V);
             const int sh = dg.sh;

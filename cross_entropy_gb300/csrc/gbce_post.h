@@ -32,6 +32,7 @@ struct PostParams {
     int64_t rows, vocab, row_stride;  // row_stride in elements
     float c_hi, c_lo;                 // log2(e) / T in two floats
     float it_hi, it_lo;               // 1 / T in two floats
+    float far;                        // logits from here on have |x| log2(e) / T >= 2^31
 
     // distillation: the teacher's entries
     const int64_t *index;       // [rows, k] columns, -1: no entry

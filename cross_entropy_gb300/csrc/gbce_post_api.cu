@@ -3,6 +3,7 @@
 // values only (rows counted, the policy loss of given log-probs, the
 // preference loss of paired sequences).  No entry point allocates memory or
 // synchronizes the host.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -622,6 +623,8 @@ PostParams post_params(const void *logits, int64_t rows, int64_t vocab, int64_t 
     p.row_stride = row_stride;
     two_floats(c, p.c_hi, p.c_lo);
     two_floats(it, p.it_hi, p.it_lo);
+    const double far = 0x1p31 / c;
+    p.far = far < FLT_MAX ? static_cast<float>(far) : HUGE_VALF;
     p.k = 1;
     p.splits = 1;
     p.keep_from = INT64_MAX;

@@ -405,14 +405,8 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             for (int u = 0; u < U; ++u)
                 raw[u] = v + u * NT < nv ? vec[v + u * NT] : none;
 #pragma unroll
-            for (int u = 0; u < U; u += 2) {
-                const float own = FastVec<T>::vmax(raw[u], raw[u + 1]);
-                st.raise_to(own, c);
-                if (own != kNegInf) {
-                    rest_add(st, raw[u], c, static_cast<const T *>(nullptr));
-                    rest_add(st, raw[u + 1], c, static_cast<const T *>(nullptr));
-                }
-            }
+            for (int u = 0; u < U; u += 2)
+                rest_take<T>(st, raw[u], raw[u + 1], FastVec<T>::vmax(raw[u], raw[u + 1]), c, p.far);
         }
         m = st.m;
         s = st.sum();
@@ -493,7 +487,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     }
 
     if (kGrad) {
-        const GradConsts gk = rest_consts(m, s, c.hi + c.lo, gs);
+        const GradConsts gk = rest_consts<T>(m, s, c.hi + c.lo, gs);
         const RowGeom gd = row_geom<T>(drow, V);
         const int first = phase + static_cast<int>(gd.head), sh = first & (VEC - 1);
         const uint4 *from = vec + first / VEC;

@@ -59,3 +59,111 @@ def test_squared_preference_takes_no_notice_of_the_sigmoids_options(gbce):  # no
     # in effect for the other kind
     assert not torch.equal(gbce.preference_loss(want.logp, off, margin=0.5).loss,
                            gbce.preference_loss(want.logp, off).loss)
+
+
+# rows, V, dtype, where they go: one, four, eight warps a row; split over a cluster; streamed, by CTAs of
+# each shape
+PLACES = [(402, 300, F32), (402, 4001, BF16), (9, 3001, F32), (20, 30000, BF16), (20, 20001, F32), (9, 60001, BF16),
+          (9, 30001, F32), (240, 60001, BF16), (600, 30001, F32), (500, 100000, BF16), (460, 50001, F32)]
+SPECIAL = 8   # rows that are looked at
+
+
+def masked_rows(rows, V, dtype, fill, K, g):
+    """Logits with masked columns at `fill`, the same with -inf there, labels, teacher columns: a random
+    quarter, a tenth, the first half, the last half, all but the label or the entries, everything (no
+    -inf: all columns alike), nothing, a single vector kept."""
+    x = torch.full((rows, V), 0.0)
+    x[:SPECIAL] = torch.randn((SPECIAL, V), generator=g) * 2.0
+    keep = torch.rand((SPECIAL, V), generator=g) < torch.tensor([0.25, 0.1, 1, 1, 0, 0, 1, 0]).unsqueeze(1)
+    keep[2, V // 2:] = False
+    keep[3, :V // 2] = False
+    keep[7, 40:48] = True
+    lab = torch.randint(0, V, (rows,), generator=g)
+    lab[2], lab[3], lab[7] = 5, V - 1, 44
+    idx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(rows)])
+    for r in range(SPECIAL):
+        if r != 5:
+            keep[r, lab[r]] = True
+    x = x.to(dtype)
+    low = fill if fill is not None else torch.finfo(dtype).min
+    far, gone = x.clone(), x.clone()
+    far[:SPECIAL][~keep] = low
+    gone[:SPECIAL][~keep] = NEG
+    gone[5] = 0.0
+    return far, gone, keep, lab, idx
+
+
+@pytest.mark.parametrize("fill,T", [(None, 1.0), (None, 0.7), (None, 2.0), (-1e9, 1.0), (-1e4, 0.7), (-1e30, 1.3)])
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_masks_of_a_low_value(gbce, rows, V, dtype, fill, T):  # noqa: F811
+    """A masked column has no mass whatever low value it holds, and columns that all hold one share it.
+    (At -1e4 and -1e9 the masks' shares underflow too; the reference has -inf there.)"""
+    g = gen(V + 7)
+    far, gone, keep, lab, _ = masked_rows(rows, V, dtype, fill, 4, g)
+    n = SPECIAL
+    lp, comp, z = ref.logp_rows(gone[:n].float(), lab[:n], T)
+    adv = torch.rand(rows, generator=g) + 0.5
+    one = torch.ones(rows, device=DEV)
+    xg, labg = gpu(far), gpu(lab)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    p = gbce.policy_loss_fwd_bwd_fused(xg, labg, gpu(adv), None, None, one, reduction="none", temperature=T,
+                                       dev_status=flag)
+    base.close(p.logp[:n], lp, base.LOGP_TOL[dtype], 2.0 ** -148, "policy logp")
+    base.rows_close(p.dlogits[:n], ref.softmax_grad(z, lab[:n], comp, adv[:n].double(), T), dtype, "policy")
+    off = torch.tensor([0, rows // 2, rows])
+    q = gbce.preference_loss_fwd_bwd_fused(xg, labg, gpu(off), temperature=T, average=True, dev_status=flag)
+    base.close(q.logp[:n], lp, base.LOGP_TOL[dtype], 2.0 ** -148, "preference logp")
+    h = float(q.seq_score[0] - q.seq_score[1])
+    drow = torch.full((n,), -0.1 / (1 + math.exp(0.1 * h)) / (rows // 2)).double()
+    if n > rows // 2:
+        drow[rows // 2:] *= -(rows // 2) / (rows - rows // 2)
+    base.rows_close(q.dlogits[:n], ref.softmax_grad(z, lab[:n], comp, -drow, T), dtype, "preference",
+                    1e-6 * drow.abs())
+    assert int(flag) == 0
+
+
+@pytest.mark.parametrize("fill,T", [(None, 1.0), (None, 0.7), (-1e9, 1.0), (-1e30, 1.3)])
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_distill_over_masks_of_a_low_value(gbce, rows, V, dtype, fill, T):  # noqa: F811
+    """... where the teacher's list holds masked columns too, its own logits there just as low."""
+    g = gen(V + 8)
+    K = 40
+    far, gone, keep, lab, idx = masked_rows(rows, V, dtype, fill, K, g)
+    n = SPECIAL
+    idx[:n, 0] = lab[:n]
+    for r in range(n):                       # (the label stays the only one of its columns)
+        idx[r, 1:][idx[r, 1:] == lab[r]] = -1
+    t = far.float().gather(1, idx.clamp(min=0)) + 0.7 * torch.randn((rows, K), generator=g)
+    t[:, 0] = far.float().gather(1, lab.unsqueeze(1))[:, 0].clamp(min=-9.0) + 1.0
+    seen = t.clone()
+    here = torch.zeros((rows, K), dtype=torch.bool)
+    here[:n] = keep.gather(1, idx[:n].clamp(min=0))
+    here[5] = True
+    seen[:n] = t[:n].masked_fill(~here[:n], NEG)
+    t[:n] = torch.where(here[:n], t[:n], torch.full_like(t[:n], -3e38 if fill is None else fill))
+    t[5], seen[5] = 0.5, 0.5
+    per, dz, move = ref.distill(gone[:n].float(), idx[:n], seen[:n], None, T)
+    one = torch.ones(rows, device=DEV)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = (gpu(far), gpu(idx), gpu(t), None)
+    out = gbce.distill_fwd_bwd_fused(*args, one, T, None, "none", dev_status=flag)
+    f = gbce.distill_fwd(*args, T, None, "none", dev_status=flag)
+    b = gbce.distill_bwd(*args, one, f.rest_state, None, T, None, "none", dev_status=flag)
+    assert int(flag) == 0
+    for what, loss, d in (("fused", out.loss, out.dlogits), ("two calls", f.loss, b)):
+        base.close(loss[:n], per, base.LOSS_TOL, ref.kl_bound(per, move).nan_to_num(0.0, 0.0, 0.0), what)
+        base.rows_close(d[:n], dz / T, dtype, what, ref.gap_bound(move) / T)
+
+
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_a_masked_label(gbce, rows, V, dtype):  # noqa: F811
+    """A label at the type's lowest value beside others that are not: log p as low, and no NaN."""
+    g = gen(V + 9)
+    x = torch.zeros((rows, V), dtype=dtype)
+    x[:2] = (torch.randn((2, V), generator=g) * 2.0).to(dtype)
+    lab = torch.randint(0, V, (rows,), generator=g)
+    x[0, lab[0]] = torch.finfo(dtype).min
+    one = torch.ones(rows, device=DEV)
+    p = gbce.policy_loss_fwd_bwd_fused(gpu(x), gpu(lab), one, one * -2.0, None, one, reduction="none")
+    assert float(p.logp[0]) < -3e38 and float(p.loss[0]) == 0 and not bool(p.dlogits[0].any())
+    assert bool(torch.isfinite(p.loss[1:]).all()) and bool(torch.isfinite(p.dlogits).all())
