@@ -718,8 +718,13 @@ __device__ __forceinline__ void rest_add_far(RestStats &st, const uint4 &a, floa
 {
     constexpr int VEC = Elem<T>::kVec;
     const float top = FastVec<T>::vmax(a);
-    if (top == kNegInf)
+    if (top == kNegInf) {
+        // nothing, unless there are NaN, which a max passes over
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+        if (((a.x ^ none) | (a.y ^ none) | (a.z ^ none) | (a.w ^ none)) != 0)
+            st.sa.x = kQuietNan;
         return;
+    }
     st.raise_to_far(top, far);
     float f[VEC];
     Elem<T>::unpack(a, f);

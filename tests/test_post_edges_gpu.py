@@ -167,3 +167,40 @@ def test_a_masked_label(gbce, rows, V, dtype):  # noqa: F811
     p = gbce.policy_loss_fwd_bwd_fused(gpu(x), gpu(lab), one, one * -2.0, None, one, reduction="none")
     assert float(p.logp[0]) < -3e38 and float(p.loss[0]) == 0 and not bool(p.dlogits[0].any())
     assert bool(torch.isfinite(p.loss[1:]).all()) and bool(torch.isfinite(p.dlogits).all())
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3])
+@pytest.mark.parametrize("rows,V,dtype", PLACES + [(3, 2, BF16), (402, 2, F32), (6, 4097, F32), (402, 1025, F32),
+                                                   (402, 257, BF16), (7, 4105, BF16)])
+def test_one_nan_wherever_it_lies(gbce, rows, V, dtype, shift):  # noqa: F811
+    """A NaN logit makes its row NaN: at either end, and between columns that are all -inf."""
+    g = gen(V + 10 + shift)
+    x = torch.zeros((rows, V), dtype=dtype)
+    x[:6] = (torch.randn((min(rows, 6), V), generator=g) * 2.0).to(dtype)
+    at = [(0, 0), (1, V - 1)]
+    lab = torch.ones(rows, dtype=torch.int64)
+    lab[1] = 0
+    if V > 64:
+        x[3], x[4], x[5] = NEG, NEG, NEG
+        for r in (3, 4, 5):
+            x[r, 1] = 1.0
+        at += [(3, V // 2), (4, V - 1), (5, 40)]
+    for r, c in at:
+        x[r, c] = NAN
+    n = min(rows, 7)
+    bad = torch.zeros(n, dtype=torch.bool)
+    bad[[r for r, _ in at]] = True
+    one = torch.ones(rows, device=DEV)
+    xg = base.on_gpu(x, shift, shift)
+    p = gbce.policy_loss_fwd_bwd_fused(xg, gpu(lab), one, None, None, one, reduction="none")
+    q = gbce.preference_loss_fwd_bwd_fused(xg, gpu(lab), [0, rows, rows], reduction="sum")
+    idx = lab.unsqueeze(1)
+    t = torch.zeros((rows, 1))
+    d = gbce.distill_fwd_bwd_fused(xg, gpu(idx), gpu(t), None, one, 1.0, None, "none")
+    f = gbce.distill_fwd(xg, gpu(idx), gpu(t), None, 1.0, None, "none")
+    b = gbce.distill_bwd(xg, gpu(idx), gpu(t), None, one, f.rest_state, None, 1.0, None, "none")
+    for v in (p.loss, p.logp, q.logp, d.loss, f.loss):
+        assert torch.equal(torch.isnan(v[:n]).cpu(), bad), v[:n]
+    for v in (p.dlogits, d.dlogits, b):
+        assert torch.equal(torch.isnan(v[:n]).all(1).cpu(), bad) and torch.equal(torch.isnan(v[:n]).any(1).cpu(), bad)
+    assert bool(torch.isnan(q.loss)) and bool(torch.isnan(q.dlogits).all())
