@@ -392,11 +392,12 @@ struct PreferenceTerms {
     float *seq_score;       // [2 pairs] or null
     float *drow;            // [rows] or null
     float *loss_out;        // reduced loss, by the last pair's CTA (null: not reduced)
-    int32_t *done;          // pairs done so far: 0 at the start
+    int32_t *done;          // pairs done so far, and kBadOffsets: 0 at the start
     int32_t *dev_status;
 };
 
 constexpr int kPairThreads = 256;
+constexpr int32_t kBadOffsets = INT32_MIN;  // (a bit beside the count, which is at most kMaxPairs)
 
 __device__ __forceinline__ bool preference_live(const PreferenceTerms &t, int64_t r)
 {
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
     __shared__ Sum2 scratch[kWarps];
     __shared__ int64_t counts[kWarps];
     __shared__ float s_d[2];
-    __shared__ int s_last;
+    __shared__ int s_last, s_bad;
     // a dependent of the kernel that wrote the log-probs; the gradient's kernel may
     // take its place meanwhile
     launch_dependents();
@@ -479,10 +480,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
             dh = static_cast<float>(-t.beta) *
                  (z > 0.0f ? small - t.eps : (1.0f - t.eps) - small);
         }
-        if (bad) {
-            loss = dh = kQuietNan;
+        if (bad)
             report(t.dev_status, GBCE_DEV_BAD_INDEX);
-        }
         t.loss_pairs[i] = loss;
         if (t.seq_score != nullptr) {
             t.seq_score[i] = static_cast<float>(score[0]);
@@ -502,15 +501,39 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
         for (int64_t r = q.lo + first; r < q.hi; r += kHalf)
             t.drow[r] = preference_live(t, r) ? d : 0.0f;
     }
-    if (t.loss_out == nullptr)
-        return;
+    __syncthreads();
     if (tid == 0) {
-        __threadfence();  // the loss before the count
-        s_last = atomicAdd(t.done, 1) == static_cast<int32_t>(t.pairs) - 1;
+        __threadfence();  // this pair's outputs before the count
+        if (bad)
+            atomicOr(t.done, kBadOffsets);
+        const int32_t before = atomicAdd(t.done, 1);
+        s_last = (before & ~kBadOffsets) == static_cast<int32_t>(t.pairs) - 1;
+        s_bad = bad || (before & kBadOffsets) != 0;
     }
     __syncthreads();
-    if (s_last) {
-        __threadfence();
+    if (!s_last)
+        return;
+    __threadfence();
+    if (s_bad) {
+        // Every step between two offsets was looked at by the pair it belongs to.  Where
+        // one goes down or leaves the rows, sequences may share rows, and no pair's
+        // scores or rows are its own.
+        for (int64_t j = tid; j < 2 * t.pairs; j += kPairThreads) {
+            if (j < t.pairs)
+                t.loss_pairs[j] = kQuietNan;
+            if (t.seq_score != nullptr)
+                t.seq_score[j] = kQuietNan;
+        }
+        if (t.drow != nullptr) {
+            const int64_t lo = t.offsets[0], hi = t.offsets[2 * t.pairs];
+            for (int64_t r = tid; r < t.rows; r += kPairThreads)
+                t.drow[r] = r >= lo && r < hi && preference_live(t, r) ? kQuietNan : 0.0f;
+        }
+        if (t.loss_out != nullptr && tid == 0)
+            *t.loss_out = kQuietNan;
+        return;
+    }
+    if (t.loss_out != nullptr) {
         s = Sum2{};
         n = 0;
         for (int64_t j = tid; j < t.pairs; j += kPairThreads)

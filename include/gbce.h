@@ -686,10 +686,10 @@ gbce_status policy_loss_fwd_bwd_fused(const void *logits, gbce_dtype dtype, int6
  * A sequence may be empty, or all of its rows left out (score 0).  Rows before
  * the first sequence or behind the last have no part in anything (log p 0, a
  * zero gradient).  Scores are summed with 48 bits.
- * Reductions are over pairs (MEAN: / pairs).  Offsets are device memory:
- * ones that decrease or leave [0, rows] set GBCE_DEV_BAD_INDEX and make the
- * losses of the pairs they belong to NaN (an end of the whole range: of all
- * pairs); no access leaves the rows.
+ * Reductions are over pairs (MEAN: / pairs).  Offsets are device memory: where
+ * one decreases or leaves [0, rows], sequences may overlap, and the call sets
+ * GBCE_DEV_BAD_INDEX and makes every loss, every score and the gradient of every
+ * live row from the first offset to the last NaN; no access leaves the rows.
  *   beta > 0; label_smoothing in [0, 0.5); margin and label_smoothing 0 with
  *   GBCE_PREFERENCE_SQUARED.
  */

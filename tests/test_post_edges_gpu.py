@@ -204,3 +204,34 @@ def test_one_nan_wherever_it_lies(gbce, rows, V, dtype, shift):  # noqa: F811
     for v in (p.dlogits, d.dlogits, b):
         assert torch.equal(torch.isnan(v[:n]).all(1).cpu(), bad) and torch.equal(torch.isnan(v[:n]).any(1).cpu(), bad)
     assert bool(torch.isnan(q.loss)) and bool(torch.isnan(q.dlogits).all())
+
+
+BAD_OFFSETS = [[0, 2, 10, 5, 7], [0, 6, 3, 9, 12], [0, 3, 6, 9, 13], [-1, 3, 6, 9, 12], [0, 3, 1 << 40, 9, 12],
+               [0, 1, 5, 6, 10, 3, 4, 8, 12], [0, 8, 2, 3, 4, 9, 12], [2, 4, 11, 10, 11], [12, 8, 6, 4, 0], [5, 9, 1, 2, 3]]
+
+
+@pytest.mark.parametrize("off", BAD_OFFSETS)
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+def test_offsets_that_are_no_use(gbce, off, reduction):  # noqa: F811
+    """Offsets that go down anywhere, or leave the rows: no pair keeps a loss, a score or a gradient."""
+    g = gen(31)
+    rows, pairs = 12, (len(off) - 1) // 2
+    x = gpu(logits_of(rows, 90, F32, g))
+    lab = torch.randint(0, 90, (rows,), generator=g)
+    lab[4] = IGNORE
+    mask = (lab != IGNORE).to(torch.uint8)
+    inside = (torch.arange(rows) >= max(off[0], 0)) & (torch.arange(rows) < min(off[-1], rows)) & (lab != IGNORE)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    opt = dict(reduction=reduction, dev_status=flag)
+    out = gbce.preference_loss_fwd_bwd_fused(x, gpu(lab), off, **opt,
+                                             grad_out=torch.ones(pairs if reduction == "none" else 1))
+    assert int(flag) == 2
+    flag.zero_()
+    two = gbce.preference_loss(torch.full((rows,), -1.0, device=DEV), off, None,
+                               torch.ones(pairs if reduction == "none" else 1), gpu(mask), **opt)
+    assert int(flag) == 2
+    for r in (out, two):
+        assert bool(torch.isnan(r.loss).all()) and bool(torch.isnan(r.seq_score).all())
+    for d in (out.dlogits, two.dlogp.view(rows, 1)):
+        assert torch.equal(torch.isnan(d).any(1).cpu(), inside) and torch.equal(torch.isnan(d).all(1).cpu(), inside)
+        assert not bool(d[gpu(~inside)].any())
