@@ -576,8 +576,10 @@ struct TokenTerms {
 
 __device__ __forceinline__ TokenTerms token_terms(float m, float s, float xy, TwoFloat inv_t)
 {
-    if (!(s > 0.0f)) {
-        const float v = (s == 0.0f && xy == xy) ? 0.0f : kQuietNan;
+    // nothing beside the label: certain, if the label itself is anything; a label of
+    // +inf, or a row that is -inf throughout, has no softmax
+    if (!(s > 0.0f) || xy == __builtin_huge_valf()) {
+        const float v = s == 0.0f && isfinite(xy) ? 0.0f : kQuietNan;
         return {v, v};
     }
     // s = 2^k f, f in [1, 2): log s = k log 2 + log f, k log 2 exact in its first part
@@ -649,7 +651,7 @@ __device__ __forceinline__ GradConsts rest_consts(float m, float s, float c, flo
     k.c = sizeof(T) == 2 && !none ? fminf(c, 0x1p30f / fabsf(m)) : c;
     k.kb = none ? 0.0f : -log2f(s);
     k.kbx = none ? 0.0f : fmaf(-m, k.c, k.kb);
-    k.gs = none && !(s != s) && m != __builtin_huge_valf() ? 0.0f : gs;
+    k.gs = none && s == s && gs == gs && m != __builtin_huge_valf() ? 0.0f : gs;
     if (sizeof(T) == 2 && !none) {
         const float kept = fmaf(m, k.c, k.kbx);  // kb as kbx has it
         k.gs *= ex2(k.kb - kept);

@@ -235,3 +235,38 @@ def test_offsets_that_are_no_use(gbce, off, reduction):  # noqa: F811
     for d in (out.dlogits, two.dlogp.view(rows, 1)):
         assert torch.equal(torch.isnan(d).any(1).cpu(), inside) and torch.equal(torch.isnan(d).all(1).cpu(), inside)
         assert not bool(d[gpu(~inside)].any())
+
+
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_rows_that_have_no_softmax(gbce, rows, V, dtype):  # noqa: F811
+    """A label of +inf, another column of +inf, a row of -inf throughout: NaN, in every loss.  A label
+    that alone is not -inf is certain."""
+    g = gen(V + 11)
+    x = torch.zeros((rows, V), dtype=dtype)
+    x[:6] = (torch.randn((6, V), generator=g) * 2.0).to(dtype)
+    lab = torch.randint(0, V, (rows,), generator=g)
+    x[0, lab[0]] = INF
+    x[1, (lab[1] + 1) % V] = INF
+    x[2] = NEG
+    x[3] = NEG
+    x[3, lab[3]] = 1.0
+    bad = torch.tensor([True, True, True, False, False, False])
+    one = torch.ones(rows, device=DEV)
+    xg, idx, t = gpu(x), gpu(lab.unsqueeze(1)), torch.zeros((rows, 1), device=DEV)
+    p = gbce.policy_loss_fwd_bwd_fused(xg, gpu(lab), one, None, None, one, reduction="none")
+    off = [0, 1, 2, 3, 4, 5, 6, 6, rows]       # six sequences of a row, an empty one, the rest
+    q = gbce.preference_loss_fwd_bwd_fused(xg, gpu(lab), off, reduction="none")
+    d = gbce.distill_fwd_bwd_fused(xg, idx, t, None, one, 1.0, None, "none")
+    f = gbce.distill_fwd(xg, idx, t, None, 1.0, None, "none")
+    b = gbce.distill_bwd(xg, idx, t, None, one, f.rest_state, None, 1.0, None, "none")
+    for v in (p.loss, p.logp, q.logp, q.seq_score, d.loss, f.loss):
+        assert torch.equal(torch.isnan(v[:6]).cpu(), bad), v[:6]
+    for v in (p.dlogits, d.dlogits, b):
+        assert torch.equal(torch.isnan(v[:6]).all(1).cpu(), bad) and torch.equal(torch.isnan(v[:6]).any(1).cpu(), bad)
+    for v in (p.logp, p.loss + 1.0, q.logp, d.loss, f.loss):
+        assert float(v[3]) == 0.0
+    for v in (p.dlogits, d.dlogits, b):
+        assert not bool(v[3].any())
+    # pair i holds sequences i and 4 + i
+    assert torch.isnan(q.loss).tolist() == [True, True, True, False]
+    assert torch.isnan(q.dlogits[:6]).all(1).tolist() == [True] * 3 + [False] + [True] * 2
