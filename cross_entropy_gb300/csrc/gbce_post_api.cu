@@ -472,10 +472,11 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pre
             loss = e * e;
             dh = 2.0f * e;
         } else {
-            // -(1 - eps) log sig(z) - eps log sig(-z) = softplus(-z) + eps z
+            // -(1 - eps) log sig(z) - eps log sig(-z) = log(1 + e^-|z|) + eps z for z > 0,
+            // + (1 - eps)(-z) for z < 0 (one product: z may be infinite)
             const float z = static_cast<float>(t.beta * (h - t.margin));
             const float e = expf(-fabsf(z)), small = e / (1.0f + e);  // sig(-|z|)
-            loss = (z > 0.0f ? 0.0f : -z) + log1pf(e) + (t.eps != 0.0f ? t.eps * z : 0.0f);
+            loss = log1pf(e) + (z <= 0.0f ? -(1.0f - t.eps) * z : t.eps != 0.0f ? t.eps * z : 0.0f);
             // sig(-z) - eps, which for z < 0 is 1 - eps - sig(z)
             dh = static_cast<float>(-t.beta) *
                  (z > 0.0f ? small - t.eps : (1.0f - t.eps) - small);

@@ -270,3 +270,17 @@ def test_rows_that_have_no_softmax(gbce, rows, V, dtype):  # noqa: F811
     # pair i holds sequences i and 4 + i
     assert torch.isnan(q.loss).tolist() == [True, True, True, False]
     assert torch.isnan(q.dlogits[:6]).all(1).tolist() == [True] * 3 + [False] + [True] * 2
+
+
+@pytest.mark.parametrize("eps", [0.0, 0.1])
+def test_smoothing_beside_an_infinite_score(gbce, eps):  # noqa: F811
+    """An answer that the policy cannot give has log p -inf: the loss of its pair is +inf where it was
+    chosen, and eps times that where it was rejected; the slope stays (1 - eps) beta and eps beta."""
+    lp = torch.tensor([-1.0, NEG, -2.0, -1.0, -1.0, -3.0, NEG, -0.5])
+    off = [0, 2, 4, 6, 8]                      # pair 0: chosen -inf; pair 1: rejected -inf
+    r = gbce.preference_loss(gpu(lp), off, label_smoothing=eps, reduction="none", grad_out=torch.ones(2), beta=0.5)
+    assert r.loss.tolist() == [INF, INF if eps else 0.0]
+    want = torch.tensor([-(1 - eps), eps, 1 - eps, -eps]).repeat_interleave(2).double() * 0.5
+    base.close(r.dlogp, want, 2 * ref.EPS32, 0.0, "dlogp")
+    nan = gbce.preference_loss(torch.full((4,), NEG, device=DEV), [0, 2, 4], label_smoothing=eps)
+    assert math.isnan(float(nan.loss))
