@@ -351,6 +351,26 @@ __device__ bool list_columns(const PostParams &p, int64_t r, const Slice &sl, co
     return bad;
 }
 
+// A teacher's logit / T.  One that is finite stays so (a mask of the lowest value,
+// T < 1): entries that are all as low still share their mass.
+__device__ __forceinline__ float teacher_logit(float raw, TwoFloat inv_t)
+{
+    return raw == kNegInf ? kNegInf : fmaxf(scaled(raw, inv_t), -3.402823466e38f);
+}
+
+// ... relative to the list's largest, and the rest's then: a list that names a column
+// twice adds log 2 to some of its logits, which one of 1e38 would swallow.
+__device__ __forceinline__ float teacher_logit(float raw, float top, TwoFloat inv_t)
+{
+    return raw == kNegInf ? kNegInf : scaled(raw - top, inv_t);
+}
+__device__ __forceinline__ float rest_logit(float rest, float top, TwoFloat inv_t)
+{
+    return rest == kNegInf || top == kNegInf
+               ? rest
+               : fminf(rest - teacher_logit(top, inv_t), 3.402823466e38f);
+}
+
 // Bring a row's entries into L2.
 __device__ __forceinline__ void prefetch_entries(const PostParams &p, int64_t r, int lane)
 {
@@ -378,7 +398,7 @@ __device__ void list_teacher(const PostParams &p, int64_t r, const T *row, const
     const TwoFloat c = {p.c_hi, p.c_lo}, inv_t = {p.it_hi, p.it_lo};
     const float inf = __builtin_huge_valf();
     const float *teacher = p.teacher + r * K;
-    const float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
+    float rest = p.teacher_rest != nullptr ? p.teacher_rest[r] : kNegInf;
     bool nan_t = !(rest < inf);
     for (int k0 = lane; k0 < K; k0 += 32 * kBatch) {
         float raw[kBatch], x[kBatch];
@@ -397,22 +417,29 @@ __device__ void list_teacher(const PostParams &p, int64_t r, const T *row, const
             nan_t |= in[b] && !(raw[b] < inf);
             if (k < K) {
                 L.x[k] = x[b];
-                L.lp[k] = raw[b] != kNegInf ? scaled(raw[b], inv_t) : kNegInf;
+                L.lp[k] = teacher_logit(raw[b], inv_t);
             }
         }
     }
     if (__any_sync(0xffffffffu, repeated != 0)) {
         // the first of several takes their sum, in entry order
+        float top = kNegInf;
+        for (int k = 0; k < K; ++k)
+            if (L.col[k] != -1) {
+                nan_t |= !(teacher[k] < inf);
+                top = fmaxf(top, teacher[k]);
+            }
+        rest = rest_logit(rest, top, inv_t);
         for (int k = lane, i = 0; k < K; k += 32, ++i) {
+            const int32_t col = L.col[k];
+            if (col < 0)
+                continue;
+            L.lp[k] = teacher_logit(teacher[k], top, inv_t);
             if (!(repeated >> i & 1u))
                 continue;
-            const int32_t col = L.col[k];
             const auto tau = [&](int j) {
-                if (L.col[j] != col && L.col[j] != -2 - col)
-                    return kNegInf;
-                const float raw = teacher[j];
-                nan_t |= !(raw < inf);
-                return raw == kNegInf ? kNegInf : scaled(raw, inv_t);
+                return L.col[j] == col || L.col[j] == -2 - col ? teacher_logit(teacher[j], top, inv_t)
+                                                               : kNegInf;
             };
             float m = kNegInf, s = 0.0f;
             for (int j = k; j < K; ++j)

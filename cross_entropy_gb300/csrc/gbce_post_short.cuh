@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
 
     // the listed logits, and -inf in their place
     const float inf = __builtin_huge_valf();
-    bool nan_t = false, nan_x = false;
+    bool nan_t = kList && !(rest < inf), nan_x = false;
     LedSum teacher = {kNegInf, 0.0f}, student = {kNegInf, 0.0f};
     const auto exp_t = [](float d) { return expf(d); };
     const auto exp_c = [&](float d) { return ex2(scaled(d, c)); };
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             if (col[b] >= 0)
                 buf[phase + col[b]] = neg_inf_as(T());
             nan_t |= col[b] >= 0 && !(tau[b] < inf);
-            tau[b] = col[b] >= 0 && tau[b] != kNegInf ? scaled(tau[b], inv_t) : kNegInf;
+            tau[b] = col[b] >= 0 ? (twice ? tau[b] : teacher_logit(tau[b], inv_t)) : kNegInf;
         }
         if (twice) {
             // the first of several takes their sum, in entry order; the others go
@@ -342,6 +342,18 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
             for (int b = 0; b < KE; ++b)
                 if (tid + b * NT < K) {
                     list_col[tid + b * NT] = col[b];
+                    list_tau[tid + b * NT] = tau[b];
+                }
+            G::sync();
+            float highest = kNegInf;
+            for (int j = 0; j < K; ++j)
+                highest = fmaxf(highest, list_tau[j]);
+            rest = rest_logit(rest, highest, inv_t);
+            G::sync();
+#pragma unroll
+            for (int b = 0; b < KE; ++b)
+                if (tid + b * NT < K) {
+                    tau[b] = teacher_logit(tau[b], highest, inv_t);
                     list_tau[tid + b * NT] = tau[b];
                 }
             G::sync();
@@ -380,10 +392,8 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
                 teacher.merge(tau[b], 0.0f, exp_t);
                 student.merge(x[b], 0.0f, exp_c);
             }
-        if (tid == 0) {
-            nan_t |= !(rest < inf);
+        if (tid == 0)
             teacher.merge(rest, 0.0f, exp_t);
-        }
     } else {
         xy = as_float(buf[phase + y]);
         G::sync();

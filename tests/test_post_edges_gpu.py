@@ -284,3 +284,37 @@ def test_smoothing_beside_an_infinite_score(gbce, eps):  # noqa: F811
     base.close(r.dlogp, want, 2 * ref.EPS32, 0.0, "dlogp")
     nan = gbce.preference_loss(torch.full((4,), NEG, device=DEV), [0, 2, 4], label_smoothing=eps)
     assert math.isnan(float(nan.loss))
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_teachers_of_the_lowest_value(gbce, rows, V, dtype, T):  # noqa: F811
+    """A list whose logits are all at the lowest value shares its mass evenly (no rest), or leaves it to
+    the rest; one among them that is not takes it."""
+    g = gen(V + 12)
+    x = torch.zeros((rows, V), dtype=dtype)
+    x[:4] = (torch.randn((4, V), generator=g) * 2.0).to(dtype)
+    idx = torch.stack([torch.randperm(V, generator=g)[:20] for _ in range(rows)])
+    t = torch.zeros((rows, 20))
+    t[:4] = torch.finfo(F32).min
+    t[1, 3] = 1.0
+    t[3, :10], idx[3, 12] = NEG, idx[3, 15]     # (a column listed twice)
+    seen = t[:4].clone()
+    seen[0], seen[3, 10:], seen[1][seen[1] < 0] = 0.0, 0.0, NEG
+    rest = torch.zeros(rows)
+    for r in (None, rest):
+        low = seen.clone()
+        if r is not None:
+            low[[0, 2, 3]] = NEG
+            r[1] = 0.5
+        else:
+            low[2] = 0.0
+        per, dz, move = ref.distill(x[:4].float(), idx[:4], low, None if r is None else r[:4], T)
+        one = torch.ones(rows, device=DEV)
+        args = (gpu(x), gpu(idx), gpu(t), gpu(r))
+        out = gbce.distill_fwd_bwd_fused(*args, one, T, None, "none")
+        f = gbce.distill_fwd(*args, T, None, "none")
+        b = gbce.distill_bwd(*args, one, f.rest_state, None, T, None, "none")
+        for loss, d in ((out.loss, out.dlogits), (f.loss, b)):
+            base.close(loss[:4], per, base.LOSS_TOL, ref.kl_bound(per, move))
+            base.rows_close(d[:4], dz / T, dtype, floor=ref.gap_bound(move) / T)
