@@ -132,7 +132,7 @@ def _per_row(x, lead, what, device):
             t = t.broadcast_to(lead)
         except RuntimeError as exc:
             raise ValueError(f"{what} must have one value per row {tuple(lead)}, or broadcast to "
-                             f"that, got {tuple(x.shape)}") from exc
+                             f"that, got {tuple(t.shape)}") from exc
     return _flat(t, rows)
 
 
