@@ -85,7 +85,8 @@ struct Sum2 {
 
 // The SFU's 2^x is low on the average: by 5.0e-8 of its value for x <= -1, by 2.1e-8
 // between -1 and 0, not at all at 0 (measured over 2^20 arguments per unit).  A sum
-// over a row would carry that in one direction in every row.
+// over a row would carry that in one direction in every row.  (A mean of one chip's
+// units: no bound of the tests rests on it, or on kSumLow.)
 constexpr float kEx2Low = 5e-8f;
 
 // 2^x for the factors that whole sums are multiplied by, without it: one more
@@ -589,8 +590,8 @@ __device__ __forceinline__ float student_logp(const StudentRow &q, float x, TwoF
 
 // What is left in a sum of what its terms' 2^x lacks: the factors, levelled two or
 // three times, overshoot by 8e-9 each.  With it log p of 1000 to 4000 rows of 100 to
-// 152064 logits, T 0.7 to 2, lies -3e-8 to 5e-8 of 1 - p from fp64's on the average, a
-// quarter of its scatter.
+// 152064 logits, T 0.7 to 2, lies -4e-8 to 5e-8 of 1 - p from fp64's on the average, half
+// of its scatter (0.8e-7 to 1.8e-7) or less.
 constexpr float kSumLow = 3.5e-8f;
 
 // log p of one column from the rest's (m, s): -log(1 + e^a), a = log s + (m - xy) / T,

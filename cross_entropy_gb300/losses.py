@@ -202,8 +202,9 @@ def distill_fwd(logits: torch.Tensor, index, teacher_logits: torch.Tensor,
     ``index`` [..., k] holds the teacher's columns of each row (-1: no entry) and
     ``teacher_logits`` [..., k] its logits there; the same temperature softens both
     sides.  ``teacher_rest`` [...] is log-sum-exp of the teacher's other logits /
-    T (a teacher given as log-probs lp: log1p(-sum exp(lp))); without it the
-    listed entries are renormalised.
+    T; without it the listed entries are renormalised.  Of a teacher given as
+    log-probs lp it is log1p(-sum exp(lp)) at T = 1 only: at another T the listed
+    log-probs do not determine it, and it has to come from the teacher's logits.
     """
     lib = load_library()
     x, code, xs = _logits(logits)

@@ -547,7 +547,10 @@ gbce_status embedding_lookup_bwd(const void *grad_out, int64_t grad_row_stride, 
  * The losses of post-training, from the same [rows, vocab] logits: z = x / T,
  * q = softmax(z) over the row's vocab columns.  A row that is left out
  * (row_mask[r] == 0, or label == ignore_index) has loss 0 and a zero gradient
- * row whatever it holds; its logits are not read.  Sums over rows are taken
+ * row whatever it holds; its logits are not read.  Columns masked with -inf or
+ * with the type's lowest value have no mass beside others (a row that is at the
+ * lowest value throughout is uniform; one that is -inf throughout, or has a NaN
+ * or a +inf, has no softmax: NaN).  Sums over rows are taken
  * with 48 bits in a fixed order; row losses and gradients are fp32 throughout,
  * dlogits rounded once.  workspace: gbce_workspace_size(rows, vocab, 1) bytes
  * unless stated, 16-byte aligned, of one call at a time (a captured graph
@@ -647,7 +650,7 @@ typedef struct gbce_policy_options {
  * vocab_slice_combine with k = 1): loss, and dlogp_out[r] = the derivative by
  * logp[r] times the upstream gradient, which those calls' backward takes as
  * grad_logp.  All of logp, advantages, old_logp, ref_logp and dlogp_out are
- * [rows] fp32; rows with row_mask[r] == 0 are not read and give 0.  dlogp_out
+ * [rows] fp32; rows with row_mask[r] == 0 give 0 whatever they hold.  dlogp_out
  * may be NULL (then grad_out too).  workspace: gbce_workspace_size(rows, 1, 1).
  */
 gbce_status policy_loss(const float *logp, int64_t rows, const uint8_t *row_mask,
