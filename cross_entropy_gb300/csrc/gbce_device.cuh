@@ -464,6 +464,19 @@ template <> struct Elem<__nv_bfloat16> {
 //   m = max x_j,   s = sum_j 2^{(x_j - m) c},   c = log2(e) / T,
 // so that s = sum_j exp((x_j - m) / T).  Excluded columns are fed as -inf.
 // The sum is kept in two packed pairs (four independent accumulators).
+//
+// A logit with x c below -2^31 (a mask of the type's lowest value, whose x c is not
+// even finite) is past what a shift can be taken off: beside any other it has no mass,
+// and it gets none.  The shift stops at 2^31, under which its exponent is below -2^7;
+// a row in which nothing else turns up has a max but a sum of 0 (finalize_logp).
+constexpr float kFarShift = 0x1p31f;
+
+// What a gathered logit adds beside its own max.
+__device__ __forceinline__ float near_one(float x, float c)
+{
+    return x * c < -kFarShift ? 0.0f : 1.0f;
+}
+
 template <bool ENT, bool SUMX = false>
 struct OnlineStats {
     static constexpr bool kSumx = SUMX;
@@ -495,7 +508,7 @@ struct OnlineStats {
             // multiplies them by 2^(nmc' - nmc), a difference of the two
             // rounded shifts (exact when they are within a factor of two), so
             // all terms keep sharing one rounding of the shift (finish)
-            const float nmc_new = -vmax * c;
+            const float nmc_new = fminf(-vmax * c, kFarShift);
             const float d = nmc_new - nmc;
             const float f = ex2(d);
             const float2 ff = make_float2(f, f);
@@ -601,10 +614,12 @@ struct OnlineStats {
     // half an ulp of m c): the sums are 2^r times their values relative to
     // m.  warp_merge_state takes r out as it moves each lane to the warp's
     // max.  Left in, a row whose logits are large (|m| / T in the hundreds)
-    // would carry ~2^-24 |m c| of error in every probability.
+    // would carry ~2^-24 |m c| of error in every probability.  (|r| <= 2^7; none
+    // where the shift stopped short of the max or nothing was met)
     __device__ __forceinline__ float residual(float c) const
     {
-        return (m == kNegInf || !(m == m)) ? 0.0f : fmaf(m, c, nmc);
+        const float r = fmaf(m, c, nmc);
+        return r > -0x1p8f ? r : 0.0f;
     }
     // ENT: the thread's sum of 2^z z.
     __device__ __forceinline__ float hsum() const
@@ -654,7 +669,7 @@ __device__ __forceinline__ void merge_max_sum_h(float &m, float &s, float &h, fl
             hv = 0.0f;
             return;
         }
-        const float d = __fmul_rn(__fsub_rn(mi, M), c);
+        const float d = fmaxf(__fmul_rn(__fsub_rn(mi, M), c), -0x1p100f);  // (finite: si may be 0)
         const float f = ex2(d);
         sv = __fmul_rn(si, f);
         hv = __fmul_rn(__fadd_rn(hi, __fmul_rn(d, si)), f);
@@ -710,7 +725,9 @@ __device__ __forceinline__ void warp_merge_state(float &m, float &s, float &h, f
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
     float sv = 0.0f, hv = HK == kHSum ? h : 0.0f;
     if (M != kNegInf && m != kNegInf) {
-        const float d = __fsub_rn(__fmul_rn(__fsub_rn(m, M), c), r);
+        float d = __fsub_rn(__fmul_rn(__fsub_rn(m, M), c), r);
+        if (HK == kHMoment)
+            d = fmaxf(d, -0x1p100f);  // (finite: s may be 0)
         const float f = ex2(d);
         sv = __fmul_rn(s, f);
         if (HK == kHMoment)
@@ -727,11 +744,18 @@ __device__ __forceinline__ void warp_merge_state(float &m, float &s, float &h, f
 // (m - x_t) / T is one IEEE division of an exact (bf16) or once-rounded
 // (fp32) difference, taken from the same values the sweep read, so log p
 // is never positive.  s == 0 (no other column, V == 1) gives log p = 0, unless
-// x_t is NaN: in a row of NaN logits the merges find no max and leave s at 0.
+// x_t is NaN: in a row of NaN logits the merges find no max and leave s at 0.  Others
+// that have a max without a sum are masks far below (OnlineStats): log p is 0 for a
+// target above them, and there is none in a row of nothing but masks.
+__device__ __forceinline__ bool alone(float m, float s, float xt)
+{
+    return s == 0.0f && (m == kNegInf ? xt == xt : xt > m);
+}
+
 __device__ __forceinline__ float finalize_logp(float m, float s, float xt, float T)
 {
     if (!(s > 0.0f))
-        return (s == 0.0f && xt == xt) ? 0.0f : __int_as_float(0x7fc00000);
+        return alone(m, s, xt) ? 0.0f : __int_as_float(0x7fc00000);
     const float a = logf(s) + (m - xt) / T;
     return -softplus(a);
 }
@@ -752,7 +776,7 @@ __device__ __forceinline__ float finalize_logp(float m, float s, float xt, float
 __device__ __forceinline__ float finalize_entropy(float m, float s, float h, float xt, float T)
 {
     if (!(s > 0.0f))
-        return (s == 0.0f && xt == xt) ? 0.0f : __int_as_float(0x7fc00000);
+        return alone(m, s, xt) ? 0.0f : __int_as_float(0x7fc00000);
     const float ls = logf(s);
     const float a = ls + (m - xt) / T;
     const float mean_u = (h / s) * 0.69314718055994531f;  // <= 0

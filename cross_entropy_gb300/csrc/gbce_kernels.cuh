@@ -1113,7 +1113,7 @@ __device__ __forceinline__ float logp_with_targets(float mS, float sS, const int
         for (int i = 0; i < j; ++i)
             dup |= (tg[i] == tj);
         if (!dup)
-            merge_max_sum(m, s, xt[j], 1.0f, c);
+            merge_max_sum(m, s, xt[j], near_one(xt[j], c), c);
     }
     return finalize_logp(m, s, xt[k], T);
 }
@@ -1147,7 +1147,7 @@ __device__ __forceinline__ float entropy_with_targets(float mS, float sS, float 
         for (int i = 1; i < j; ++i)
             dup |= (tg[i] == tj);
         if (!dup)
-            merge_max_sum_h(m, s, h, xt[j], 1.0f, 0.0f, c);
+            merge_max_sum_h(m, s, h, xt[j], near_one(xt[j], c), 0.0f, c);
     }
     rescan = m > xt[0] && s < 1.03125f && isfinite(m);
     return finalize_entropy(m, s, h, xt[0], T);
