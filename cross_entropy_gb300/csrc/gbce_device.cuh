@@ -386,6 +386,28 @@ __device__ __forceinline__ float fmax3(float a, float b, float c)
     return d;
 }
 
+// The same maxima where a NaN operand yields NaN.
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Max of v over the warp's active lanes, in one warp-wide reduction; a NaN
 // lane is ignored unless every lane is NaN.
 __device__ __forceinline__ float warp_max_active(float v)
@@ -469,13 +491,9 @@ template <> struct Elem<__nv_bfloat16> {
 // even finite) is past what a shift can be taken off: beside any other it has no mass,
 // and it gets none.  The shift stops at 2^31, under which its exponent is below -2^7;
 // a row in which nothing else turns up has a max but a sum of 0 (finalize_logp).
-constexpr float kFarShift = 0x1p31f;
-
-// What a gathered logit adds beside its own max.
-__device__ __forceinline__ float near_one(float x, float c)
-{
-    return x * c < -kFarShift ? 0.0f : 1.0f;
-}
+// Beside moments the max stops at -2^100, so that what a merge multiplies a sum of 0
+// with is finite.
+constexpr float kFarShift = 0x1p31f, kFarMax = -0x1p100f;
 
 template <bool ENT, bool SUMX = false>
 struct OnlineStats {
@@ -520,7 +538,7 @@ struct OnlineStats {
             }
             sa = fmul2(sa, ff);
             sb = fmul2(sb, ff);
-            m = vmax;
+            m = ENT ? fmaxf(vmax, kFarMax) : vmax;
             nmc = nmc_new;
         }
         return vmax != kNegInf;
@@ -568,7 +586,8 @@ struct OnlineStats {
         }
     }
 
-    // Fold N unpacked values (masked columns already -inf).
+    // Fold N unpacked values (masked columns already -inf) whose max is vmax (NaN where
+    // one of them is and nothing above -inf).
     template <int N>
     __device__ __forceinline__ void add(const float (&f)[N], float vmax, float c)
     {
@@ -669,7 +688,7 @@ __device__ __forceinline__ void merge_max_sum_h(float &m, float &s, float &h, fl
             hv = 0.0f;
             return;
         }
-        const float d = fmaxf(__fmul_rn(__fsub_rn(mi, M), c), -0x1p100f);  // (finite: si may be 0)
+        const float d = __fmul_rn(__fsub_rn(mi, M), c);
         const float f = ex2(d);
         sv = __fmul_rn(si, f);
         hv = __fmul_rn(__fadd_rn(hi, __fmul_rn(d, si)), f);
@@ -725,9 +744,7 @@ __device__ __forceinline__ void warp_merge_state(float &m, float &s, float &h, f
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(m));
     float sv = 0.0f, hv = HK == kHSum ? h : 0.0f;
     if (M != kNegInf && m != kNegInf) {
-        float d = __fsub_rn(__fmul_rn(__fsub_rn(m, M), c), r);
-        if (HK == kHMoment)
-            d = fmaxf(d, -0x1p100f);  // (finite: s may be 0)
+        const float d = __fsub_rn(__fmul_rn(__fsub_rn(m, M), c), r);
         const float f = ex2(d);
         sv = __fmul_rn(s, f);
         if (HK == kHMoment)

@@ -139,7 +139,7 @@ __device__ __forceinline__ void stats_vector(S &st, const uint4 &raw, int32_t co
     float vmax = f[0];
 #pragma unroll
     for (int e = 1; e < VEC; ++e)
-        vmax = fmaxf(vmax, f[e]);
+        vmax = fmax_nan(vmax, f[e]);
     st.add<VEC>(f, vmax, c);
 }
 
@@ -165,6 +165,23 @@ template <> struct FastVec<__nv_bfloat16> {
     {
         return unpack_max(bf16x2_max(pmax(a), pmax(b)));
     }
+    // ... NaN where there is one
+    __device__ static __forceinline__ uint32_t pmax_nan(const uint4 &a)
+    {
+        return bf16x2_max_nan(bf16x2_max_nan(a.x, a.y), bf16x2_max_nan(a.z, a.w));
+    }
+    __device__ static __forceinline__ float unpack_max_nan(uint32_t m)
+    {
+        return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    __device__ static __forceinline__ float vmax_nan(const uint4 &a)
+    {
+        return unpack_max_nan(pmax_nan(a));
+    }
+    __device__ static __forceinline__ float vmax_nan(const uint4 &a, const uint4 &b)
+    {
+        return unpack_max_nan(bf16x2_max_nan(pmax_nan(a), pmax_nan(b)));
+    }
     template <typename S>
     __device__ static __forceinline__ void add(S &st, const uint4 &a, float c)
     {
@@ -189,6 +206,19 @@ template <> struct FastVec<float> {
         return fmax3(fmax3(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z)),
                      fmax3(__uint_as_float(a.w), __uint_as_float(b.x), __uint_as_float(b.y)),
                      fmaxf(__uint_as_float(b.z), __uint_as_float(b.w)));
+    }
+    // ... NaN where there is one
+    __device__ static __forceinline__ float vmax_nan(const uint4 &a)
+    {
+        return fmax_nan(fmax3_nan(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z)),
+                        __uint_as_float(a.w));
+    }
+    __device__ static __forceinline__ float vmax_nan(const uint4 &a, const uint4 &b)
+    {
+        return fmax3_nan(
+            fmax3_nan(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z)),
+            fmax3_nan(__uint_as_float(a.w), __uint_as_float(b.x), __uint_as_float(b.y)),
+            fmax_nan(__uint_as_float(b.z), __uint_as_float(b.w)));
     }
     template <typename S>
     __device__ static __forceinline__ void add(S &st, const uint4 &a, float c)
@@ -406,7 +436,7 @@ __device__ __forceinline__ void stats_capped_target(S &st, const uint4 &raw, int
         st.sumx_add(f[e]);
         if (is_target<KMAX>(tg, col0 + e))
             f[e] = kNegInf;
-        vm = fmaxf(vm, f[e]);
+        vm = fmax_nan(vm, f[e]);
     }
     st.template add<VEC>(f, vm, c);
 }
@@ -472,7 +502,7 @@ __device__ __forceinline__ void stats_one(S &st, const uint4 &a, int32_t va, int
         nt = next_target_vector<KMAX>(tv, v0, v1, tid, nc, va);
         return;
     }
-    if (st.raise_to(FastVec<T>::vmax(a), c))
+    if (st.raise_to(FastVec<T>::vmax_nan(a), c))  // (a NaN: to be added, with no new max)
         FastVec<T>::add(st, a, c);
     else
         st.sumx_add(kNegInf);  // the whole vector is -inf
@@ -494,7 +524,7 @@ __device__ __forceinline__ void stats_two(S &st, const uint4 &a, const uint4 &b,
 {
     constexpr int VEC = Elem<T>::kVec;
     const bool hit = check && static_cast<uint32_t>(nt - va) <= static_cast<uint32_t>(vb - va);
-    const float own = hit ? kNegInf : FastVec<T>::vmax(a, b);
+    const float own = hit ? kNegInf : FastVec<T>::vmax_nan(a, b);
     const float wmax = WARP_MAX ? warp_max_active(own) : own;
     if (hit) {
         stats_vector<T, KMAX>(st, a, col0 + va * VEC, tg, c);
@@ -1095,6 +1125,19 @@ __device__ __forceinline__ void grad_capped_chunk(const uint4 *chunk, T *dbase, 
     }
 }
 
+// Gathered logit x into (m, s[, h]).  One far below (OnlineStats) adds nothing; a NaN
+// stays one where nothing else has been met.
+template <int HK>
+__device__ __forceinline__ void merge_target(float &m, float &s, float &h, float x, float c)
+{
+    const bool far = x > kNegInf && x * c < -kFarShift;
+    merge_state<HK>(m, s, h, far ? fmaxf(x, kFarMax) : x, far ? 0.0f : 1.0f, 0.0f, c);
+    if (x != x) {
+        m = fmaxf(m, 0.0f);
+        s = x;
+    }
+}
+
 // log p of target k, whose "others" are every column outside the target set
 // S (already folded into (mS, sS)) plus the distinct members of S other
 // than target k itself.
@@ -1103,7 +1146,7 @@ __device__ __forceinline__ float logp_with_targets(float mS, float sS, const int
                                                    const float *xt, int K, int k, float c,
                                                    float T)
 {
-    float m = mS, s = sS;
+    float m = mS, s = sS, unused = 0.0f;
     const int32_t tk = tg[k];
     for (int j = 0; j < K; ++j) {
         const int32_t tj = tg[j];
@@ -1113,7 +1156,7 @@ __device__ __forceinline__ float logp_with_targets(float mS, float sS, const int
         for (int i = 0; i < j; ++i)
             dup |= (tg[i] == tj);
         if (!dup)
-            merge_max_sum(m, s, xt[j], near_one(xt[j], c), c);
+            merge_target<kHNone>(m, s, unused, xt[j], c);
     }
     return finalize_logp(m, s, xt[k], T);
 }
@@ -1147,7 +1190,7 @@ __device__ __forceinline__ float entropy_with_targets(float mS, float sS, float 
         for (int i = 1; i < j; ++i)
             dup |= (tg[i] == tj);
         if (!dup)
-            merge_max_sum_h(m, s, h, xt[j], near_one(xt[j], c), 0.0f, c);
+            merge_target<kHMoment>(m, s, h, xt[j], c);
     }
     rescan = m > xt[0] && s < 1.03125f && isfinite(m);
     return finalize_entropy(m, s, h, xt[0], T);
@@ -1622,6 +1665,8 @@ __global__ void __launch_bounds__(kRowThreads, (MODE != kModeFused && KMAX <= 4)
         if (kEnt && alive && isnan(h) && !isnan(s))
             h = rescan_entropy_moment<T, KMAX>(row, g, V, v0, v1, split == 0,
                                                split == p.splits - 1, tg, c, st.nmc, tid, NC);
+        if (isnan(s))  // (of a thread that met -inf besides, or nothing: its NaN must count)
+            m = fmaxf(m, 0.0f);
         warp_merge_state<kH>(m, s, h, c, st.residual(c));
         if (lane == 0) {
             red_m[warp] = m;

@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(PersistShape<CAP>::kThreads, PersistShape<CAP>
         // warps' states itself (no second barrier to broadcast log p)
         const int rb = static_cast<int>(live_rows++ & 1u);
         float m = st.m, s = st.sum(), sx = SMOOTH ? st.xsum() : 0.0f;
+        if (isnan(s))  // (of a thread that met -inf besides, or nothing: its NaN must count)
+            m = fmaxf(m, 0.0f);
         warp_merge_state<SMOOTH ? kHSum : kHNone>(m, s, sx, c, st.residual(c));
         if (CAP)
             in_range = __all_sync(0xffffffffu, in_range);

@@ -150,3 +150,45 @@ def test_slices_that_are_masked_out(dtype):
     d = torch.cat([gbce.vocab_slice_grad(y[:, a:b], idx, a, V, one, logp, xt, row_state=state)
                    for a, b in zip(cuts, cuts[1:])], 1)
     norms_close(d, -torch.softmax(z, 1).scatter(1, idx, torch.expm1(want)), dtype, "slices")
+
+
+@pytest.mark.parametrize("rows,V,dtype", PLACES + [(8, 2, F32), (8, 2, BF16), (8, 4097, F32), (8, 1025, F32),
+                                                   (8, 257, BF16), (2000, 4105, BF16)])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_one_nan_wherever_it_lies(rows, V, dtype, shift):
+    """A NaN logit makes its row NaN: at either end, and between columns that are all -inf."""
+    g = torch.Generator(device=DEV).manual_seed(V + shift)
+    buf = torch.zeros(rows * (V + shift) + shift, dtype=dtype, device=DEV)
+    x = buf[shift:].view(rows, V + shift)[:, :V]
+    x.copy_(torch.randn((rows, V), generator=g, device=DEV) * 2.0)
+    lab = torch.ones(rows, dtype=torch.int64, device=DEV)
+    lab[1] = 0
+    at = [(0, 0), (1, V - 1)]
+    if V > 64:
+        x[3:6] = NEG
+        x[3:6, 1] = 1.0
+        at += [(3, V // 2), (4, V - 1), (5, 40)]
+    for r, c in at:
+        x[r, c] = NAN
+    bad = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    bad[[r for r, _ in at]] = True
+    one = torch.ones(rows, device=DEV)
+    idx = torch.stack([lab, 1 - lab], 1)
+    sel, H = gbce.selective_logsoftmax(x, lab, with_entropy=True)
+    two, H2 = gbce.selective_logsoftmax(x, idx, with_entropy=True)
+    f = gbce.ce_fwd(x, lab, reduction="none")
+    c = gbce.ce_fwd(x, lab, reduction="none", softcap=30.0)
+    u = gbce.ce_fwd_bwd_fused(x, lab, one, reduction="none")
+    n = gbce.ce_fwd_bwd_fused_noalloc(x, lab, one, reduction="none")
+    only = gbce.selective_logsoftmax(x, lab)
+    b = gbce.ce_bwd(x, lab, one, f.logp, reduction="none")
+    s = gbce.selective_logsoftmax_bwd(x, lab, one, only)
+    for name, v in dict(sel=sel, H=H, H2=H2, two=two[:, 0], ce=f.loss, cap=c.loss, fused=u.loss, noalloc=n.loss,
+                        only=only).items():
+        assert torch.equal(torch.isnan(v), bad), name
+    for name, d in dict(fused=u.dlogits, noalloc=n.dlogits, ce_bwd=b, selective_bwd=s).items():
+        assert torch.equal(torch.isnan(d).all(1), bad) and torch.equal(torch.isnan(d).any(1), bad), name
+    if shift == 0 and V > 64:
+        cuts = [0, V // 3, V // 2, V]
+        parts = [gbce.vocab_slice_stats(x[:, i:j], lab, i, V) for i, j in zip(cuts, cuts[1:])]
+        assert torch.equal(torch.isnan(gbce.vocab_slice_combine(torch.stack(parts), cuts, lab.view(-1, 1))[0]).view(-1), bad)
