@@ -124,16 +124,17 @@ struct RestStats {
             nmc = nmc_new;
         }
     }
-    // (a vmax that is not far lies beside another thread's far one, which drops it)
-    __device__ __forceinline__ void raise_to_far(float vmax, float far)
+    // A far max (or the one there is) and what was added to it.
+    __device__ __forceinline__ void add_far(float2 max_sum)
     {
-        if (vmax > m && fabsf(vmax) >= far) {
+        if (max_sum.x > m) {
             const float2 zero = make_float2(0.0f, 0.0f);
             sa = fmul2(sa, zero);  // (a NaN stays)
             sb = fmul2(sb, zero);
-            m = vmax;
-            nmc = vmax > 0.0f ? kNegInf : __builtin_huge_valf();
+            m = max_sum.x;
+            nmc = m > 0.0f ? kNegInf : __builtin_huge_valf();
         }
+        sa.x += max_sum.y;
     }
     // (the large part of x c meets the shift first, where the two cancel: what is
     // rounded is the exponent's own size, and at the max it is residual()'s very steps)
@@ -154,8 +155,8 @@ struct RestStats {
             raise_to(x, c);
             sa.x += ex2(fmaf(x, c.lo, fmaf(x, c.hi, nmc)));
         } else if (x != kNegInf) {
-            raise_to_far(x, far);
-            sa.x += far_term(x, m);
+            const float top = x > m ? x : m;
+            add_far(make_float2(top, far_term(x, top)));
         }
     }
     // What a logit adds beside a far max `top`: +inf and NaN have no softmax.
@@ -742,25 +743,37 @@ __device__ __forceinline__ void rest_add(RestStats &st, const uint4 &a, TwoFloat
            make_float2(__uint_as_float(a.z), __uint_as_float(a.w)), c);
 }
 
-// ... and one whose largest logit is far, NaN or -inf (few are).
-template <typename T>
-__device__ __forceinline__ void rest_add_far(RestStats &st, const uint4 &a, float far)
+__device__ __forceinline__ uint4 all_neg_inf(float)
+{
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+}
+__device__ __forceinline__ uint4 all_neg_inf(__nv_bfloat16)
+{
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+}
+
+// Two vectors whose largest logit is far, NaN or -inf, beside a max m: the new max,
+// and what they add to it.  Out of line, for few are and the sweeps' loops stay short.
+template <typename T> static __device__ __noinline__ float2 far_pair(uint4 a, uint4 b, float m, float far)
 {
     constexpr int VEC = Elem<T>::kVec;
-    const float top = FastVec<T>::vmax(a);
+    const float top = FastVec<T>::vmax(a, b);
     if (top == kNegInf) {
         // nothing, unless there are NaN, which a max passes over
-        constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        if (((a.x ^ none) | (a.y ^ none) | (a.z ^ none) | (a.w ^ none)) != 0)
-            st.sa.x = kQuietNan;
-        return;
+        const uint32_t none = all_neg_inf(T()).x;
+        const uint32_t other = (a.x ^ none) | (a.y ^ none) | (a.z ^ none) | (a.w ^ none) |
+                               (b.x ^ none) | (b.y ^ none) | (b.z ^ none) | (b.w ^ none);
+        return make_float2(m, other == 0 ? 0.0f : kQuietNan);
     }
-    st.raise_to_far(top, far);
-    float f[VEC];
+    // (a top that is not far lies beside another thread's far one, which drops it)
+    const float M = top > m && fabsf(top) >= far ? top : m;
+    float f[VEC], g[VEC], s = 0.0f;
     Elem<T>::unpack(a, f);
+    Elem<T>::unpack(b, g);
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-        st.sa.x += RestStats::far_term(f[e], st.m);
+        s += RestStats::far_term(f[e], M) + RestStats::far_term(g[e], M);
+    return make_float2(M, s);
 }
 
 // One vector, and two with `top` the largest of them, or of the warp's.
@@ -772,7 +785,7 @@ __device__ __forceinline__ void rest_take(RestStats &st, const uint4 &a, TwoFloa
         st.raise_to(top, c);
         rest_add(st, a, c, static_cast<const T *>(nullptr));
     } else {
-        rest_add_far<T>(st, a, far);
+        st.add_far(far_pair<T>(a, all_neg_inf(T()), st.m, far));
     }
 }
 
@@ -785,8 +798,7 @@ __device__ __forceinline__ void rest_take(RestStats &st, const uint4 &a, const u
         rest_add(st, a, c, static_cast<const T *>(nullptr));
         rest_add(st, b, c, static_cast<const T *>(nullptr));
     } else {
-        rest_add_far<T>(st, a, far);
-        rest_add_far<T>(st, b, far);
+        st.add_far(far_pair<T>(a, b, st.m, far));
     }
 }
 

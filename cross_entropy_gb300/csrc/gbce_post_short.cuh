@@ -407,8 +407,7 @@ __global__ void __launch_bounds__(RowGroup<W>::kCta, W == 8 ? 4 : 8)
     if (kStats) {
         constexpr int U = 4;
         RestStats st;
-        uint4 none;
-        none.x = none.y = none.z = none.w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+        const uint4 none = all_neg_inf(T());
         for (int v = tid; v < nv; v += U * NT) {
             uint4 raw[U];
 #pragma unroll
