@@ -18,8 +18,8 @@
 // row before, and finishes the loss of each swept row.  What bounds it is HBM:
 // logits once in, gradients once out; the gradient pass reads its row from L2.
 // At 8192 x 152064 bf16, of 6.79 TB/s measured for a copy: distillation with 64
-// entries 787 us (0.91), policy loss with 15% of the rows left out 717 us (0.95),
-// preference loss of 4096 rows, whose logits are read twice, 487 us (0.94 of the
+// entries 778 us (0.92), policy loss with 15% of the rows left out 725 us (0.94),
+// preference loss of 4096 rows, whose logits are read twice, 490 us (0.93 of the
 // bytes it moves).
 #pragma once
 

@@ -77,16 +77,16 @@ cudaError_t launch_post_short(const PostParams &p, int op, int pass, cudaStream_
 
 // Bytes of a row up to which it goes there, unless it is one of a few and longer
 // than kShortAlwaysBytes.  Two CTAs of the longest fit an SM.  Streamed / kept, us:
-// policy loss, 4000 x 8192 bf16 41 / 28, 1922 x 32768 50 / 45, 8000 x 35000 187 / 175, 4000 x
-// 50000 133 / 131; preference loss, 4000 x 50000 174 / 167; distillation, 8192 x 2000 77 / 22,
-// 8192 x 32768 204 / 177, 1000 x 40000 47 / 41, 4000 x 40000 127 / 127; of 140 KB and more:
+// policy loss, 4000 x 8192 bf16 50 / 29, 1922 x 32768 52 / 48, 8000 x 35000 198 / 182, 4000 x
+// 50000 135 / 140; preference loss, 4000 x 50000 174 / 173; distillation, 8192 x 2000 114 / 24,
+// 8192 x 32768 205 / 186, 1000 x 40000 47 / 41, 4000 x 40000 124 / 130; of 140 KB and more:
 // policy loss, 8000 x 70000 363 / 488, 1500 x 100000 117 / 132.
 constexpr int64_t kShortRowBytes = 104 * 1024, kShortAlwaysBytes = 64 * 1024, kShortFewest = 16;
 // ... to one warp (where there are more rows than kShortFewRows), to four, to
-// eight.  One / two / four / eight warps, us: policy loss, 8192 x 300 bf16 13 / - / 30 / 52,
-// 8192 x 4000 29 / 38 / 38 / 61, 4000 x 8192 32 / 32 / 29 / 38, 8000 x 12000 80 / 70 / 66 / 82;
-// preference loss, 4000 x 20000 112 / 89 / 75 / 78; policy loss, 1922 x 32768 - / - / 48 / 45.
-// Few rows: distillation, 100 x 3000 one warp 8.4, four 7.2; 1000 x 2000 9.1, 10.5.
+// eight.  One / four / eight warps, us: policy loss, 8192 x 300 bf16 12 / 30 / 54, 8192 x
+// 4000 30 / 39 / 64, 4000 x 8192 30 / 29 / 39, 8000 x 12000 80 / 68 / 87; preference loss,
+// 4000 x 20000 - / 72 / 75; policy loss, 1922 x 32768 - / 50 / 48.  Few rows: distillation,
+// 100 x 3000 one warp 8.0, four 6.7; 1000 x 2000 9.0, 9.5.
 constexpr int64_t kShortWarpBytes = 8192, kShortMidBytes = 49152, kShortFewRows = 400;
 // The most shared memory a CTA of theirs takes.
 constexpr int kShortSmemMax = kShortRowBytes + 64 + 8 * kMaxListed;
