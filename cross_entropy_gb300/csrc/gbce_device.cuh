@@ -487,13 +487,13 @@ template <> struct Elem<__nv_bfloat16> {
 // so that s = sum_j exp((x_j - m) / T).  Excluded columns are fed as -inf.
 // The sum is kept in two packed pairs (four independent accumulators).
 //
-// A logit with x c below -2^31 (a mask of the type's lowest value, whose x c is not
+// A logit with x c below -2^32 (a mask of the type's lowest value, whose x c is not
 // even finite) is past what a shift can be taken off: beside any other it has no mass,
-// and it gets none.  The shift stops at 2^31, under which its exponent is below -2^7;
+// and it gets none.  The shift stops at 2^32, under which its exponent is -2^8 or less;
 // a row in which nothing else turns up has a max but a sum of 0 (finalize_logp).
 // Beside moments the max stops at -2^100, so that what a merge multiplies a sum of 0
 // with is finite.
-constexpr float kFarShift = 0x1p31f, kFarMax = -0x1p100f;
+constexpr float kFarShift = 0x1p32f, kFarMax = -0x1p100f;
 
 template <bool ENT, bool SUMX = false>
 struct OnlineStats {

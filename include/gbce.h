@@ -37,9 +37,9 @@
  *    carry the fp32 rounding of cap * tanh(x / cap) in every exponent.  A
  *    backward call takes the forward's fp32 log p and entropy as they are.
  *  - Masked columns and NaN.  A logit of -inf, or one so far below (x / T under
- *    -1.5e9, the type's lowest value for one) that no shift can be taken off it,
+ *    -1.48e9, the type's lowest value for one) that no shift can be taken off it,
  *    has no mass beside any other.  Except in the losses of post-training, a row
- *    that holds nothing else (and is not all -inf) is NaN.  A NaN logit makes its
+ *    that holds nothing else (and is not all -inf) can be NaN; under -2.98e9 it is.  A NaN logit makes its
  *    row's outputs NaN, and no other row's.
  *  - Asynchrony.  Every call only enqueues work on `stream` and returns; it
  *    never synchronizes the host.  The returned status reports HOST-side

@@ -192,3 +192,18 @@ def test_one_nan_wherever_it_lies(rows, V, dtype, shift):
         cuts = [0, V // 3, V // 2, V]
         parts = [gbce.vocab_slice_stats(x[:, i:j], lab, i, V) for i, j in zip(cuts, cuts[1:])]
         assert torch.equal(torch.isnan(gbce.vocab_slice_combine(torch.stack(parts), cuts, lab.view(-1, 1))[0]).view(-1), bad)
+
+
+@pytest.mark.parametrize("rows,V,dtype", PLACES)
+def test_logits_far_from_zero_at_a_low_temperature(rows, V, dtype):
+    """x / T of -1.34e9 to -1.48e9: x c above -2^31, so every row keeps its log p.  (Below it the shift's
+    half step is 128, and 2^-128 is not a normal number: some rows' sums are 0, and their log p NaN.)"""
+    g = torch.Generator(device=DEV).manual_seed(V + 5)
+    T = 2.0 ** -26
+    x = (-22.0 + 2.0 * torch.rand((rows, V), generator=g, device=DEV)).to(dtype)
+    lab = torch.randint(0, V, (rows,), generator=g, device=DEV)
+    x[0, lab[0]] = -19.0
+    z = x.double() / T
+    want = torch.log_softmax(z, 1).gather(1, lab.unsqueeze(1))[:, 0]
+    for got in (gbce.selective_logsoftmax(x, lab, T), -gbce.ce_fwd(x, lab, temperature=T, reduction="none").loss):
+        assert bool(((got.double() - want).abs() <= LOGP_TOL[dtype] * want.abs() + 1e-30).all())
